@@ -46,6 +46,17 @@ SIGNATURES = {
     "agoq_gemm_accumulate": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _U64, _P]),
     "agoq_gemm_laaq_quantize": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _U64, _P]),
     "taco_gemm_workspace_bytes": (ctypes.c_int, [_I64, _I64, _I64, _P]),
+    "fp8_pitch": (ctypes.c_int64, [_I64]),
+    "fp8_quantize": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P]),
+    "fp8_quantize_weight": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P]),
+    "fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I64, _I64, _I64, _P, _I32, _P]),
+    "fp8_linear_workspace_bytes": (ctypes.c_int, [_I64, _I64, _I64, _I32, _P]),
+    "fp8_linear": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _U64, _P]),
+    "fp8_linear_backward": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I32, _P, _U64, _P]),
+    "rmsnorm_gate_residual": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _F32, _F32, _I64, _I64, _P, _P, _P, _P]),
+    "rmsnorm_gate_residual_workspace_bytes": (ctypes.c_int, [_I64, _I64, _I32, _P]),
+    "rmsnorm_gate_residual_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32, _F32, _F32, _I64, _I64,
+                                                      _P, _P, _P, _P, _P, _P, _U64, _P]),
     "taco_host_pipeline_create": (ctypes.c_int, [_I32, _I64, _I64, _I32, _I32, _I32,
                                                  ctypes.POINTER(ctypes.c_void_p),
                                                  ctypes.POINTER(ctypes.c_uint64)]),

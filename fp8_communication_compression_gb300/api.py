@@ -9,6 +9,7 @@ libtaco.so.  Every step of the codec runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Sequence
 
 import torch
@@ -438,6 +439,281 @@ def agoq_gemm_laaq_quantize(a: torch.Tensor, b: torch.Tensor, bits: int = 4, blo
                                              ws, ws_bytes, _stream_handle(stream))
     _lib.check("agoq_gemm_laaq_quantize", st)
     return packed, scale
+
+
+# ------------------------------------------- block-scaled FP8 matrices --
+
+def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """An output or workspace for a call on ``stream``: memory of the current
+    stream's pool, kept from reuse until work queued on ``stream`` is done."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _need2(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> None:
+    _need(t, name, dtypes)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+
+
+def _matrix(x: torch.Tensor, name: str):
+    """(rows, columns) of a bf16 matrix; leading dimensions count as rows."""
+    _need(x, name, (torch.bfloat16,))
+    if x.dim() < 2:
+        raise ValueError(f"{name} must have at least two dimensions")
+    cols = x.shape[-1]
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    return rows, cols
+
+
+def fp8_pitch(cols: int) -> int:
+    """Length of a row of codes: ``cols`` rounded up to a multiple of 16."""
+    return -(-cols // 16) * 16
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def fp8_quantize(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, stream=None):
+    """x bf16 [..., cols], as a matrix of ``rows`` rows, to E4M3 codes with one
+    power-of-two scale (an E8M0 byte, 2^(byte - 127)) per block of 128.
+
+    ``rowwise``: (codes uint8 [rows, fp8_pitch(cols)], scale uint8
+    [ceil(cols / 128), rows]), blocks along the rows.  ``colwise``: (codes_t
+    [cols, fp8_pitch(rows)], scale_t [ceil(rows / 128), cols]), the transposed
+    matrix in blocks along its own rows.  With both, all four from one pass
+    over x.  The padding codes are zero (NaN in a block that holds an Inf or
+    a NaN)."""
+    rows, cols = _matrix(x, "x")
+    if not (rowwise or colwise):
+        raise ValueError("rowwise or colwise must be set")
+    dev, u8 = x.device, torch.uint8
+    out = ()
+    if rowwise:
+        out += (_new((rows, fp8_pitch(cols)), u8, dev, stream), _new((_blocks(cols), rows), u8, dev, stream))
+    if colwise:
+        out += (_new((cols, fp8_pitch(rows)), u8, dev, stream), _new((_blocks(rows), cols), u8, dev, stream))
+    ptrs = [t.data_ptr() for t in out]
+    ptrs = ptrs if len(ptrs) == 4 else ptrs + [None, None] if rowwise else [None, None] + ptrs
+    st = _lib.load().fp8_quantize(x.data_ptr(), rows, cols, *ptrs, _stream_handle(stream))
+    _lib.check("fp8_quantize", st)
+    return out
+
+
+def fp8_quantize_weight(w: torch.Tensor, stream=None):
+    """A weight bf16 [N, K] in 128 x 128 tiles, one scale byte each: (codes
+    uint8 [N, fp8_pitch(K)], scale uint8 [ceil(K / 128), ceil(N / 128)], codes_t
+    [K, fp8_pitch(N)], scale_t [ceil(N / 128), ceil(K / 128)]); the transposed
+    codes are the operand of the gradient at the layer's input."""
+    N, K = _matrix(w, "w")
+    dev, u8 = w.device, torch.uint8
+    out = (_new((N, fp8_pitch(K)), u8, dev, stream), _new((_blocks(K), _blocks(N)), u8, dev, stream),
+           _new((K, fp8_pitch(N)), u8, dev, stream), _new((_blocks(N), _blocks(K)), u8, dev, stream))
+    st = _lib.load().fp8_quantize_weight(w.data_ptr(), N, K, *[t.data_ptr() for t in out], _stream_handle(stream))
+    _lib.check("fp8_quantize_weight", st)
+    return out
+
+
+def _out_dtype(out: torch.Tensor | None, out_dtype: torch.dtype) -> torch.dtype:
+    dt = out_dtype if out is None else out.dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the output is bfloat16 or float32, not {dt}")
+    return dt
+
+
+def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+             out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """a @ b.T of two quantised matrices on the tensor cores: a uint8 [M, P]
+    with a_scale [ceil(P / 128), M]; b uint8 [N, P] with b_scale [ceil(P / 128),
+    N], or one byte per 128 rows [ceil(P / 128), ceil(N / 128)] (a weight).
+    fp32 accumulation in a fixed order; bf16 or fp32 [M, N]."""
+    _need(a, "a", _U8)
+    _need(b, "b", _U8)
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError("a must be [M, P] and b [N, P]")
+    (M, P), N = a.shape, b.shape[0]
+    _need2(a_scale, "a_scale", (torch.uint8,), _blocks(P), M)
+    tiles = b_scale.dim() == 2 and b_scale.shape[1] != N
+    _need2(b_scale, "b_scale", (torch.uint8,), _blocks(P), _blocks(N) if tiles else N)
+    dt = _out_dtype(out, out_dtype)
+    if out is None:
+        out = _new((M, N), dt, a.device, stream)
+    else:
+        _need2(out, "out", (dt,), M, N)
+    st = _lib.load().fp8_gemm(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), int(tiles), M, N, P,
+                              out.data_ptr(), int(dt == torch.bfloat16), _stream_handle(stream))
+    _lib.check("fp8_gemm", st)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_workspace_bytes(M: int, N: int, K: int, backward: int) -> int:
+    v = ctypes.c_uint64(0)
+    _lib.check("fp8_linear_workspace_bytes",
+               _lib.load().fp8_linear_workspace_bytes(M, N, K, backward, ctypes.byref(v)))
+    return int(v.value)
+
+
+def fp8_linear(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
+               out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """A linear layer in FP8: x bf16 [..., K], quantised in blocks of 128 along
+    its rows, times the transpose of a weight [N, K] held as
+    fp8_quantize_weight's (codes, scale); bf16 or fp32 [..., N]."""
+    M, K = _matrix(x, "x")
+    _need(codes, "codes", _U8)
+    if codes.dim() != 2 or codes.shape[1] != fp8_pitch(K):
+        raise ValueError(f"codes has shape {tuple(codes.shape)}, expected (N, {fp8_pitch(K)})")
+    N = codes.shape[0]
+    _need2(scale, "scale", (torch.uint8,), _blocks(K), _blocks(N))
+    dt = _out_dtype(out, out_dtype)
+    if out is None:
+        out = _new((*x.shape[:-1], N), dt, x.device, stream)
+    else:
+        _need(out, "out", (dt,), M * N)
+    nbytes = _linear_workspace_bytes(M, N, K, 0)
+    ws = _new(nbytes, torch.uint8, x.device, stream)
+    st = _lib.load().fp8_linear(x.data_ptr(), codes.data_ptr(), scale.data_ptr(), M, N, K, out.data_ptr(),
+                                int(dt == torch.bfloat16), ws.data_ptr(), nbytes, _stream_handle(stream))
+    _lib.check("fp8_linear", st)
+    return out
+
+
+def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor, codes_t: torch.Tensor, scale_t: torch.Tensor,
+                        dw_dtype: torch.dtype = torch.float32, need_dx: bool = True, need_dw: bool = True,
+                        stream=None):
+    """Gradients of fp8_linear: dy bf16 [..., N], x bf16 [..., K], the weight's
+    transposed (codes_t, scale_t).  Returns (dx bf16 like x, dw [N, K] fp32 or
+    bf16); dy is quantised along its rows for dx and, like x, in blocks of
+    128 rows for dw, in one pass.  ``need_dx`` / ``need_dw`` = False: None in
+    that place."""
+    M, N = _matrix(dy, "dy")
+    Mx, K = _matrix(x, "x")
+    if Mx != M:
+        raise ValueError(f"dy has {M} rows and x {Mx}")
+    if not (need_dx or need_dw):
+        raise ValueError("need_dx or need_dw must be set")
+    _need2(codes_t, "codes_t", _U8, K, fp8_pitch(N))
+    _need2(scale_t, "scale_t", (torch.uint8,), _blocks(N), _blocks(K))
+    dt = _out_dtype(None, dw_dtype)
+    dx = _new(x.shape, torch.bfloat16, x.device, stream) if need_dx else None
+    dw = _new((N, K), dt, x.device, stream) if need_dw else None
+    nbytes = _linear_workspace_bytes(M, N, K, 1)
+    ws = _new(nbytes, torch.uint8, x.device, stream)
+    st = _lib.load().fp8_linear_backward(dy.data_ptr(), x.data_ptr(), codes_t.data_ptr(), scale_t.data_ptr(), M, N, K,
+                                         dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None,
+                                         int(dt == torch.bfloat16), ws.data_ptr(), nbytes, _stream_handle(stream))
+    _lib.check("fp8_linear_backward", st)
+    return dx, dw
+
+
+# ------------------------------------------------- norms around a block --
+
+def _gate_mode(gate: torch.Tensor | None, T: int, d: int) -> int:
+    """TACO_GATE_* of a gate: None, fp32 [d], fp32 [T, 1] or bf16 [T, d]."""
+    if gate is None:
+        return 0
+    if isinstance(gate, torch.Tensor) and gate.dtype == torch.bfloat16:
+        _need2(gate, "gate", (torch.bfloat16,), T, d)
+        return 3
+    _need(gate, "gate", (torch.float32,))
+    if gate.dim() == 1 and gate.shape[0] == d:
+        return 1
+    if gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] == 1:
+        return 2
+    raise ValueError(f"gate has shape {tuple(gate.shape)}, expected fp32 ({d},), fp32 ({T}, 1) or bf16 ({T}, {d})")
+
+
+def _norm_args(y, h, gain_post, gain_pre, gate):
+    T, d = _matrix(y, "y")
+    _need(h, "h", (torch.bfloat16,))
+    if h.shape != y.shape:
+        raise ValueError(f"y has shape {tuple(y.shape)} and h {tuple(h.shape)}")
+    _need(gain_post, "gain_post", (torch.float32,), d)
+    _need(gain_pre, "gain_pre", (torch.float32,), d)
+    return T, d, _gate_mode(gate, T, d)
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def rmsnorm_gate_residual(y: torch.Tensor, h: torch.Tensor, gain_post: torch.Tensor, gain_pre: torch.Tensor,
+                          gate: torch.Tensor | None = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                          stream=None):
+    """The norms between one block and the next, in one pass:
+
+        z = rmsnorm(y) * gain_post;  h_new = residual_scale * h + gate * z
+        n = rmsnorm(h_new) * gain_pre
+
+    y (the block's output) and h (the residual stream) bf16 [..., d]; gains
+    fp32 [d]; gate None, fp32 [d], fp32 [T, 1] or bf16 [T, d] with T the
+    number of rows.  Returns (h_new, n), bf16 like y; n is taken from h_new
+    before its rounding."""
+    T, d, mode = _norm_args(y, h, gain_post, gain_pre, gate)
+    h_new = _new(y.shape, torch.bfloat16, y.device, stream)
+    n = _new(y.shape, torch.bfloat16, y.device, stream)
+    st = _lib.load().rmsnorm_gate_residual(y.data_ptr(), h.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
+                                           _ptr(gate), mode, residual_scale, eps, T, d, h_new.data_ptr(),
+                                           n.data_ptr(), None, _stream_handle(stream))
+    _lib.check("rmsnorm_gate_residual", st)
+    return h_new, n
+
+
+def rmsnorm_gate_residual_fp8(y: torch.Tensor, h: torch.Tensor, gain_post: torch.Tensor, gain_pre: torch.Tensor,
+                              gate: torch.Tensor | None = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                              stream=None):
+    """rmsnorm_gate_residual with n quantised as it is written: (h_new, codes
+    uint8 [T, fp8_pitch(d)], scale uint8 [ceil(d / 128), T]), the operand of
+    fp8_gemm (blocks of 128 along the rows, from the fp32 n)."""
+    T, d, mode = _norm_args(y, h, gain_post, gain_pre, gate)
+    h_new = _new(y.shape, torch.bfloat16, y.device, stream)
+    codes = _new((T, fp8_pitch(d)), torch.uint8, y.device, stream)
+    scale = _new((_blocks(d), T), torch.uint8, y.device, stream)
+    st = _lib.load().rmsnorm_gate_residual(y.data_ptr(), h.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
+                                           _ptr(gate), mode, residual_scale, eps, T, d, h_new.data_ptr(),
+                                           codes.data_ptr(), scale.data_ptr(), _stream_handle(stream))
+    _lib.check("rmsnorm_gate_residual", st)
+    return h_new, codes, scale
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_workspace_bytes(T: int, d: int, mode: int, device: int) -> int:
+    v = ctypes.c_uint64(0)
+    _lib.check("rmsnorm_gate_residual_workspace_bytes",
+               _lib.load().rmsnorm_gate_residual_workspace_bytes(T, d, mode, ctypes.byref(v)))
+    return int(v.value)
+
+
+def rmsnorm_gate_residual_backward(dn: torch.Tensor, dh_new: torch.Tensor, y: torch.Tensor, h_new: torch.Tensor,
+                                   gain_post: torch.Tensor, gain_pre: torch.Tensor, gate: torch.Tensor | None = None,
+                                   residual_scale: float = 1.0, eps: float = 1e-6, stream=None):
+    """Gradients of rmsnorm_gate_residual from those at n and h_new (bf16
+    [..., d]), y and the forward's h_new: (dy, dh, dgain_post, dgain_pre,
+    dgate); dgate has the gate's shape and type (None without one).  The gain
+    gradients are summed over the rows in a fixed order."""
+    T, d, mode = _norm_args(y, h_new, gain_post, gain_pre, gate)
+    for t, name in ((dn, "dn"), (dh_new, "dh_new")):
+        _need(t, name, (torch.bfloat16,))
+        if t.shape != y.shape:
+            raise ValueError(f"y has shape {tuple(y.shape)} and {name} {tuple(t.shape)}")
+    dev = y.device
+    dy, dh = _new(y.shape, torch.bfloat16, dev, stream), _new(y.shape, torch.bfloat16, dev, stream)
+    dg_post = _new((d,), torch.float32, dev, stream)
+    dg_pre = _new((d,), torch.float32, dev, stream)
+    dgate = None if gate is None else _new(gate.shape, gate.dtype, dev, stream)
+    nbytes = _norm_workspace_bytes(T, d, mode, dev.index)
+    ws = _new(nbytes, torch.uint8, dev, stream)
+    st = _lib.load().rmsnorm_gate_residual_backward(
+        dn.data_ptr(), dh_new.data_ptr(), y.data_ptr(), h_new.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
+        _ptr(gate), mode, residual_scale, eps, T, d, dy.data_ptr(), dh.data_ptr(), dg_post.data_ptr(),
+        dg_pre.data_ptr(), _ptr(dgate), ws.data_ptr(), nbytes, _stream_handle(stream))
+    _lib.check("rmsnorm_gate_residual_backward", st)
+    return dy, dh, dg_post, dg_pre, dgate
 
 
 def taco_device_error(clear: bool = True) -> int:

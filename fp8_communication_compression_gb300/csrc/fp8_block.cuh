@@ -1,0 +1,46 @@
+// The FP8 operand format of the block-scaled products: E4M3 codes with one
+// power-of-two scale (an E8M0 byte, 2^(byte - 127)) per block of 128.
+//
+//   E = the smallest integer with amax <= 448 2^E, at least -127
+//   code = E4M3(x 2^-E), byte = E + 127; byte 127 for a block of zeros
+//
+// 448 is 1.75 2^8, so E is amax's exponent - 8, and one more where its
+// fraction is above 1.75: an integer addition to amax's bit pattern that
+// carries into the exponent.  x 2^-E is exact (the scale is a power of two
+// and the product cannot overflow), so the only rounding is the one to
+// E4M3 (nearest even), and the codes do not depend on the precision or the
+// order of the arithmetic.  A block that holds an Inf or a NaN gets the
+// format's NaN scale (byte 255) and NaN codes, so that it stays visible in
+// every product that reads it.
+#pragma once
+
+#include <cstdint>
+
+#include "device_utils.cuh"
+
+namespace taco {
+
+constexpr int kFp8Block = 128;
+
+// Codes are stored in rows padded with zero codes to a multiple of 16 bytes
+// (the stride a TMA tensor map needs).
+__host__ __device__ inline int64_t fp8_pitch(int64_t n) { return (n + 15) & ~int64_t(15); }
+
+// Scale byte from the bit pattern of max |x| (fp32, the sign bit clear; an
+// unsigned maximum of such patterns puts Inf and NaN on top).
+__device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax_bits)
+{
+    if (amax_bits >= 0x7F800000u)
+        return 255u;
+    const int b = static_cast<int>((amax_bits + 0x1FFFFFu) >> 23) - 8;
+    return amax_bits == 0u ? 127u : static_cast<uint32_t>(b > 0 ? b : 0);
+}
+
+// 2^-E of a scale byte; NaN for the NaN scale.  (Bytes of finite blocks are
+// at most 247, so the exponent field 254 - byte is that of a normal number.)
+__device__ __forceinline__ float fp8_inv_scale(uint32_t byte)
+{
+    return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : (254u - byte) << 23);
+}
+
+}  // namespace taco

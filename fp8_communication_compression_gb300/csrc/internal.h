@@ -94,9 +94,51 @@ cudaError_t launch_gemm_laaq_quantize(const void *a_bf16, const void *b_bf16, in
 // (0 when it takes none).
 cudaError_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, uint64_t *bytes);
 
+// Block-scaled FP8 operands (fp8_quantize.cu; format in fp8_block.cuh): codes
+// [rows][pitch(cols)] with scale bytes [ceil(cols / 128)][rows], and / or
+// codes_t [cols][pitch(rows)] with scale_t [ceil(rows / 128)][cols]; null
+// codes: that direction is left out.  tiles: one byte per 128 x 128 tile,
+// scale [ceil(cols / 128)][ceil(rows / 128)] and scale_t its transpose.
+cudaError_t launch_fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, bool tiles, uint8_t *codes,
+                                uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, cudaStream_t stream);
+// out[M][N] = A B^T of such operands (fp8_gemm.cu): codes a [M][K], b [N][K]
+// (K the padded row length, a multiple of 16).
+cudaError_t launch_fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
+                            bool b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, bool out_bf16,
+                            cudaStream_t stream);
+
+// The norms around a block (norm_kernels.cu).  n_scale null: n_out is bf16
+// [T][d]; else FP8 codes [T][pitch(d)] and n_scale [ceil(d / 128)][T].
+struct NormForward {
+    const void *y, *h;
+    const float *g_post, *g_pre;
+    const void *gate;
+    int gate_mode;
+    float residual_scale, eps;
+    int64_t T, d;
+    void *h_out, *n_out;
+    uint8_t *n_scale;
+};
+cudaError_t launch_norm_forward(const NormForward &a, cudaStream_t stream);
+struct NormBackward {
+    const void *dn, *dh_out, *y, *h_out;
+    const float *g_post, *g_pre;
+    const void *gate;
+    int gate_mode;
+    float residual_scale, eps;
+    int64_t T, d;
+    void *dy, *dh;
+    float *dg_post, *dg_pre;
+    void *dgate, *workspace;
+};
+cudaError_t launch_norm_backward(const NormBackward &a, cudaStream_t stream);
+cudaError_t norm_backward_workspace(int64_t T, int64_t d, int gate_mode, uint64_t *bytes);
+
 cudaError_t launch_watchdog_selftest(cudaStream_t stream);
 cudaError_t read_codec_error(uint32_t *flags, bool clear);
 cudaError_t read_gemm_error(uint32_t *flags, bool clear);
+cudaError_t read_fp8_error(uint32_t *flags, bool clear);
+cudaError_t read_norm_error(uint32_t *flags, bool clear);
 
 // Launches `kernel` with programmatic stream serialization allowed, so that
 // it can be scheduled while the previous kernel in the stream drains (every

@@ -11,6 +11,7 @@
 #include <new>
 
 #include "../../include/taco.h"
+#include "fp8_block.cuh"
 #include "internal.h"
 
 namespace taco {
@@ -527,6 +528,295 @@ taco_status taco_e4m3_encode(const float *x, int64_t n, uint8_t *codes, taco_str
     return from_cuda(taco::launch_e4m3_encode(x, n, codes, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int64_t fp8_pitch(int64_t cols) { return taco::fp8_pitch(cols); }
+
+// Sizes whose tile grids and TMA coordinates fit the kernels' 32-bit indices.
+static bool fp8_dims_fit(int64_t rows, int64_t cols)
+{
+    constexpr int64_t kMax = int64_t(1) << 30;
+    return rows <= kMax && cols <= kMax && ((rows + 127) / 128) * ((cols + 127) / 128) <= kMax;
+}
+
+static int64_t fp8_blocks(int64_t n) { return (n + 127) / 128; }
+
+// A buffer of a call: no output may overlap an input or another output.
+struct Span {
+    const void *p;
+    uint64_t n;
+};
+
+static bool apart(const Span *outs, int n_outs, const Span *ins, int n_ins)
+{
+    for (int i = 0; i < n_outs; ++i) {
+        for (int j = i + 1; j < n_outs; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return false;
+        for (int j = 0; j < n_ins; ++j)
+            if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n))
+                return false;
+    }
+    return true;
+}
+
+static taco_status fp8_quantize_any(const void *x, int64_t rows, int64_t cols, bool tiles, uint8_t *codes,
+                                    uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, taco_stream_t stream)
+{
+    if (rows < 0 || cols < 0)
+        return TACO_ERR_INVALID_ARG;
+    if (!fp8_dims_fit(rows, cols))
+        return TACO_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0)
+        return TACO_OK;
+    if ((codes == nullptr) != (scale == nullptr) || (codes_t == nullptr) != (scale_t == nullptr) ||
+        (!codes && !codes_t) || !x)
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || (codes && !aligned(codes, 16)) || (codes_t && !aligned(codes_t, 16)))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t r = rows, c = cols, rb = fp8_blocks(rows), cb = fp8_blocks(cols);
+    const Span outs[4] = {{codes, codes ? r * taco::fp8_pitch(cols) : 0},
+                          {scale, scale ? cb * (tiles ? rb : r) : 0},
+                          {codes_t, codes_t ? c * taco::fp8_pitch(rows) : 0},
+                          {scale_t, scale_t ? rb * (tiles ? cb : c) : 0}};
+    const Span ins[1] = {{x, 2 * r * c}};
+    if (!apart(outs, 4, ins, 1))
+        return TACO_ERR_INVALID_ARG;
+    return from_cuda(taco::launch_fp8_quantize(x, rows, cols, tiles, codes, scale, codes_t, scale_t,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+taco_status fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scale,
+                         uint8_t *codes_t, uint8_t *scale_t, taco_stream_t stream)
+{
+    return fp8_quantize_any(x_bf16, rows, cols, false, codes, scale, codes_t, scale_t, stream);
+}
+
+taco_status fp8_quantize_weight(const void *x_bf16, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scale,
+                                uint8_t *codes_t, uint8_t *scale_t, taco_stream_t stream)
+{
+    return fp8_quantize_any(x_bf16, rows, cols, true, codes, scale, codes_t, scale_t, stream);
+}
+
+taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
+                     int32_t b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, int32_t out_is_bf16,
+                     taco_stream_t stream)
+{
+    if (M < 0 || N < 0 || K < 0 || K % 16 != 0)
+        return TACO_ERR_INVALID_ARG;
+    if (!fp8_dims_fit(M, K) || !fp8_dims_fit(N, K) || !fp8_dims_fit(M, N))
+        return TACO_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0)
+        return TACO_OK;
+    if (!out || (K > 0 && (!a || !a_scale || !b || !b_scale)))
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || (K > 0 && (!aligned(a, 16) || !aligned(b, 16))))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t m = M, n = N, k = K, kb = fp8_blocks(K);
+    const Span outs[1] = {{out, m * n * (out_is_bf16 ? 2 : 4)}};
+    const Span ins[4] = {{a, m * k}, {b, n * k}, {a_scale, kb * m}, {b_scale, kb * (b_scale_tiles ? fp8_blocks(N) : n)}};
+    if (!apart(outs, 1, ins, 4))
+        return TACO_ERR_INVALID_ARG;
+    return from_cuda(taco::launch_fp8_gemm(a, a_scale, b, b_scale, b_scale_tiles != 0, M, N, K, out, out_is_bf16 != 0,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The pieces of a linear layer's workspace, each 256-byte aligned: a
+// quantised matrix [rows][cols] is its codes and its scales.
+static uint64_t fp8_piece(int64_t rows, int64_t cols, uint64_t *scale_at)
+{
+    const auto up = [](uint64_t v) { return (v + 255) & ~uint64_t(255); };
+    const uint64_t codes = up(static_cast<uint64_t>(rows) * taco::fp8_pitch(cols));
+    if (scale_at)
+        *scale_at = codes;
+    return codes + up(static_cast<uint64_t>(fp8_blocks(cols)) * rows);
+}
+
+taco_status fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward, uint64_t *bytes)
+{
+    if (!bytes || M < 0 || N < 0 || K < 0)
+        return TACO_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (!fp8_dims_fit(M, K) || !fp8_dims_fit(N, K) || !fp8_dims_fit(M, N))
+        return TACO_ERR_UNSUPPORTED;
+    *bytes = backward ? fp8_piece(M, N, nullptr) + fp8_piece(N, M, nullptr) + fp8_piece(K, M, nullptr)
+                      : fp8_piece(M, K, nullptr);
+    return TACO_OK;
+}
+
+taco_status fp8_linear(const void *x_bf16, const uint8_t *codes, const uint8_t *scale, int64_t M, int64_t N,
+                       int64_t K, void *y, int32_t y_is_bf16, void *workspace, uint64_t workspace_bytes,
+                       taco_stream_t stream)
+{
+    uint64_t need = 0, scale_at = 0;
+    taco_status st = fp8_linear_workspace_bytes(M, N, K, 0, &need);
+    if (st != TACO_OK || M == 0 || N == 0)
+        return st;
+    if (K > 0 && (!x_bf16 || !codes || !scale || !workspace))
+        return TACO_ERR_INVALID_ARG;
+    if (!y || workspace_bytes < need)
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(workspace, 256))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t pk = taco::fp8_pitch(K), n = N;
+    const Span outs[2] = {{y, static_cast<uint64_t>(M) * n * (y_is_bf16 ? 2 : 4)}, {workspace, need}};
+    const Span ins[3] = {{x_bf16, 2 * static_cast<uint64_t>(M) * K},
+                         {codes, n * pk},
+                         {scale, static_cast<uint64_t>(fp8_blocks(K)) * fp8_blocks(N)}};
+    if (!apart(outs, 2, ins, 3))
+        return TACO_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    fp8_piece(M, K, &scale_at);
+    if (K > 0 && (st = fp8_quantize(x_bf16, M, K, ws, ws + scale_at, nullptr, nullptr, stream)) != TACO_OK)
+        return st;
+    return fp8_gemm(ws, ws + scale_at, codes, scale, 1, M, N, pk, y, y_is_bf16, stream);
+}
+
+taco_status fp8_linear_backward(const void *dy_bf16, const void *x_bf16, const uint8_t *codes_t,
+                                const uint8_t *scale_t, int64_t M, int64_t N, int64_t K, void *dx_bf16, void *dw,
+                                int32_t dw_is_bf16, void *workspace, uint64_t workspace_bytes,
+                                taco_stream_t stream)
+{
+    uint64_t need = 0;
+    taco_status st = fp8_linear_workspace_bytes(M, N, K, 1, &need);
+    if (st != TACO_OK)
+        return st;
+    const bool want_dx = dx_bf16 && M > 0 && K > 0, want_dw = dw && N > 0 && K > 0;
+    if (!dx_bf16 && !dw && M > 0 && N > 0 && K > 0)
+        return TACO_ERR_INVALID_ARG;
+    if (!want_dx && !want_dw)
+        return TACO_OK;
+    const bool data = M > 0 && N > 0;  // else both gradients are sums over nothing
+    if (data && (!dy_bf16 || !workspace || workspace_bytes < need || (want_dx && (!codes_t || !scale_t)) ||
+                 (want_dw && !x_bf16)))
+        return TACO_ERR_INVALID_ARG;
+    if ((want_dx && !aligned(dx_bf16, 16)) || (want_dw && !aligned(dw, 16)) ||
+        (data && (!aligned(dy_bf16, 16) || !aligned(workspace, 256) || (want_dx && !aligned(codes_t, 16)) ||
+                  (want_dw && !aligned(x_bf16, 16)))))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t m = M, n = N, k = K, pn = taco::fp8_pitch(N), pm = taco::fp8_pitch(M);
+    const Span outs[3] = {{dx_bf16, want_dx ? 2 * m * k : 0},
+                          {dw, want_dw ? n * k * (dw_is_bf16 ? 2 : 4) : 0},
+                          {workspace, data ? need : 0}};
+    const Span ins[4] = {{dy_bf16, data ? 2 * m * n : 0},
+                         {x_bf16, data && want_dw ? 2 * m * k : 0},
+                         {codes_t, data && want_dx ? k * pn : 0},
+                         {scale_t, data && want_dx ? static_cast<uint64_t>(fp8_blocks(N)) * fp8_blocks(K) : 0}};
+    if (!apart(outs, 3, ins, 4))
+        return TACO_ERR_INVALID_ARG;
+    if (!data) {
+        if (want_dx && (st = fp8_gemm(nullptr, nullptr, nullptr, nullptr, 1, M, K, 0, dx_bf16, 1, stream)) != TACO_OK)
+            return st;
+        return want_dw ? fp8_gemm(nullptr, nullptr, nullptr, nullptr, 0, N, K, 0, dw, dw_is_bf16, stream) : TACO_OK;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint64_t s0 = 0, s1 = 0, s2 = 0;
+    uint8_t *q = ws, *qt = q + fp8_piece(M, N, &s0), *xt = qt + fp8_piece(N, M, &s1);
+    fp8_piece(K, M, &s2);
+    if ((st = fp8_quantize(dy_bf16, M, N, want_dx ? q : nullptr, want_dx ? q + s0 : nullptr, want_dw ? qt : nullptr,
+                           want_dw ? qt + s1 : nullptr, stream)) != TACO_OK)
+        return st;
+    if (want_dw && (st = fp8_quantize(x_bf16, M, K, nullptr, nullptr, xt, xt + s2, stream)) != TACO_OK)
+        return st;
+    if (want_dx && (st = fp8_gemm(q, q + s0, codes_t, scale_t, 1, M, K, pn, dx_bf16, 1, stream)) != TACO_OK)
+        return st;
+    return want_dw ? fp8_gemm(qt, qt + s1, xt, xt + s2, 0, N, K, pm, dw, dw_is_bf16, stream) : TACO_OK;
+}
+
+// Shared checks of the norms around a block.
+static taco_status check_norm(int64_t T, int64_t d, int32_t gate_mode, float residual_scale, float eps)
+{
+    if (T < 0 || d < 1 || !std::isfinite(residual_scale) || !positive_finite(eps))
+        return TACO_ERR_INVALID_ARG;
+    if (gate_mode < TACO_GATE_NONE || gate_mode > TACO_GATE_FULL)
+        return TACO_ERR_INVALID_ARG;
+    if (d > TACO_NORM_MAX_D || T > (int64_t(1) << 40))
+        return TACO_ERR_UNSUPPORTED;
+    return TACO_OK;
+}
+
+static bool gate_aligned(const void *gate, int32_t mode)
+{
+    return mode == TACO_GATE_NONE || aligned(gate, mode == TACO_GATE_TOKEN ? 4 : 16);
+}
+
+static uint64_t gate_bytes(int32_t mode, int64_t T, int64_t d)
+{
+    return mode == TACO_GATE_NONE ? 0 : mode == TACO_GATE_CHANNEL ? 4 * d : mode == TACO_GATE_TOKEN ? 4 * T : 2 * T * d;
+}
+
+taco_status rmsnorm_gate_residual(const void *y, const void *h, const float *g_post, const float *g_pre,
+                                  const void *gate, int32_t gate_mode, float residual_scale, float eps, int64_t T,
+                                  int64_t d, void *h_out, void *n, uint8_t *n_scale, taco_stream_t stream)
+{
+    taco_status st = check_norm(T, d, gate_mode, residual_scale, eps);
+    if (st != TACO_OK || T == 0)
+        return st;
+    if (!y || !h || !g_post || !g_pre || !h_out || !n || (gate_mode != TACO_GATE_NONE) != (gate != nullptr))
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(h, 16) || !aligned(g_post, 16) || !aligned(g_pre, 16) || !aligned(h_out, 16) ||
+        !aligned(n, 16) || !gate_aligned(gate, gate_mode))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t td = 2 * static_cast<uint64_t>(T) * d, d4 = 4 * static_cast<uint64_t>(d);
+    const Span outs[3] = {{h_out, td},
+                          {n, n_scale ? static_cast<uint64_t>(T) * taco::fp8_pitch(d) : td},
+                          {n_scale, n_scale ? static_cast<uint64_t>(fp8_blocks(d)) * T : 0}};
+    const Span ins[5] = {{y, td}, {h, td}, {g_post, d4}, {g_pre, d4}, {gate, gate_bytes(gate_mode, T, d)}};
+    if (!apart(outs, 3, ins, 5))
+        return TACO_ERR_INVALID_ARG;
+    return from_cuda(taco::launch_norm_forward(
+        {y, h, g_post, g_pre, gate, gate_mode, residual_scale, eps, T, d, h_out, n, n_scale},
+        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+taco_status rmsnorm_gate_residual_workspace_bytes(int64_t T, int64_t d, int32_t gate_mode, uint64_t *bytes)
+{
+    if (!bytes)
+        return TACO_ERR_INVALID_ARG;
+    *bytes = 0;
+    taco_status st = check_norm(T, d, gate_mode, 1.0f, 1.0f);
+    if (st != TACO_OK || T == 0)
+        return st;
+    return from_cuda(taco::norm_backward_workspace(T, d, gate_mode, bytes));
+}
+
+taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, const void *y, const void *h_out,
+                                           const float *g_post, const float *g_pre, const void *gate,
+                                           int32_t gate_mode, float residual_scale, float eps, int64_t T, int64_t d,
+                                           void *dy, void *dh, float *dg_post, float *dg_pre, void *dgate,
+                                           void *workspace, uint64_t workspace_bytes, taco_stream_t stream)
+{
+    taco_status st = check_norm(T, d, gate_mode, residual_scale, eps);
+    if (st != TACO_OK)
+        return st;
+    if (!dg_post || !dg_pre || (gate_mode != TACO_GATE_NONE && !dgate && (T > 0 || gate_mode == TACO_GATE_CHANNEL)) ||
+        (gate_mode == TACO_GATE_NONE && dgate))
+        return TACO_ERR_INVALID_ARG;
+    if (T > 0 && (!dn || !dh_out || !y || !h_out || !g_post || !g_pre || !dy || !dh || !workspace ||
+                  (gate_mode != TACO_GATE_NONE) != (gate != nullptr)))
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(dg_post, 4) || !aligned(dg_pre, 4) || !gate_aligned(dgate, gate_mode) ||
+        (T > 0 && (!aligned(dn, 16) || !aligned(dh_out, 16) || !aligned(y, 16) || !aligned(h_out, 16) ||
+                   !aligned(g_post, 16) || !aligned(g_pre, 16) || !gate_aligned(gate, gate_mode) ||
+                   !aligned(dy, 16) || !aligned(dh, 16) || !aligned(workspace, 256))))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t td = 2 * static_cast<uint64_t>(T) * d, d4 = 4 * static_cast<uint64_t>(d);
+    const uint64_t gb = gate_bytes(gate_mode, T, d);
+    uint64_t need = 0;
+    if (T > 0) {
+        cudaError_t e = taco::norm_backward_workspace(T, d, gate_mode, &need);
+        if (e != cudaSuccess)
+            return TACO_ERR_CUDA;
+        if (workspace_bytes < need)
+            return TACO_ERR_INVALID_ARG;
+    }
+    const Span outs[6] = {{dy, td}, {dh, td}, {dg_post, d4}, {dg_pre, d4}, {dgate, dgate ? gb : 0}, {workspace, need}};
+    const Span ins[7] = {{dn, td}, {dh_out, td}, {y, td}, {h_out, td}, {g_post, d4}, {g_pre, d4}, {gate, gb}};
+    if (!apart(outs, 6, ins, T > 0 ? 7 : 0))
+        return TACO_ERR_INVALID_ARG;
+    return from_cuda(taco::launch_norm_backward({dn, dh_out, y, h_out, g_post, g_pre, gate, gate_mode, residual_scale,
+                                                 eps, T, d, dy, dh, dg_post, dg_pre, dgate, workspace},
+                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
 struct taco_host_pipeline {
     taco::HostPipeline *impl;
 };
@@ -597,11 +887,13 @@ taco_status taco_device_error(uint32_t *flags_out, int32_t clear)
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess)
         return TACO_ERR_CUDA;
-    uint32_t codec = 0, gemm = 0;
+    uint32_t codec = 0, gemm = 0, fp8 = 0, norm = 0;
     if ((e = taco::read_codec_error(&codec, clear != 0)) != cudaSuccess ||
-        (e = taco::read_gemm_error(&gemm, clear != 0)) != cudaSuccess)
+        (e = taco::read_gemm_error(&gemm, clear != 0)) != cudaSuccess ||
+        (e = taco::read_fp8_error(&fp8, clear != 0)) != cudaSuccess ||
+        (e = taco::read_norm_error(&norm, clear != 0)) != cudaSuccess)
         return from_cuda(e);
-    *flags_out = codec | gemm;
+    *flags_out = codec | gemm | fp8 | norm;
     return TACO_OK;
 }
 

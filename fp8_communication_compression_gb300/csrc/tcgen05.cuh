@@ -88,6 +88,46 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
+// ------------------------------------------------- block-scaled FP8 MMA --
+
+// Instruction descriptor of kind::mxf8f6f4 with E4M3 A and B (formats 0),
+// E8M0 scales (bit 23), both operands K-major, scale bytes at position 0 of
+// their 32-bit words: N >> 3 (bits 17-22), M >> 4 (bits 24-28, M = 128).
+__host__ __device__ constexpr uint32_t idesc_mxf8(int n)
+{
+    return (1u << 23) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T for one 128 x N x 32 step of E4M3 values,
+// each product row scaled by its E8M0 bytes at sfa_tmem (4 columns: row r in
+// lane r % 32 of column r / 32, repeated in all four lane quarters) and
+// sfb_tmem (the same for B's rows); issued by one thread.
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
+        "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+// Copies 32 rows of 16 bytes (512 contiguous bytes of shared memory, eight-
+// row groups 128 bytes apart, no swizzle) into 4 columns of tensor memory,
+// row r to lane r of each of the four lane quarters: the scale bytes of 128
+// operand rows, row r at byte 16 (r % 32) + 4 (r / 32).  Runs in order with
+// the MMAs the same thread issues.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem_addr)
+{
+    uint64_t d = static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(128 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
 // The mbarrier at `bar` receives one arrival once every MMA this thread has
 // issued so far has completed (and has finished reading shared memory).
 __device__ __forceinline__ void mma_commit(uint32_t bar)

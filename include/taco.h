@@ -480,12 +480,121 @@ taco_status taco_two_shot_host_noalloc(int32_t P, int64_t rows, int64_t d, int32
                                        const void *x_host_bf16, float *out_host, float e_target,
                                        float eps, taco_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Block-scaled FP8 matrices and their products.
+ *
+ * An FP8 operand is a matrix of E4M3 codes with one scale byte per block of
+ * 128 values along its rows; a block's values are code * 2^(byte - 127), the
+ * byte - 127 being the smallest E >= -127 with max |x| <= 448 2^E (byte 127
+ * for a block of zeros).  x 2^-E is exact and is rounded once, to nearest
+ * even.  A block holding an Inf or a NaN gets byte 255, codes 0x7F or 0xFF,
+ * and makes every product that reads it NaN.
+ *
+ * Layout: codes [rows][P], P = fp8_pitch(cols) (cols rounded up to a multiple
+ * of 16, the padding zero, NaN in a NaN block); scale
+ * [ceil(cols / 128)][rows].  Code pointers are 16-byte aligned.
+ */
+int64_t fp8_pitch(int64_t cols);
+
+/*
+ * fp8_quantize - x bf16 [rows][cols] (16-byte aligned) to
+ *   codes   [rows][fp8_pitch(cols)], scale   [ceil(cols / 128)][rows]  and / or
+ *   codes_t [cols][fp8_pitch(rows)], scale_t [ceil(rows / 128)][cols]
+ * (the transposed matrix, in blocks of 128 along its own rows), in one pass.
+ * codes and scale, or codes_t and scale_t, may both be null.
+ *
+ * fp8_quantize_weight - the same with one scale byte per 128 x 128 tile:
+ * scale [ceil(cols / 128)][ceil(rows / 128)], scale_t its transpose; codes_t
+ * are the transposed codes.
+ */
+taco_status fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scale,
+                         uint8_t *codes_t, uint8_t *scale_t, taco_stream_t stream);
+taco_status fp8_quantize_weight(const void *x_bf16, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scale,
+                                uint8_t *codes_t, uint8_t *scale_t, taco_stream_t stream);
+
+/*
+ * fp8_gemm - out[M][N] = A B^T on the tensor cores, accumulated in fp32 with
+ * the scales applied, rounded once if out_is_bf16.  a: codes [M][K], a_scale
+ * [ceil(K / 128)][M]; b: codes [N][K], b_scale [ceil(K / 128)][N], or with
+ * b_scale_tiles != 0 [ceil(K / 128)][ceil(N / 128)].  K is the padded row
+ * length, a multiple of 16 (K = 0: zeros).  out is 16-byte aligned.  The
+ * summation order is fixed: the same inputs give the same bits.
+ */
+taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
+                     int32_t b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, int32_t out_is_bf16,
+                     taco_stream_t stream);
+
+/*
+ * fp8_linear - y[M][N] = Q(x) W^T: x bf16 [M][K] quantised along its rows
+ * into the workspace, then fp8_gemm with a weight [N][K] quantised by
+ * fp8_quantize_weight (codes, scale).
+ *
+ * fp8_linear_backward - dx[M][K] = Q(dy) W (bf16; from codes_t and scale_t)
+ * and dw[N][K] = Q(dy^T) Q(x^T)^T (blocks of 128 rows of dy and x; bf16 or
+ * fp32).  dx (with codes_t and scale_t) or dw (with x) may be null: that
+ * gradient is left out.  M = 0 gives dw = 0.
+ *
+ * The workspace (256-byte aligned, at least the bytes that
+ * fp8_linear_workspace_bytes gives; its contents need not be kept) holds the
+ * quantised activations.
+ */
+taco_status fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward, uint64_t *bytes);
+taco_status fp8_linear(const void *x_bf16, const uint8_t *codes, const uint8_t *scale, int64_t M, int64_t N,
+                       int64_t K, void *y, int32_t y_is_bf16, void *workspace, uint64_t workspace_bytes,
+                       taco_stream_t stream);
+taco_status fp8_linear_backward(const void *dy_bf16, const void *x_bf16, const uint8_t *codes_t,
+                                const uint8_t *scale_t, int64_t M, int64_t N, int64_t K, void *dx_bf16, void *dw,
+                                int32_t dw_is_bf16, void *workspace, uint64_t workspace_bytes,
+                                taco_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The norms around a block, with its gate and residual scale.  Per token
+ * (row of d values):
+ *
+ *   z = y / sqrt(mean(y^2) + eps) * g_post
+ *   h_out = residual_scale * h + gate * z
+ *   n = h_out / sqrt(mean(h_out^2) + eps) * g_pre
+ *
+ * y (the block's output), h (the residual stream), h_out: bf16 [T][d],
+ * 16-byte aligned; g_post, g_pre: fp32 [d], 16-byte aligned.  n is taken from
+ * h_out before its rounding.  gate_mode says what `gate` is:
+ *   TACO_GATE_NONE     1 (gate null)
+ *   TACO_GATE_CHANNEL  fp32 [d], 16-byte aligned
+ *   TACO_GATE_TOKEN    fp32 [T]
+ *   TACO_GATE_FULL     bf16 [T][d], 16-byte aligned
+ * n_scale null: n is bf16 [T][d].  Else n holds FP8 codes [T][fp8_pitch(d)]
+ * and n_scale their scale bytes [ceil(d / 128)][T].
+ * 1 <= d <= TACO_NORM_MAX_D; eps > 0.
+ *
+ * The backward pass takes dn and dh_out (gradients at n and h_out, bf16
+ * [T][d]), y and h_out, and gives dy, dh (bf16 [T][d]), dg_post, dg_pre (fp32
+ * [d], summed over tokens in a fixed order) and dgate (fp32 [d], fp32 [T] or
+ * bf16 [T][d], as the gate; null for TACO_GATE_NONE).  Both statistics are
+ * recomputed from y and h_out.  T = 0 gives zero dg_post, dg_pre and channel
+ * dgate.  The workspace is 256-byte aligned.
+ */
+#define TACO_GATE_NONE 0
+#define TACO_GATE_CHANNEL 1
+#define TACO_GATE_TOKEN 2
+#define TACO_GATE_FULL 3
+#define TACO_NORM_MAX_D 16384
+taco_status rmsnorm_gate_residual(const void *y, const void *h, const float *g_post, const float *g_pre,
+                                  const void *gate, int32_t gate_mode, float residual_scale, float eps, int64_t T,
+                                  int64_t d, void *h_out, void *n, uint8_t *n_scale, taco_stream_t stream);
+taco_status rmsnorm_gate_residual_workspace_bytes(int64_t T, int64_t d, int32_t gate_mode, uint64_t *bytes);
+taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, const void *y, const void *h_out,
+                                           const float *g_post, const float *g_pre, const void *gate,
+                                           int32_t gate_mode, float residual_scale, float eps, int64_t T, int64_t d,
+                                           void *dy, void *dh, float *dg_post, float *dg_pre, void *dgate,
+                                           void *workspace, uint64_t workspace_bytes, taco_stream_t stream);
+
 /*
  * taco_device_error - watchdog flags of the kernels on the current device.
  * Every in-kernel wait gives up after about a second and sets a bit here
  * (bit 0: compressor, bit 1: decompressor, bit 4: taco_watchdog_selftest,
  * bit 5: the GEMMs taco_gemm_compress, agoq_gemm_accumulate and
- * agoq_gemm_laaq_quantize).
+ * agoq_gemm_laaq_quantize, bit 6: fp8_gemm and the calls built on it, bit 7:
+ * rmsnorm_gate_residual and its backward pass).
  * Synchronises the device.  With clear != 0 the flags are reset to 0 after
  * reading.
  */
