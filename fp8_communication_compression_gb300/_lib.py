@@ -47,6 +47,7 @@ SIGNATURES = {
     "agoq_gemm_laaq_quantize": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _U64, _P]),
     "taco_gemm_workspace_bytes": (ctypes.c_int, [_I64, _I64, _I64, _P]),
     "fp8_pitch": (ctypes.c_int64, [_I64]),
+    "fp8_scale_bytes": (ctypes.c_int64, [_I64, _I64]),
     "fp8_quantize": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P]),
     "fp8_quantize_weight": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P]),
     "fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I64, _I64, _I64, _P, _I32, _P]),

@@ -479,25 +479,43 @@ def _blocks(n: int) -> int:
     return -(-n // 128)
 
 
+def _scale_shape(rows: int, cols: int):
+    """Shape of the scales of a [rows, cols] matrix: 512-byte pieces of 128
+    rows and four blocks."""
+    return (-(-rows // 128), -(-cols // 512), 512)
+
+
+def fp8_scales(scale: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
+    """The scale bytes [ceil(cols / 128), rows] of a [rows, cols] matrix's
+    scales, one of block b and row r at [b, r] (a copy in plain order)."""
+    _need(scale, "scale", (torch.uint8,))
+    T, G, _ = _scale_shape(rows, cols)
+    if tuple(scale.shape) != (T, G, 512):
+        raise ValueError(f"scale has shape {tuple(scale.shape)}, expected {(T, G, 512)}")
+    # [tile][group][row % 32][row % 128 / 32][block % 4]
+    return scale.view(T, G, 32, 4, 4).permute(1, 4, 0, 3, 2).reshape(4 * G, 128 * T)[:_blocks(cols), :rows].contiguous()
+
+
 def fp8_quantize(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, stream=None):
     """x bf16 [..., cols], as a matrix of ``rows`` rows, to E4M3 codes with one
     power-of-two scale (an E8M0 byte, 2^(byte - 127)) per block of 128.
 
     ``rowwise``: (codes uint8 [rows, fp8_pitch(cols)], scale uint8
-    [ceil(cols / 128), rows]), blocks along the rows.  ``colwise``: (codes_t
-    [cols, fp8_pitch(rows)], scale_t [ceil(rows / 128), cols]), the transposed
+    [ceil(rows / 128), ceil(cols / 512), 512]), blocks along the rows.
+    ``colwise``: (codes_t [cols, fp8_pitch(rows)], scale_t), the transposed
     matrix in blocks along its own rows.  With both, all four from one pass
-    over x.  The padding codes are zero (NaN in a block that holds an Inf or
-    a NaN)."""
+    over x.  The scales lie as the tensor core reads them; fp8_scales gives
+    them in plain order.  The padding codes are zero (NaN in a block that
+    holds an Inf or a NaN)."""
     rows, cols = _matrix(x, "x")
     if not (rowwise or colwise):
         raise ValueError("rowwise or colwise must be set")
     dev, u8 = x.device, torch.uint8
     out = ()
     if rowwise:
-        out += (_new((rows, fp8_pitch(cols)), u8, dev, stream), _new((_blocks(cols), rows), u8, dev, stream))
+        out += (_new((rows, fp8_pitch(cols)), u8, dev, stream), _new(_scale_shape(rows, cols), u8, dev, stream))
     if colwise:
-        out += (_new((cols, fp8_pitch(rows)), u8, dev, stream), _new((_blocks(rows), cols), u8, dev, stream))
+        out += (_new((cols, fp8_pitch(rows)), u8, dev, stream), _new(_scale_shape(cols, rows), u8, dev, stream))
     ptrs = [t.data_ptr() for t in out]
     ptrs = ptrs if len(ptrs) == 4 else ptrs + [None, None] if rowwise else [None, None] + ptrs
     st = _lib.load().fp8_quantize(x.data_ptr(), rows, cols, *ptrs, _stream_handle(stream))
@@ -526,20 +544,29 @@ def _out_dtype(out: torch.Tensor | None, out_dtype: torch.dtype) -> torch.dtype:
     return dt
 
 
+def _need_scale(t: torch.Tensor, name: str, rows: int, cols: int) -> None:
+    _need(t, name, (torch.uint8,))
+    if tuple(t.shape) != _scale_shape(rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {_scale_shape(rows, cols)}")
+
+
 def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
              out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """a @ b.T of two quantised matrices on the tensor cores: a uint8 [M, P]
-    with a_scale [ceil(P / 128), M]; b uint8 [N, P] with b_scale [ceil(P / 128),
-    N], or one byte per 128 rows [ceil(P / 128), ceil(N / 128)] (a weight).
-    fp32 accumulation in a fixed order; bf16 or fp32 [M, N]."""
+    with a_scale, b uint8 [N, P] with b_scale, as fp8_quantize gives them, or
+    a weight's b_scale [ceil(P / 128), ceil(N / 128)].  fp32 accumulation in a
+    fixed order; bf16 or fp32 [M, N]."""
     _need(a, "a", _U8)
     _need(b, "b", _U8)
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise ValueError("a must be [M, P] and b [N, P]")
     (M, P), N = a.shape, b.shape[0]
-    _need2(a_scale, "a_scale", (torch.uint8,), _blocks(P), M)
-    tiles = b_scale.dim() == 2 and b_scale.shape[1] != N
-    _need2(b_scale, "b_scale", (torch.uint8,), _blocks(P), _blocks(N) if tiles else N)
+    _need_scale(a_scale, "a_scale", M, P)
+    tiles = isinstance(b_scale, torch.Tensor) and b_scale.dim() == 2
+    if tiles:
+        _need2(b_scale, "b_scale", (torch.uint8,), _blocks(P), _blocks(N))
+    else:
+        _need_scale(b_scale, "b_scale", N, P)
     dt = _out_dtype(out, out_dtype)
     if out is None:
         out = _new((M, N), dt, a.device, stream)
@@ -668,12 +695,12 @@ def rmsnorm_gate_residual_fp8(y: torch.Tensor, h: torch.Tensor, gain_post: torch
                               gate: torch.Tensor | None = None, residual_scale: float = 1.0, eps: float = 1e-6,
                               stream=None):
     """rmsnorm_gate_residual with n quantised as it is written: (h_new, codes
-    uint8 [T, fp8_pitch(d)], scale uint8 [ceil(d / 128), T]), the operand of
-    fp8_gemm (blocks of 128 along the rows, from the fp32 n)."""
+    uint8 [T, fp8_pitch(d)], scale), the operand of fp8_gemm as fp8_quantize
+    gives it (blocks of 128 along the rows, from the fp32 n)."""
     T, d, mode = _norm_args(y, h, gain_post, gain_pre, gate)
     h_new = _new(y.shape, torch.bfloat16, y.device, stream)
     codes = _new((T, fp8_pitch(d)), torch.uint8, y.device, stream)
-    scale = _new((_blocks(d), T), torch.uint8, y.device, stream)
+    scale = _new(_scale_shape(T, d), torch.uint8, y.device, stream)
     st = _lib.load().rmsnorm_gate_residual(y.data_ptr(), h.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
                                            _ptr(gate), mode, residual_scale, eps, T, d, h_new.data_ptr(),
                                            codes.data_ptr(), scale.data_ptr(), _stream_handle(stream))

@@ -26,6 +26,22 @@ constexpr int kFp8Block = 128;
 // (the stride a TMA tensor map needs).
 __host__ __device__ inline int64_t fp8_pitch(int64_t n) { return (n + 15) & ~int64_t(15); }
 
+// Scales are stored as the tensor core reads them: a 512-byte piece holds the
+// bytes of 128 rows for four consecutive blocks, row r's four bytes in the
+// word at 16 (r % 32) + 4 (r / 32); pieces [ceil(rows / 128)][ceil(blocks /
+// 4)].  Bytes of rows and blocks past the matrix's end are not read into any
+// result.
+__host__ __device__ inline int64_t fp8_scale_bytes(int64_t rows, int64_t cols)
+{
+    return ((rows + 127) / 128) * ((cols + 511) / 512) * 512;
+}
+
+// Where block b's byte of a row lies; groups = ceil(blocks / 4).
+__host__ __device__ inline int64_t fp8_scale_at(int64_t row, int64_t b, int64_t groups)
+{
+    return ((row >> 7) * groups + (b >> 2)) * 512 + ((row & 31) << 4) + (((row >> 5) & 3) << 2) + (b & 3);
+}
+
 // Scale byte from the bit pattern of max |x| (fp32, the sign bit clear; an
 // unsigned maximum of such patterns puts Inf and NaN on top).
 __device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax_bits)

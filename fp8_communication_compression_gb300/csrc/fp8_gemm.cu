@@ -5,22 +5,28 @@
 // A and B hold E4M3 codes in rows along the contraction, with one E8M0 byte
 // per block of 128 (per row, or for B per 128 x 128 tile).  tcgen05.mma
 // kind::mxf8f6f4 applies the scales itself while it accumulates in fp32, so
-// no partial sum leaves tensor memory before the end of the contraction;
-// the result is rounded once, to bf16 or not at all.  The instruction takes
-// a scale per 32 values: each of the four 32-wide steps of a block reads the
-// block's byte.
-//
-// Two kernels share the stage pipeline below.
+// no partial sum leaves tensor memory on the way; a bf16 result is rounded
+// once.  The instruction takes a scale per 32 values: each of the four
+// 32-wide steps of a block reads the block's byte, one of the four in its
+// row's scale word (the words hold four blocks, fp8_block.cuh), so a 512-byte
+// piece of the stored scales serves 128 rows for four blocks and goes through
+// a bulk copy and one tcgen05.cp as it is.  Scales of 128 x 128 tiles are
+// spread over such pieces by a warp of their own.
 //
 // fp8_gemm_kernel (many tiles): persistent, one CTA per SM, tiles of 128 x
-//   BN.  Warp 0 streams 128-byte-wide tiles of A and B by TMA through an
-//   mbarrier ring; warp 6 reads the block's scale bytes and lays them out
-//   for tcgen05.cp in the same ring slot; one thread of warp 1 copies them to
-//   tensor memory and issues the MMAs; warps 2-5 store finished tiles.
-//   Tensor memory holds the scales (2 x 12 columns, alternating between
-//   blocks) and two accumulators.  At BN = 256 the two overlap by 32
-//   columns: the epilogue drains these first and the next tile's MMAs start
-//   while it works on the rest.
+//   256.  Warp 0 streams 128-byte-wide pieces of A and B by TMA through an
+//   mbarrier ring, and the scales through a ring of their own; one thread of
+//   warp 1 copies scales to tensor memory and issues the MMAs; warps 2-5
+//   store finished tiles; warp 6 spreads tile scales.  Tensor memory holds
+//   the scales (two sets of 12 columns) and two accumulators, which overlap
+//   by 32 columns: the epilogue drains these first, and the next tile's MMAs
+//   start while it works on the rest.  Where the last round of tiles would
+//   leave more than half of the SMs idle, its tiles are cut in two (128 x
+//   128).  An fp32 result over more than 2048 values is summed in pieces: the
+//   tensor core's accumulator truncates, which biases long coherent sums
+//   (measured on a weight gradient over 4096 tokens: 1.9e-6 of its norm in
+//   one piece, where an fp32 matrix product has 3.7e-7), so each piece leaves
+//   tensor memory and is added to the output by a rounding fp32 reduction.
 //
 // fp8_gemm_split_kernel (few tiles: single tokens to small batches): the
 //   roles of the operands are exchanged - B's rows (weights) take the 128
@@ -67,68 +73,39 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 
 __device__ __forceinline__ void report_timeout() { atomicOr(&g_fp8_error, kErrFp8); }
 
-// Scale bytes of one operand: [blocks][rows], or [blocks][ceil(rows / 128)]
-// with one byte per 128 rows.
+// The scales of one operand: 512-byte pieces [row tile][group of four
+// blocks], or (tiles) bytes [block][row tile].
 struct Scales {
     const uint8_t *p;
-    int64_t rows;
+    int64_t row_tiles;
     bool tiles;
 };
 
-// Four blocks' scale bytes of GROUPS x 128 operand rows, as loaded: lane l
-// holds rows 128 g + 32 c + l.
-template <int GROUPS> struct ScaleBatch {
-    uint32_t v[4][GROUPS][4];
-
-    __device__ __forceinline__ void load(const Scales &s, int64_t row0, int kb, int kb_end, int lane)
-    {
-        const int64_t stride = s.tiles ? (s.rows + 127) / 128 : s.rows;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int64_t row = row0 + 128 * g + 32 * c + lane;
-                    v[k][g][c] = 127u;
-                    if (kb + k < kb_end && row < s.rows)
-                        v[k][g][c] = __ldg(s.p + (kb + k) * stride + (s.tiles ? row >> 7 : row));
-                }
-    }
-    // block k's bytes into the 512-byte areas at `dst`, each byte repeated
-    // over its word
-    __device__ __forceinline__ void store(int k, uint32_t dst, int lane) const
-    {
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            const uint32_t *w = v[k][g];
-            sts128(dst + 512 * g + 16 * lane, w[0] * 0x01010101u, w[1] * 0x01010101u, w[2] * 0x01010101u,
-                   w[3] * 0x01010101u);
-        }
-    }
-};
-
-// Shared-memory layout of a ring of `stages` slots for operand tiles of 128
-// and `bn` rows, scale areas beside them, and `extra` bytes.
+// Shared-memory layout: a ring of `stages` slots for operand pieces of 128
+// and `bn` rows, `extra` bytes, a ring of scale slots of `sf_bytes` (128 A or
+// lane-side rows, then the others), barriers.
+constexpr int kScaleSlots = 3;
 struct Ring {
-    uint32_t base, stage_bytes, scales, scale_bytes, extra, bars;
+    uint32_t base, stage_bytes, scales, sf_bytes, extra, bars;
     int stages;
     __device__ __forceinline__ uint32_t a(int s) const { return base + s * stage_bytes; }
     __device__ __forceinline__ uint32_t b(int s) const { return base + s * stage_bytes + kTileA; }
-    __device__ __forceinline__ uint32_t sf(int s) const { return scales + s * scale_bytes; }
+    __device__ __forceinline__ uint32_t sf(int s) const { return scales + s * sf_bytes; }
     __device__ __forceinline__ uint32_t full(int s) const { return bars + 8 * s; }
     __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8 * (kMaxStages + s); }
-    __device__ __forceinline__ uint32_t acc_full(int a) const { return bars + 8 * (2 * kMaxStages + a); }
-    __device__ __forceinline__ uint32_t acc_free(int a) const { return bars + 8 * (2 * kMaxStages + 2 + a); }
-    __device__ __forceinline__ uint32_t drain() const { return bars + 8 * (2 * kMaxStages + 4); }
-    __device__ __forceinline__ uint32_t tmem_slot() const { return bars + 8 * (2 * kMaxStages + 5); }
+    __device__ __forceinline__ uint32_t sf_full(int s) const { return bars + 8 * (2 * kMaxStages + s); }
+    __device__ __forceinline__ uint32_t sf_empty(int s) const { return bars + 8 * (2 * kMaxStages + kScaleSlots + s); }
+    __device__ __forceinline__ uint32_t acc_full(int a) const { return bars + 8 * (2 * kMaxStages + 6 + a); }
+    __device__ __forceinline__ uint32_t acc_free(int a) const { return bars + 8 * (2 * kMaxStages + 8 + a); }
+    __device__ __forceinline__ uint32_t drain() const { return bars + 8 * (2 * kMaxStages + 10); }
+    __device__ __forceinline__ uint32_t tmem_slot() const { return bars + 8 * (2 * kMaxStages + 11); }
 };
-constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 5) + 16;
+static_assert(kScaleSlots == 3, "barrier numbers above");
+constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 11) + 16;
 
 __host__ __device__ constexpr uint32_t stage_bytes_of(int bn) { return kTileA + 128u * bn; }
 
-__device__ __forceinline__ Ring make_ring(const uint8_t *smem, int bn, int stages, uint32_t scale_bytes,
-                                          uint32_t extra)
+__device__ __forceinline__ Ring make_ring(const uint8_t *smem, int bn, int stages, uint32_t sf_bytes, uint32_t extra)
 {
     Ring r;
     r.base = (smem_u32(smem) + 1023u) & ~1023u;
@@ -136,62 +113,138 @@ __device__ __forceinline__ Ring make_ring(const uint8_t *smem, int bn, int stage
     r.stage_bytes = stage_bytes_of(bn);
     r.extra = r.base + stages * r.stage_bytes;
     r.scales = r.extra + extra;
-    r.scale_bytes = scale_bytes;
-    r.bars = r.scales + stages * scale_bytes;
+    r.sf_bytes = sf_bytes;
+    r.bars = r.scales + kScaleSlots * sf_bytes;
     return r;
 }
 
-// A position in the ring: slot and the parity of its use.
+// (one thread)  tile_scales: warp 6 also arrives on a scale slot.
+__device__ __forceinline__ void init_barriers(const Ring &r, bool tile_scales)
+{
+    for (int s = 0; s < r.stages; ++s) {
+        mbar_init(r.full(s), 1);
+        mbar_init(r.empty(s), 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+        mbar_init(r.sf_full(s), tile_scales ? 2 : 1);
+        mbar_init(r.sf_empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+        mbar_init(r.acc_full(a), 1);
+        mbar_init(r.acc_free(a), 4);  // one arrival per epilogue warp
+    }
+    mbar_init(r.drain(), 1);
+    fence_barrier_init();
+}
+
+// A position in a ring: slot and the parity of its use.
 struct Slot {
     int s = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ void next(int stages)
+    __device__ __forceinline__ void next(int n)
     {
-        if (++s == stages) {
+        if (++s == n) {
             s = 0;
             phase ^= 1;
         }
     }
 };
 
-// One block of the contraction: its scales to tensor memory, then four MMAs
-// of 32 values each.
-__device__ __forceinline__ void mma_block(const Ring &r, int s, uint32_t d, uint32_t sfa, uint32_t sfb,
-                                          int b_groups, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    tmem_copy_scales(sfa, r.sf(s));
-    tmem_copy_scales(sfb, r.sf(s) + 512);
-    if (b_groups > 1)
-        tmem_copy_scales(sfb + 4, r.sf(s) + 1024);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// A new group of four blocks starts at kb (or the contraction's range does).
+__device__ __forceinline__ bool starts_group(int kb, int kb0) { return (kb & 3) == 0 || kb == kb0; }
+
+// Four MMAs of 32 values each: one block of the contraction, whose scales
+// are byte kb % 4 of their words.
+__device__ __forceinline__ void mma_block(const Ring &r, int s, uint32_t d, uint32_t sfa, uint32_t sfb, uint32_t idesc,
+                                          int kb, bool accumulate)
+{
     const uint64_t ad = smem_desc_k_sw128(r.a(s)), bd = smem_desc_k_sw128(r.b(s));
+    const uint32_t id = idesc_scale_byte(idesc, kb & 3);
 #pragma unroll
     for (int k = 0; k < 4; ++k)  // 32 codes = 32 bytes = 2 descriptor units
-        mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc, sfa, sfb, accumulate || k != 0);
+        mma_mxf8(d, ad + 2 * k, bd + 2 * k, id, sfa, sfb, accumulate || k != 0);
     mma_commit(r.empty(s));  // the slot is free once these have read it
+}
+
+// (warp 6)  Tile scales of blocks 4 g .. 4 g + 3 for row tiles t and t + 1:
+// lanes 0-3 hold tile t's bytes, lanes 4-7 tile t + 1's.
+__device__ __forceinline__ uint32_t load_tile_scales(const Scales &s, int g, int64_t t, int KB, int lane)
+{
+    const int kb = 4 * g + (lane & 3);
+    const int64_t tile = t + ((lane >> 2) & 1);
+    return lane < 8 && kb < KB && tile < s.row_tiles ? __ldg(s.p + kb * s.row_tiles + tile) : 127u;
+}
+
+// Spreads them over the 512-byte pieces at dst (`pieces` of them).
+__device__ __forceinline__ void spread_tile_scales(uint32_t v, uint32_t dst, int pieces, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w |= __shfl_sync(0xFFFFFFFFu, v, 4 * i + j) << (8 * j);
+        if (i < pieces)
+            sts128(dst + 512 * i + 16 * lane, w, w, w, w);
+    }
 }
 
 // ------------------------------------------------------------ many tiles --
 
+constexpr int kBN = 256;
 constexpr uint32_t kStaging = 4 * 4096;   // 4 KB per epilogue warp
+constexpr int kStages = 4;
+constexpr uint32_t kAcc1 = 224;            // second accumulator: columns 224 .. 479
 constexpr uint32_t kSfColumn = 480;        // tensor-memory columns 480 .. 503: scales
 constexpr int kGroupM = 16;                // row tiles walked together (operands shared through L2)
+constexpr uint32_t kGemmSmem = 1024 + kStages * stage_bytes_of(kBN) + kStaging + kScaleSlots * 1536 + kBarBytes;
+static_assert(kGemmSmem <= kSmemLimit, "shared memory per CTA");
 
-struct TileWalk {
-    int tiles_m, tiles_n;
-    __device__ __forceinline__ void at(int idx, int &tm, int &tn) const
+// The work of the grid: `full` whole tiles, then the others as two halves
+// each; every item in `segs` pieces of `seg_kb` blocks.
+struct Work {
+    int tiles_m, tiles_n, full, items, segs, seg_kb, KB;
+    int64_t N;
+    // Item idx: its row tile, its first column, and its width (256 or 128).
+    // False for the second half of a tile that has none.
+    __device__ __forceinline__ bool at(int idx, int &tm, int64_t &n0, int &bn) const
     {
-        const int per = kGroupM * tiles_n, g = idx / per, r = idx - g * per;
+        const int t = idx < full ? idx : full + (idx - full) / 2;
+        const int per = kGroupM * tiles_n, g = t / per, r = t - g * per;
         const int left = tiles_m - g * kGroupM, gm = left < kGroupM ? left : kGroupM;
-        tn = r / gm;
+        const int tn = r / gm;
         tm = g * kGroupM + (r - tn * gm);
+        n0 = static_cast<int64_t>(tn) * kBN;
+        bn = kBN;
+        if (idx >= full) {
+            n0 += 128 * ((idx - full) & 1);
+            bn = 128;
+        }
+        if (N - n0 <= 128)
+            bn = 128;
+        return n0 < N;
+    }
+    __device__ __forceinline__ int first(int seg) const { return seg * seg_kb; }
+    __device__ __forceinline__ int last(int seg) const
+    {
+        const int e = (seg + 1) * seg_kb;
+        return e < KB ? e : KB;
     }
 };
 
 // 32 columns of a warp's 32 rows: rounded into the staging area and stored,
 // by TMA where the output's rows allow it (`tma`), else element by element
 // with the lanes along the row.
+// `add` (fp32 only): added to what is there.
 template <bool BF16>
-__device__ __forceinline__ void store_chunk(const float (&x)[32], uint32_t stage, int lane, bool tma,
+__device__ __forceinline__ void store_chunk(const float (&x)[32], uint32_t stage, int lane, bool tma, bool add,
                                             const CUtensorMap *map, void *out, int64_t M, int64_t N, int64_t row0,
                                             int64_t col0)
 {
@@ -222,8 +275,12 @@ __device__ __forceinline__ void store_chunk(const float (&x)[32], uint32_t stage
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (row0 < M && col0 < N)
-                tma_store_2d(map, static_cast<int32_t>(col0), static_cast<int32_t>(row0), stage);
+            if (row0 < M && col0 < N) {
+                if (!BF16 && add)
+                    tma_add_2d(map, static_cast<int32_t>(col0), static_cast<int32_t>(row0), stage);
+                else
+                    tma_store_2d(map, static_cast<int32_t>(col0), static_cast<int32_t>(row0), stage);
+            }
             bulk_commit();
         }
     } else {
@@ -241,9 +298,11 @@ __device__ __forceinline__ void store_chunk(const float (&x)[32], uint32_t stage
                 if (col < N)
                     static_cast<uint16_t *>(out)[(row0 + r) * N + col] = h;
             } else {
-                const uint32_t w = lds32(stage + 128 * r + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3));
-                if (col < N)
-                    static_cast<uint32_t *>(out)[(row0 + r) * N + col] = w;
+                const float v = __uint_as_float(lds32(stage + 128 * r + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)));
+                if (col < N) {
+                    float *o = static_cast<float *>(out) + (row0 + r) * N + col;
+                    *o = add ? *o + v : v;
+                }
             }
         }
         __syncwarp();
@@ -253,30 +312,16 @@ __device__ __forceinline__ void store_chunk(const float (&x)[32], uint32_t stage
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
-                    const __grid_constant__ CUtensorMap o_map, Scales sa, Scales sb, void *__restrict__ out,
-                    int64_t M, int64_t N, int KB, int BN, int stages, TileWalk walk, int tma_out)
+                    const __grid_constant__ CUtensorMap o_map, Scales sa, Scales sb, void *out, int64_t M, int64_t N,
+                    Work work, int tma_out)
 {
     extern __shared__ uint8_t smem_raw[];
-    const Ring r = make_ring(smem_raw, BN, stages, 1536, kStaging);
+    const Ring r = make_ring(smem_raw, kBN, kStages, 1536, kStaging);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ntiles = walk.tiles_m * walk.tiles_n;
-    // the second accumulator's first column; above 240 columns the two share
-    // some
-    const bool overlap = 2 * BN > static_cast<int>(kSfColumn);
-    const uint32_t acc1 = overlap ? kSfColumn - BN : BN;
+    const int groups = (work.KB + 3) / 4;  // scale pieces per row tile
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(r.full(s), 2);   // the TMA warp's expect-tx arrival and the scale warp's
-            mbar_init(r.empty(s), 1);
-        }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(r.acc_full(a), 1);
-            mbar_init(r.acc_free(a), 4);   // one arrival per epilogue warp
-        }
-        mbar_init(r.drain(), 1);
-        fence_barrier_init();
-    }
+    if (threadIdx.x == 0)
+        init_barriers(r, sb.tiles);
     if (warp == 1) {
         tmem_alloc(r.tmem_slot(), 512);
         tmem_relinquish_alloc_permit();
@@ -291,62 +336,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             tma_prefetch_map(&a_map);
             tma_prefetch_map(&b_map);
-            Slot p;
-            int64_t issued = 0;
+            Slot p, f;
+            int64_t issued = 0, scales = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; ok && idx < ntiles; idx += gridDim.x) {
-                int tm, tn;
-                walk.at(idx, tm, tn);
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(r.empty(p.s), p.phase ^ 1)) {
-                        report_timeout();
-                        ok = false;
-                        break;
+            for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
+                int tm, bn;
+                int64_t n0;
+                if (!work.at(idx, tm, n0, bn))
+                    continue;
+                for (int seg = 0; ok && seg < work.segs; ++seg) {
+                    const int kb0 = work.first(seg), kb1 = work.last(seg);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (starts_group(kb, kb0)) {
+                            if (!mbar_wait(r.sf_empty(f.s), f.phase ^ 1)) {
+                                report_timeout();
+                                ok = false;
+                                break;
+                            }
+                            const int pieces = bn / 128;
+                            mbar_arrive_expect_tx(r.sf_full(f.s), sb.tiles ? 512 : 512 + 512 * pieces);
+                            bulk_load(r.sf(f.s), sa.p + (static_cast<int64_t>(tm) * groups + (kb >> 2)) * 512, 512,
+                                      r.sf_full(f.s));
+                            if (!sb.tiles)
+                                for (int i = 0; i < pieces; ++i)
+                                    bulk_load(r.sf(f.s) + 512 + 512 * i,
+                                              sb.p + ((n0 / 128 + i) * groups + (kb >> 2)) * 512, 512, r.sf_full(f.s));
+                            f.next(kScaleSlots);
+                            ++scales;
+                        }
+                        if (!mbar_wait(r.empty(p.s), p.phase ^ 1)) {
+                            report_timeout();
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(r.full(p.s), stage_bytes_of(bn));
+                        tma_load_2d(r.a(p.s), &a_map, kb * 128, tm * 128, r.full(p.s));
+                        tma_load_2d(r.b(p.s), &b_map, kb * 128, static_cast<int32_t>(n0), r.full(p.s));
+                        if (bn > 128)
+                            tma_load_2d(r.b(p.s) + kTileA, &b_map, kb * 128, static_cast<int32_t>(n0) + 128,
+                                        r.full(p.s));
+                        p.next(kStages);
+                        ++issued;
                     }
-                    mbar_arrive_expect_tx(r.full(p.s), r.stage_bytes);
-                    tma_load_2d(r.a(p.s), &a_map, kb * 128, tm * 128, r.full(p.s));
-                    tma_load_2d(r.b(p.s), &b_map, kb * 128, tn * BN, r.full(p.s));
-                    p.next(stages);
-                    ++issued;
                 }
             }
             // leave no load in flight into this CTA's shared memory
-            for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
-                mbar_wait(r.full(static_cast<int>(i % stages)), static_cast<uint32_t>(i / stages) & 1);
+            for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                mbar_wait(r.full(static_cast<int>(i % kStages)), static_cast<uint32_t>(i / kStages) & 1);
+            for (int64_t i = scales > kScaleSlots ? scales - kScaleSlots : 0; i < scales; ++i)
+                mbar_wait(r.sf_full(static_cast<int>(i % kScaleSlots)), static_cast<uint32_t>(i / kScaleSlots) & 1);
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = idesc_mxf8(BN);
-            const int groups = BN > 128 ? 2 : 1;
-            Slot p;
-            int i = 0;
-            uint32_t blk = 0;
+            Slot p, f;
+            int i = 0;  // accumulations done: items times segments
+            uint32_t set = 0, sfa = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; ok && idx < ntiles; idx += gridDim.x, ++i) {
-                // the epilogue has drained this accumulator's last tile (i -
-                // 2); or, where the two overlap, the columns shared with
-                // tile i - 1 (which it reaches after all of tile i - 2)
-                const int j = overlap ? i - 1 : i - 2;
-                if (j >= 0 && !mbar_wait(r.acc_free(j & 1), (j >> 1) & 1)) {
-                    report_timeout();
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d = tmem + (i & 1 ? acc1 : 0u);
-                for (int kb = 0; kb < KB; ++kb, ++blk) {
-                    if (!mbar_wait(r.full(p.s), p.phase)) {
+            for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
+                int tm, bn;
+                int64_t n0;
+                if (!work.at(idx, tm, n0, bn))
+                    continue;
+                const uint32_t idesc = idesc_mxf8(bn);
+                for (int seg = 0; ok && seg < work.segs; ++seg, ++i) {
+                    // the epilogue has drained the columns this accumulator
+                    // shares with accumulation i - 1 (which it reaches after
+                    // all of i - 2, this accumulator's last)
+                    if (i > 0 && !mbar_wait(r.acc_free((i - 1) & 1), ((i - 1) >> 1) & 1)) {
                         report_timeout();
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t sfa = tmem + kSfColumn + 12 * (blk & 1);
-                    mma_block(r, p.s, d, sfa, sfa + 4, groups, idesc, kb != 0);
-                    p.next(stages);
+                    const uint32_t d = tmem + (i & 1 ? kAcc1 : 0u);
+                    const int kb0 = work.first(seg), kb1 = work.last(seg);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (starts_group(kb, kb0)) {
+                            if (!mbar_wait(r.sf_full(f.s), f.phase)) {
+                                report_timeout();
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after_sync();
+                            sfa = tmem + kSfColumn + 12 * set;
+                            set ^= 1;
+                            tmem_copy_scales(sfa, r.sf(f.s));
+                            tmem_copy_scales(sfa + 4, r.sf(f.s) + 512);
+                            if (bn > 128)
+                                tmem_copy_scales(sfa + 8, r.sf(f.s) + 1024);
+                            mma_commit(r.sf_empty(f.s));
+                            f.next(kScaleSlots);
+                        }
+                        if (!mbar_wait(r.full(p.s), p.phase)) {
+                            report_timeout();
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        mma_block(r, p.s, d, sfa, sfa + 4, idesc, kb, kb != kb0);
+                        p.next(kStages);
+                    }
+                    if (ok)
+                        mma_commit(r.acc_full(i & 1));
                 }
-                if (ok)
-                    mma_commit(r.acc_full(i & 1));
             }
             if (!ok) {  // tensor memory is freed below: wait for what was issued
                 mma_commit(r.drain());
@@ -354,86 +446,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 6) {
-        Slot p;
-        bool ok = true;
-        ScaleBatch<1> ba, na;
-        ScaleBatch<2> bb, nb;
-        int idx = blockIdx.x, tm = 0, tn = 0;
-        if (idx < ntiles) {
-            walk.at(idx, tm, tn);
-            ba.load(sa, static_cast<int64_t>(tm) * 128, 0, KB, lane);
-            bb.load(sb, static_cast<int64_t>(tn) * BN, 0, KB, lane);
-        }
-        int kb = 0;
-        while (ok && idx < ntiles) {
-            // the next batch's loads in flight while this one is handed on
-            int nidx = idx, nkb = kb + 4;
-            if (nkb >= KB) {
-                nkb = 0;
-                nidx += gridDim.x;
-                if (nidx < ntiles)
-                    walk.at(nidx, tm, tn);
-            }
-            if (nidx < ntiles) {
-                na.load(sa, static_cast<int64_t>(tm) * 128, nkb, KB, lane);
-                nb.load(sb, static_cast<int64_t>(tn) * BN, nkb, KB, lane);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (!ok || kb + k >= KB)
+        if (sb.tiles) {
+            Slot f;
+            bool ok = true;
+            for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
+                int tm, bn;
+                int64_t n0;
+                if (!work.at(idx, tm, n0, bn))
                     continue;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.empty(p.s), p.phase ^ 1))) {
-                    if (lane == 0)
-                        report_timeout();
-                    ok = false;
-                    continue;
+                for (int seg = 0; ok && seg < work.segs; ++seg) {
+                    const int g1 = (work.last(seg) + 3) / 4;
+                    int g = work.first(seg) / 4;
+                    uint32_t v = load_tile_scales(sb, g, n0 / 128, work.KB, lane);
+                    for (; g < g1; ++g) {
+                        const uint32_t nv = load_tile_scales(sb, g + 1, n0 / 128, work.KB, lane);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.sf_empty(f.s), f.phase ^ 1))) {
+                            if (lane == 0)
+                                report_timeout();
+                            ok = false;
+                            break;
+                        }
+                        spread_tile_scales(v, r.sf(f.s) + 512, bn / 128, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(r.sf_full(f.s));
+                        f.next(kScaleSlots);
+                        v = nv;
+                    }
                 }
-                ba.store(k, r.sf(p.s), lane);
-                bb.store(k, r.sf(p.s) + 512, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(r.full(p.s));
-                p.next(stages);
             }
-            ba = na;
-            bb = nb;
-            idx = nidx;
-            kb = nkb;
         }
     } else {
         const int q = warp & 3;
         const uint32_t staging = r.extra + 4096 * q;
-        const int chunks = BN / 32;
         int i = 0;
         uint32_t area = 0;  // bf16: the staging area of the next chunk, 0 or 2048
-        for (int idx = blockIdx.x; idx < ntiles; idx += gridDim.x, ++i) {
-            int tm, tn;
-            walk.at(idx, tm, tn);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.acc_full(i & 1), (i >> 1) & 1))) {
-                if (lane == 0)
-                    report_timeout();
-                break;
-            }
-            tc_fence_after_sync();
-            const uint32_t tq = tmem + (i & 1 ? acc1 : 0u) + (static_cast<uint32_t>(32 * q) << 16);
-            const int64_t row0 = static_cast<int64_t>(tm) * 128 + 32 * q, col0 = static_cast<int64_t>(tn) * BN;
-            // the first accumulator shares its last columns with the second,
-            // which shares its first: drain those first
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                const int j = i & 1 ? c : chunks - 1 - c;
-                float x[32];
-                tmem_load_32(tq + 32 * j, x);
-                if (c == (overlap ? 0 : chunks - 1)) {
-                    tc_fence_before_sync();
-                    __syncwarp();
+        bool ok = true;
+        for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
+            int tm, bn;
+            int64_t n0;
+            if (!work.at(idx, tm, n0, bn))
+                continue;
+            for (int seg = 0; seg < work.segs; ++seg, ++i) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.acc_full(i & 1), (i >> 1) & 1))) {
                     if (lane == 0)
-                        mbar_arrive(r.acc_free(i & 1));
+                        report_timeout();
+                    ok = false;
+                    break;
                 }
-                store_chunk<BF16>(x, staging + area, lane, tma_out != 0, &o_map, out, M, N, row0, col0 + 32 * j);
-                if (BF16)
-                    area ^= 2048;
+                tc_fence_after_sync();
+                // an earlier piece's stores are complete before this one is added
+                if (seg > 0 && lane == 0)
+                    bulk_wait_all();
+                const uint32_t tq = tmem + (i & 1 ? kAcc1 : 0u) + (static_cast<uint32_t>(32 * q) << 16);
+                const int64_t row0 = static_cast<int64_t>(tm) * 128 + 32 * q;
+                const int chunks = bn / 32;
+                // the first accumulator shares its last columns with the
+                // second, which shares its first: drain those first
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    const int j = i & 1 ? c : chunks - 1 - c;
+                    float x[32];
+                    tmem_load_32(tq + 32 * j, x);
+                    if (c == 0) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(r.acc_free(i & 1));
+                    }
+                    store_chunk<BF16>(x, staging + area, lane, tma_out != 0, seg > 0, &o_map, out, M, N, row0,
+                                      n0 + 32 * j);
+                    if (BF16)
+                        area ^= 2048;
+                }
             }
         }
         if (lane == 0)
@@ -478,7 +564,8 @@ template <bool BF16> __device__ __forceinline__ void store_one(void *out, int64_
 }
 
 // CTA `rank` of the cluster of tile t takes blocks KB rank / S .. KB (rank +
-// 1) / S of the contraction.  Lanes: rows of B (n); columns: rows of A (m).
+// 1) / S of the contraction.  Lanes: rows of B (n); columns: rows of A (m),
+// BN of them from a multiple of 128.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
     fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
@@ -489,19 +576,14 @@ __global__ void __launch_bounds__(kThreads)
     const Ring r = make_ring(smem_raw, BN, stages, 1024, 0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % split, tile = blockIdx.x / split;
-    const int64_t n0 = static_cast<int64_t>(tile / tiles_m) * 128, m0 = static_cast<int64_t>(tile % tiles_m) * BN;
+    const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
+    const int64_t n0 = static_cast<int64_t>(tn) * 128, m0 = static_cast<int64_t>(tm) * 128;
     const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / split);
+    const int groups = (KB + 3) / 4;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(r.full(s), 2);
-            mbar_init(r.empty(s), 1);
-        }
-        mbar_init(r.acc_full(0), 1);
-        mbar_init(r.drain(), 1);
-        fence_barrier_init();
-    }
+    if (threadIdx.x == 0)
+        init_barriers(r, sb.tiles);
     if (warp == 1) {
         tmem_alloc(r.tmem_slot(), kSplitTmem);
         tmem_relinquish_alloc_permit();
@@ -514,9 +596,23 @@ __global__ void __launch_bounds__(kThreads)
 
     if (warp == 0) {
         if (lane == 0) {
-            Slot p;
-            int issued = 0;
+            Slot p, f;
+            int issued = 0, scales = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
+                if (starts_group(kb, kb0)) {
+                    if (!mbar_wait(r.sf_empty(f.s), f.phase ^ 1)) {
+                        report_timeout();
+                        break;
+                    }
+                    mbar_arrive_expect_tx(r.sf_full(f.s), sb.tiles ? 512 : 1024);
+                    bulk_load(r.sf(f.s) + 512, sa.p + (static_cast<int64_t>(tm) * groups + (kb >> 2)) * 512, 512,
+                              r.sf_full(f.s));
+                    if (!sb.tiles)
+                        bulk_load(r.sf(f.s), sb.p + (static_cast<int64_t>(tn) * groups + (kb >> 2)) * 512, 512,
+                                  r.sf_full(f.s));
+                    f.next(kScaleSlots);
+                    ++scales;
+                }
                 if (!mbar_wait(r.empty(p.s), p.phase ^ 1)) {
                     report_timeout();
                     break;
@@ -529,21 +625,37 @@ __global__ void __launch_bounds__(kThreads)
             }
             for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
                 mbar_wait(r.full(i % stages), static_cast<uint32_t>(i / stages) & 1);
+            for (int i = scales > kScaleSlots ? scales - kScaleSlots : 0; i < scales; ++i)
+                mbar_wait(r.sf_full(i % kScaleSlots), static_cast<uint32_t>(i / kScaleSlots) & 1);
         }
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t idesc = idesc_mxf8(BN);
-            Slot p;
+            Slot p, f;
+            uint32_t set = 0, sf = 0;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
+                if (starts_group(kb, kb0)) {
+                    if (!mbar_wait(r.sf_full(f.s), f.phase)) {
+                        report_timeout();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    sf = tmem + 128 + 8 * set;
+                    set ^= 1;
+                    tmem_copy_scales(sf, r.sf(f.s));
+                    tmem_copy_scales(sf + 4, r.sf(f.s) + 512);
+                    mma_commit(r.sf_empty(f.s));
+                    f.next(kScaleSlots);
+                }
                 if (!mbar_wait(r.full(p.s), p.phase)) {
                     report_timeout();
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                const uint32_t sf = tmem + 128 + 8 * (kb & 1);
-                mma_block(r, p.s, tmem, sf, sf + 4, 1, idesc, kb != kb0);
+                mma_block(r, p.s, tmem, sf, sf + 4, idesc, kb, kb != kb0);
                 p.next(stages);
             }
             mma_commit(ok ? r.acc_full(0) : r.drain());
@@ -551,29 +663,25 @@ __global__ void __launch_bounds__(kThreads)
                 mbar_wait(r.drain(), 0);
         }
     } else if (warp == 6) {
-        Slot p;
-        bool ok = true;
-        ScaleBatch<1> ba, bb;
-        for (int kb = kb0; ok && kb < kb1; kb += 4) {
-            bb.load(sb, n0, kb, kb1, lane);
-            ba.load(sa, m0, kb, kb1, lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (!ok || kb + k >= kb1)
-                    continue;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.empty(p.s), p.phase ^ 1))) {
+        if (sb.tiles) {
+            Slot f;
+            const int g1 = (kb1 + 3) / 4;
+            int g = kb0 / 4;
+            uint32_t v = load_tile_scales(sb, g, tn, KB, lane);
+            for (; g < g1; ++g) {
+                const uint32_t nv = load_tile_scales(sb, g + 1, tn, KB, lane);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.sf_empty(f.s), f.phase ^ 1))) {
                     if (lane == 0)
                         report_timeout();
-                    ok = false;
-                    continue;
+                    break;
                 }
-                bb.store(k, r.sf(p.s), lane);
-                ba.store(k, r.sf(p.s) + 512, lane);
+                spread_tile_scales(v, r.sf(f.s), 1, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(r.full(p.s));
-                p.next(stages);
+                    mbar_arrive(r.sf_full(f.s));
+                f.next(kScaleSlots);
+                v = nv;
             }
         }
     } else {
@@ -650,98 +758,97 @@ struct Plan {
     int bn, split;
 };
 
-// Which kernel, tile width and split a product takes.
-Plan plan_gemm(int64_t M, int64_t N, int KB, int sms)
+// Few tiles: fewer than half the SMs would get a 128 x 256 one.
+bool few_tiles(int64_t M, int64_t N, int sms) { return ceil_div(M, 128) * ceil_div(N, kBN) < sms / 2; }
+
+template <bool BF16>
+cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
+                      void *out, const DeviceInfo &di, cudaStream_t stream)
 {
-    Plan p{};
-    const int64_t tm = ceil_div(M, 128);
-    if (tm * ceil_div(N, 256) >= sms / 2) {
-        // whole rounds of one tile per SM: the width whose rounds cost least
-        double best = 0.0;
-        for (int bn = 256; bn >= 128; bn -= 32) {
-            const double cost = static_cast<double>(ceil_div(tm * ceil_div(N, bn), sms)) * (bn + 8);
-            if (p.bn == 0 || cost < best) {
-                best = cost;
-                p.bn = bn;
-            }
-        }
-        p.split = 1;
-        return p;
-    }
-    p.split_kernel = true;
-    p.bn = static_cast<int>(M >= 128 ? 128 : ceil_div(M, 16) * 16);
-    const int64_t tiles = ceil_div(N, 128) * ceil_div(M, p.bn);
-    p.split = 1;
-    while (p.split < 8 && tiles * (p.split + 1) <= 2 * sms && KB / (p.split + 1) >= 2)
-        ++p.split;
-    return p;
+    const int KB = static_cast<int>(ceil_div(K, 128));
+    const int bn = static_cast<int>(M >= 128 ? 128 : ceil_div(M, 16) * 16);
+    const int tiles_m = static_cast<int>(ceil_div(M, 128));
+    const int64_t tiles = ceil_div(N, 128) * tiles_m;
+    int split = 1;
+    while (split < 8 && tiles * (split + 1) <= 2 * di.num_sms && KB / (split + 1) >= 2)
+        ++split;
+    CUtensorMap am, bm;
+    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a), K, M, K, 128, bn) != 0 ||
+        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b), K, N, K, 128, 128) != 0)
+        return cudaErrorInvalidValue;
+    static std::atomic<bool> set[kMaxDevices];
+    cudaError_t e = ensure_smem(fp8_gemm_split_kernel<BF16>, kSmemLimit / 2, di.device, set);
+    if (e != cudaSuccess)
+        return e;
+    // two CTAs share an SM; the ring also holds the partial sums (512 bytes
+    // a column)
+    const uint32_t per = stage_bytes_of(bn), fixed = 1024 + kScaleSlots * 1024 + kBarBytes;
+    int stages = static_cast<int>((kSmemLimit / 2 - 1024 - fixed) / per);
+    const int need = static_cast<int>(ceil_div(KB, split)), least = static_cast<int>(ceil_div(512 * bn, per));
+    stages = stages > kMaxStages ? kMaxStages : stages;
+    stages = stages > need ? need : stages;
+    stages = stages < least ? least : stages;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = static_cast<unsigned>(tiles * split);
+    cfg.blockDim = kThreads;
+    cfg.dynamicSmemBytes = fixed + stages * per;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, sa, sb, out, M, N, KB, bn, stages, tiles_m,
+                              split);
+}
+
+template <bool BF16>
+cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
+                      void *out, const DeviceInfo &di, cudaStream_t stream)
+{
+    CUtensorMap am, bm, om;
+    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a), K, M, K, 128, 128) != 0 ||
+        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b), K, N, K, 128, 128) != 0)
+        return cudaErrorInvalidValue;
+    static std::atomic<bool> set[kMaxDevices];
+    cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16>, kGemmSmem, di.device, set);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t row_bytes = static_cast<uint64_t>(N) * (BF16 ? 2 : 4);
+    const int tma_out = row_bytes % 16 == 0;
+    om = am;
+    if (tma_out && encode_tensor_map_2d(&om, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                        out, N, M, row_bytes, 32, 32,
+                                        BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) != 0)
+        return cudaErrorInvalidValue;
+    Work w;
+    w.KB = static_cast<int>(ceil_div(K, 128));
+    w.N = N;
+    w.tiles_m = static_cast<int>(ceil_div(M, 128));
+    w.tiles_n = static_cast<int>(ceil_div(N, kBN));
+    // fp32: pieces of at most 16 blocks, whole scale groups each
+    w.segs = BF16 ? 1 : static_cast<int>(ceil_div(w.KB, 16));
+    w.seg_kb = static_cast<int>(ceil_div(ceil_div(w.KB, w.segs), 4) * 4);
+    w.segs = static_cast<int>(ceil_div(w.KB, w.seg_kb));
+    // a last round that fills at most half of the SMs goes in halves
+    const int tiles = w.tiles_m * w.tiles_n, rem = tiles % di.num_sms;
+    w.full = rem <= di.num_sms / 2 ? tiles - rem : tiles;
+    w.items = w.full + 2 * (tiles - w.full);
+    const int grid = w.items < di.num_sms ? w.items : di.num_sms;
+    return launch_pdl(fp8_gemm_kernel<BF16>, grid, kThreads, kGemmSmem, stream, am, bm, om, sa, sb, out, M, N, w,
+                      tma_out);
 }
 
 template <bool BF16>
 cudaError_t run_gemm(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
                      void *out, const DeviceInfo &di, cudaStream_t stream)
 {
-    const int KB = static_cast<int>(ceil_div(K, 128));
-    const Plan p = plan_gemm(M, N, KB, di.num_sms);
-    CUtensorMap am, bm, om;
-    const uint32_t arows = p.split_kernel ? p.bn : 128, brows = p.split_kernel ? 128 : p.bn;
-    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a), K, M, K, 128, arows) != 0 ||
-        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b), K, N, K, 128, brows) != 0)
-        return cudaErrorInvalidValue;
-    if (p.split_kernel) {
-        static std::atomic<bool> set[kMaxDevices];
-        const uint32_t per = stage_bytes_of(p.bn) + 1024;
-        // two CTAs share an SM; the ring also holds the partial sums (512
-        // bytes a column)
-        int stages = static_cast<int>((kSmemLimit / 2 - 2048 - kBarBytes) / per);
-        const int need = static_cast<int>(ceil_div(KB, p.split));
-        const int min_stages = static_cast<int>(ceil_div(512 * p.bn, stage_bytes_of(p.bn)));
-        stages = stages > kMaxStages ? kMaxStages : stages;
-        stages = stages > need ? need : stages;
-        stages = stages < min_stages ? min_stages : stages;
-        const uint32_t smem = 1024 + stages * per + kBarBytes;
-        cudaError_t e = ensure_smem(fp8_gemm_split_kernel<BF16>, kSmemLimit / 2, di.device, set);
-        if (e != cudaSuccess)
-            return e;
-        const int tiles_m = static_cast<int>(ceil_div(M, p.bn));
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = static_cast<unsigned>(ceil_div(N, 128) * tiles_m * p.split);
-        cfg.blockDim = kThreads;
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = p.split;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, sa, sb, out, M, N, KB, p.bn, stages,
-                                  tiles_m, p.split);
-    }
-    static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16>, kSmemLimit, di.device, set);
-    if (e != cudaSuccess)
-        return e;
-    const uint32_t es = BF16 ? 2 : 4;
-    const int tma_out = (static_cast<uint64_t>(N) * es) % 16 == 0;
-    om = am;
-    if (tma_out &&
-        encode_tensor_map_2d(&om, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out, N, M,
-                             static_cast<uint64_t>(N) * es, 32, 32,
-                             BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) != 0)
-        return cudaErrorInvalidValue;
-    const uint32_t per = stage_bytes_of(p.bn) + 1536;
-    int stages = static_cast<int>((kSmemLimit - 1024 - kStaging - kBarBytes) / per);
-    stages = stages > kMaxStages ? kMaxStages : stages;
-    const uint32_t smem = 1024 + stages * per + kStaging + kBarBytes;
-    TileWalk walk{static_cast<int>(ceil_div(M, 128)), static_cast<int>(ceil_div(N, p.bn))};
-    const int64_t tiles = static_cast<int64_t>(walk.tiles_m) * walk.tiles_n;
-    const int grid = static_cast<int>(tiles < di.num_sms ? tiles : di.num_sms);
-    return launch_pdl(fp8_gemm_kernel<BF16>, grid, kThreads, smem, stream, am, bm, om, sa, sb, out, M, N, KB, p.bn,
-                      stages, walk, tma_out);
+    return few_tiles(M, N, di.num_sms) ? run_split<BF16>(a, sa, b, sb, M, N, K, out, di, stream)
+                                       : run_tiles<BF16>(a, sa, b, sb, M, N, K, out, di, stream);
 }
 
 }  // namespace
@@ -770,7 +877,7 @@ cudaError_t launch_fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint
     cudaError_t e = current_device_info(&di);
     if (e != cudaSuccess)
         return e;
-    const Scales sa{a_scale, M, false}, sb{b_scale, N, b_scale_tiles};
+    const Scales sa{a_scale, ceil_div(M, 128), false}, sb{b_scale, ceil_div(N, 128), b_scale_tiles};
     return out_bf16 ? run_gemm<true>(a, sa, b, sb, M, N, K, out, di, stream)
                     : run_gemm<false>(a, sa, b, sb, M, N, K, out, di, stream);
 }

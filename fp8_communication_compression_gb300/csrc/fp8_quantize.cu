@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kQThreads)
 #pragma unroll
                 for (int i = 1; i < 8; ++i)
                     b = cc == i ? byte[i] : b;
-                scale[tc * rows + r + cc] = static_cast<uint8_t>(b);
+                scale[fp8_scale_at(r + cc, tc, (col_tiles + 3) / 4)] = static_cast<uint8_t>(b);
             }
         }
 #pragma unroll
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kQThreads)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (c + j < cols)
-                    scale_t[tr * cols + c + j] = static_cast<uint8_t>(byte[j]);
+                    scale_t[fp8_scale_at(c + j, tr, ((rows + 127) / 128 + 3) / 4)] = static_cast<uint8_t>(byte[j]);
         }
         uint8_t *t = reinterpret_cast<uint8_t *>(tile_t) + (((rg >> 1) ^ (cc & 7)) << 4) + ((rg & 1) << 3);
 #pragma unroll

@@ -95,9 +95,8 @@ cudaError_t launch_gemm_laaq_quantize(const void *a_bf16, const void *b_bf16, in
 cudaError_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, uint64_t *bytes);
 
 // Block-scaled FP8 operands (fp8_quantize.cu; format in fp8_block.cuh): codes
-// [rows][pitch(cols)] with scale bytes [ceil(cols / 128)][rows], and / or
-// codes_t [cols][pitch(rows)] with scale_t [ceil(rows / 128)][cols]; null
-// codes: that direction is left out.  tiles: one byte per 128 x 128 tile,
+// [rows][pitch(cols)] with their scales, and / or codes_t
+// [cols][pitch(rows)] with scale_t; null codes: that direction is left out.  tiles: one byte per 128 x 128 tile,
 // scale [ceil(cols / 128)][ceil(rows / 128)] and scale_t its transpose.
 cudaError_t launch_fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, bool tiles, uint8_t *codes,
                                 uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, cudaStream_t stream);
@@ -108,7 +107,7 @@ cudaError_t launch_fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint
                             cudaStream_t stream);
 
 // The norms around a block (norm_kernels.cu).  n_scale null: n_out is bf16
-// [T][d]; else FP8 codes [T][pitch(d)] and n_scale [ceil(d / 128)][T].
+// [T][d]; else FP8 codes [T][pitch(d)] and their scales n_scale.
 struct NormForward {
     const void *y, *h;
     const float *g_post, *g_pre;

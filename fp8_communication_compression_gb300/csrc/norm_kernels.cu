@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kMaxThreads)
                         make_uint2(f32x4_to_e4m3x4(g[0] * f, g[1] * f, g[2] * f, g[3] * f),
                                    f32x4_to_e4m3x4(g[4] * f, g[5] * f, g[6] * f, g[7] * f));
                 if ((threadIdx.x & 15) == 0 && c < d)
-                    n_scale[(c >> 7) * T + row] = static_cast<uint8_t>(byte);
+                    n_scale[fp8_scale_at(row, c >> 7, (d + 511) / 512)] = static_cast<uint8_t>(byte);
             } else {
                 store_bf16x8<VEC>(static_cast<uint16_t *>(n_out) + row * d, c, d, g);
             }

@@ -529,6 +529,7 @@ taco_status taco_e4m3_encode(const float *x, int64_t n, uint8_t *codes, taco_str
 }
 
 int64_t fp8_pitch(int64_t cols) { return taco::fp8_pitch(cols); }
+int64_t fp8_scale_bytes(int64_t rows, int64_t cols) { return taco::fp8_scale_bytes(rows, cols); }
 
 // Sizes whose tile grids and TMA coordinates fit the kernels' 32-bit indices.
 static bool fp8_dims_fit(int64_t rows, int64_t cols)
@@ -570,13 +571,14 @@ static taco_status fp8_quantize_any(const void *x, int64_t rows, int64_t cols, b
     if ((codes == nullptr) != (scale == nullptr) || (codes_t == nullptr) != (scale_t == nullptr) ||
         (!codes && !codes_t) || !x)
         return TACO_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || (codes && !aligned(codes, 16)) || (codes_t && !aligned(codes_t, 16)))
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(codes_t, 16) ||
+        (!tiles && (!aligned(scale, 16) || !aligned(scale_t, 16))))
         return TACO_ERR_MISALIGNED;
     const uint64_t r = rows, c = cols, rb = fp8_blocks(rows), cb = fp8_blocks(cols);
     const Span outs[4] = {{codes, codes ? r * taco::fp8_pitch(cols) : 0},
-                          {scale, scale ? cb * (tiles ? rb : r) : 0},
+                          {scale, !scale ? 0 : tiles ? cb * rb : taco::fp8_scale_bytes(rows, cols)},
                           {codes_t, codes_t ? c * taco::fp8_pitch(rows) : 0},
-                          {scale_t, scale_t ? rb * (tiles ? cb : c) : 0}};
+                          {scale_t, !scale_t ? 0 : tiles ? cb * rb : taco::fp8_scale_bytes(cols, rows)}};
     const Span ins[1] = {{x, 2 * r * c}};
     if (!apart(outs, 4, ins, 1))
         return TACO_ERR_INVALID_ARG;
@@ -608,11 +610,16 @@ taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b,
         return TACO_OK;
     if (!out || (K > 0 && (!a || !a_scale || !b || !b_scale)))
         return TACO_ERR_INVALID_ARG;
-    if (!aligned(out, 16) || (K > 0 && (!aligned(a, 16) || !aligned(b, 16))))
+    if (!aligned(out, 16) || (K > 0 && (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scale, 16) ||
+                                        (!b_scale_tiles && !aligned(b_scale, 16)))))
         return TACO_ERR_MISALIGNED;
-    const uint64_t m = M, n = N, k = K, kb = fp8_blocks(K);
+    const uint64_t m = M, n = N, k = K;
     const Span outs[1] = {{out, m * n * (out_is_bf16 ? 2 : 4)}};
-    const Span ins[4] = {{a, m * k}, {b, n * k}, {a_scale, kb * m}, {b_scale, kb * (b_scale_tiles ? fp8_blocks(N) : n)}};
+    const Span ins[4] = {{a, m * k},
+                         {b, n * k},
+                         {a_scale, static_cast<uint64_t>(taco::fp8_scale_bytes(M, K))},
+                         {b_scale, static_cast<uint64_t>(b_scale_tiles ? fp8_blocks(K) * fp8_blocks(N)
+                                                                       : taco::fp8_scale_bytes(N, K))}};
     if (!apart(outs, 1, ins, 4))
         return TACO_ERR_INVALID_ARG;
     return from_cuda(taco::launch_fp8_gemm(a, a_scale, b, b_scale, b_scale_tiles != 0, M, N, K, out, out_is_bf16 != 0,
@@ -627,7 +634,7 @@ static uint64_t fp8_piece(int64_t rows, int64_t cols, uint64_t *scale_at)
     const uint64_t codes = up(static_cast<uint64_t>(rows) * taco::fp8_pitch(cols));
     if (scale_at)
         *scale_at = codes;
-    return codes + up(static_cast<uint64_t>(fp8_blocks(cols)) * rows);
+    return codes + up(taco::fp8_scale_bytes(rows, cols));
 }
 
 taco_status fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward, uint64_t *bytes)
@@ -753,12 +760,12 @@ taco_status rmsnorm_gate_residual(const void *y, const void *h, const float *g_p
     if (!y || !h || !g_post || !g_pre || !h_out || !n || (gate_mode != TACO_GATE_NONE) != (gate != nullptr))
         return TACO_ERR_INVALID_ARG;
     if (!aligned(y, 16) || !aligned(h, 16) || !aligned(g_post, 16) || !aligned(g_pre, 16) || !aligned(h_out, 16) ||
-        !aligned(n, 16) || !gate_aligned(gate, gate_mode))
+        !aligned(n, 16) || !aligned(n_scale, 16) || !gate_aligned(gate, gate_mode))
         return TACO_ERR_MISALIGNED;
     const uint64_t td = 2 * static_cast<uint64_t>(T) * d, d4 = 4 * static_cast<uint64_t>(d);
     const Span outs[3] = {{h_out, td},
                           {n, n_scale ? static_cast<uint64_t>(T) * taco::fp8_pitch(d) : td},
-                          {n_scale, n_scale ? static_cast<uint64_t>(fp8_blocks(d)) * T : 0}};
+                          {n_scale, n_scale ? static_cast<uint64_t>(taco::fp8_scale_bytes(T, d)) : 0}};
     const Span ins[5] = {{y, td}, {h, td}, {g_post, d4}, {g_pre, d4}, {gate, gate_bytes(gate_mode, T, d)}};
     if (!apart(outs, 3, ins, 5))
         return TACO_ERR_INVALID_ARG;

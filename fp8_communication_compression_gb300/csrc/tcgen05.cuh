@@ -91,15 +91,21 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
 // ------------------------------------------------- block-scaled FP8 MMA --
 
 // Instruction descriptor of kind::mxf8f6f4 with E4M3 A and B (formats 0),
-// E8M0 scales (bit 23), both operands K-major, scale bytes at position 0 of
-// their 32-bit words: N >> 3 (bits 17-22), M >> 4 (bits 24-28, M = 128).
+// E8M0 scales (bit 23), both operands K-major: N >> 3 (bits 17-22), M >> 4
+// (bits 24-28, M = 128).  The scale is byte 0 of its 32-bit word unless
+// idesc_scale_byte picks another (bits 4-5 for B, 29-30 for A).
 __host__ __device__ constexpr uint32_t idesc_mxf8(int n)
 {
     return (1u << 23) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
+__host__ __device__ constexpr uint32_t idesc_scale_byte(uint32_t idesc, int i)
+{
+    return idesc | (static_cast<uint32_t>(i) << 4) | (static_cast<uint32_t>(i) << 29);
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T for one 128 x N x 32 step of E4M3 values,
-// each product row scaled by its E8M0 bytes at sfa_tmem (4 columns: row r in
+// each product row scaled by its E8M0 byte at sfa_tmem (4 columns: row r in
 // lane r % 32 of column r / 32, repeated in all four lane quarters) and
 // sfb_tmem (the same for B's rows); issued by one thread.
 __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -116,7 +122,7 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint6
 
 // Copies 32 rows of 16 bytes (512 contiguous bytes of shared memory, eight-
 // row groups 128 bytes apart, no swizzle) into 4 columns of tensor memory,
-// row r to lane r of each of the four lane quarters: the scale bytes of 128
+// row r to lane r of each of the four lane quarters: the scale words of 128
 // operand rows, row r at byte 16 (r % 32) + 4 (r / 32).  Runs in order with
 // the MMAs the same thread issues.
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem_addr)

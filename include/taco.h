@@ -491,15 +491,23 @@ taco_status taco_two_shot_host_noalloc(int32_t P, int64_t rows, int64_t d, int32
  * and makes every product that reads it NaN.
  *
  * Layout: codes [rows][P], P = fp8_pitch(cols) (cols rounded up to a multiple
- * of 16, the padding zero, NaN in a NaN block); scale
- * [ceil(cols / 128)][rows].  Code pointers are 16-byte aligned.
+ * of 16, the padding zero, NaN in a NaN block).  Scales lie as the tensor
+ * core reads them, in 512-byte pieces [ceil(rows / 128)][ceil(cols / 512)]:
+ * the byte of row r and block b is at
+ *   (r / 128 * ceil(cols / 512) + b / 4) * 512 + r % 32 * 16 + r % 128 / 32 * 4
+ *   + b % 4,
+ * fp8_scale_bytes(rows, cols) bytes in all; bytes that belong to no row or
+ * block are neither written nor used.  Code and scale pointers are 16-byte
+ * aligned.  A weight's scales are one byte per 128 x 128 tile instead:
+ * [ceil(cols / 128)][ceil(rows / 128)].
  */
 int64_t fp8_pitch(int64_t cols);
+int64_t fp8_scale_bytes(int64_t rows, int64_t cols);
 
 /*
  * fp8_quantize - x bf16 [rows][cols] (16-byte aligned) to
- *   codes   [rows][fp8_pitch(cols)], scale   [ceil(cols / 128)][rows]  and / or
- *   codes_t [cols][fp8_pitch(rows)], scale_t [ceil(rows / 128)][cols]
+ *   codes   [rows][fp8_pitch(cols)], scale   (rows, cols)  and / or
+ *   codes_t [cols][fp8_pitch(rows)], scale_t (cols, rows)
  * (the transposed matrix, in blocks of 128 along its own rows), in one pass.
  * codes and scale, or codes_t and scale_t, may both be null.
  *
@@ -514,11 +522,11 @@ taco_status fp8_quantize_weight(const void *x_bf16, int64_t rows, int64_t cols, 
 
 /*
  * fp8_gemm - out[M][N] = A B^T on the tensor cores, accumulated in fp32 with
- * the scales applied, rounded once if out_is_bf16.  a: codes [M][K], a_scale
- * [ceil(K / 128)][M]; b: codes [N][K], b_scale [ceil(K / 128)][N], or with
- * b_scale_tiles != 0 [ceil(K / 128)][ceil(N / 128)].  K is the padded row
- * length, a multiple of 16 (K = 0: zeros).  out is 16-byte aligned.  The
- * summation order is fixed: the same inputs give the same bits.
+ * the scales applied, rounded once if out_is_bf16.  a: codes [M][K] with
+ * a_scale; b: codes [N][K] with b_scale, of rows or, with b_scale_tiles != 0,
+ * of 128 x 128 tiles (any alignment).  K is the padded row length, a multiple
+ * of 16 (K = 0: zeros).  out is 16-byte aligned.  The summation order is
+ * fixed: the same inputs give the same bits.
  */
 taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
                      int32_t b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, int32_t out_is_bf16,
@@ -563,7 +571,7 @@ taco_status fp8_linear_backward(const void *dy_bf16, const void *x_bf16, const u
  *   TACO_GATE_TOKEN    fp32 [T]
  *   TACO_GATE_FULL     bf16 [T][d], 16-byte aligned
  * n_scale null: n is bf16 [T][d].  Else n holds FP8 codes [T][fp8_pitch(d)]
- * and n_scale their scale bytes [ceil(d / 128)][T].
+ * and n_scale (16-byte aligned) their fp8_scale_bytes(T, d) scale bytes.
  * 1 <= d <= TACO_NORM_MAX_D; eps > 0.
  *
  * The backward pass takes dn and dh_out (gradients at n and h_out, bf16

@@ -26,6 +26,12 @@ def test_pitch(lib):
         assert lib.fp8_pitch(n) == api.fp8_pitch(n) == -(-n // 16) * 16
 
 
+def test_scale_bytes_and_their_plain_order(lib):
+    for rows, cols in ((1, 1), (128, 512), (129, 513), (300, 2560)):
+        assert lib.fp8_scale_bytes(rows, cols) == -(-rows // 128) * -(-cols // 512) * 512
+        assert math.prod(api._scale_shape(rows, cols)) == lib.fp8_scale_bytes(rows, cols)
+
+
 @pytest.mark.parametrize("fn", ["fp8_quantize", "fp8_quantize_weight"])
 def test_quantize_validation(lib, fn):
     f = lambda x=A, rows=64, cols=256, c=A * 2, s=A * 3, ct=A * 4, st=A * 5: getattr(lib, fn)(
@@ -38,8 +44,9 @@ def test_quantize_validation(lib, fn):
     assert f(c=None) == INVALID and f(st=None) == INVALID     # half a direction
     assert f(c=None, s=None, ct=None, st=None) == INVALID     # nothing to do
     assert f(x=A + 8) == MISALIGNED and f(c=A * 2 + 8) == MISALIGNED and f(ct=A * 4 + 4) == MISALIGNED
+    assert (f(s=A * 3 + 8) == MISALIGNED) == (fn == "fp8_quantize")
     assert f(c=A) == INVALID                                  # codes over the input
-    assert f(s=A * 2 + 64 * 256 - 1) == INVALID               # scales over the last code
+    assert f(s=A * 2 + 64 * 256 - 16) == INVALID              # scales over the last codes
     assert f(ct=A * 2 + 16) == INVALID                        # the two code matrices overlap
 
 
@@ -53,7 +60,7 @@ def test_gemm_validation(lib):
     assert f(M=(1 << 30) + 1) == UNSUPPORTED
     for k in ("a", "sa", "b", "sb", "o"):
         assert f(**{k: None}) == INVALID
-    for k in ("a", "b", "o"):
+    for k in ("a", "sa", "b", "sb", "o"):
         assert f(**{k: A * 7 + 8}) == MISALIGNED
     for at in (A, A * 2, A * 3, A * 4):
         assert f(o=at) == INVALID                             # output over an input
@@ -111,7 +118,8 @@ def test_norm_validation(lib):
         assert f(**{k: A * 9 + 8}) == MISALIGNED
     assert f(mode=3, g=A * 5 + 8) == MISALIGNED and f(mode=2, g=A * 5 + 2) == MISALIGNED
     assert f(o=A) == INVALID and f(n=A * 6 + 16) == INVALID and f(mode=1, g=A * 6) == INVALID
-    assert f(ns=A * 7 + 8 * 256 - 1) == INVALID                # scales over the codes
+    assert f(ns=A * 7 + 8 * 256 - 16) == INVALID               # scales over the codes
+    assert f(ns=A * 8 + 8) == MISALIGNED
 
     v = ctypes.c_uint64(0)
     assert lib.rmsnorm_gate_residual_workspace_bytes(8, 256, 0, None) == INVALID

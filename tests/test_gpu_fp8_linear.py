@@ -38,7 +38,8 @@ def check_codes(codes, scale, x, tiles):
     assert codes.shape == (rows, api.fp8_pitch(cols))
     assert torch.equal(R.code_values(codes)[:, :cols], q)
     assert not codes[:, cols:].any()
-    assert torch.equal(scale.cpu().long() - 127, E)
+    plain = scale if tiles else api.fp8_scales(scale, rows, cols)
+    assert torch.equal(plain.cpu().long() - 127, E)
 
 
 SHAPES = [(1, 1), (1, 4096), (2, 17), (8, 128), (127, 129), (128, 128), (130, 250), (257, 1000), (300, 392), (5, 8200)]
@@ -52,8 +53,9 @@ def test_quantize_is_exact_in_both_directions(rows, cols):
     ct, st = api.fp8_quantize(x, rowwise=False, colwise=True)
     check_codes(ct, st, x.t().contiguous(), False)
     both = api.fp8_quantize(x, colwise=True)
-    for a, b in zip(both, (c, s, ct, st)):
-        assert torch.equal(a, b)
+    assert torch.equal(both[0], c) and torch.equal(both[2], ct)
+    check_codes(both[0], both[1], x, False)
+    check_codes(both[2], both[3], x.t().contiguous(), False)
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -71,14 +73,15 @@ def test_quantize_marks_blocks_with_inf_or_nan():
     x = activation(6, 300, 3)
     x[0, 5], x[2, 140], x[4, 299] = math.nan, math.inf, -math.inf
     c, s = api.fp8_quantize(x)
+    plain = api.fp8_scales(s, 6, 300)
     bad = {(0, 0), (2, 1), (4, 2)}
     for r in range(6):
         for b in range(3):
             nan_codes = torch.isnan(R.code_values(c[r, 128 * b:min(128 * b + 128, 300)]))
             if (r, b) in bad:
-                assert s[b, r] == 255 and nan_codes.all()
+                assert plain[b, r] == 255 and nan_codes.all()
             else:
-                assert s[b, r] != 255 and not nan_codes.any()
+                assert plain[b, r] != 255 and not nan_codes.any()
     w = api.fp8_quantize_weight(activation(64, 300, 4, zero_rows=False)[4:].contiguous() * 1e-3)
     y = api.fp8_linear(x[4:5], w[0], w[1])
     assert torch.isnan(y).all()
@@ -93,7 +96,24 @@ def integer_operand(rows, K, seed):
     g = torch.Generator().manual_seed(seed)
     v = torch.randint(-4, 5, (rows, K), generator=g).float()
     codes = v.to(torch.float8_e4m3fn).view(torch.uint8)
-    return codes.cuda(), torch.randint(126, 129, (-(-K // 128), rows), generator=g).to(torch.uint8).cuda()
+    plain = torch.randint(126, 129, (-(-K // 128), rows), generator=g).to(torch.uint8)
+    return codes.cuda(), laid_out(plain, rows, K).cuda()
+
+
+def laid_out(plain, rows, K):
+    """Scale bytes [blocks, rows] in the stored layout; 0xFF (NaN) in the
+    places that belong to no row or block."""
+    G = -(-K // 512)
+    out = torch.full((-(-rows // 128) * G * 512,), 255, dtype=torch.uint8)
+    r, b = torch.arange(rows)[None], torch.arange(plain.shape[0])[:, None]
+    at = ((r // 128 * G + b // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + b % 4)
+    out[at.reshape(-1)] = plain.reshape(-1)
+    return out.view(-(-rows // 128), G, 512)
+
+
+def row_values(codes, scale):
+    rows, K = codes.shape
+    return R.values(codes, api.fp8_scales(scale, rows, K))
 
 
 # (M, N, K): single tokens, sizes that fill no tile, split contractions,
@@ -111,7 +131,7 @@ def test_gemm_of_whole_numbers_is_exact(M, N, K, dtype):
     # every product and partial sum is a multiple of 2^-2 below 2^18
     a, sa = integer_operand(M, K, 5)
     b, sb = integer_operand(N, K, 6)
-    ref = R.values(a, sa) @ R.values(b, sb).t()
+    ref = row_values(a, sa) @ row_values(b, sb).t()
     out = torch.full((M, N), math.nan, dtype=dtype, device="cuda")
     api.fp8_gemm(a, sa, b, sb, out=out)
     assert torch.equal(out.cpu().double(), ref.to(dtype).double())
@@ -123,7 +143,7 @@ def test_gemm_with_a_tiled_weight(M, N, K):
     b, _ = integer_operand(N, K, 8)
     sb = torch.randint(126, 129, (-(-K // 128), -(-N // 128)), generator=torch.Generator().manual_seed(9))
     sb = sb.to(torch.uint8).cuda()
-    ref = R.values(a, sa) @ R.values(b, sb, tiles=True).t()
+    ref = row_values(a, sa) @ R.values(b, sb, tiles=True).t()
     assert torch.equal(api.fp8_gemm(a, sa, b, sb, torch.float32).cpu().double(), ref)
 
 
@@ -202,7 +222,7 @@ def test_empty_sizes():
     dx, dw = api.fp8_linear_backward(e(0, 40), e(0, 96), w[2], w[3])
     assert dx.shape == (0, 96) and dw.shape == (40, 96) and not dw.any()
     c, s = api.fp8_quantize(e(3, 0))
-    assert c.shape == (3, 0) and s.shape == (0, 3)
+    assert c.shape == (3, 0) and s.shape == (1, 0, 512)
     w0 = torch.empty((40, 0), dtype=torch.uint8, device="cuda")
     s0 = torch.empty((0, 1), dtype=torch.uint8, device="cuda")
     y = api.fp8_linear(e(3, 0), w0, s0)
@@ -276,7 +296,8 @@ def test_outputs_stay_inside_their_buffers():
     for rows, cols in ((1, 17), (129, 257), (300, 200)):
         x = activation(rows, cols, 50)
         P, Pt, cb, rb = api.fp8_pitch(cols), api.fp8_pitch(rows), -(-cols // 128), -(-rows // 128)
-        for fn, sizes in ((lib.fp8_quantize, (rows * P, cb * rows, cols * Pt, rb * cols)),
+        for fn, sizes in ((lib.fp8_quantize, (rows * P, lib.fp8_scale_bytes(rows, cols), cols * Pt,
+                                              lib.fp8_scale_bytes(cols, rows))),
                           (lib.fp8_quantize_weight, (rows * P, cb * rb, cols * Pt, cb * rb))):
             bufs = [guarded(n) for n in sizes]
             assert fn(x.data_ptr(), rows, cols, *[p for _, p in bufs], stream) == 0
