@@ -28,7 +28,7 @@ def _stream_handle(stream: torch.cuda.Stream | None) -> ctypes.c_void_p:
 def _need(t: torch.Tensor, name: str, dtypes, numel: int | None = None) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
@@ -443,6 +443,21 @@ def agoq_gemm_laaq_quantize(a: torch.Tensor, b: torch.Tensor, bits: int = 4, blo
 
 # ------------------------------------------- block-scaled FP8 matrices --
 
+# These calls are made once or several times per layer, also for a single
+# token, so what they do on the host counts: the stream is taken as the raw
+# handle (current_stream() builds an object, 3 us on this host's Arm cores),
+# shapes are read once, and no tensor operation runs besides torch.empty.
+
+_BF = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_BYTE = (torch.uint8,)
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """Raw handle of ``stream``, or of the current stream of t's device."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
     """An output or workspace for a call on ``stream``: memory of the current
     stream's pool, kept from reuse until work queued on ``stream`` is done."""
@@ -452,22 +467,31 @@ def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tenso
     return t
 
 
+def _new_like(x: torch.Tensor, stream) -> torch.Tensor:
+    t = torch.empty_like(x)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _need2(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> None:
     _need(t, name, dtypes)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
 
 
 def _matrix(x: torch.Tensor, name: str):
     """(rows, columns) of a bf16 matrix; leading dimensions count as rows."""
-    _need(x, name, (torch.bfloat16,))
-    if x.dim() < 2:
+    _need(x, name, _BF)
+    shape = x.shape
+    if len(shape) == 2:
+        return shape
+    if len(shape) < 2:
         raise ValueError(f"{name} must have at least two dimensions")
-    cols = x.shape[-1]
     rows = 1
-    for n in x.shape[:-1]:
+    for n in shape[:-1]:
         rows *= n
-    return rows, cols
+    return rows, shape[-1]
 
 
 def fp8_pitch(cols: int) -> int:
@@ -488,7 +512,7 @@ def _scale_shape(rows: int, cols: int):
 def fp8_scales(scale: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
     """The scale bytes [ceil(cols / 128), rows] of a [rows, cols] matrix's
     scales, one of block b and row r at [b, r] (a copy in plain order)."""
-    _need(scale, "scale", (torch.uint8,))
+    _need(scale, "scale", _BYTE)
     T, G, _ = _scale_shape(rows, cols)
     if tuple(scale.shape) != (T, G, 512):
         raise ValueError(f"scale has shape {tuple(scale.shape)}, expected {(T, G, 512)}")
@@ -518,7 +542,7 @@ def fp8_quantize(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, s
         out += (_new((cols, fp8_pitch(rows)), u8, dev, stream), _new(_scale_shape(cols, rows), u8, dev, stream))
     ptrs = [t.data_ptr() for t in out]
     ptrs = ptrs if len(ptrs) == 4 else ptrs + [None, None] if rowwise else [None, None] + ptrs
-    st = _lib.load().fp8_quantize(x.data_ptr(), rows, cols, *ptrs, _stream_handle(stream))
+    st = _lib.load().fp8_quantize(x.data_ptr(), rows, cols, *ptrs, _stream_of(x, stream))
     _lib.check("fp8_quantize", st)
     return out
 
@@ -532,7 +556,7 @@ def fp8_quantize_weight(w: torch.Tensor, stream=None):
     dev, u8 = w.device, torch.uint8
     out = (_new((N, fp8_pitch(K)), u8, dev, stream), _new((_blocks(K), _blocks(N)), u8, dev, stream),
            _new((K, fp8_pitch(N)), u8, dev, stream), _new((_blocks(N), _blocks(K)), u8, dev, stream))
-    st = _lib.load().fp8_quantize_weight(w.data_ptr(), N, K, *[t.data_ptr() for t in out], _stream_handle(stream))
+    st = _lib.load().fp8_quantize_weight(w.data_ptr(), N, K, *[t.data_ptr() for t in out], _stream_of(w, stream))
     _lib.check("fp8_quantize_weight", st)
     return out
 
@@ -545,7 +569,7 @@ def _out_dtype(out: torch.Tensor | None, out_dtype: torch.dtype) -> torch.dtype:
 
 
 def _need_scale(t: torch.Tensor, name: str, rows: int, cols: int) -> None:
-    _need(t, name, (torch.uint8,))
+    _need(t, name, _BYTE)
     if tuple(t.shape) != _scale_shape(rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {_scale_shape(rows, cols)}")
 
@@ -564,7 +588,7 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
     _need_scale(a_scale, "a_scale", M, P)
     tiles = isinstance(b_scale, torch.Tensor) and b_scale.dim() == 2
     if tiles:
-        _need2(b_scale, "b_scale", (torch.uint8,), _blocks(P), _blocks(N))
+        _need2(b_scale, "b_scale", _BYTE, _blocks(P), _blocks(N))
     else:
         _need_scale(b_scale, "b_scale", N, P)
     dt = _out_dtype(out, out_dtype)
@@ -573,7 +597,7 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
     else:
         _need2(out, "out", (dt,), M, N)
     st = _lib.load().fp8_gemm(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), int(tiles), M, N, P,
-                              out.data_ptr(), int(dt == torch.bfloat16), _stream_handle(stream))
+                              out.data_ptr(), int(dt == torch.bfloat16), _stream_of(a, stream))
     _lib.check("fp8_gemm", st)
     return out
 
@@ -593,19 +617,20 @@ def fp8_linear(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
     fp8_quantize_weight's (codes, scale); bf16 or fp32 [..., N]."""
     M, K = _matrix(x, "x")
     _need(codes, "codes", _U8)
-    if codes.dim() != 2 or codes.shape[1] != fp8_pitch(K):
-        raise ValueError(f"codes has shape {tuple(codes.shape)}, expected (N, {fp8_pitch(K)})")
-    N = codes.shape[0]
-    _need2(scale, "scale", (torch.uint8,), _blocks(K), _blocks(N))
+    shape = codes.shape
+    if len(shape) != 2 or shape[1] != fp8_pitch(K):
+        raise ValueError(f"codes has shape {tuple(shape)}, expected (N, {fp8_pitch(K)})")
+    N = shape[0]
+    _need2(scale, "scale", _BYTE, _blocks(K), _blocks(N))
     dt = _out_dtype(out, out_dtype)
     if out is None:
         out = _new((*x.shape[:-1], N), dt, x.device, stream)
     else:
         _need(out, "out", (dt,), M * N)
     nbytes = _linear_workspace_bytes(M, N, K, 0)
-    ws = _new(nbytes, torch.uint8, x.device, stream)
+    ws = _new(nbytes, torch.uint8, x.device, stream) if nbytes else None
     st = _lib.load().fp8_linear(x.data_ptr(), codes.data_ptr(), scale.data_ptr(), M, N, K, out.data_ptr(),
-                                int(dt == torch.bfloat16), ws.data_ptr(), nbytes, _stream_handle(stream))
+                                int(dt == torch.bfloat16), _ptr(ws), nbytes, _stream_of(x, stream))
     _lib.check("fp8_linear", st)
     return out
 
@@ -625,15 +650,15 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor, codes_t: torch.Tensor
     if not (need_dx or need_dw):
         raise ValueError("need_dx or need_dw must be set")
     _need2(codes_t, "codes_t", _U8, K, fp8_pitch(N))
-    _need2(scale_t, "scale_t", (torch.uint8,), _blocks(N), _blocks(K))
+    _need2(scale_t, "scale_t", _BYTE, _blocks(N), _blocks(K))
     dt = _out_dtype(None, dw_dtype)
-    dx = _new(x.shape, torch.bfloat16, x.device, stream) if need_dx else None
+    dx = _new_like(x, stream) if need_dx else None
     dw = _new((N, K), dt, x.device, stream) if need_dw else None
     nbytes = _linear_workspace_bytes(M, N, K, 1)
     ws = _new(nbytes, torch.uint8, x.device, stream)
     st = _lib.load().fp8_linear_backward(dy.data_ptr(), x.data_ptr(), codes_t.data_ptr(), scale_t.data_ptr(), M, N, K,
                                          dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None,
-                                         int(dt == torch.bfloat16), ws.data_ptr(), nbytes, _stream_handle(stream))
+                                         int(dt == torch.bfloat16), ws.data_ptr(), nbytes, _stream_of(x, stream))
     _lib.check("fp8_linear_backward", st)
     return dx, dw
 
@@ -645,23 +670,23 @@ def _gate_mode(gate: torch.Tensor | None, T: int, d: int) -> int:
     if gate is None:
         return 0
     if isinstance(gate, torch.Tensor) and gate.dtype == torch.bfloat16:
-        _need2(gate, "gate", (torch.bfloat16,), T, d)
+        _need2(gate, "gate", _BF, T, d)
         return 3
-    _need(gate, "gate", (torch.float32,))
-    if gate.dim() == 1 and gate.shape[0] == d:
+    _need(gate, "gate", _F32)
+    if gate.shape == (d,):
         return 1
-    if gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] == 1:
+    if gate.shape == (T, 1):
         return 2
     raise ValueError(f"gate has shape {tuple(gate.shape)}, expected fp32 ({d},), fp32 ({T}, 1) or bf16 ({T}, {d})")
 
 
 def _norm_args(y, h, gain_post, gain_pre, gate):
     T, d = _matrix(y, "y")
-    _need(h, "h", (torch.bfloat16,))
+    _need(h, "h", _BF)
     if h.shape != y.shape:
         raise ValueError(f"y has shape {tuple(y.shape)} and h {tuple(h.shape)}")
-    _need(gain_post, "gain_post", (torch.float32,), d)
-    _need(gain_pre, "gain_pre", (torch.float32,), d)
+    _need(gain_post, "gain_post", _F32, d)
+    _need(gain_pre, "gain_pre", _F32, d)
     return T, d, _gate_mode(gate, T, d)
 
 
@@ -682,11 +707,10 @@ def rmsnorm_gate_residual(y: torch.Tensor, h: torch.Tensor, gain_post: torch.Ten
     number of rows.  Returns (h_new, n), bf16 like y; n is taken from h_new
     before its rounding."""
     T, d, mode = _norm_args(y, h, gain_post, gain_pre, gate)
-    h_new = _new(y.shape, torch.bfloat16, y.device, stream)
-    n = _new(y.shape, torch.bfloat16, y.device, stream)
+    h_new, n = _new_like(y, stream), _new_like(y, stream)
     st = _lib.load().rmsnorm_gate_residual(y.data_ptr(), h.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
                                            _ptr(gate), mode, residual_scale, eps, T, d, h_new.data_ptr(),
-                                           n.data_ptr(), None, _stream_handle(stream))
+                                           n.data_ptr(), None, _stream_of(y, stream))
     _lib.check("rmsnorm_gate_residual", st)
     return h_new, n
 
@@ -698,12 +722,12 @@ def rmsnorm_gate_residual_fp8(y: torch.Tensor, h: torch.Tensor, gain_post: torch
     uint8 [T, fp8_pitch(d)], scale), the operand of fp8_gemm as fp8_quantize
     gives it (blocks of 128 along the rows, from the fp32 n)."""
     T, d, mode = _norm_args(y, h, gain_post, gain_pre, gate)
-    h_new = _new(y.shape, torch.bfloat16, y.device, stream)
+    h_new = _new_like(y, stream)
     codes = _new((T, fp8_pitch(d)), torch.uint8, y.device, stream)
     scale = _new(_scale_shape(T, d), torch.uint8, y.device, stream)
     st = _lib.load().rmsnorm_gate_residual(y.data_ptr(), h.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
                                            _ptr(gate), mode, residual_scale, eps, T, d, h_new.data_ptr(),
-                                           codes.data_ptr(), scale.data_ptr(), _stream_handle(stream))
+                                           codes.data_ptr(), scale.data_ptr(), _stream_of(y, stream))
     _lib.check("rmsnorm_gate_residual", st)
     return h_new, codes, scale
 
@@ -725,20 +749,20 @@ def rmsnorm_gate_residual_backward(dn: torch.Tensor, dh_new: torch.Tensor, y: to
     gradients are summed over the rows in a fixed order."""
     T, d, mode = _norm_args(y, h_new, gain_post, gain_pre, gate)
     for t, name in ((dn, "dn"), (dh_new, "dh_new")):
-        _need(t, name, (torch.bfloat16,))
+        _need(t, name, _BF)
         if t.shape != y.shape:
             raise ValueError(f"y has shape {tuple(y.shape)} and {name} {tuple(t.shape)}")
     dev = y.device
-    dy, dh = _new(y.shape, torch.bfloat16, dev, stream), _new(y.shape, torch.bfloat16, dev, stream)
+    dy, dh = _new_like(y, stream), _new_like(y, stream)
     dg_post = _new((d,), torch.float32, dev, stream)
     dg_pre = _new((d,), torch.float32, dev, stream)
-    dgate = None if gate is None else _new(gate.shape, gate.dtype, dev, stream)
+    dgate = None if gate is None else _new_like(gate, stream)
     nbytes = _norm_workspace_bytes(T, d, mode, dev.index)
     ws = _new(nbytes, torch.uint8, dev, stream)
     st = _lib.load().rmsnorm_gate_residual_backward(
         dn.data_ptr(), dh_new.data_ptr(), y.data_ptr(), h_new.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
         _ptr(gate), mode, residual_scale, eps, T, d, dy.data_ptr(), dh.data_ptr(), dg_post.data_ptr(),
-        dg_pre.data_ptr(), _ptr(dgate), ws.data_ptr(), nbytes, _stream_handle(stream))
+        dg_pre.data_ptr(), _ptr(dgate), ws.data_ptr(), nbytes, _stream_of(y, stream))
     _lib.check("rmsnorm_gate_residual_backward", st)
     return dy, dh, dg_post, dg_pre, dgate
 

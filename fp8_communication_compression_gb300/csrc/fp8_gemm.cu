@@ -540,16 +540,24 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank)
+// The address of CTA `rank`'s shared memory at this CTA's address `addr`.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank)
 {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
     return v;
 }
 
+constexpr int kMaxSplit = 8;               // portable cluster size
 constexpr uint32_t kSplitTmem = 256;       // accumulator: columns 0 .. 127, scales from 128
 
 template <bool BF16> __device__ __forceinline__ void store_one(void *out, int64_t at, float v)
@@ -717,15 +725,45 @@ __global__ void __launch_bounds__(kThreads)
     if (split > 1) {
         __syncwarp();
         cluster_sync();
-        // this CTA's share of the columns: the 128 rows of a column across
-        // four warps, the partials added in the order of the split
-        const int t = threadIdx.x;
-        if (t < 128 && n0 + t < N) {
-            for (int c = rank; c < BN && m0 + c < M; c += split) {
-                float acc = 0.0f;
-                for (int p = 0; p < split; ++p)
-                    acc += ld_cluster_f32(r.base + 4 * (128 * c + t), p);
-                store_one<BF16>(out, (m0 + c) * N + n0 + t, acc);
+        // this CTA's share of the columns, a column a warp (four rows a
+        // lane): the S partials' loads in flight together, then added in the
+        // order of the split
+        const int64_t n = n0 + 4 * lane;
+        uint32_t parts[kMaxSplit];
+#pragma unroll
+        for (int p = 0; p < kMaxSplit; ++p)
+            parts[p] = map_cluster(r.base, p < split ? p : 0) + 16 * lane;
+        for (int c = rank + split * warp; c < BN && m0 + c < M; c += split * (kThreads / 32)) {
+            float4 v[kMaxSplit];
+#pragma unroll
+            for (int p = 0; p < kMaxSplit; ++p)
+                if (p < split)
+                    v[p] = ld_cluster_f32x4(parts[p] + 512 * c);
+            float4 acc = v[0];
+#pragma unroll
+            for (int p = 1; p < kMaxSplit; ++p)
+                if (p < split) {
+                    acc.x += v[p].x;
+                    acc.y += v[p].y;
+                    acc.z += v[p].z;
+                    acc.w += v[p].w;
+                }
+            const int64_t at = (m0 + c) * N + n;
+            if (n + 3 < N && (N & 3) == 0) {
+                if constexpr (BF16)
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
+                        make_uint2(f32x2_to_bf16x2(acc.x, acc.y), f32x2_to_bf16x2(acc.z, acc.w));
+                else
+                    *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = acc;
+            } else {
+                if (n < N)
+                    store_one<BF16>(out, at, acc.x);
+                if (n + 1 < N)
+                    store_one<BF16>(out, at + 1, acc.y);
+                if (n + 2 < N)
+                    store_one<BF16>(out, at + 2, acc.z);
+                if (n + 3 < N)
+                    store_one<BF16>(out, at + 3, acc.w);
             }
         }
         __syncwarp();
@@ -770,7 +808,7 @@ cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
     const int tiles_m = static_cast<int>(ceil_div(M, 128));
     const int64_t tiles = ceil_div(N, 128) * tiles_m;
     int split = 1;
-    while (split < 8 && tiles * (split + 1) <= 2 * di.num_sms && KB / (split + 1) >= 2)
+    while (split < kMaxSplit && tiles * (split + 1) <= 2 * di.num_sms && KB / (split + 1) >= 2)
         ++split;
     CUtensorMap am, bm;
     if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a), K, M, K, 128, bn) != 0 ||

@@ -105,6 +105,11 @@ cudaError_t launch_fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, 
 cudaError_t launch_fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
                             bool b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, bool out_bf16,
                             cudaStream_t stream);
+// fp8_linear for few tokens without a workspace (fp8_decode.cu), where
+// fp8_decode_takes(M, K); scale: a weight's (128 x 128 tiles).
+bool fp8_decode_takes(int64_t M, int64_t K);
+cudaError_t launch_fp8_decode(const void *x_bf16, const uint8_t *codes, const uint8_t *scale, int64_t M, int64_t N,
+                              int64_t K, void *y, bool y_bf16, cudaStream_t stream);
 
 // The norms around a block (norm_kernels.cu).  n_scale null: n_out is bf16
 // [T][d]; else FP8 codes [T][pitch(d)] and their scales n_scale.

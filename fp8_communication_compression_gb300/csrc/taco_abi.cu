@@ -645,7 +645,7 @@ taco_status fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t 
     if (!fp8_dims_fit(M, K) || !fp8_dims_fit(N, K) || !fp8_dims_fit(M, N))
         return TACO_ERR_UNSUPPORTED;
     *bytes = backward ? fp8_piece(M, N, nullptr) + fp8_piece(N, M, nullptr) + fp8_piece(K, M, nullptr)
-                      : fp8_piece(M, K, nullptr);
+              : taco::fp8_decode_takes(M, K) ? 0 : fp8_piece(M, K, nullptr);
     return TACO_OK;
 }
 
@@ -657,9 +657,7 @@ taco_status fp8_linear(const void *x_bf16, const uint8_t *codes, const uint8_t *
     taco_status st = fp8_linear_workspace_bytes(M, N, K, 0, &need);
     if (st != TACO_OK || M == 0 || N == 0)
         return st;
-    if (K > 0 && (!x_bf16 || !codes || !scale || !workspace))
-        return TACO_ERR_INVALID_ARG;
-    if (!y || workspace_bytes < need)
+    if (!y || workspace_bytes < need || (need > 0 && !workspace) || (K > 0 && (!x_bf16 || !codes || !scale)))
         return TACO_ERR_INVALID_ARG;
     if (!aligned(y, 16) || !aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(workspace, 256))
         return TACO_ERR_MISALIGNED;
@@ -670,6 +668,9 @@ taco_status fp8_linear(const void *x_bf16, const uint8_t *codes, const uint8_t *
                          {scale, static_cast<uint64_t>(fp8_blocks(K)) * fp8_blocks(N)}};
     if (!apart(outs, 2, ins, 3))
         return TACO_ERR_INVALID_ARG;
+    if (K > 0 && need == 0)  // few tokens: one kernel
+        return from_cuda(taco::launch_fp8_decode(x_bf16, codes, scale, M, N, K, y, y_is_bf16 != 0,
+                                                 reinterpret_cast<cudaStream_t>(stream)));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     fp8_piece(M, K, &scale_at);
     if (K > 0 && (st = fp8_quantize(x_bf16, M, K, ws, ws + scale_at, nullptr, nullptr, stream)) != TACO_OK)
