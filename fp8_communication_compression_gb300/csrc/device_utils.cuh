@@ -31,13 +31,23 @@ __device__ __forceinline__ uint64_t global_timer_ns()
 // grid to complete and its memory to be visible).  Without that launch
 // attribute the instruction is a no-op.
 //
-// No kernel here triggers its dependents early (griddepcontrol.
+// No codec kernel triggers its dependents early (griddepcontrol.
 // launch_dependents): a dependent grid is released when its predecessor
 // completes.  Measured on GB300 in the back-to-back compress -> reduce ->
 // decompress step at the GPT-6.7B size, an early trigger at the start of
 // every kernel made the step slower: 122.1 us against 120.3 us with the
 // 16-element shard reduce, and 132.7 us against 118.9 us with the
 // 32-element one.
+
+// (The calls of the FP8 linear layer and of the norms do: see below.)
+//
+// pdl_trigger() at the start of a kernel lets the next grid of the stream
+// start as soon as this one's CTAs leave room; every kernel still waits for
+// its predecessor's end in pdl_wait() before it touches memory.  It pays
+// where a layer's kernels are short (a few us) and their launch latency
+// shows.
+
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -326,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(r.tmem_slot(), 512);
         tmem_relinquish_alloc_permit();
     }
+    if (work.items <= 2 * static_cast<int>(gridDim.x))
+        pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
     __syncthreads();
@@ -596,6 +598,7 @@ __global__ void __launch_bounds__(kThreads)
         tmem_alloc(r.tmem_slot(), kSplitTmem);
         tmem_relinquish_alloc_permit();
     }
+    pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
     __syncthreads();

@@ -23,6 +23,10 @@ namespace taco {
 namespace {
 
 constexpr int kQThreads = 256;
+// The next grid may start early after a small one (its product's prologue
+// runs meanwhile: 37 x 2560 -> 10240 in 8.7 instead of 10.5 us); after a large
+// one that costs bandwidth (both directions of 8192 x 4096: 35 us against 31).
+constexpr int kTriggerCtas = 608;
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
@@ -50,6 +54,8 @@ __global__ void __launch_bounds__(kQThreads)
     const int64_t r0 = tr * 128, c0 = tc * 128;
     const int64_t r = r0 + 8 * rg, c = c0 + 8 * cc;
     const int64_t pitch = fp8_pitch(cols), pitch_t = fp8_pitch(rows);
+    if (gridDim.x <= kTriggerCtas)
+        pdl_trigger();
     pdl_wait();
 
     uint32_t v[8][4];

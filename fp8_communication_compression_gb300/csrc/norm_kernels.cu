@@ -241,6 +241,8 @@ __global__ void __launch_bounds__(kMaxThreads)
         ring.src[2] = static_cast<const uint16_t *>(gate);
     ring_init(ring, smem_raw, smem_u32(bars), T, d, slots);
     const float inv_d = 1.0f / static_cast<float>(d);
+    if (T <= 4 * static_cast<int64_t>(gridDim.x))  // short: the next kernel's launch overlaps it
+        pdl_trigger();
     pdl_wait();
     ring.start();
     for (int64_t row = blockIdx.x; row < T; row += gridDim.x, ++ring.it) {
@@ -350,6 +352,8 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1)
     ring_init(ring, smem_raw, smem_u32(bars), T, d, slots);
     const float inv_d = 1.0f / static_cast<float>(d);
     float a_pre[V][8] = {}, a_post[V][8] = {};
+    if (T <= 4 * static_cast<int64_t>(gridDim.x))  // short: the next kernel's launch overlaps it
+        pdl_trigger();
     pdl_wait();
     ring.start();
     for (int64_t row = blockIdx.x; row < T; row += gridDim.x, ++ring.it) {

@@ -535,7 +535,7 @@ taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b,
 /*
  * fp8_linear - y[M][N] = Q(x) W^T: x bf16 [M][K] quantised along its rows
  * into the workspace, then fp8_gemm with a weight [N][K] quantised by
- * fp8_quantize_weight (codes, scale); up to four tokens in one kernel without
+ * fp8_quantize_weight (codes, scale); up to eight tokens in one kernel without
  * a workspace (fp8_linear_workspace_bytes gives 0, the pointer may be null).
  *
  * fp8_linear_backward - dx[M][K] = Q(dy) W (bf16; from codes_t and scale_t)

@@ -154,6 +154,23 @@ def product_bound(A, B, dtype):
     return ref, tol + (2.0 ** -8 * ref.abs() if dtype == torch.bfloat16 else 0)
 
 
+@pytest.mark.parametrize("M", [1, 2, 5, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 1), (16, 128), (130, 250), (301, 1040), (6000, 144), (40, 16384), (24, 16400)])
+def test_few_tokens_of_whole_numbers_are_exact(M, N, K):
+    # x whole numbers up to 4 with a 448 in every block (scale 1), weights
+    # whole numbers with any tile scale: sums are whole multiples below 2^24
+    g = torch.Generator().manual_seed(17)
+    x = torch.randint(-4, 5, (M, K), generator=g).double()
+    x[:, ::128] = 448.0
+    codes, _ = integer_operand(N, api.fp8_pitch(K), 18)
+    codes[:, K:] = 0
+    scale = torch.randint(126, 129, (-(-K // 128), -(-N // 128)), generator=g).to(torch.uint8).cuda()
+    ref = x @ R.values(codes, scale, tiles=True)[:, :K].t()
+    for dtype in (torch.float32, torch.bfloat16):
+        y = api.fp8_linear(x.bfloat16().cuda(), codes, scale, dtype)
+        assert torch.equal(y.cpu().double(), ref.to(dtype).double())
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (7, 256, 2560), (130, 513, 777), (1200, 2400, 320)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_linear_and_its_gradients(M, N, K, dtype):
