@@ -24,11 +24,13 @@
 // are rounded once, when they are stored.
 //
 // Bound by HBM: 8 bytes an element forward, 12 backward.  A CTA takes whole
-// rows in turn, 8 V columns a thread.  Rows arrive by bulk copies into a ring
-// of row slots in shared memory, several rows ahead of the row being worked
-// on, so the loads do not wait for the two block-wide sums that every row
-// needs; outputs go straight from registers in 16-byte stores.  Rows that
-// are not a multiple of 16 bytes are read element by element.
+// rows in turn, 8 V columns a thread and RPI rows at a time, with the gains
+// of its columns in registers.  Rows arrive by bulk copies into a ring of row
+// slots in shared memory, several rows ahead of those being worked on, so
+// the loads do not wait for the two block-wide sums that every row needs;
+// outputs go straight from registers in 16-byte stores.  Two rows at a time
+// (up to 4096 columns) share a barrier and hide each other's latencies.
+// Rows that are not a multiple of 16 bytes are read element by element.
 //
 // The gains' gradients are summed over a CTA's rows in registers, written as
 // one partial row per CTA, and added over the CTAs in a fixed order by a
@@ -49,7 +51,7 @@ namespace {
 
 constexpr uint32_t kErrNorm = 128u;
 constexpr int kMaxThreads = 512;
-constexpr int kMaxSlots = 4;
+constexpr int kMaxSlots = 8;
 
 // Gate modes (include/taco.h).
 constexpr int kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3;
@@ -111,66 +113,82 @@ template <bool VEC> __device__ __forceinline__ void store_bf16x8(uint16_t *p, in
 }
 
 // The CTA's rows blockIdx.x, + gridDim.x, ...: NT bf16 tensors' rows, NT
-// row-sized pieces to a slot.
+// row-sized pieces to a slot.  `row` and `slot` are those of the first row
+// being worked on, row(i) and slot i places on those of the ones after it.
 template <int NT, bool VEC> struct RowRing {
     const uint16_t *src[NT];
     uint32_t buf, bars, slots, row_bytes;
-    int64_t T;
+    int64_t T, row0;
     int d;
-    int64_t it = 0;  // rows consumed by this CTA
+    uint32_t slot = 0, phase = 0;
     bool dead = false;
 
-    __device__ __forceinline__ void issue(int64_t n)  // this CTA's n-th row (one thread)
+    __device__ __forceinline__ int64_t row(int i) const { return row0 + static_cast<int64_t>(i) * gridDim.x; }
+    __device__ __forceinline__ uint32_t slot_of(int i) const
     {
-        const int64_t row = blockIdx.x + n * gridDim.x;
-        if (row >= T)
+        const uint32_t s = slot + i;
+        return s >= slots ? s - slots : s;
+    }
+    __device__ __forceinline__ void issue(int64_t r, uint32_t s)  // row r into slot s (one thread)
+    {
+        if (r >= T)
             return;
-        const uint32_t s = static_cast<uint32_t>(n % slots), bar = bars + 8 * s;
+        const uint32_t bar = bars + 8 * s;
         mbar_arrive_expect_tx(bar, NT * row_bytes);
 #pragma unroll
         for (int k = 0; k < NT; ++k)
-            bulk_load(buf + (s * NT + k) * row_bytes, src[k] + row * d, row_bytes, bar);
+            bulk_load(buf + (s * NT + k) * row_bytes, src[k] + r * d, row_bytes, bar);
     }
     __device__ __forceinline__ void start()
     {
+        row0 = blockIdx.x;
         if (VEC && threadIdx.x == 0)
-            for (uint32_t n = 0; n < slots; ++n)
-                issue(n);
+            for (uint32_t s = 0; s < slots; ++s)
+                issue(row(s), s);
     }
-    // The current row has landed (or is read directly).
-    __device__ __forceinline__ void wait()
+    // Row i has landed (or is read directly).
+    __device__ __forceinline__ void wait(int i)
     {
-        if (VEC && !dead &&
-            !mbar_wait(bars + 8 * static_cast<uint32_t>(it % slots), static_cast<uint32_t>(it / slots) & 1)) {
+        if (VEC && !dead && row(i) < T && !mbar_wait(bars + 8 * slot_of(i), phase ^ (slot + i >= slots))) {
             atomicOr(&g_norm_error, kErrNorm);
             dead = true;
             // the thread that issues stops issuing: wait for what is in flight
             if (threadIdx.x == 0)
-                for (int64_t n = it; n < it + slots && blockIdx.x + n * gridDim.x < T; ++n)
-                    mbar_wait(bars + 8 * static_cast<uint32_t>(n % slots), static_cast<uint32_t>(n / slots) & 1);
+                for (int j = i; j < static_cast<int>(slots) && row(j) < T; ++j)
+                    mbar_wait(bars + 8 * slot_of(j), phase ^ (slot + j >= slots));
         }
     }
-    // Columns c .. c + 7 of tensor k's current row, zeros past the end.
-    __device__ __forceinline__ uint4 get(int k, int c) const
+    // Columns c .. c + 7 of tensor k's row i, zeros past the end.
+    __device__ __forceinline__ uint4 get(int i, int k, int c) const
     {
+        if (row(i) >= T)
+            return make_uint4(0, 0, 0, 0);
         if (VEC) {
             if (c >= d || dead)
                 return make_uint4(0, 0, 0, 0);
-            return lds128(buf + (static_cast<uint32_t>(it % slots) * NT + k) * row_bytes + 2 * c);
+            return lds128(buf + (slot_of(i) * NT + k) * row_bytes + 2 * c);
         }
-        const uint16_t *p = src[k] + (blockIdx.x + it * gridDim.x) * d + c;
+        const uint16_t *p = src[k] + row(i) * d + c;
         uint32_t e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             e[j] = c + j < d ? __ldg(p + j) : 0u;
         return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
     }
-    // Every thread has read the current row (a barrier lies behind): refill
-    // its slot.
-    __device__ __forceinline__ void refill()
+    // Every thread has read row i (a barrier lies behind): refill its slot.
+    __device__ __forceinline__ void refill(int i)
     {
         if (VEC && threadIdx.x == 0 && !dead)
-            issue(it + slots);
+            issue(row(i + static_cast<int>(slots)), slot_of(i));
+    }
+    __device__ __forceinline__ void next(int rows)
+    {
+        row0 = row(rows);
+        slot += rows;
+        if (slot >= slots) {
+            slot -= slots;
+            phase ^= 1;
+        }
     }
 };
 
@@ -222,9 +240,10 @@ __device__ __forceinline__ void ring_init(RowRing<NT, VEC> &ring, uint8_t *smem,
 // ---------------------------------------------------------------- forward --
 
 // V groups of 8 columns a thread (group v: columns 8 (threadIdx.x + v
-// blockDim.x)); GATE a gate mode; FP8: n as codes and scales.
-template <int V, int GATE, bool FP8, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads)
+// blockDim.x)), RPI rows at a time; GATE a gate mode; FP8: n as codes and
+// scales.
+template <int V, int RPI, int GATE, bool FP8, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads, 1)
     norm_forward_kernel(const uint16_t *__restrict__ y, const uint16_t *__restrict__ h,
                         const float *__restrict__ g_post, const float *__restrict__ g_pre,
                         const void *__restrict__ gate, float s, float eps, int64_t T, int d, int slots,
@@ -233,7 +252,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     constexpr int NT = GATE == kGateFull ? 3 : 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kMaxSlots];
-    __shared__ float red[2][16];
+    __shared__ float red[2][16 * RPI];
     RowRing<NT, VEC> ring;
     ring.src[0] = y;
     ring.src[1] = h;
@@ -245,83 +264,110 @@ __global__ void __launch_bounds__(kMaxThreads)
         pdl_trigger();
     pdl_wait();
     ring.start();
-    for (int64_t row = blockIdx.x; row < T; row += gridDim.x, ++ring.it) {
-        ring.wait();
-        uint4 qy[V], qh[V], qg[V];
-        float sum[1] = {0.0f};
+    // the columns' gains: a channel gate joins g_post
+    float gp[V][8], gq[V][8];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (threadIdx.x + v * blockDim.x);
-            qy[v] = ring.get(0, c);
-            qh[v] = ring.get(1, c);
-            if constexpr (GATE == kGateFull)
-                qg[v] = ring.get(2, c);
-            float x[8];
-            unpack8(qy[v], x);
+    for (int v = 0; v < V; ++v) {
+        const int c = 8 * (threadIdx.x + v * blockDim.x);
+        load_f32x8<VEC>(g_post, c, d, gp[v]);
+        load_f32x8<VEC>(g_pre, c, d, gq[v]);
+        if constexpr (GATE == kGateChannel) {
+            float w[8];
+            load_f32x8<VEC>(static_cast<const float *>(gate), c, d, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                sum[0] = fmaf(x[j], x[j], sum[0]);
+                gp[v][j] *= w[j];
         }
-        float gt = 1.0f;
-        if constexpr (GATE == kGateToken)
-            gt = __ldg(static_cast<const float *>(gate) + row);
-        block_sum(sum, red[0]);
-        ring.refill();
-        const float ry = rsqrtf(sum[0] * inv_d + eps);
-        float h2[V][8];
-        sum[0] = 0.0f;
+    }
+    for (; ring.row(0) < T; ring.next(RPI)) {
+        uint4 qy[RPI][V], qh[RPI][V], qg[RPI][V];
+        float sum[RPI], gt[RPI];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (threadIdx.x + v * blockDim.x);
-            float x[8], g[8];
-            unpack8(qy[v], x);
-            unpack8(qh[v], h2[v]);
-            load_f32x8<VEC>(g_post, c, d, g);
+        for (int i = 0; i < RPI; ++i) {
+            ring.wait(i);
+            sum[i] = 0.0f;
+            gt[i] = 1.0f;
+            if constexpr (GATE == kGateToken)
+                if (ring.row(i) < T)
+                    gt[i] = __ldg(static_cast<const float *>(gate) + ring.row(i));
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = x[j] * ry * g[j];
-            if constexpr (GATE == kGateChannel)
-                load_f32x8<VEC>(static_cast<const float *>(gate), c, d, g);
-            if constexpr (GATE == kGateFull)
-                unpack8(qg[v], g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float z = GATE == kGateNone ? x[j] : GATE == kGateToken ? gt * x[j] : g[j] * x[j];
-                h2[v][j] = fmaf(s, h2[v][j], z);
-                sum[0] = fmaf(h2[v][j], h2[v][j], sum[0]);
-            }
-            store_bf16x8<VEC>(h_out + row * d, c, d, h2[v]);
-        }
-        block_sum(sum, red[1]);
-        const float rh = rsqrtf(sum[0] * inv_d + eps);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (threadIdx.x + v * blockDim.x);
-            float g[8];
-            load_f32x8<VEC>(g_pre, c, d, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                g[j] = h2[v][j] * rh * g[j];
-            if constexpr (FP8) {
-                // the block's maximum: 16 lanes of 8 columns
-                uint32_t m = 0;
+            for (int v = 0; v < V; ++v) {
+                const int c = 8 * (threadIdx.x + v * blockDim.x);
+                qy[i][v] = ring.get(i, 0, c);
+                qh[i][v] = ring.get(i, 1, c);
+                if constexpr (GATE == kGateFull)
+                    qg[i][v] = ring.get(i, 2, c);
+                float x[8];
+                unpack8(qy[i][v], x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    m = max(m, __float_as_uint(g[j]) & 0x7FFFFFFFu);
+                    sum[i] = fmaf(x[j], x[j], sum[i]);
+            }
+        }
+        block_sum(sum, red[0]);
 #pragma unroll
-                for (int k = 8; k >= 1; k >>= 1)
-                    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
-                const uint32_t byte = fp8_scale_byte(m);
-                const float f = fp8_inv_scale(byte);
-                const int64_t pitch = fp8_pitch(d);
-                if (c < pitch)
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(n_out) + row * pitch + c) =
-                        make_uint2(f32x4_to_e4m3x4(g[0] * f, g[1] * f, g[2] * f, g[3] * f),
-                                   f32x4_to_e4m3x4(g[4] * f, g[5] * f, g[6] * f, g[7] * f));
-                if ((threadIdx.x & 15) == 0 && c < d)
-                    n_scale[fp8_scale_at(row, c >> 7, (d + 511) / 512)] = static_cast<uint8_t>(byte);
-            } else {
-                store_bf16x8<VEC>(static_cast<uint16_t *>(n_out) + row * d, c, d, g);
+        for (int i = 0; i < RPI; ++i)
+            ring.refill(i);
+        float h2[RPI][V][8];
+#pragma unroll
+        for (int i = 0; i < RPI; ++i) {
+            const float ry = rsqrtf(sum[i] * inv_d + eps) * gt[i];
+            sum[i] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = 8 * (threadIdx.x + v * blockDim.x);
+                float x[8], w[8];
+                unpack8(qy[i][v], x);
+                unpack8(qh[i][v], h2[i][v]);
+                if constexpr (GATE == kGateFull)
+                    unpack8(qg[i][v], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float z = x[j] * ry * gp[v][j];
+                    if constexpr (GATE == kGateFull)
+                        z *= w[j];
+                    h2[i][v][j] = fmaf(s, h2[i][v][j], z);
+                    sum[i] = fmaf(h2[i][v][j], h2[i][v][j], sum[i]);
+                }
+                if (ring.row(i) < T)
+                    store_bf16x8<VEC>(h_out + ring.row(i) * d, c, d, h2[i][v]);
+            }
+        }
+        block_sum(sum, red[1]);
+#pragma unroll
+        for (int i = 0; i < RPI; ++i) {
+            const int64_t row = ring.row(i);
+            if (row >= T)
+                break;
+            const float rh = rsqrtf(sum[i] * inv_d + eps);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = 8 * (threadIdx.x + v * blockDim.x);
+                float g[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    g[j] = h2[i][v][j] * rh * gq[v][j];
+                if constexpr (FP8) {
+                    // the block's maximum: 16 lanes of 8 columns
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        m = max(m, __float_as_uint(g[j]) & 0x7FFFFFFFu);
+#pragma unroll
+                    for (int k = 8; k >= 1; k >>= 1)
+                        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
+                    const uint32_t byte = fp8_scale_byte(m);
+                    const float f = fp8_inv_scale(byte);
+                    const int64_t pitch = fp8_pitch(d);
+                    if (c < pitch)
+                        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(n_out) + row * pitch + c) =
+                            make_uint2(f32x4_to_e4m3x4(g[0] * f, g[1] * f, g[2] * f, g[3] * f),
+                                       f32x4_to_e4m3x4(g[4] * f, g[5] * f, g[6] * f, g[7] * f));
+                    if ((threadIdx.x & 15) == 0 && c < d)
+                        n_scale[fp8_scale_at(row, c >> 7, (d + 511) / 512)] = static_cast<uint8_t>(byte);
+                } else {
+                    store_bf16x8<VEC>(static_cast<uint16_t *>(n_out) + row * d, c, d, g);
+                }
             }
         }
     }
@@ -329,8 +375,8 @@ __global__ void __launch_bounds__(kMaxThreads)
 
 // --------------------------------------------------------------- backward --
 
-template <int V, int GATE, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1)
+template <int V, int RPI, int GATE, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads, 1)
     norm_backward_kernel(const uint16_t *__restrict__ dn, const uint16_t *__restrict__ dh2,
                          const uint16_t *__restrict__ y, const uint16_t *__restrict__ h2,
                          const float *__restrict__ g_post, const float *__restrict__ g_pre,
@@ -339,9 +385,12 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1)
                          float *__restrict__ partial)
 {
     constexpr int NT = GATE == kGateFull ? 5 : 4;
+    // more columns a thread: no registers left for the gains, which are then
+    // read (from L1) where they are used
+    constexpr bool KEEP = V == 1;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kMaxSlots];
-    __shared__ float red[2][48];
+    __shared__ float red[2][48 * RPI];
     RowRing<NT, VEC> ring;
     ring.src[0] = dn;
     ring.src[1] = dh2;
@@ -356,110 +405,146 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1)
         pdl_trigger();
     pdl_wait();
     ring.start();
-    for (int64_t row = blockIdx.x; row < T; row += gridDim.x, ++ring.it) {
-        ring.wait();
-        uint4 qn[V], qd[V], qy[V], qh[V], qg[V];
-        float sum[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (threadIdx.x + v * blockDim.x);
-            qn[v] = ring.get(0, c);
-            qd[v] = ring.get(1, c);
-            qy[v] = ring.get(2, c);
-            qh[v] = ring.get(3, c);
-            if constexpr (GATE == kGateFull)
-                qg[v] = ring.get(4, c);
-            float a[8], b[8], g[8];
-            unpack8(qh[v], a);
-            unpack8(qn[v], b);
-            load_f32x8<VEC>(g_pre, c, d, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sum[0] = fmaf(a[j], a[j], sum[0]);
-                sum[1] = fmaf(b[j] * g[j], a[j], sum[1]);
-            }
-            unpack8(qy[v], a);
+    // the columns' gains: a channel gate joins g_post (the sum a_post holds
+    // neither)
+    float gp[KEEP ? V : 1][8], gq[KEEP ? V : 1][8];
+    auto post_gain = [&](int v, float (&g)[8]) {
+        const int c = 8 * (threadIdx.x + v * blockDim.x);
+        load_f32x8<VEC>(g_post, c, d, g);
+        if constexpr (GATE == kGateChannel) {
+            float w[8];
+            load_f32x8<VEC>(static_cast<const float *>(gate), c, d, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                sum[2] = fmaf(a[j], a[j], sum[2]);
+                g[j] *= w[j];
         }
-        float gt = 1.0f;
-        if constexpr (GATE == kGateToken)
-            gt = __ldg(static_cast<const float *>(gate) + row);
-        block_sum(sum, red[0]);
-        ring.refill();
-        const float rh = rsqrtf(sum[0] * inv_d + eps), ry = rsqrtf(sum[2] * inv_d + eps);
-        const float ch = rh * rh * rh * (sum[1] * inv_d);
-        float G[V][8];
-        float dot[1] = {0.0f};
+    };
+    if constexpr (KEEP) {
+        post_gain(0, gp[0]);
+        load_f32x8<VEC>(g_pre, 8 * threadIdx.x, d, gq[0]);
+    }
+    for (; ring.row(0) < T; ring.next(RPI)) {
+        uint4 qn[RPI][V], qd[RPI][V], qy[RPI][V], qh[RPI][V], qg[RPI][V];
+        float sum[3 * RPI], gt[RPI];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (threadIdx.x + v * blockDim.x);
-            float a[8], b[8], g[8];
-            unpack8(qh[v], a);
-            unpack8(qn[v], b);
-            unpack8(qd[v], G[v]);
-            load_f32x8<VEC>(g_pre, c, d, g);
+        for (int i = 0; i < RPI; ++i) {
+            ring.wait(i);
+            sum[3 * i] = sum[3 * i + 1] = sum[3 * i + 2] = 0.0f;
+            gt[i] = 1.0f;
+            if constexpr (GATE == kGateToken)
+                if (ring.row(i) < T)
+                    gt[i] = __ldg(static_cast<const float *>(gate) + ring.row(i));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a_pre[v][j] = fmaf(b[j], a[j] * rh, a_pre[v][j]);
-                G[v][j] = fmaf(-a[j], ch, fmaf(rh * b[j], g[j], G[v][j]));
-                b[j] = s * G[v][j];
-            }
-            store_bf16x8<VEC>(dh + row * d, c, d, b);
-            // y r_y G: the sum over tokens behind dg_post and a channel
-            // gate's gradient
-            unpack8(qy[v], a);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                b[j] = a[j] * ry * G[v][j];
-            load_f32x8<VEC>(g_post, c, d, g);
-            if constexpr (GATE == kGateFull) {
-                float e[8], w[8];
-                unpack8(qg[v], w);
+            for (int v = 0; v < V; ++v) {
+                const int c = 8 * (threadIdx.x + v * blockDim.x);
+                qn[i][v] = ring.get(i, 0, c);
+                qd[i][v] = ring.get(i, 1, c);
+                qy[i][v] = ring.get(i, 2, c);
+                qh[i][v] = ring.get(i, 3, c);
+                if constexpr (GATE == kGateFull)
+                    qg[i][v] = ring.get(i, 4, c);
+                if constexpr (!KEEP)
+                    load_f32x8<VEC>(g_pre, c, d, gq[0]);
+                float a[8], b[8];
+                unpack8(qh[i][v], a);
+                unpack8(qn[i][v], b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    e[j] = b[j] * g[j];
-                    b[j] *= w[j];
-                    dot[0] = fmaf(b[j], g[j], dot[0]);
-                    a_post[v][j] += b[j];
+                    sum[3 * i] = fmaf(a[j], a[j], sum[3 * i]);
+                    sum[3 * i + 1] = fmaf(b[j] * gq[0][j], a[j], sum[3 * i + 1]);
                 }
-                store_bf16x8<VEC>(static_cast<uint16_t *>(dgate) + row * d, c, d, e);
-            } else {
-                float w[8];
-                if constexpr (GATE == kGateChannel)
-                    load_f32x8<VEC>(static_cast<const float *>(gate), c, d, w);
+                unpack8(qy[i][v], a);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sum[3 * i + 2] = fmaf(a[j], a[j], sum[3 * i + 2]);
+            }
+        }
+        block_sum(sum, red[0]);
+#pragma unroll
+        for (int i = 0; i < RPI; ++i)
+            ring.refill(i);
+        float G[RPI][V][8], dot[RPI], ry[RPI];
+#pragma unroll
+        for (int i = 0; i < RPI; ++i) {
+            // a row past the end is all zeros and adds nothing
+            const float rh = rsqrtf(sum[3 * i] * inv_d + eps);
+            const float ch = rh * rh * rh * (sum[3 * i + 1] * inv_d);
+            ry[i] = rsqrtf(sum[3 * i + 2] * inv_d + eps);
+            dot[i] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = 8 * (threadIdx.x + v * blockDim.x);
+                if constexpr (!KEEP) {
+                    load_f32x8<VEC>(g_pre, c, d, gq[0]);
+                    post_gain(v, gp[0]);
+                }
+                float a[8], b[8];
+                unpack8(qh[i][v], a);
+                unpack8(qn[i][v], b);
+                unpack8(qd[i][v], G[i][v]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    dot[0] = fmaf(b[j], GATE == kGateChannel ? g[j] * w[j] : g[j], dot[0]);
-                    a_post[v][j] = GATE == kGateToken ? fmaf(gt, b[j], a_post[v][j]) : a_post[v][j] + b[j];
+                    const float u = rh * b[j];
+                    a_pre[v][j] = fmaf(u, a[j], a_pre[v][j]);
+                    G[i][v][j] = fmaf(-a[j], ch, fmaf(u, gq[0][j], G[i][v][j]));
+                    b[j] = s * G[i][v][j];
+                }
+                if (ring.row(i) < T)
+                    store_bf16x8<VEC>(dh + ring.row(i) * d, c, d, b);
+                // y r_y G: the sum over tokens behind dg_post and a channel
+                // gate's gradient
+                unpack8(qy[i][v], a);
+                if constexpr (GATE == kGateFull) {
+                    float e[8], w[8];
+                    unpack8(qg[i][v], w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float t = a[j] * ry[i] * G[i][v][j];
+                        e[j] = t * gp[0][j];
+                        dot[i] = fmaf(e[j], w[j], dot[i]);
+                        a_post[v][j] = fmaf(t, w[j], a_post[v][j]);
+                    }
+                    if (ring.row(i) < T)
+                        store_bf16x8<VEC>(static_cast<uint16_t *>(dgate) + ring.row(i) * d, c, d, e);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float t = a[j] * ry[i] * G[i][v][j];
+                        dot[i] = fmaf(t, gp[0][j], dot[i]);
+                        a_post[v][j] = GATE == kGateToken ? fmaf(gt[i], t, a_post[v][j]) : a_post[v][j] + t;
+                    }
                 }
             }
         }
         block_sum(dot, red[1]);  // sum of (y r_y) G g_post (and a channel's or element's gate)
-        if constexpr (GATE == kGateToken)
-            if (threadIdx.x == 0)
-                static_cast<float *>(dgate)[row] = dot[0];
-        const float cy = ry * ry * (gt * dot[0] * inv_d);
-        const float rg = ry * gt;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (threadIdx.x + v * blockDim.x);
-            float a[8], g[8], w[8];
-            unpack8(qy[v], a);
-            load_f32x8<VEC>(g_post, c, d, g);
-            if constexpr (GATE == kGateChannel)
-                load_f32x8<VEC>(static_cast<const float *>(gate), c, d, w);
-            if constexpr (GATE == kGateFull)
-                unpack8(qg[v], w);
+        for (int i = 0; i < RPI; ++i) {
+            const int64_t row = ring.row(i);
+            if (row >= T)
+                break;
+            if constexpr (GATE == kGateToken)
+                if (threadIdx.x == 0)
+                    static_cast<float *>(dgate)[row] = dot[i];
+            const float cy = ry[i] * ry[i] * (gt[i] * dot[i] * inv_d);
+            const float rg = ry[i] * gt[i];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float u = rg * g[j];
-                if constexpr (GATE == kGateChannel || GATE == kGateFull)
-                    u *= w[j];
-                a[j] = fmaf(u, G[v][j], -a[j] * cy);
+            for (int v = 0; v < V; ++v) {
+                const int c = 8 * (threadIdx.x + v * blockDim.x);
+                if constexpr (!KEEP)
+                    post_gain(v, gp[0]);
+                float a[8], w[8];
+                unpack8(qy[i][v], a);
+                if constexpr (GATE == kGateFull)
+                    unpack8(qg[i][v], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float u = rg * gp[0][j];
+                    if constexpr (GATE == kGateFull)
+                        u *= w[j];
+                    a[j] = fmaf(u, G[i][v][j], -a[j] * cy);
+                }
+                store_bf16x8<VEC>(dy + row * d, c, d, a);
             }
-            store_bf16x8<VEC>(dy + row * d, c, d, a);
         }
     }
 #pragma unroll
@@ -475,20 +560,20 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1)
     }
 }
 
-// Sums the CTAs' partial rows in a fixed order: 32 columns a CTA, eight
+// Sums the CTAs' partial rows in a fixed order: 32 columns a CTA, sixteen
 // groups of rows in turn, then the groups.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
     norm_gains_kernel(const float *__restrict__ partial, int ctas, int d, int gate_mode,
                       const float *__restrict__ g_post, const float *__restrict__ gate, float *__restrict__ dg_pre,
                       float *__restrict__ dg_post, float *__restrict__ dgate)
 {
-    __shared__ float part[2][8][33];
+    __shared__ float part[2][16][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     pdl_wait();
     float a = 0.0f, b = 0.0f;
     if (c < d)
-#pragma unroll 4
-        for (int i = grp; i < ctas; i += 8) {
+#pragma unroll 5
+        for (int i = grp; i < ctas; i += 16) {
             a += partial[static_cast<int64_t>(i) * 2 * d + c];
             b += partial[static_cast<int64_t>(i) * 2 * d + d + c];
         }
@@ -498,7 +583,7 @@ __global__ void __launch_bounds__(256)
     if (grp == 0 && c < d) {
         a = b = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
             a += part[0][i][lane];
             b += part[1][i][lane];
         }
@@ -520,23 +605,26 @@ struct NormPlan {
 
 constexpr uint32_t kSmemPerSm = 227 * 1024;
 
-NormPlan plan_norm(int64_t T, int d, int tensors, int per_sm_threads, int sms)
+// regs: the registers a thread of the kernel takes, for how many CTAs share
+// an SM.
+NormPlan plan_norm(int64_t T, int d, int tensors, int regs, int sms)
 {
     NormPlan p;
     const int units = (d + 7) / 8;
     p.v = units <= kMaxThreads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
     p.threads = ((units + p.v - 1) / p.v + 31) / 32 * 32;
-    int per_sm = per_sm_threads / p.threads;
+    int per_sm = 65536 / (regs * p.threads);
     per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
     p.slots = 0;
     p.smem = 0;
     if (d % 8 == 0) {
+        // at least four rows a CTA in the ring where they fit
         const uint32_t slot = static_cast<uint32_t>(tensors) * 2 * d;
-        while (per_sm > 1 && 2 * slot + 2048 > kSmemPerSm / per_sm)
+        while (per_sm > 1 && 4 * slot + 2048 > kSmemPerSm / per_sm)
             --per_sm;
         const uint32_t room = kSmemPerSm / per_sm - 2048;
         p.slots = static_cast<int>(room / slot);
-        p.slots = p.slots > kMaxSlots ? kMaxSlots : p.slots < 1 ? 1 : p.slots;
+        p.slots = p.slots > kMaxSlots ? kMaxSlots : p.slots;
         p.smem = 128 + p.slots * slot;
     }
     const int64_t most = static_cast<int64_t>(per_sm) * sms;
@@ -546,7 +634,7 @@ NormPlan plan_norm(int64_t T, int d, int tensors, int per_sm_threads, int sms)
 
 NormPlan plan_backward(int64_t T, int d, int gate_mode, int sms)
 {
-    return plan_norm(T, d, gate_mode == kGateFull ? 5 : 4, d <= 8 * kMaxThreads ? 1024 : 512, sms);
+    return plan_norm(T, d, gate_mode == kGateFull ? 5 : 4, 128, sms);
 }
 
 constexpr int kMaxDevices = 64;
@@ -561,14 +649,17 @@ template <class K> cudaError_t allow_smem(K kernel, int device, std::atomic<bool
     return e;
 }
 
+// Two rows at a time where a thread has one group of columns.
+constexpr int rows_at_once(int v) { return v == 1 ? 2 : 1; }
+
 template <int V, int GATE, bool FP8, bool VEC>
 cudaError_t run_forward(const NormPlan &p, const NormForward &a, int device, cudaStream_t stream)
 {
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = allow_smem(norm_forward_kernel<V, GATE, FP8, VEC>, device, set);
+    cudaError_t e = allow_smem(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC>, device, set);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(norm_forward_kernel<V, GATE, FP8, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
+    return launch_pdl(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
                       static_cast<const uint16_t *>(a.y), static_cast<const uint16_t *>(a.h), a.g_post, a.g_pre,
                       a.gate, a.residual_scale, a.eps, a.T, static_cast<int>(a.d), p.slots,
                       static_cast<uint16_t *>(a.h_out), a.n_out, a.n_scale);
@@ -578,10 +669,10 @@ template <int V, int GATE, bool VEC>
 cudaError_t run_backward(const NormPlan &p, const NormBackward &a, int device, cudaStream_t stream)
 {
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = allow_smem(norm_backward_kernel<V, GATE, VEC>, device, set);
+    cudaError_t e = allow_smem(norm_backward_kernel<V, rows_at_once(V), GATE, VEC>, device, set);
     if (e != cudaSuccess)
         return e;
-    e = launch_pdl(norm_backward_kernel<V, GATE, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
+    e = launch_pdl(norm_backward_kernel<V, rows_at_once(V), GATE, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
                    static_cast<const uint16_t *>(a.dn), static_cast<const uint16_t *>(a.dh_out),
                    static_cast<const uint16_t *>(a.y), static_cast<const uint16_t *>(a.h_out), a.g_post, a.g_pre,
                    a.gate, a.residual_scale, a.eps, a.T, static_cast<int>(a.d), p.slots,
@@ -589,7 +680,7 @@ cudaError_t run_backward(const NormPlan &p, const NormBackward &a, int device, c
                    static_cast<float *>(a.workspace));
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(norm_gains_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), dim3(256), 0, stream,
+    return launch_pdl(norm_gains_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), dim3(512), 0, stream,
                       static_cast<const float *>(a.workspace), p.grid, static_cast<int>(a.d), GATE, a.g_post,
                       static_cast<const float *>(a.gate), a.dg_pre, a.dg_post, static_cast<float *>(a.dgate));
 }
@@ -651,7 +742,7 @@ cudaError_t launch_norm_forward(const NormForward &a, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const int d = static_cast<int>(a.d);
-    const NormPlan p = plan_norm(a.T, d, a.gate_mode == kGateFull ? 3 : 2, 1024, di.num_sms);
+    const NormPlan p = plan_norm(a.T, d, a.gate_mode == kGateFull ? 3 : 2, d <= 16 * kMaxThreads ? 96 : 128, di.num_sms);
     const bool vec = d % 8 == 0;
     switch (p.v) {
     case 1:
