@@ -63,41 +63,56 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// Eight values in four float2 registers: the arithmetic runs as packed
+// fp32x2 instructions (two lanes each).
+struct F8 {
+    float2 v[4];
+};
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
 // Eight bf16 values of a packed 16-byte unit.
-__device__ __forceinline__ void unpack8(const uint4 &q, float (&x)[8])
+__device__ __forceinline__ F8 unpack8(const uint4 &q)
 {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16lo_to_f32(w[i]);
-        x[2 * i + 1] = bf16hi_to_f32(w[i]);
-    }
+    F8 x;
+    x.v[0] = make_float2(bf16lo_to_f32(q.x), bf16hi_to_f32(q.x));
+    x.v[1] = make_float2(bf16lo_to_f32(q.y), bf16hi_to_f32(q.y));
+    x.v[2] = make_float2(bf16lo_to_f32(q.z), bf16hi_to_f32(q.z));
+    x.v[3] = make_float2(bf16lo_to_f32(q.w), bf16hi_to_f32(q.w));
+    return x;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+__device__ __forceinline__ uint4 pack8(const F8 &x)
 {
-    return make_uint4(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
-                      f32x2_to_bf16x2(x[6], x[7]));
+    return make_uint4(f32x2_to_bf16x2(x.v[0].x, x.v[0].y), f32x2_to_bf16x2(x.v[1].x, x.v[1].y),
+                      f32x2_to_bf16x2(x.v[2].x, x.v[2].y), f32x2_to_bf16x2(x.v[3].x, x.v[3].y));
 }
 
 // Columns c .. c + 7 of fp32 vectors of d values (zeros past the end).
-template <bool VEC> __device__ __forceinline__ void load_f32x8(const float *p, int c, int d, float (&x)[8])
+template <bool VEC> __device__ __forceinline__ F8 load_f32x8(const float *p, int c, int d)
 {
+    F8 x;
     if (VEC) {
         float4 a = make_float4(0, 0, 0, 0), b = a;
         if (c < d) {
             a = __ldg(reinterpret_cast<const float4 *>(p + c));
             b = __ldg(reinterpret_cast<const float4 *>(p + c) + 1);
         }
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        x.v[0] = make_float2(a.x, a.y);
+        x.v[1] = make_float2(a.z, a.w);
+        x.v[2] = make_float2(b.x, b.y);
+        x.v[3] = make_float2(b.z, b.w);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = c + j < d ? __ldg(p + c + j) : 0.0f;
+        for (int j = 0; j < 4; ++j)
+            x.v[j] = make_float2(c + 2 * j < d ? __ldg(p + c + 2 * j) : 0.0f,
+                                 c + 2 * j + 1 < d ? __ldg(p + c + 2 * j + 1) : 0.0f);
     }
+    return x;
 }
 
-template <bool VEC> __device__ __forceinline__ void store_bf16x8(uint16_t *p, int c, int d, const float (&x)[8])
+template <bool VEC> __device__ __forceinline__ void store_bf16x8(uint16_t *p, int c, int d, const F8 &x)
 {
     const uint4 q = pack8(x);
     if (VEC) {
@@ -192,30 +207,55 @@ template <int NT, bool VEC> struct RowRing {
     }
 };
 
-// Sums of K values over the CTA; every thread gets them.  `red` holds K * 16
-// floats; two calls in turn use two of them, so that one barrier a call is
-// enough.
+// Sums of K values over the CTA; every thread gets them.  `red` holds 16
+// floats for each of K values rounded up to a power of two; two calls in turn
+// use two of them, so that one barrier a call is enough.  A warp sums all K
+// together: in each halving step a lane passes on half of its values and
+// keeps the other half, so that the K sums take about K + 5 shuffles and
+// land in groups of lanes; the warps' sums are added the same way.
+__host__ __device__ constexpr int pow2_at_least(int k) { return k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : 8; }
+
 template <int K> __device__ __forceinline__ void block_sum(float (&v)[K], float *red)
 {
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], s);
+    constexpr int P = pow2_at_least(K);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0)
+    float x[P];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            red[16 * k + warp] = v[k];
+    for (int k = 0; k < P; ++k)
+        x[k] = k < K ? v[k] : 0.0f;
+    // after the step with distance s, a lane whose bit s is set holds the
+    // upper half of the values
+    int dist = 16;
+#pragma unroll
+    for (int n = P; n > 1; n >>= 1, dist >>= 1) {
+        const bool up = lane & dist;
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const float give = up ? x[k] : x[k + n / 2], keep = up ? x[k + n / 2] : x[k];
+            x[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, dist);
+        }
+    }
+#pragma unroll
+    for (int s = 16 / P; s >= 1; s >>= 1)
+        x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], s);
+    // lanes 32 / P i .. hold value i
+    if ((lane & (32 / P - 1)) == 0)
+        red[16 * (lane / (32 / P)) + warp] = x[0];
     __syncthreads();
+    // lane l adds the sums of 16 P / 32 warps of value l / (32 / P)
+    constexpr int Q = P >= 2 ? P / 2 : 1;   // warps a lane adds
+    constexpr int L = 16 / Q;               // lanes to a value
+    const int i = lane / L < P ? lane / L : P - 1, w0 = (lane % L) * Q;
+    float sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        sum += w0 + q < warps ? red[16 * i + w0 + q] : 0.0f;
+#pragma unroll
+    for (int s = L / 2; s >= 1; s >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        v[k] = (lane & 15) < warps ? red[16 * k + (lane & 15)] : 0.0f;
-#pragma unroll
-    for (int s = 8; s >= 1; s >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], s);
+        v[k] = P == 1 ? sum : __shfl_sync(0xFFFFFFFFu, sum, k * L);
 }
 
 template <int NT, bool VEC>
@@ -252,7 +292,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     constexpr int NT = GATE == kGateFull ? 3 : 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kMaxSlots];
-    __shared__ float red[2][16 * RPI];
+    __shared__ float red[2][16 * pow2_at_least(RPI)];
     RowRing<NT, VEC> ring;
     ring.src[0] = y;
     ring.src[1] = h;
@@ -265,18 +305,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     pdl_wait();
     ring.start();
     // the columns' gains: a channel gate joins g_post
-    float gp[V][8], gq[V][8];
+    F8 gp[V], gq[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = 8 * (threadIdx.x + v * blockDim.x);
-        load_f32x8<VEC>(g_post, c, d, gp[v]);
-        load_f32x8<VEC>(g_pre, c, d, gq[v]);
+        gp[v] = load_f32x8<VEC>(g_post, c, d);
+        gq[v] = load_f32x8<VEC>(g_pre, c, d);
         if constexpr (GATE == kGateChannel) {
-            float w[8];
-            load_f32x8<VEC>(static_cast<const float *>(gate), c, d, w);
+            const F8 w = load_f32x8<VEC>(static_cast<const float *>(gate), c, d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                gp[v][j] *= w[j];
+            for (int j = 0; j < 4; ++j)
+                gp[v].v[j] = gp[v].v[j] * w.v[j];
         }
     }
     for (; ring.row(0) < T; ring.next(RPI)) {
@@ -285,11 +324,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
             ring.wait(i);
-            sum[i] = 0.0f;
             gt[i] = 1.0f;
             if constexpr (GATE == kGateToken)
                 if (ring.row(i) < T)
                     gt[i] = __ldg(static_cast<const float *>(gate) + ring.row(i));
+            float2 ss = both(0.0f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = 8 * (threadIdx.x + v * blockDim.x);
@@ -297,41 +336,42 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 qh[i][v] = ring.get(i, 1, c);
                 if constexpr (GATE == kGateFull)
                     qg[i][v] = ring.get(i, 2, c);
-                float x[8];
-                unpack8(qy[i][v], x);
+                const F8 x = unpack8(qy[i][v]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    sum[i] = fmaf(x[j], x[j], sum[i]);
+                for (int j = 0; j < 4; ++j)
+                    ss = fma2(x.v[j], x.v[j], ss);
             }
+            sum[i] = ss.x + ss.y;
         }
         block_sum(sum, red[0]);
 #pragma unroll
         for (int i = 0; i < RPI; ++i)
             ring.refill(i);
-        float h2[RPI][V][8];
+        F8 h2[RPI][V];
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
-            const float ry = rsqrtf(sum[i] * inv_d + eps) * gt[i];
-            sum[i] = 0.0f;
+            const float2 ry = both(rsqrtf(sum[i] * inv_d + eps) * gt[i]), s2 = both(s);
+            float2 ss = both(0.0f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = 8 * (threadIdx.x + v * blockDim.x);
-                float x[8], w[8];
-                unpack8(qy[i][v], x);
-                unpack8(qh[i][v], h2[i][v]);
+                const F8 x = unpack8(qy[i][v]);
+                h2[i][v] = unpack8(qh[i][v]);
+                F8 w;
                 if constexpr (GATE == kGateFull)
-                    unpack8(qg[i][v], w);
+                    w = unpack8(qg[i][v]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float z = x[j] * ry * gp[v][j];
+                for (int j = 0; j < 4; ++j) {
+                    float2 z = x.v[j] * ry * gp[v].v[j];
                     if constexpr (GATE == kGateFull)
-                        z *= w[j];
-                    h2[i][v][j] = fmaf(s, h2[i][v][j], z);
-                    sum[i] = fmaf(h2[i][v][j], h2[i][v][j], sum[i]);
+                        z = z * w.v[j];
+                    h2[i][v].v[j] = fma2(s2, h2[i][v].v[j], z);
+                    ss = fma2(h2[i][v].v[j], h2[i][v].v[j], ss);
                 }
                 if (ring.row(i) < T)
                     store_bf16x8<VEC>(h_out + ring.row(i) * d, c, d, h2[i][v]);
             }
+            sum[i] = ss.x + ss.y;
         }
         block_sum(sum, red[1]);
 #pragma unroll
@@ -339,34 +379,37 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             const int64_t row = ring.row(i);
             if (row >= T)
                 break;
-            const float rh = rsqrtf(sum[i] * inv_d + eps);
+            const float2 rh = both(rsqrtf(sum[i] * inv_d + eps));
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = 8 * (threadIdx.x + v * blockDim.x);
-                float g[8];
+                F8 n;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    g[j] = h2[i][v][j] * rh * gq[v][j];
+                for (int j = 0; j < 4; ++j)
+                    n.v[j] = h2[i][v].v[j] * rh * gq[v].v[j];
                 if constexpr (FP8) {
                     // the block's maximum: 16 lanes of 8 columns
                     uint32_t m = 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        m = max(m, __float_as_uint(g[j]) & 0x7FFFFFFFu);
+                    for (int j = 0; j < 4; ++j)
+                        m = max(m, max(__float_as_uint(n.v[j].x) & 0x7FFFFFFFu, __float_as_uint(n.v[j].y) & 0x7FFFFFFFu));
 #pragma unroll
                     for (int k = 8; k >= 1; k >>= 1)
                         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
                     const uint32_t byte = fp8_scale_byte(m);
-                    const float f = fp8_inv_scale(byte);
+                    const float2 f = both(fp8_inv_scale(byte));
                     const int64_t pitch = fp8_pitch(d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        n.v[j] = n.v[j] * f;
                     if (c < pitch)
                         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(n_out) + row * pitch + c) =
-                            make_uint2(f32x4_to_e4m3x4(g[0] * f, g[1] * f, g[2] * f, g[3] * f),
-                                       f32x4_to_e4m3x4(g[4] * f, g[5] * f, g[6] * f, g[7] * f));
+                            make_uint2(f32x4_to_e4m3x4(n.v[0].x, n.v[0].y, n.v[1].x, n.v[1].y),
+                                       f32x4_to_e4m3x4(n.v[2].x, n.v[2].y, n.v[3].x, n.v[3].y));
                     if ((threadIdx.x & 15) == 0 && c < d)
                         n_scale[fp8_scale_at(row, c >> 7, (d + 511) / 512)] = static_cast<uint8_t>(byte);
                 } else {
-                    store_bf16x8<VEC>(static_cast<uint16_t *>(n_out) + row * d, c, d, g);
+                    store_bf16x8<VEC>(static_cast<uint16_t *>(n_out) + row * d, c, d, n);
                 }
             }
         }
@@ -390,7 +433,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     constexpr bool KEEP = V == 1;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kMaxSlots];
-    __shared__ float red[2][48 * RPI];
+    __shared__ float red[2][16 * pow2_at_least(3 * RPI)];
     RowRing<NT, VEC> ring;
     ring.src[0] = dn;
     ring.src[1] = dh2;
@@ -400,28 +443,32 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         ring.src[4] = static_cast<const uint16_t *>(gate);
     ring_init(ring, smem_raw, smem_u32(bars), T, d, slots);
     const float inv_d = 1.0f / static_cast<float>(d);
-    float a_pre[V][8] = {}, a_post[V][8] = {};
+    F8 a_pre[V], a_post[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            a_pre[v].v[j] = a_post[v].v[j] = both(0.0f);
     if (T <= 4 * static_cast<int64_t>(gridDim.x))  // short: the next kernel's launch overlaps it
         pdl_trigger();
     pdl_wait();
     ring.start();
     // the columns' gains: a channel gate joins g_post (the sum a_post holds
     // neither)
-    float gp[KEEP ? V : 1][8], gq[KEEP ? V : 1][8];
-    auto post_gain = [&](int v, float (&g)[8]) {
-        const int c = 8 * (threadIdx.x + v * blockDim.x);
-        load_f32x8<VEC>(g_post, c, d, g);
+    F8 gp[KEEP ? V : 1], gq[KEEP ? V : 1];
+    auto post_gain = [&](int c) {
+        F8 g = load_f32x8<VEC>(g_post, c, d);
         if constexpr (GATE == kGateChannel) {
-            float w[8];
-            load_f32x8<VEC>(static_cast<const float *>(gate), c, d, w);
+            const F8 w = load_f32x8<VEC>(static_cast<const float *>(gate), c, d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                g[j] *= w[j];
+            for (int j = 0; j < 4; ++j)
+                g.v[j] = g.v[j] * w.v[j];
         }
+        return g;
     };
     if constexpr (KEEP) {
-        post_gain(0, gp[0]);
-        load_f32x8<VEC>(g_pre, 8 * threadIdx.x, d, gq[0]);
+        gp[0] = post_gain(8 * threadIdx.x);
+        gq[0] = load_f32x8<VEC>(g_pre, 8 * threadIdx.x, d);
     }
     for (; ring.row(0) < T; ring.next(RPI)) {
         uint4 qn[RPI][V], qd[RPI][V], qy[RPI][V], qh[RPI][V], qg[RPI][V];
@@ -429,11 +476,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
             ring.wait(i);
-            sum[3 * i] = sum[3 * i + 1] = sum[3 * i + 2] = 0.0f;
             gt[i] = 1.0f;
             if constexpr (GATE == kGateToken)
                 if (ring.row(i) < T)
                     gt[i] = __ldg(static_cast<const float *>(gate) + ring.row(i));
+            float2 s0 = both(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = 8 * (threadIdx.x + v * blockDim.x);
@@ -444,77 +491,75 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 if constexpr (GATE == kGateFull)
                     qg[i][v] = ring.get(i, 4, c);
                 if constexpr (!KEEP)
-                    load_f32x8<VEC>(g_pre, c, d, gq[0]);
-                float a[8], b[8];
-                unpack8(qh[i][v], a);
-                unpack8(qn[i][v], b);
+                    gq[0] = load_f32x8<VEC>(g_pre, c, d);
+                const F8 a = unpack8(qh[i][v]), b = unpack8(qn[i][v]), y8 = unpack8(qy[i][v]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sum[3 * i] = fmaf(a[j], a[j], sum[3 * i]);
-                    sum[3 * i + 1] = fmaf(b[j] * gq[0][j], a[j], sum[3 * i + 1]);
+                for (int j = 0; j < 4; ++j) {
+                    s0 = fma2(a.v[j], a.v[j], s0);
+                    s1 = fma2(b.v[j] * gq[0].v[j], a.v[j], s1);
+                    s2 = fma2(y8.v[j], y8.v[j], s2);
                 }
-                unpack8(qy[i][v], a);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    sum[3 * i + 2] = fmaf(a[j], a[j], sum[3 * i + 2]);
             }
+            sum[3 * i] = s0.x + s0.y;
+            sum[3 * i + 1] = s1.x + s1.y;
+            sum[3 * i + 2] = s2.x + s2.y;
         }
         block_sum(sum, red[0]);
 #pragma unroll
         for (int i = 0; i < RPI; ++i)
             ring.refill(i);
-        float G[RPI][V][8], dot[RPI], ry[RPI];
+        F8 G[RPI][V];
+        float dot[RPI], ry[RPI];
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
             // a row past the end is all zeros and adds nothing
-            const float rh = rsqrtf(sum[3 * i] * inv_d + eps);
-            const float ch = rh * rh * rh * (sum[3 * i + 1] * inv_d);
+            const float r1 = rsqrtf(sum[3 * i] * inv_d + eps);
+            const float2 rh = both(r1), ch = both(-r1 * r1 * r1 * (sum[3 * i + 1] * inv_d));
             ry[i] = rsqrtf(sum[3 * i + 2] * inv_d + eps);
-            dot[i] = 0.0f;
+            const float2 ry2 = both(ry[i]), gt2 = both(gt[i]), s2 = both(s);
+            float2 dd = both(0.0f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = 8 * (threadIdx.x + v * blockDim.x);
                 if constexpr (!KEEP) {
-                    load_f32x8<VEC>(g_pre, c, d, gq[0]);
-                    post_gain(v, gp[0]);
+                    gq[0] = load_f32x8<VEC>(g_pre, c, d);
+                    gp[0] = post_gain(c);
                 }
-                float a[8], b[8];
-                unpack8(qh[i][v], a);
-                unpack8(qn[i][v], b);
-                unpack8(qd[i][v], G[i][v]);
+                const F8 a = unpack8(qh[i][v]), b = unpack8(qn[i][v]);
+                G[i][v] = unpack8(qd[i][v]);
+                F8 o;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float u = rh * b[j];
-                    a_pre[v][j] = fmaf(u, a[j], a_pre[v][j]);
-                    G[i][v][j] = fmaf(-a[j], ch, fmaf(u, gq[0][j], G[i][v][j]));
-                    b[j] = s * G[i][v][j];
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = rh * b.v[j];
+                    a_pre[v].v[j] = fma2(u, a.v[j], a_pre[v].v[j]);
+                    G[i][v].v[j] = fma2(a.v[j], ch, fma2(u, gq[0].v[j], G[i][v].v[j]));
+                    o.v[j] = s2 * G[i][v].v[j];
                 }
                 if (ring.row(i) < T)
-                    store_bf16x8<VEC>(dh + ring.row(i) * d, c, d, b);
+                    store_bf16x8<VEC>(dh + ring.row(i) * d, c, d, o);
                 // y r_y G: the sum over tokens behind dg_post and a channel
                 // gate's gradient
-                unpack8(qy[i][v], a);
-                if constexpr (GATE == kGateFull) {
-                    float e[8], w[8];
-                    unpack8(qg[i][v], w);
+                const F8 y8 = unpack8(qy[i][v]);
+                F8 w;
+                if constexpr (GATE == kGateFull)
+                    w = unpack8(qg[i][v]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float t = a[j] * ry[i] * G[i][v][j];
-                        e[j] = t * gp[0][j];
-                        dot[i] = fmaf(e[j], w[j], dot[i]);
-                        a_post[v][j] = fmaf(t, w[j], a_post[v][j]);
-                    }
-                    if (ring.row(i) < T)
-                        store_bf16x8<VEC>(static_cast<uint16_t *>(dgate) + ring.row(i) * d, c, d, e);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float t = a[j] * ry[i] * G[i][v][j];
-                        dot[i] = fmaf(t, gp[0][j], dot[i]);
-                        a_post[v][j] = GATE == kGateToken ? fmaf(gt[i], t, a_post[v][j]) : a_post[v][j] + t;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 t = y8.v[j] * ry2 * G[i][v].v[j];
+                    if constexpr (GATE == kGateFull) {
+                        o.v[j] = t * gp[0].v[j];
+                        dd = fma2(o.v[j], w.v[j], dd);
+                        a_post[v].v[j] = fma2(t, w.v[j], a_post[v].v[j]);
+                    } else {
+                        dd = fma2(t, gp[0].v[j], dd);
+                        a_post[v].v[j] = GATE == kGateToken ? fma2(gt2, t, a_post[v].v[j]) : __fadd2_rn(a_post[v].v[j], t);
                     }
                 }
+                if constexpr (GATE == kGateFull)
+                    if (ring.row(i) < T)
+                        store_bf16x8<VEC>(static_cast<uint16_t *>(dgate) + ring.row(i) * d, c, d, o);
             }
+            dot[i] = dd.x + dd.y;
         }
         block_sum(dot, red[1]);  // sum of (y r_y) G g_post (and a channel's or element's gate)
 #pragma unroll
@@ -525,25 +570,23 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             if constexpr (GATE == kGateToken)
                 if (threadIdx.x == 0)
                     static_cast<float *>(dgate)[row] = dot[i];
-            const float cy = ry[i] * ry[i] * (gt[i] * dot[i] * inv_d);
-            const float rg = ry[i] * gt[i];
+            const float2 cy = both(-ry[i] * ry[i] * (gt[i] * dot[i] * inv_d)), rg = both(ry[i] * gt[i]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = 8 * (threadIdx.x + v * blockDim.x);
                 if constexpr (!KEEP)
-                    post_gain(v, gp[0]);
-                float a[8], w[8];
-                unpack8(qy[i][v], a);
+                    gp[0] = post_gain(c);
+                F8 o = unpack8(qy[i][v]), w;
                 if constexpr (GATE == kGateFull)
-                    unpack8(qg[i][v], w);
+                    w = unpack8(qg[i][v]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float u = rg * gp[0][j];
+                for (int j = 0; j < 4; ++j) {
+                    float2 u = rg * gp[0].v[j];
                     if constexpr (GATE == kGateFull)
-                        u *= w[j];
-                    a[j] = fmaf(u, G[i][v][j], -a[j] * cy);
+                        u = u * w.v[j];
+                    o.v[j] = fma2(u, G[i][v].v[j], o.v[j] * cy);
                 }
-                store_bf16x8<VEC>(dy + row * d, c, d, a);
+                store_bf16x8<VEC>(dy + row * d, c, d, o);
             }
         }
     }
@@ -552,11 +595,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         const int c = 8 * (threadIdx.x + v * blockDim.x);
         float *p = partial + static_cast<int64_t>(blockIdx.x) * 2 * d;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < d) {
-                p[c + j] = a_pre[v][j];
-                p[d + c + j] = a_post[v][j];
+        for (int j = 0; j < 4; ++j) {
+            if (c + 2 * j < d) {
+                p[c + 2 * j] = a_pre[v].v[j].x;
+                p[d + c + 2 * j] = a_post[v].v[j].x;
             }
+            if (c + 2 * j + 1 < d) {
+                p[c + 2 * j + 1] = a_pre[v].v[j].y;
+                p[d + c + 2 * j + 1] = a_post[v].v[j].y;
+            }
+        }
     }
 }
 
