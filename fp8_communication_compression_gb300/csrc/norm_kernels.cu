@@ -207,15 +207,16 @@ template <int NT, bool VEC> struct RowRing {
     }
 };
 
-// Sums of K values over the CTA; every thread gets them.  `red` holds 16
-// floats for each of K values rounded up to a power of two; two calls in turn
+// Sums of K values over the CTA of at most WARPS warps; every thread gets
+// them.  `red` holds WARPS floats for each of K values rounded up to a power
+// of two; two calls in turn
 // use two of them, so that one barrier a call is enough.  A warp sums all K
 // together: in each halving step a lane passes on half of its values and
 // keeps the other half, so that the K sums take about K + 5 shuffles and
 // land in groups of lanes; the warps' sums are added the same way.
 __host__ __device__ constexpr int pow2_at_least(int k) { return k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : 8; }
 
-template <int K> __device__ __forceinline__ void block_sum(float (&v)[K], float *red)
+template <int WARPS, int K> __device__ __forceinline__ void block_sum(float (&v)[K], float *red)
 {
     constexpr int P = pow2_at_least(K);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -240,16 +241,15 @@ template <int K> __device__ __forceinline__ void block_sum(float (&v)[K], float 
         x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], s);
     // lanes 32 / P i .. hold value i
     if ((lane & (32 / P - 1)) == 0)
-        red[16 * (lane / (32 / P)) + warp] = x[0];
+        red[WARPS * (lane / (32 / P)) + warp] = x[0];
     __syncthreads();
-    // lane l adds the sums of 16 P / 32 warps of value l / (32 / P)
-    constexpr int Q = P >= 2 ? P / 2 : 1;   // warps a lane adds
-    constexpr int L = 16 / Q;               // lanes to a value
+    constexpr int Q = P * WARPS >= 32 ? P * WARPS / 32 : 1;  // warps a lane adds
+    constexpr int L = WARPS / Q;                             // lanes to a value
     const int i = lane / L < P ? lane / L : P - 1, w0 = (lane % L) * Q;
     float sum = 0.0f;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-        sum += w0 + q < warps ? red[16 * i + w0 + q] : 0.0f;
+        sum += w0 + q < warps ? red[WARPS * i + w0 + q] : 0.0f;
 #pragma unroll
     for (int s = L / 2; s >= 1; s >>= 1)
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             }
             sum[i] = ss.x + ss.y;
         }
-        block_sum(sum, red[0]);
+        block_sum<16>(sum, red[0]);
 #pragma unroll
         for (int i = 0; i < RPI; ++i)
             ring.refill(i);
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             }
             sum[i] = ss.x + ss.y;
         }
-        block_sum(sum, red[1]);
+        block_sum<16>(sum, red[1]);
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
             const int64_t row = ring.row(i);
@@ -418,8 +418,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
 // --------------------------------------------------------------- backward --
 
-template <int V, int RPI, int GATE, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+// MAXT: the most threads of a CTA (512, or 768 with one row at a time in 80
+// registers).
+template <int V, int RPI, int MAXT, int GATE, bool VEC>
+__global__ void __launch_bounds__(MAXT, 1)
     norm_backward_kernel(const uint16_t *__restrict__ dn, const uint16_t *__restrict__ dh2,
                          const uint16_t *__restrict__ y, const uint16_t *__restrict__ h2,
                          const float *__restrict__ g_post, const float *__restrict__ g_pre,
@@ -431,9 +433,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     // more columns a thread: no registers left for the gains, which are then
     // read (from L1) where they are used
     constexpr bool KEEP = V == 1;
+    constexpr int WARPS = MAXT > 512 ? 32 : 16;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kMaxSlots];
-    __shared__ float red[2][16 * pow2_at_least(3 * RPI)];
+    __shared__ float red[2][WARPS * pow2_at_least(3 * RPI)];
     RowRing<NT, VEC> ring;
     ring.src[0] = dn;
     ring.src[1] = dh2;
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             sum[3 * i + 1] = s1.x + s1.y;
             sum[3 * i + 2] = s2.x + s2.y;
         }
-        block_sum(sum, red[0]);
+        block_sum<WARPS>(sum, red[0]);
 #pragma unroll
         for (int i = 0; i < RPI; ++i)
             ring.refill(i);
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             }
             dot[i] = dd.x + dd.y;
         }
-        block_sum(dot, red[1]);  // sum of (y r_y) G g_post (and a channel's or element's gate)
+        block_sum<WARPS>(dot, red[1]);  // sum of (y r_y) G g_post (and a channel's or element's gate)
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
             const int64_t row = ring.row(i);
@@ -653,13 +656,13 @@ struct NormPlan {
 
 constexpr uint32_t kSmemPerSm = 227 * 1024;
 
-// regs: the registers a thread of the kernel takes, for how many CTAs share
-// an SM.
-NormPlan plan_norm(int64_t T, int d, int tensors, int regs, int sms)
+// max_threads: the most threads with one group of columns each; regs: the
+// registers a thread of the kernel takes, for how many CTAs share an SM.
+NormPlan plan_norm(int64_t T, int d, int tensors, int max_threads, int regs, int sms)
 {
     NormPlan p;
     const int units = (d + 7) / 8;
-    p.v = units <= kMaxThreads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
+    p.v = units <= max_threads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
     p.threads = ((units + p.v - 1) / p.v + 31) / 32 * 32;
     int per_sm = 65536 / (regs * p.threads);
     per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
@@ -680,9 +683,23 @@ NormPlan plan_norm(int64_t T, int d, int tensors, int regs, int sms)
     return p;
 }
 
+NormPlan plan_forward(int64_t T, int d, int gate_mode, int sms)
+{
+    return plan_norm(T, d, gate_mode == kGateFull ? 3 : 2, kMaxThreads, d <= 16 * kMaxThreads ? 96 : 128, sms);
+}
+
+// Backward, one group of columns a thread: two rows at a time in 128
+// registers up to 512 threads, above that (up to 768) one row at a time in
+// 80.  Measured at 8192 rows, one against two rows: 1024 columns 32 and 28
+// us, 4096 96 and 77 us; at 5120, 106 us against 167 with two groups of
+// columns a thread.
+constexpr int kWide = 768;
+bool one_row(int d) { return d > 8 * kMaxThreads && d <= 8 * kWide; }
+
 NormPlan plan_backward(int64_t T, int d, int gate_mode, int sms)
 {
-    return plan_norm(T, d, gate_mode == kGateFull ? 5 : 4, 128, sms);
+    const bool one = one_row(d);
+    return plan_norm(T, d, gate_mode == kGateFull ? 5 : 4, one ? kWide : kMaxThreads, one ? 80 : 128, sms);
 }
 
 constexpr int kMaxDevices = 64;
@@ -713,14 +730,14 @@ cudaError_t run_forward(const NormPlan &p, const NormForward &a, int device, cud
                       static_cast<uint16_t *>(a.h_out), a.n_out, a.n_scale);
 }
 
-template <int V, int GATE, bool VEC>
+template <int V, int RPI, int MAXT, int GATE, bool VEC>
 cudaError_t run_backward(const NormPlan &p, const NormBackward &a, int device, cudaStream_t stream)
 {
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = allow_smem(norm_backward_kernel<V, rows_at_once(V), GATE, VEC>, device, set);
+    cudaError_t e = allow_smem(norm_backward_kernel<V, RPI, MAXT, GATE, VEC>, device, set);
     if (e != cudaSuccess)
         return e;
-    e = launch_pdl(norm_backward_kernel<V, rows_at_once(V), GATE, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
+    e = launch_pdl(norm_backward_kernel<V, RPI, MAXT, GATE, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
                    static_cast<const uint16_t *>(a.dn), static_cast<const uint16_t *>(a.dh_out),
                    static_cast<const uint16_t *>(a.y), static_cast<const uint16_t *>(a.h_out), a.g_post, a.g_pre,
                    a.gate, a.residual_scale, a.eps, a.T, static_cast<int>(a.d), p.slots,
@@ -753,18 +770,28 @@ template <int V, bool VEC> cudaError_t forward_gate(const NormPlan &p, const Nor
     }
 }
 
-template <int V, bool VEC> cudaError_t backward_gate(const NormPlan &p, const NormBackward &a, int dev, cudaStream_t s)
+template <int V, int RPI, int MAXT, bool VEC>
+cudaError_t backward_gate(const NormPlan &p, const NormBackward &a, int dev, cudaStream_t s)
 {
     switch (a.gate_mode) {
     case kGateNone:
-        return run_backward<V, kGateNone, VEC>(p, a, dev, s);
+        return run_backward<V, RPI, MAXT, kGateNone, VEC>(p, a, dev, s);
     case kGateChannel:
-        return run_backward<V, kGateChannel, VEC>(p, a, dev, s);
+        return run_backward<V, RPI, MAXT, kGateChannel, VEC>(p, a, dev, s);
     case kGateToken:
-        return run_backward<V, kGateToken, VEC>(p, a, dev, s);
+        return run_backward<V, RPI, MAXT, kGateToken, VEC>(p, a, dev, s);
     default:
-        return run_backward<V, kGateFull, VEC>(p, a, dev, s);
+        return run_backward<V, RPI, MAXT, kGateFull, VEC>(p, a, dev, s);
     }
+}
+
+template <bool VEC> cudaError_t backward_shape(const NormPlan &p, const NormBackward &a, int dev, cudaStream_t s)
+{
+    if (p.v == 1)
+        return one_row(static_cast<int>(a.d)) ? backward_gate<1, 1, kWide, VEC>(p, a, dev, s)
+                                              : backward_gate<1, 2, kMaxThreads, VEC>(p, a, dev, s);
+    return p.v == 2 ? backward_gate<2, 1, kMaxThreads, VEC>(p, a, dev, s)
+                    : backward_gate<4, 1, kMaxThreads, VEC>(p, a, dev, s);
 }
 
 }  // namespace
@@ -790,7 +817,7 @@ cudaError_t launch_norm_forward(const NormForward &a, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const int d = static_cast<int>(a.d);
-    const NormPlan p = plan_norm(a.T, d, a.gate_mode == kGateFull ? 3 : 2, d <= 16 * kMaxThreads ? 96 : 128, di.num_sms);
+    const NormPlan p = plan_forward(a.T, d, a.gate_mode, di.num_sms);
     const bool vec = d % 8 == 0;
     switch (p.v) {
     case 1:
@@ -827,15 +854,8 @@ cudaError_t launch_norm_backward(const NormBackward &a, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const NormPlan p = plan_backward(a.T, static_cast<int>(a.d), a.gate_mode, di.num_sms);
-    const bool vec = a.d % 8 == 0;
-    switch (p.v) {
-    case 1:
-        return vec ? backward_gate<1, true>(p, a, di.device, stream) : backward_gate<1, false>(p, a, di.device, stream);
-    case 2:
-        return vec ? backward_gate<2, true>(p, a, di.device, stream) : backward_gate<2, false>(p, a, di.device, stream);
-    default:
-        return vec ? backward_gate<4, true>(p, a, di.device, stream) : backward_gate<4, false>(p, a, di.device, stream);
-    }
+    return a.d % 8 == 0 ? backward_shape<true>(p, a, di.device, stream)
+                        : backward_shape<false>(p, a, di.device, stream);
 }
 
 }  // namespace taco
