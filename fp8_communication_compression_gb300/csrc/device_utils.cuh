@@ -147,15 +147,6 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int32_t x, 
                  : "memory");
 }
 
-// The same, adding fp32 values to what is there.
-__device__ __forceinline__ void tma_add_2d(const CUtensorMap *map, int32_t x, int32_t y, uint32_t src)
-{
-    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(src)
-                 : "memory");
-}
-
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Wait until no bulk group of this thread is still reading shared memory.

@@ -16,17 +16,20 @@
 // fp8_gemm_kernel (many tiles): persistent, one CTA per SM, tiles of 128 x
 //   256.  Warp 0 streams 128-byte-wide pieces of A and B by TMA through an
 //   mbarrier ring, and the scales through a ring of their own; one thread of
-//   warp 1 copies scales to tensor memory and issues the MMAs; warps 2-5
-//   store finished tiles; warp 6 spreads tile scales.  Tensor memory holds
-//   the scales (two sets of 12 columns) and two accumulators, which overlap
-//   by 32 columns: the epilogue drains these first, and the next tile's MMAs
-//   start while it works on the rest.  Where the last round of tiles would
-//   leave more than half of the SMs idle, its tiles are cut in two (128 x
-//   128).  An fp32 result over more than 2048 values is summed in pieces: the
-//   tensor core's accumulator truncates, which biases long coherent sums
-//   (measured on a weight gradient over 4096 tokens: 1.9e-6 of its norm in
-//   one piece, where an fp32 matrix product has 3.7e-7), so each piece leaves
-//   tensor memory and is added to the output by a rounding fp32 reduction.
+//   warp 1 copies scales to tensor memory and issues the MMAs; warp 2 spreads
+//   tile scales; warps 3-10 store finished tiles.  The CTAs of a cluster of
+//   two take tiles one above the other: each loads half of their common B and
+//   multicasts it to both, since the path from L2 bounds the kernel (alone, a
+//   CTA needs 48 KB for 0.27 us of MMAs, 27 TB/s over 152 SMs, and 22 were
+//   measured).  Tensor memory holds the scales (two sets of 12 columns) and
+//   two accumulators, which overlap by 32 columns: the epilogue drains these
+//   first, and the next tile's MMAs start while it works on the rest.  Where
+//   the last round of tiles would leave more than half of the SMs idle, its
+//   tiles are cut in two (128 x 128).  An fp32 result over more than 1536
+//   values is summed in pieces: the tensor core's accumulator truncates,
+//   which biases long coherent sums (measured on a weight gradient over 4096
+//   tokens: 1.9e-6 of its norm in one piece, where an fp32 matrix product has
+//   3.7e-7), so each piece is added in the epilogue's registers, rounded.
 //
 // fp8_gemm_split_kernel (few tiles: single tokens to small batches): the
 //   roles of the operands are exchanged - B's rows (weights) take the 128
@@ -54,7 +57,7 @@ __device__ unsigned int g_fp8_error;
 namespace {
 
 constexpr uint32_t kErrFp8 = 64u;
-constexpr int kThreads = 224;  // warps: 0 TMA, 1 MMA, 2-5 epilogue, 6 scales
+constexpr int kThreads = 224;  // split kernel's warps: 0 TMA, 1 MMA, 2-5 epilogue, 6 scales
 constexpr int kMaxStages = 10;
 constexpr uint32_t kTileA = 128 * 128;
 constexpr uint32_t kSmemLimit = 232448;
@@ -118,12 +121,13 @@ __device__ __forceinline__ Ring make_ring(const uint8_t *smem, int bn, int stage
     return r;
 }
 
-// (one thread)  tile_scales: warp 6 also arrives on a scale slot.
-__device__ __forceinline__ void init_barriers(const Ring &r, bool tile_scales)
+// (one thread)  tile_scales: a warp of its own also arrives on a scale slot;
+// readers: the CTAs whose MMAs read what a stage's loads bring.
+__device__ __forceinline__ void init_barriers(const Ring &r, bool tile_scales, int readers, int epilogue_warps)
 {
     for (int s = 0; s < r.stages; ++s) {
         mbar_init(r.full(s), 1);
-        mbar_init(r.empty(s), 1);
+        mbar_init(r.empty(s), readers);
     }
     for (int s = 0; s < kScaleSlots; ++s) {
         mbar_init(r.sf_full(s), tile_scales ? 2 : 1);
@@ -131,7 +135,7 @@ __device__ __forceinline__ void init_barriers(const Ring &r, bool tile_scales)
     }
     for (int a = 0; a < 2; ++a) {
         mbar_init(r.acc_full(a), 1);
-        mbar_init(r.acc_free(a), 4);  // one arrival per epilogue warp
+        mbar_init(r.acc_free(a), epilogue_warps);
     }
     mbar_init(r.drain(), 1);
     fence_barrier_init();
@@ -161,7 +165,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 __device__ __forceinline__ bool starts_group(int kb, int kb0) { return (kb & 3) == 0 || kb == kb0; }
 
 // Four MMAs of 32 values each: one block of the contraction, whose scales
-// are byte kb % 4 of their words.
+// are byte kb % 4 of their words.  PAIR: the slot is freed in both CTAs.
+template <bool PAIR>
 __device__ __forceinline__ void mma_block(const Ring &r, int s, uint32_t d, uint32_t sfa, uint32_t sfb, uint32_t idesc,
                                           int kb, bool accumulate)
 {
@@ -170,7 +175,11 @@ __device__ __forceinline__ void mma_block(const Ring &r, int s, uint32_t d, uint
 #pragma unroll
     for (int k = 0; k < 4; ++k)  // 32 codes = 32 bytes = 2 descriptor units
         mma_mxf8(d, ad + 2 * k, bd + 2 * k, id, sfa, sfb, accumulate || k != 0);
-    mma_commit(r.empty(s));  // the slot is free once these have read it
+    // the slot is free once these have read it
+    if (PAIR)
+        mma_commit_cluster(r.empty(s), 3);
+    else
+        mma_commit(r.empty(s));
 }
 
 // (warp 6)  Tile scales of blocks 4 g .. 4 g + 3 for row tiles t and t + 1:
@@ -199,28 +208,45 @@ __device__ __forceinline__ void spread_tile_scales(uint32_t v, uint32_t dst, int
 // ------------------------------------------------------------ many tiles --
 
 constexpr int kBN = 256;
-constexpr uint32_t kStaging = 4 * 4096;   // 4 KB per epilogue warp
+constexpr int kGThreads = 352;             // warps: 0 TMA, 1 MMA, 2 scales, 3-10 epilogue
+constexpr uint32_t kStaging = 8 * 2048;   // 2 KB per epilogue warp
 constexpr int kStages = 4;
 constexpr uint32_t kAcc1 = 224;            // second accumulator: columns 224 .. 479
 constexpr uint32_t kSfColumn = 480;        // tensor-memory columns 480 .. 503: scales
 constexpr int kGroupM = 16;                // row tiles walked together (operands shared through L2)
+constexpr int kPieceBlocks = 12;           // fp32: most blocks summed in tensor memory
 constexpr uint32_t kGemmSmem = 1024 + kStages * stage_bytes_of(kBN) + kStaging + kScaleSlots * 1536 + kBarBytes;
 static_assert(kGemmSmem <= kSmemLimit, "shared memory per CTA");
 
-// The work of the grid: `full` whole tiles, then the others as two halves
-// each; every item in `segs` pieces of `seg_kb` blocks.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// All threads of the cluster's CTAs meet (barrier.cluster is defined below
+// for the split kernel as well).
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The work of the grid, in units of one CTA's or (PAIR) two CTAs' tiles, one
+// above the other: `full` whole ones, then the others as two halves each;
+// every item in `segs` pieces of `seg_kb` blocks.
 struct Work {
-    int tiles_m, tiles_n, full, items, segs, seg_kb, KB;
+    int units_m, tiles_n, full, items, segs, seg_kb, KB, group;
     int64_t N;
-    // Item idx: its row tile, its first column, and its width (256 or 128).
+    // Item idx: its row unit, its first column, and its width (256 or 128).
     // False for the second half of a tile that has none.
-    __device__ __forceinline__ bool at(int idx, int &tm, int64_t &n0, int &bn) const
+    __device__ __forceinline__ bool at(int idx, int &um, int64_t &n0, int &bn) const
     {
         const int t = idx < full ? idx : full + (idx - full) / 2;
-        const int per = kGroupM * tiles_n, g = t / per, r = t - g * per;
-        const int left = tiles_m - g * kGroupM, gm = left < kGroupM ? left : kGroupM;
+        const int per = group * tiles_n, g = t / per, r = t - g * per;
+        const int left = units_m - g * group, gm = left < group ? left : group;
         const int tn = r / gm;
-        tm = g * kGroupM + (r - tn * gm);
+        um = g * group + (r - tn * gm);
         n0 = static_cast<int64_t>(tn) * kBN;
         bn = kBN;
         if (idx >= full) {
@@ -239,99 +265,90 @@ struct Work {
     }
 };
 
-// 32 columns of a warp's 32 rows: rounded into the staging area and stored,
-// by TMA where the output's rows allow it (`tma`), else element by element
-// with the lanes along the row.
-// `add` (fp32 only): added to what is there.
+// 64 bytes of each of a warp's 32 rows (32 bf16 or 16 fp32 columns) from the
+// rows' packed words through the staging area to the output, by TMA where
+// the output's rows allow it (`tma`), else element by element with the lanes
+// along the row.
 template <bool BF16>
-__device__ __forceinline__ void store_chunk(const float (&x)[32], uint32_t stage, int lane, bool tma, bool add,
+__device__ __forceinline__ void store_chunk(const uint32_t (&w)[16], uint32_t stage, int lane, bool tma,
                                             const CUtensorMap *map, void *out, int64_t M, int64_t N, int64_t row0,
                                             int64_t col0)
 {
-    if (lane == 0) {
-        // the store that used this staging area before has read it (bf16
-        // has two areas in turn, fp32 one)
-        if (BF16)
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        else
-            bulk_wait_read_all();
-    }
+    if (lane == 0)
+        bulk_wait_read_all();  // the store that used this staging area before has read it
     __syncwarp();
-    if constexpr (BF16) {
-        const uint32_t row = stage + 64 * lane, swz = (lane >> 1) & 3;
+    const uint32_t row = stage + 64 * lane, swz = (lane >> 1) & 3;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            sts128(row + ((j ^ swz) << 4), f32x2_to_bf16x2(x[8 * j], x[8 * j + 1]),
-                   f32x2_to_bf16x2(x[8 * j + 2], x[8 * j + 3]), f32x2_to_bf16x2(x[8 * j + 4], x[8 * j + 5]),
-                   f32x2_to_bf16x2(x[8 * j + 6], x[8 * j + 7]));
-    } else {
-        const uint32_t row = stage + 128 * lane, swz = lane & 7;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            sts128(row + ((j ^ swz) << 4), __float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
-                   __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
-    }
+    for (int j = 0; j < 4; ++j)
+        sts128(row + ((j ^ swz) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     if (tma) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (row0 < M && col0 < N) {
-                if (!BF16 && add)
-                    tma_add_2d(map, static_cast<int32_t>(col0), static_cast<int32_t>(row0), stage);
-                else
-                    tma_store_2d(map, static_cast<int32_t>(col0), static_cast<int32_t>(row0), stage);
-            }
+            if (row0 < M && col0 < N)
+                tma_store_2d(map, static_cast<int32_t>(col0), static_cast<int32_t>(row0), stage);
             bulk_commit();
         }
     } else {
         __syncwarp();
-        const int64_t col = col0 + lane;
-#pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-            if (row0 + r >= M)
-                break;
-            if constexpr (BF16) {
+        if constexpr (BF16) {
+            const int64_t col = col0 + lane;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+                if (row0 + r >= M)
+                    break;
                 uint16_t h;
                 asm volatile("ld.shared.u16 %0, [%1];"
                              : "=h"(h)
                              : "r"(stage + 64 * r + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
                 if (col < N)
                     static_cast<uint16_t *>(out)[(row0 + r) * N + col] = h;
-            } else {
-                const float v = __uint_as_float(lds32(stage + 128 * r + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)));
-                if (col < N) {
-                    float *o = static_cast<float *>(out) + (row0 + r) * N + col;
-                    *o = add ? *o + v : v;
-                }
+            }
+        } else {  // two rows at a time
+            const int l = lane & 15;
+            const int64_t col = col0 + l;
+#pragma unroll 8
+            for (int r = lane >> 4; r < 32; r += 2) {
+                if (row0 + r >= M)
+                    break;
+                const uint32_t v = lds32(stage + 64 * r + (((l >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (l & 3));
+                if (col < N)
+                    static_cast<uint32_t *>(out)[(row0 + r) * N + col] = v;
             }
         }
         __syncwarp();
     }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+// PAIR: the two CTAs of a cluster work on the same columns, this one on row
+// tile 2 um + rank.
+template <bool BF16, bool PAIR>
+__global__ void __launch_bounds__(kGThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
-                    const __grid_constant__ CUtensorMap o_map, Scales sa, Scales sb, void *out, int64_t M, int64_t N,
-                    Work work, int tma_out)
+                    const __grid_constant__ CUtensorMap o_map, Scales sa, Scales sb, void *__restrict__ out, int64_t M,
+                    int64_t N, Work work, int tma_out)
 {
     extern __shared__ uint8_t smem_raw[];
     const Ring r = make_ring(smem_raw, kBN, kStages, 1536, kStaging);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (work.KB + 3) / 4;  // scale pieces per row tile
+    const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
+    const int idx0 = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
 
     if (threadIdx.x == 0)
-        init_barriers(r, sb.tiles);
+        init_barriers(r, sb.tiles, PAIR ? 2 : 1, 8);
     if (warp == 1) {
         tmem_alloc(r.tmem_slot(), 512);
         tmem_relinquish_alloc_permit();
     }
-    if (work.items <= 2 * static_cast<int>(gridDim.x))
+    if (work.items <= 2 * step)
         pdl_trigger();
     pdl_wait();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (PAIR)
+        cluster_sync();  // the other CTA's barriers are ready
     const uint32_t tmem = lds32(r.tmem_slot());
 
     if (warp == 0) {
@@ -341,11 +358,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             Slot p, f;
             int64_t issued = 0, scales = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
-                int tm, bn;
+            for (int idx = idx0; ok && idx < work.items; idx += step) {
+                int um, bn;
                 int64_t n0;
-                if (!work.at(idx, tm, n0, bn))
+                if (!work.at(idx, um, n0, bn))
                     continue;
+                const int tm = PAIR ? 2 * um + rank : um;
+                // (a row tile past the last one has no scales: any do)
+                const uint8_t *sap = sa.p + static_cast<int64_t>(tm < sa.row_tiles ? tm : 0) * groups * 512;
                 for (int seg = 0; ok && seg < work.segs; ++seg) {
                     const int kb0 = work.first(seg), kb1 = work.last(seg);
                     for (int kb = kb0; kb < kb1; ++kb) {
@@ -357,8 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             const int pieces = bn / 128;
                             mbar_arrive_expect_tx(r.sf_full(f.s), sb.tiles ? 512 : 512 + 512 * pieces);
-                            bulk_load(r.sf(f.s), sa.p + (static_cast<int64_t>(tm) * groups + (kb >> 2)) * 512, 512,
-                                      r.sf_full(f.s));
+                            bulk_load(r.sf(f.s), sap + (kb >> 2) * 512, 512, r.sf_full(f.s));
                             if (!sb.tiles)
                                 for (int i = 0; i < pieces; ++i)
                                     bulk_load(r.sf(f.s) + 512 + 512 * i,
@@ -371,12 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = false;
                             break;
                         }
+                        const int32_t kc = kb * 128, nc = static_cast<int32_t>(n0);
                         mbar_arrive_expect_tx(r.full(p.s), stage_bytes_of(bn));
-                        tma_load_2d(r.a(p.s), &a_map, kb * 128, tm * 128, r.full(p.s));
-                        tma_load_2d(r.b(p.s), &b_map, kb * 128, static_cast<int32_t>(n0), r.full(p.s));
-                        if (bn > 128)
-                            tma_load_2d(r.b(p.s) + kTileA, &b_map, kb * 128, static_cast<int32_t>(n0) + 128,
-                                        r.full(p.s));
+                        tma_load_2d(r.a(p.s), &a_map, kc, tm * 128, r.full(p.s));
+                        if (bn > 128 && PAIR) {  // this CTA's half of B, for both
+                            tma_load_2d_cluster(r.b(p.s) + rank * kTileA, &b_map, kc, nc + 128 * rank, r.full(p.s), 3);
+                        } else {
+                            tma_load_2d(r.b(p.s), &b_map, kc, nc, r.full(p.s));
+                            if (bn > 128)
+                                tma_load_2d(r.b(p.s) + kTileA, &b_map, kc, nc + 128, r.full(p.s));
+                        }
                         p.next(kStages);
                         ++issued;
                     }
@@ -394,16 +417,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0;  // accumulations done: items times segments
             uint32_t set = 0, sfa = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
-                int tm, bn;
+            for (int idx = idx0; ok && idx < work.items; idx += step) {
+                int um, bn;
                 int64_t n0;
-                if (!work.at(idx, tm, n0, bn))
+                if (!work.at(idx, um, n0, bn))
                     continue;
                 const uint32_t idesc = idesc_mxf8(bn);
                 for (int seg = 0; ok && seg < work.segs; ++seg, ++i) {
-                    // the epilogue has drained the columns this accumulator
-                    // shares with accumulation i - 1 (which it reaches after
-                    // all of i - 2, this accumulator's last)
+                    // every epilogue warp has drained the columns this
+                    // accumulator shares with accumulation i - 1 and, before
+                    // that, all of i - 2, this accumulator's last
                     if (i > 0 && !mbar_wait(r.acc_free((i - 1) & 1), ((i - 1) >> 1) & 1)) {
                         report_timeout();
                         ok = false;
@@ -435,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         tc_fence_after_sync();
-                        mma_block(r, p.s, d, sfa, sfa + 4, idesc, kb, kb != kb0);
+                        mma_block<PAIR>(r, p.s, d, sfa, sfa + 4, idesc, kb, kb != kb0);
                         p.next(kStages);
                     }
                     if (ok)
@@ -447,14 +470,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(r.drain(), 0);
             }
         }
-    } else if (warp == 6) {
+    } else if (warp == 2) {
         if (sb.tiles) {
             Slot f;
             bool ok = true;
-            for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
-                int tm, bn;
+            for (int idx = idx0; ok && idx < work.items; idx += step) {
+                int um, bn;
                 int64_t n0;
-                if (!work.at(idx, tm, n0, bn))
+                if (!work.at(idx, um, n0, bn))
                     continue;
                 for (int seg = 0; ok && seg < work.segs; ++seg) {
                     const int g1 = (work.last(seg) + 3) / 4;
@@ -480,55 +503,107 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        const int q = warp & 3;
-        const uint32_t staging = r.extra + 4096 * q;
+        // warps 3-6 take columns 0 .. 127 of a tile, upwards, 7-10 columns 255
+        // .. 128: the columns that the accumulators share, the second's first
+        // 32 and the first's last 32, come first
+        const int q = warp & 3, half = (warp - 3) >> 2;
+        const uint32_t staging = r.extra + 2048 * (warp - 3);
         int i = 0;
-        uint32_t area = 0;  // bf16: the staging area of the next chunk, 0 or 2048
         bool ok = true;
-        for (int idx = blockIdx.x; ok && idx < work.items; idx += gridDim.x) {
-            int tm, bn;
+        for (int idx = idx0; ok && idx < work.items; idx += step) {
+            int um, bn;
             int64_t n0;
-            if (!work.at(idx, tm, n0, bn))
+            if (!work.at(idx, um, n0, bn))
                 continue;
-            for (int seg = 0; seg < work.segs; ++seg, ++i) {
+            const bool mine = 128 * half < bn;
+            const int64_t row0 = static_cast<int64_t>(PAIR ? 2 * um + rank : um) * 128 + 32 * q;
+            const int64_t col0 = n0 + 128 * half;
+            auto wait_full = [&]() {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.acc_full(i & 1), (i >> 1) & 1))) {
                     if (lane == 0)
                         report_timeout();
-                    ok = false;
-                    break;
+                    return false;
                 }
                 tc_fence_after_sync();
-                // an earlier piece's stores are complete before this one is added
-                if (seg > 0 && lane == 0)
-                    bulk_wait_all();
-                const uint32_t tq = tmem + (i & 1 ? kAcc1 : 0u) + (static_cast<uint32_t>(32 * q) << 16);
-                const int64_t row0 = static_cast<int64_t>(tm) * 128 + 32 * q;
-                const int chunks = bn / 32;
-                // the first accumulator shares its last columns with the
-                // second, which shares its first: drain those first
+                return true;
+            };
+            // this warp has read the shared columns (if they are its own),
+            // and all of its earlier tiles
+            auto free_shared = [&]() {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(r.acc_free(i & 1));
+            };
+            auto columns = [&]() {
+                return tmem + (i & 1 ? kAcc1 : 0u) + 128 * half + (static_cast<uint32_t>(32 * q) << 16);
+            };
+            if constexpr (BF16) {
+                if (!(ok = wait_full()))
+                    break;
+                if (!mine) {
+                    free_shared();
+                } else {
+                    const uint32_t tq = columns();
 #pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
-                    const int j = i & 1 ? c : chunks - 1 - c;
-                    float x[32];
-                    tmem_load_32(tq + 32 * j, x);
-                    if (c == 0) {
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(r.acc_free(i & 1));
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = half ? 3 - c : c;
+                        float x[32];
+                        tmem_load_32(tq + 32 * j, x);
+                        if (c == 0)
+                            free_shared();
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            w[k] = f32x2_to_bf16x2(x[2 * k], x[2 * k + 1]);
+                        store_chunk<true>(w, staging, lane, tma_out != 0, &o_map, out, M, N, row0, col0 + 32 * j);
                     }
-                    store_chunk<BF16>(x, staging + area, lane, tma_out != 0, seg > 0, &o_map, out, M, N, row0,
-                                      n0 + 32 * j);
-                    if (BF16)
-                        area ^= 2048;
                 }
+                ++i;
+            } else {
+                float sum[8][16] = {};  // 16 columns each, in the order they are read
+                for (int seg = 0; seg < work.segs; ++seg, ++i) {
+                    if (!(ok = wait_full()))
+                        break;
+                    if (!mine) {
+                        free_shared();
+                        continue;
+                    }
+                    const uint32_t tq = columns();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float x[16];
+                        tmem_load_16(tq + 16 * (half ? 7 - j : j), x);
+                        if (j == 1)
+                            free_shared();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            sum[j][k] += x[k];
+                    }
+                }
+                if (!ok)
+                    break;
+                if (mine)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            w[k] = __float_as_uint(sum[j][k]);
+                        store_chunk<false>(w, staging, lane, tma_out != 0, &o_map, out, M, N, row0,
+                                           col0 + 16 * (half ? 7 - j : j));
+                    }
             }
         }
         if (lane == 0)
             bulk_wait_all();
     }
     tc_fence_before_sync();
-    __syncthreads();
+    __syncwarp();
+    if (PAIR)
+        cluster_sync();  // no CTA leaves while the other's loads or arrivals may still reach it
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
@@ -536,11 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------- few tiles --
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // The address of CTA `rank`'s shared memory at this CTA's address `addr`.
 __device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank)
@@ -593,7 +663,7 @@ __global__ void __launch_bounds__(kThreads)
     const int groups = (KB + 3) / 4;
 
     if (threadIdx.x == 0)
-        init_barriers(r, sb.tiles);
+        init_barriers(r, sb.tiles, 1, 4);
     if (warp == 1) {
         tmem_alloc(r.tmem_slot(), kSplitTmem);
         tmem_relinquish_alloc_permit();
@@ -666,7 +736,7 @@ __global__ void __launch_bounds__(kThreads)
                     break;
                 }
                 tc_fence_after_sync();
-                mma_block(r, p.s, tmem, sf, sf + 4, idesc, kb, kb != kb0);
+                mma_block<false>(r, p.s, tmem, sf, sf + 4, idesc, kb, kb != kb0);
                 p.next(stages);
             }
             mma_commit(ok ? r.acc_full(0) : r.drain());
@@ -802,6 +872,9 @@ struct Plan {
 // Few tiles: fewer than half the SMs would get a 128 x 256 one.
 bool few_tiles(int64_t M, int64_t N, int sms) { return ceil_div(M, 128) * ceil_div(N, kBN) < sms / 2; }
 
+// Pairs of row tiles where they leave no CTA without one.
+bool use_pairs(int64_t M, int64_t N, int sms) { return ceil_div(M, 128) % 2 == 0 || ceil_div(M, 128) >= 9; }
+
 template <bool BF16>
 cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
                       void *out, const DeviceInfo &di, cudaStream_t stream)
@@ -847,7 +920,7 @@ cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
                               split);
 }
 
-template <bool BF16>
+template <bool BF16, bool PAIR>
 cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
                       void *out, const DeviceInfo &di, cudaStream_t stream)
 {
@@ -856,40 +929,56 @@ cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
         encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b), K, N, K, 128, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16>, kGemmSmem, di.device, set);
+    cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16, PAIR>, kGemmSmem, di.device, set);
     if (e != cudaSuccess)
         return e;
     const uint64_t row_bytes = static_cast<uint64_t>(N) * (BF16 ? 2 : 4);
     const int tma_out = row_bytes % 16 == 0;
     om = am;
     if (tma_out && encode_tensor_map_2d(&om, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                                        out, N, M, row_bytes, 32, 32,
-                                        BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) != 0)
+                                        out, N, M, row_bytes, BF16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B) != 0)
         return cudaErrorInvalidValue;
     Work w;
     w.KB = static_cast<int>(ceil_div(K, 128));
     w.N = N;
-    w.tiles_m = static_cast<int>(ceil_div(M, 128));
+    w.units_m = static_cast<int>(ceil_div(M, PAIR ? 256 : 128));
     w.tiles_n = static_cast<int>(ceil_div(N, kBN));
-    // fp32: pieces of at most 16 blocks, whole scale groups each
-    w.segs = BF16 ? 1 : static_cast<int>(ceil_div(w.KB, 16));
+    w.group = PAIR ? kGroupM / 2 : kGroupM;
+    // fp32: pieces of whole scale groups
+    w.segs = BF16 ? 1 : static_cast<int>(ceil_div(w.KB, kPieceBlocks));
     w.seg_kb = static_cast<int>(ceil_div(ceil_div(w.KB, w.segs), 4) * 4);
     w.segs = static_cast<int>(ceil_div(w.KB, w.seg_kb));
     // a last round that fills at most half of the SMs goes in halves
-    const int tiles = w.tiles_m * w.tiles_n, rem = tiles % di.num_sms;
-    w.full = rem <= di.num_sms / 2 ? tiles - rem : tiles;
+    const int slots = PAIR ? di.num_sms / 2 : di.num_sms;
+    const int tiles = w.units_m * w.tiles_n, rem = tiles % slots;
+    w.full = rem <= slots / 2 ? tiles - rem : tiles;
     w.items = w.full + 2 * (tiles - w.full);
-    const int grid = w.items < di.num_sms ? w.items : di.num_sms;
-    return launch_pdl(fp8_gemm_kernel<BF16>, grid, kThreads, kGemmSmem, stream, am, bm, om, sa, sb, out, M, N, w,
-                      tma_out);
+    const int grid = (w.items < slots ? w.items : slots) * (PAIR ? 2 : 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = static_cast<unsigned>(grid);
+    cfg.blockDim = kGThreads;
+    cfg.dynamicSmemBytes = kGemmSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BF16, PAIR>, am, bm, om, sa, sb, out, M, N, w, tma_out);
 }
 
 template <bool BF16>
 cudaError_t run_gemm(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
                      void *out, const DeviceInfo &di, cudaStream_t stream)
 {
-    return few_tiles(M, N, di.num_sms) ? run_split<BF16>(a, sa, b, sb, M, N, K, out, di, stream)
-                                       : run_tiles<BF16>(a, sa, b, sb, M, N, K, out, di, stream);
+    if (few_tiles(M, N, di.num_sms))
+        return run_split<BF16>(a, sa, b, sb, M, N, K, out, di, stream);
+    return use_pairs(M, N, di.num_sms) ? run_tiles<BF16, true>(a, sa, b, sb, M, N, K, out, di, stream)
+                                       : run_tiles<BF16, false>(a, sa, b, sb, M, N, K, out, di, stream);
 }
 
 }  // namespace
