@@ -15,21 +15,26 @@
 //
 // fp8_gemm_kernel (many tiles): persistent, one CTA per SM, tiles of 128 x
 //   256.  Warp 0 streams 128-byte-wide pieces of A and B by TMA through an
-//   mbarrier ring, and the scales through a ring of their own; one thread of
-//   warp 1 copies scales to tensor memory and issues the MMAs; warp 2 spreads
-//   tile scales; warps 3-10 store finished tiles.  The CTAs of a cluster of
-//   two take tiles one above the other: each loads half of their common B and
-//   multicasts it to both, since the path from L2 bounds the kernel (alone, a
-//   CTA needs 48 KB for 0.27 us of MMAs, 27 TB/s over 152 SMs, and 22 were
-//   measured).  Tensor memory holds the scales (two sets of 12 columns) and
-//   two accumulators, which overlap by 32 columns: the epilogue drains these
-//   first, and the next tile's MMAs start while it works on the rest.  Where
-//   the last round of tiles would leave more than half of the SMs idle, its
-//   tiles are cut in two (128 x 128).  An fp32 result over more than 1536
-//   values is summed in pieces: the tensor core's accumulator truncates,
-//   which biases long coherent sums (measured on a weight gradient over 4096
-//   tokens: 1.9e-6 of its norm in one piece, where an fp32 matrix product has
-//   3.7e-7), so each piece is added in the epilogue's registers, rounded.
+//   mbarrier ring; warp 2 fetches the scales through a ring of their own, two
+//   groups ahead, and spreads tile scales; warp 1 copies scales to tensor
+//   memory and issues the MMAs; warps 3-10 store finished tiles.  Tensor
+//   memory holds the scales (two sets of 12 columns) and two accumulators,
+//   which overlap by 32 columns: the epilogue drains these first, and the
+//   next tile's MMAs start while it works on the rest.  Where the last round
+//   of tiles would leave more than half of the SMs idle, its tiles are cut in
+//   two (128 x 128).
+//   What bounds it: the MMAs alone run at 512 clocks for a block of 128 (the
+//   peak), the loads at 192 KB in flight per SM and the latency of L2 under
+//   load (8192 x 4096 x 16384 of zeros at 2070 MHz: four stages 299 us, three
+//   352, two 559; the MMAs alone would take 222), and with real operands the
+//   power limit (1.75 GHz).  Sharing B between two CTAs, by multicast or as a
+//   cta_group::2 pair with six stages of 32 KB, took the same time or a
+//   little longer (88 against 86 us at 8192 x 4096 x 4096).
+//   An fp32 result over more than 1536 values is summed in pieces: the tensor
+//   core's accumulator truncates, which biases long coherent sums (measured
+//   on a weight gradient over 4096 tokens: 1.9e-6 of its norm in one piece,
+//   where an fp32 matrix product has 3.7e-7; 6.2e-7 in pieces), so each piece
+//   is added in the epilogue's registers, rounded.
 //
 // fp8_gemm_split_kernel (few tiles: single tokens to small batches): the
 //   roles of the operands are exchanged - B's rows (weights) take the 128
@@ -87,27 +92,30 @@ struct Scales {
 // Shared-memory layout: a ring of `stages` slots for operand pieces of 128
 // and `bn` rows, `extra` bytes, a ring of scale slots of `sf_bytes` (128 A or
 // lane-side rows, then the others), barriers.
-constexpr int kScaleSlots = 3;
+constexpr int kScaleSlots = 4;
 struct Ring {
     uint32_t base, stage_bytes, scales, sf_bytes, extra, bars;
     int stages;
     __device__ __forceinline__ uint32_t a(int s) const { return base + s * stage_bytes; }
     __device__ __forceinline__ uint32_t b(int s) const { return base + s * stage_bytes + kTileA; }
     __device__ __forceinline__ uint32_t sf(int s) const { return scales + s * sf_bytes; }
-    __device__ __forceinline__ uint32_t full(int s) const { return bars + 8 * s; }
-    __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8 * (kMaxStages + s); }
-    __device__ __forceinline__ uint32_t sf_full(int s) const { return bars + 8 * (2 * kMaxStages + s); }
-    __device__ __forceinline__ uint32_t sf_empty(int s) const { return bars + 8 * (2 * kMaxStages + kScaleSlots + s); }
-    __device__ __forceinline__ uint32_t acc_full(int a) const { return bars + 8 * (2 * kMaxStages + 6 + a); }
-    __device__ __forceinline__ uint32_t acc_free(int a) const { return bars + 8 * (2 * kMaxStages + 8 + a); }
-    __device__ __forceinline__ uint32_t drain() const { return bars + 8 * (2 * kMaxStages + 10); }
-    __device__ __forceinline__ uint32_t tmem_slot() const { return bars + 8 * (2 * kMaxStages + 11); }
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
+    __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar(kMaxStages + s); }
+    // scales: landed / ready / copied
+    __device__ __forceinline__ uint32_t sf_load(int s) const { return bar(2 * kMaxStages + s); }
+    __device__ __forceinline__ uint32_t sf_full(int s) const { return bar(2 * kMaxStages + kScaleSlots + s); }
+    __device__ __forceinline__ uint32_t sf_empty(int s) const { return bar(2 * kMaxStages + 2 * kScaleSlots + s); }
+    __device__ __forceinline__ uint32_t acc_full(int a) const { return bar(2 * kMaxStages + 3 * kScaleSlots + a); }
+    __device__ __forceinline__ uint32_t acc_free(int a) const { return bar(2 * kMaxStages + 3 * kScaleSlots + 2 + a); }
+    __device__ __forceinline__ uint32_t drain() const { return bar(2 * kMaxStages + 3 * kScaleSlots + 4); }
+    __device__ __forceinline__ uint32_t tmem_slot() const { return bar(2 * kMaxStages + 3 * kScaleSlots + 5); }
 };
-static_assert(kScaleSlots == 3, "barrier numbers above");
-constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 11) + 16;
+constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 3 * kScaleSlots + 5) + 16;
 
 __host__ __device__ constexpr uint32_t stage_bytes_of(int bn) { return kTileA + 128u * bn; }
 
+// bn: the operand rows beside A's 128 that a stage of this CTA holds.
 __device__ __forceinline__ Ring make_ring(const uint8_t *smem, int bn, int stages, uint32_t sf_bytes, uint32_t extra)
 {
     Ring r;
@@ -121,16 +129,16 @@ __device__ __forceinline__ Ring make_ring(const uint8_t *smem, int bn, int stage
     return r;
 }
 
-// (one thread)  tile_scales: a warp of its own also arrives on a scale slot;
-// readers: the CTAs whose MMAs read what a stage's loads bring.
-__device__ __forceinline__ void init_barriers(const Ring &r, bool tile_scales, int readers, int epilogue_warps)
+// (one thread)  sf_arrivals: the arrivals that make a scale slot ready.
+__device__ __forceinline__ void init_barriers(const Ring &r, int sf_arrivals, int epilogue_warps)
 {
     for (int s = 0; s < r.stages; ++s) {
         mbar_init(r.full(s), 1);
-        mbar_init(r.empty(s), readers);
+        mbar_init(r.empty(s), 1);
     }
     for (int s = 0; s < kScaleSlots; ++s) {
-        mbar_init(r.sf_full(s), tile_scales ? 2 : 1);
+        mbar_init(r.sf_load(s), 1);
+        mbar_init(r.sf_full(s), sf_arrivals);
         mbar_init(r.sf_empty(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -164,25 +172,19 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // A new group of four blocks starts at kb (or the contraction's range does).
 __device__ __forceinline__ bool starts_group(int kb, int kb0) { return (kb & 3) == 0 || kb == kb0; }
 
-// Four MMAs of 32 values each: one block of the contraction, whose scales
-// are byte kb % 4 of their words.  PAIR: the slot is freed in both CTAs.
-template <bool PAIR>
+// (the elected thread)  Four MMAs of 32 values each: one block of the
+// contraction, whose scales are byte kb % 4 of their words.
 __device__ __forceinline__ void mma_block(const Ring &r, int s, uint32_t d, uint32_t sfa, uint32_t sfb, uint32_t idesc,
-                                          int kb, bool accumulate)
+                                          int kb, uint32_t accumulate)
 {
-    const uint64_t ad = smem_desc_k_sw128(r.a(s)), bd = smem_desc_k_sw128(r.b(s));
-    const uint32_t id = idesc_scale_byte(idesc, kb & 3);
+    const uint32_t a = smem_desc_lo(r.a(s)), b = smem_desc_lo(r.b(s)), id = idesc_scale_byte(idesc, kb & 3);
 #pragma unroll
     for (int k = 0; k < 4; ++k)  // 32 codes = 32 bytes = 2 descriptor units
-        mma_mxf8(d, ad + 2 * k, bd + 2 * k, id, sfa, sfb, accumulate || k != 0);
-    // the slot is free once these have read it
-    if (PAIR)
-        mma_commit_cluster(r.empty(s), 3);
-    else
-        mma_commit(r.empty(s));
+        mma_mxf8(d, a + 2 * k, b + 2 * k, id, sfa, sfb, k == 0 ? accumulate : 1u);
+    mma_commit(r.empty(s));  // the slot is free once these have read it
 }
 
-// (warp 6)  Tile scales of blocks 4 g .. 4 g + 3 for row tiles t and t + 1:
+// (one warp)  Tile scales of blocks 4 g .. 4 g + 3 for row tiles t and t + 1:
 // lanes 0-3 hold tile t's bytes, lanes 4-7 tile t + 1's.
 __device__ __forceinline__ uint32_t load_tile_scales(const Scales &s, int g, int64_t t, int KB, int lane)
 {
@@ -218,35 +220,20 @@ constexpr int kPieceBlocks = 12;           // fp32: most blocks summed in tensor
 constexpr uint32_t kGemmSmem = 1024 + kStages * stage_bytes_of(kBN) + kStaging + kScaleSlots * 1536 + kBarBytes;
 static_assert(kGemmSmem <= kSmemLimit, "shared memory per CTA");
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// All threads of the cluster's CTAs meet (barrier.cluster is defined below
-// for the split kernel as well).
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The work of the grid, in units of one CTA's or (PAIR) two CTAs' tiles, one
-// above the other: `full` whole ones, then the others as two halves each;
-// every item in `segs` pieces of `seg_kb` blocks.
+// The work of the grid: `full` whole tiles, then the others as two halves
+// each; every item in `segs` pieces of `seg_kb` blocks.
 struct Work {
-    int units_m, tiles_n, full, items, segs, seg_kb, KB, group;
+    int tiles_m, tiles_n, full, items, segs, seg_kb, KB;
     int64_t N;
-    // Item idx: its row unit, its first column, and its width (256 or 128).
+    // Item idx: its row tile, its first column, and its width (256 or 128).
     // False for the second half of a tile that has none.
-    __device__ __forceinline__ bool at(int idx, int &um, int64_t &n0, int &bn) const
+    __device__ __forceinline__ bool at(int idx, int &tm, int64_t &n0, int &bn) const
     {
         const int t = idx < full ? idx : full + (idx - full) / 2;
-        const int per = group * tiles_n, g = t / per, r = t - g * per;
-        const int left = units_m - g * group, gm = left < group ? left : group;
+        const int per = kGroupM * tiles_n, g = t / per, r = t - g * per;
+        const int left = tiles_m - g * kGroupM, gm = left < kGroupM ? left : kGroupM;
         const int tn = r / gm;
-        um = g * group + (r - tn * gm);
+        tm = g * kGroupM + (r - tn * gm);
         n0 = static_cast<int64_t>(tn) * kBN;
         bn = kBN;
         if (idx >= full) {
@@ -262,6 +249,31 @@ struct Work {
     {
         const int e = (seg + 1) * seg_kb;
         return e < KB ? e : KB;
+    }
+};
+
+// The groups of four blocks of a CTA's items, in order.
+struct ScaleWalk {
+    const Work &w;
+    int idx, step, g, tm, bn;
+    int64_t n0;
+    bool more;
+    __device__ __forceinline__ ScaleWalk(const Work &work, int idx0, int by) : w(work), idx(idx0 - by), step(by)
+    {
+        item();
+    }
+    __device__ __forceinline__ void item()
+    {
+        do {
+            idx += step;
+            more = idx < w.items;
+        } while (more && !w.at(idx, tm, n0, bn));
+        g = 0;
+    }
+    __device__ __forceinline__ void next()  // pieces start at whole groups: every group once
+    {
+        if (4 * ++g >= w.KB)
+            item();
     }
 };
 
@@ -320,9 +332,7 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&w)[16], uint32_t st
     }
 }
 
-// PAIR: the two CTAs of a cluster work on the same columns, this one on row
-// tile 2 um + rank.
-template <bool BF16, bool PAIR>
+template <bool BF16>
 __global__ void __launch_bounds__(kGThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                     const __grid_constant__ CUtensorMap o_map, Scales sa, Scales sb, void *__restrict__ out, int64_t M,
@@ -330,13 +340,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
 {
     extern __shared__ uint8_t smem_raw[];
     const Ring r = make_ring(smem_raw, kBN, kStages, 1536, kStaging);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int groups = (work.KB + 3) / 4;  // scale pieces per row tile
-    const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
-    const int idx0 = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+    const int step = gridDim.x;
 
     if (threadIdx.x == 0)
-        init_barriers(r, sb.tiles, PAIR ? 2 : 1, 8);
+        init_barriers(r, 1, 8);
     if (warp == 1) {
         tmem_alloc(r.tmem_slot(), 512);
         tmem_relinquish_alloc_permit();
@@ -347,160 +356,159 @@ __global__ void __launch_bounds__(kGThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (PAIR)
-        cluster_sync();  // the other CTA's barriers are ready
     const uint32_t tmem = lds32(r.tmem_slot());
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp == 0) {  // the whole warp, so that operands stay uniform; one thread issues
+        if (elect_one()) {
             tma_prefetch_map(&a_map);
             tma_prefetch_map(&b_map);
-            Slot p, f;
-            int64_t issued = 0, scales = 0;
-            bool ok = true;
-            for (int idx = idx0; ok && idx < work.items; idx += step) {
-                int um, bn;
-                int64_t n0;
-                if (!work.at(idx, um, n0, bn))
-                    continue;
-                const int tm = PAIR ? 2 * um + rank : um;
-                // (a row tile past the last one has no scales: any do)
-                const uint8_t *sap = sa.p + static_cast<int64_t>(tm < sa.row_tiles ? tm : 0) * groups * 512;
-                for (int seg = 0; ok && seg < work.segs; ++seg) {
-                    const int kb0 = work.first(seg), kb1 = work.last(seg);
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        if (starts_group(kb, kb0)) {
-                            if (!mbar_wait(r.sf_empty(f.s), f.phase ^ 1)) {
-                                report_timeout();
-                                ok = false;
-                                break;
-                            }
-                            const int pieces = bn / 128;
-                            mbar_arrive_expect_tx(r.sf_full(f.s), sb.tiles ? 512 : 512 + 512 * pieces);
-                            bulk_load(r.sf(f.s), sap + (kb >> 2) * 512, 512, r.sf_full(f.s));
-                            if (!sb.tiles)
-                                for (int i = 0; i < pieces; ++i)
-                                    bulk_load(r.sf(f.s) + 512 + 512 * i,
-                                              sb.p + ((n0 / 128 + i) * groups + (kb >> 2)) * 512, 512, r.sf_full(f.s));
-                            f.next(kScaleSlots);
-                            ++scales;
-                        }
-                        if (!mbar_wait(r.empty(p.s), p.phase ^ 1)) {
-                            report_timeout();
+        }
+        __syncwarp();
+        Slot p;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int idx = blockIdx.x; ok && idx < work.items; idx += step) {
+            int tm, bn;
+            int64_t n0;
+            if (!work.at(idx, tm, n0, bn))
+                continue;
+            const int32_t mc = tm * 128, nc = static_cast<int32_t>(n0);
+            for (int kb = 0; kb < work.KB; ++kb) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.empty(p.s), p.phase ^ 1))) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const int32_t kc = kb * 128;
+                    mbar_arrive_expect_tx(r.full(p.s), stage_bytes_of(bn));
+                    tma_load_2d(r.a(p.s), &a_map, kc, mc, r.full(p.s));
+                    tma_load_2d(r.b(p.s), &b_map, kc, nc, r.full(p.s));
+                    if (bn > 128)
+                        tma_load_2d(r.b(p.s) + kTileA, &b_map, kc, nc + 128, r.full(p.s));
+                }
+                __syncwarp();
+                p.next(kStages);
+                ++issued;
+            }
+        }
+        if (!ok && lane == 0)
+            report_timeout();
+        // leave no load in flight into this CTA's shared memory
+        for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            mbar_wait(r.full(static_cast<int>(i % kStages)), static_cast<uint32_t>(i / kStages) & 1);
+    } else if (warp == 1) {  // likewise
+        Slot p, f;
+        int i = 0;  // accumulations done: items times segments
+        uint32_t set = 0, sfa = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity)); };
+        for (int idx = blockIdx.x; ok && idx < work.items; idx += step) {
+            int tm, bn;
+            int64_t n0;
+            if (!work.at(idx, tm, n0, bn))
+                continue;
+            const uint32_t idesc = idesc_mxf8(bn);
+            for (int seg = 0; ok && seg < work.segs; ++seg, ++i) {
+                // every epilogue warp has drained the columns this
+                // accumulator shares with accumulation i - 1 and, before
+                // that, all of i - 2, this accumulator's last
+                if (i > 0 && !wait(r.acc_free((i - 1) & 1), ((i - 1) >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + (i & 1 ? kAcc1 : 0u);
+                const int kb0 = work.first(seg), kb1 = work.last(seg);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (starts_group(kb, kb0)) {
+                        if (!wait(r.sf_full(f.s), f.phase)) {
                             ok = false;
                             break;
                         }
-                        const int32_t kc = kb * 128, nc = static_cast<int32_t>(n0);
-                        mbar_arrive_expect_tx(r.full(p.s), stage_bytes_of(bn));
-                        tma_load_2d(r.a(p.s), &a_map, kc, tm * 128, r.full(p.s));
-                        if (bn > 128 && PAIR) {  // this CTA's half of B, for both
-                            tma_load_2d_cluster(r.b(p.s) + rank * kTileA, &b_map, kc, nc + 128 * rank, r.full(p.s), 3);
-                        } else {
-                            tma_load_2d(r.b(p.s), &b_map, kc, nc, r.full(p.s));
-                            if (bn > 128)
-                                tma_load_2d(r.b(p.s) + kTileA, &b_map, kc, nc + 128, r.full(p.s));
-                        }
-                        p.next(kStages);
-                        ++issued;
-                    }
-                }
-            }
-            // leave no load in flight into this CTA's shared memory
-            for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                mbar_wait(r.full(static_cast<int>(i % kStages)), static_cast<uint32_t>(i / kStages) & 1);
-            for (int64_t i = scales > kScaleSlots ? scales - kScaleSlots : 0; i < scales; ++i)
-                mbar_wait(r.sf_full(static_cast<int>(i % kScaleSlots)), static_cast<uint32_t>(i / kScaleSlots) & 1);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            Slot p, f;
-            int i = 0;  // accumulations done: items times segments
-            uint32_t set = 0, sfa = 0;
-            bool ok = true;
-            for (int idx = idx0; ok && idx < work.items; idx += step) {
-                int um, bn;
-                int64_t n0;
-                if (!work.at(idx, um, n0, bn))
-                    continue;
-                const uint32_t idesc = idesc_mxf8(bn);
-                for (int seg = 0; ok && seg < work.segs; ++seg, ++i) {
-                    // every epilogue warp has drained the columns this
-                    // accumulator shares with accumulation i - 1 and, before
-                    // that, all of i - 2, this accumulator's last
-                    if (i > 0 && !mbar_wait(r.acc_free((i - 1) & 1), ((i - 1) >> 1) & 1)) {
-                        report_timeout();
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t d = tmem + (i & 1 ? kAcc1 : 0u);
-                    const int kb0 = work.first(seg), kb1 = work.last(seg);
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        if (starts_group(kb, kb0)) {
-                            if (!mbar_wait(r.sf_full(f.s), f.phase)) {
-                                report_timeout();
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after_sync();
-                            sfa = tmem + kSfColumn + 12 * set;
-                            set ^= 1;
+                        tc_fence_after_sync();
+                        sfa = tmem + kSfColumn + 12 * set;
+                        set ^= 1;
+                        if (elect_one()) {
                             tmem_copy_scales(sfa, r.sf(f.s));
                             tmem_copy_scales(sfa + 4, r.sf(f.s) + 512);
                             if (bn > 128)
                                 tmem_copy_scales(sfa + 8, r.sf(f.s) + 1024);
                             mma_commit(r.sf_empty(f.s));
-                            f.next(kScaleSlots);
                         }
-                        if (!mbar_wait(r.full(p.s), p.phase)) {
-                            report_timeout();
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after_sync();
-                        mma_block<PAIR>(r, p.s, d, sfa, sfa + 4, idesc, kb, kb != kb0);
-                        p.next(kStages);
+                        __syncwarp();
+                        f.next(kScaleSlots);
                     }
-                    if (ok)
-                        mma_commit(r.acc_full(i & 1));
+                    if (!wait(r.full(p.s), p.phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    if (elect_one())
+                        mma_block(r, p.s, d, sfa, sfa + 4, idesc, kb, kb != kb0);
+                    __syncwarp();
+                    p.next(kStages);
                 }
-            }
-            if (!ok) {  // tensor memory is freed below: wait for what was issued
-                mma_commit(r.drain());
-                mbar_wait(r.drain(), 0);
+                if (ok && elect_one())
+                    mma_commit(r.acc_full(i & 1));
+                __syncwarp();
             }
         }
-    } else if (warp == 2) {
-        if (sb.tiles) {
-            Slot f;
-            bool ok = true;
-            for (int idx = idx0; ok && idx < work.items; idx += step) {
-                int um, bn;
-                int64_t n0;
-                if (!work.at(idx, um, n0, bn))
-                    continue;
-                for (int seg = 0; ok && seg < work.segs; ++seg) {
-                    const int g1 = (work.last(seg) + 3) / 4;
-                    int g = work.first(seg) / 4;
-                    uint32_t v = load_tile_scales(sb, g, n0 / 128, work.KB, lane);
-                    for (; g < g1; ++g) {
-                        const uint32_t nv = load_tile_scales(sb, g + 1, n0 / 128, work.KB, lane);
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.sf_empty(f.s), f.phase ^ 1))) {
-                            if (lane == 0)
-                                report_timeout();
-                            ok = false;
-                            break;
-                        }
-                        spread_tile_scales(v, r.sf(f.s) + 512, bn / 128, lane);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(r.sf_full(f.s));
-                        f.next(kScaleSlots);
-                        v = nv;
-                    }
-                }
+        if (!ok) {  // tensor memory is freed below: wait for what was issued
+            if (elect_one()) {
+                report_timeout();
+                mma_commit(r.drain());
             }
+            __syncwarp();
+            mbar_wait(r.drain(), 0);
+        }
+    } else if (warp == 2) {
+        // Scales, two groups ahead of the one being handed on: their loads
+        // run on their own, not behind the stages'.
+        ScaleWalk ahead(work, blockIdx.x, step), now(work, blockIdx.x, step);
+        Slot fa, f;
+        bool ok = true;
+        auto issue = [&]() {
+            if (!ahead.more)
+                return true;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.sf_empty(fa.s), fa.phase ^ 1)))
+                return false;
+            if (elect_one()) {
+                const int pieces = sb.tiles ? 0 : ahead.bn / 128;
+                mbar_arrive_expect_tx(r.sf_load(fa.s), 512 + 512 * pieces);
+                bulk_load(r.sf(fa.s), sa.p + (static_cast<int64_t>(ahead.tm) * groups + ahead.g) * 512, 512,
+                          r.sf_load(fa.s));
+                for (int i = 0; i < pieces; ++i)
+                    bulk_load(r.sf(fa.s) + 512 + 512 * i, sb.p + ((ahead.n0 / 128 + i) * groups + ahead.g) * 512, 512,
+                              r.sf_load(fa.s));
+            }
+            __syncwarp();
+            fa.next(kScaleSlots);
+            ahead.next();
+            return true;
+        };
+        ok = issue() && issue();
+        uint32_t v = now.more && sb.tiles ? load_tile_scales(sb, now.g, now.n0 / 128, work.KB, lane) : 0u;
+        while (ok && now.more) {
+            const int pieces = now.bn / 128;
+            now.next();
+            const uint32_t nv = now.more && sb.tiles ? load_tile_scales(sb, now.g, now.n0 / 128, work.KB, lane) : 0u;
+            if (!(ok = issue() && __all_sync(0xFFFFFFFFu, mbar_wait(r.sf_load(f.s), f.phase))))
+                break;
+            if (sb.tiles)
+                spread_tile_scales(v, r.sf(f.s) + 512, pieces, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(r.sf_full(f.s));
+            f.next(kScaleSlots);
+            v = nv;
+        }
+        if (!ok) {
+            if (lane == 0)
+                report_timeout();
+            // leave none of them in flight
+            for (; f.s != fa.s || f.phase != fa.phase; f.next(kScaleSlots))
+                mbar_wait(r.sf_load(f.s), f.phase);
         }
     } else {
         // warps 3-6 take columns 0 .. 127 of a tile, upwards, 7-10 columns 255
@@ -510,13 +518,13 @@ __global__ void __launch_bounds__(kGThreads, 1)
         const uint32_t staging = r.extra + 2048 * (warp - 3);
         int i = 0;
         bool ok = true;
-        for (int idx = idx0; ok && idx < work.items; idx += step) {
-            int um, bn;
+        for (int idx = blockIdx.x; ok && idx < work.items; idx += step) {
+            int tm, bn;
             int64_t n0;
-            if (!work.at(idx, um, n0, bn))
+            if (!work.at(idx, tm, n0, bn))
                 continue;
             const bool mine = 128 * half < bn;
-            const int64_t row0 = static_cast<int64_t>(PAIR ? 2 * um + rank : um) * 128 + 32 * q;
+            const int64_t row0 = static_cast<int64_t>(tm) * 128 + 32 * q;
             const int64_t col0 = n0 + 128 * half;
             auto wait_full = [&]() {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.acc_full(i & 1), (i >> 1) & 1))) {
@@ -571,14 +579,14 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     }
                     const uint32_t tq = columns();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float x[16];
-                        tmem_load_16(tq + 16 * (half ? 7 - j : j), x);
-                        if (j == 1)
+                    for (int j = 0; j < 16; ++j) {
+                        float x[8];
+                        tmem_load_8(tq + 16 * (half ? 7 - j / 2 : j / 2) + 8 * (j & 1), x);
+                        if (j == 3)
                             free_shared();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            sum[j][k] += x[k];
+                        for (int k = 0; k < 8; ++k)
+                            sum[j / 2][8 * (j & 1) + k] += x[k];
                     }
                 }
                 if (!ok)
@@ -599,11 +607,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             bulk_wait_all();
     }
     tc_fence_before_sync();
-    __syncwarp();
-    if (PAIR)
-        cluster_sync();  // no CTA leaves while the other's loads or arrivals may still reach it
-    else
-        __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
@@ -611,6 +615,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
 }
 
 // ------------------------------------------------------------- few tiles --
+
+// All threads of the cluster's CTAs meet.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // The address of CTA `rank`'s shared memory at this CTA's address `addr`.
 __device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank)
@@ -654,7 +664,7 @@ __global__ void __launch_bounds__(kThreads)
 {
     extern __shared__ uint8_t smem_raw[];
     const Ring r = make_ring(smem_raw, BN, stages, 1024, 0);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = blockIdx.x % split, tile = blockIdx.x / split;
     const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
     const int64_t n0 = static_cast<int64_t>(tn) * 128, m0 = static_cast<int64_t>(tm) * 128;
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(kThreads)
     const int groups = (KB + 3) / 4;
 
     if (threadIdx.x == 0)
-        init_barriers(r, sb.tiles, 1, 4);
+        init_barriers(r, sb.tiles ? 2 : 1, 4);
     if (warp == 1) {
         tmem_alloc(r.tmem_slot(), kSplitTmem);
         tmem_relinquish_alloc_permit();
@@ -676,73 +686,86 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t tmem = lds32(r.tmem_slot());
 
     if (warp == 0) {
-        if (lane == 0) {
-            Slot p, f;
-            int issued = 0, scales = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (starts_group(kb, kb0)) {
-                    if (!mbar_wait(r.sf_empty(f.s), f.phase ^ 1)) {
-                        report_timeout();
-                        break;
-                    }
+        Slot p, f;
+        int issued = 0, scales = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (starts_group(kb, kb0)) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.sf_empty(f.s), f.phase ^ 1))) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
                     mbar_arrive_expect_tx(r.sf_full(f.s), sb.tiles ? 512 : 1024);
                     bulk_load(r.sf(f.s) + 512, sa.p + (static_cast<int64_t>(tm) * groups + (kb >> 2)) * 512, 512,
                               r.sf_full(f.s));
                     if (!sb.tiles)
                         bulk_load(r.sf(f.s), sb.p + (static_cast<int64_t>(tn) * groups + (kb >> 2)) * 512, 512,
                                   r.sf_full(f.s));
-                    f.next(kScaleSlots);
-                    ++scales;
                 }
-                if (!mbar_wait(r.empty(p.s), p.phase ^ 1)) {
-                    report_timeout();
-                    break;
-                }
+                __syncwarp();
+                f.next(kScaleSlots);
+                ++scales;
+            }
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.empty(p.s), p.phase ^ 1))) {
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
                 mbar_arrive_expect_tx(r.full(p.s), r.stage_bytes);
                 tma_load_2d(r.a(p.s), &b_map, kb * 128, static_cast<int32_t>(n0), r.full(p.s));
                 tma_load_2d(r.b(p.s), &a_map, kb * 128, static_cast<int32_t>(m0), r.full(p.s));
-                p.next(stages);
-                ++issued;
             }
-            for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-                mbar_wait(r.full(i % stages), static_cast<uint32_t>(i / stages) & 1);
-            for (int i = scales > kScaleSlots ? scales - kScaleSlots : 0; i < scales; ++i)
-                mbar_wait(r.sf_full(i % kScaleSlots), static_cast<uint32_t>(i / kScaleSlots) & 1);
+            __syncwarp();
+            p.next(stages);
+            ++issued;
         }
+        if (!ok && lane == 0)
+            report_timeout();
+        for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+            mbar_wait(r.full(i % stages), static_cast<uint32_t>(i / stages) & 1);
+        for (int i = scales > kScaleSlots ? scales - kScaleSlots : 0; i < scales; ++i)
+            mbar_wait(r.sf_full(i % kScaleSlots), static_cast<uint32_t>(i / kScaleSlots) & 1);
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_mxf8(BN);
-            Slot p, f;
-            uint32_t set = 0, sf = 0;
-            bool ok = true;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (starts_group(kb, kb0)) {
-                    if (!mbar_wait(r.sf_full(f.s), f.phase)) {
-                        report_timeout();
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    sf = tmem + 128 + 8 * set;
-                    set ^= 1;
-                    tmem_copy_scales(sf, r.sf(f.s));
-                    tmem_copy_scales(sf + 4, r.sf(f.s) + 512);
-                    mma_commit(r.sf_empty(f.s));
-                    f.next(kScaleSlots);
-                }
-                if (!mbar_wait(r.full(p.s), p.phase)) {
-                    report_timeout();
+        const uint32_t idesc = idesc_mxf8(BN);
+        Slot p, f;
+        uint32_t set = 0, sf = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (starts_group(kb, kb0)) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.sf_full(f.s), f.phase))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                mma_block<false>(r, p.s, tmem, sf, sf + 4, idesc, kb, kb != kb0);
-                p.next(stages);
+                sf = tmem + 128 + 8 * set;
+                set ^= 1;
+                if (elect_one()) {
+                    tmem_copy_scales(sf, r.sf(f.s));
+                    tmem_copy_scales(sf + 4, r.sf(f.s) + 512);
+                    mma_commit(r.sf_empty(f.s));
+                }
+                __syncwarp();
+                f.next(kScaleSlots);
             }
-            mma_commit(ok ? r.acc_full(0) : r.drain());
-            if (!ok)
-                mbar_wait(r.drain(), 0);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.full(p.s), p.phase))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            if (elect_one())
+                mma_block(r, p.s, tmem, sf, sf + 4, idesc, kb, kb != kb0);
+            __syncwarp();
+            p.next(stages);
         }
+        if (elect_one()) {
+            if (!ok)
+                report_timeout();
+            mma_commit(ok ? r.acc_full(0) : r.drain());
+        }
+        __syncwarp();
+        if (!ok)
+            mbar_wait(r.drain(), 0);
     } else if (warp == 6) {
         if (sb.tiles) {
             Slot f;
@@ -869,11 +892,20 @@ struct Plan {
     int bn, split;
 };
 
-// Few tiles: fewer than half the SMs would get a 128 x 256 one.
-bool few_tiles(int64_t M, int64_t N, int sms) { return ceil_div(M, 128) * ceil_div(N, kBN) < sms / 2; }
-
-// Pairs of row tiles where they leave no CTA without one.
-bool use_pairs(int64_t M, int64_t N, int sms) { return ceil_div(M, 128) % 2 == 0 || ceil_div(M, 128) >= 9; }
+// Which kernel: the split one where the other would leave more than half of
+// the SMs without a tile and either there are at most 64 tokens and the
+// contraction is at least 12 blocks long, or it is at least 48 blocks long and
+// a quarter of the SMs cover the 128 x 128 tiles.  Measured, split against
+// tiles: 37 x 10240 x 2560 8.9 and 12.1 us, 64 x 4096 x 4096 9.3 and 10.9, 64 x
+// 1024 x 1024 6.5 and 5.7, 128 x 4096 x 4096 13.2 and 11.3, 512 x 4096 x 4096
+// 16.3 and 11.7, 300 x 300 x 8192 10.6 and 20.8.
+bool use_split(int64_t M, int64_t N, int64_t K, int sms)
+{
+    const int64_t KB = ceil_div(K, 128);
+    if (ceil_div(M, 128) * ceil_div(N, kBN) >= sms / 2)
+        return false;
+    return (M <= 64 && KB >= 12) || (KB >= 48 && ceil_div(M, 128) * ceil_div(N, 128) * 4 <= sms);
+}
 
 template <bool BF16>
 cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
@@ -920,7 +952,7 @@ cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
                               split);
 }
 
-template <bool BF16, bool PAIR>
+template <bool BF16>
 cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
                       void *out, const DeviceInfo &di, cudaStream_t stream)
 {
@@ -929,7 +961,7 @@ cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
         encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b), K, N, K, 128, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16, PAIR>, kGemmSmem, di.device, set);
+    cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16>, kGemmSmem, di.device, set);
     if (e != cudaSuccess)
         return e;
     const uint64_t row_bytes = static_cast<uint64_t>(N) * (BF16 ? 2 : 4);
@@ -941,44 +973,27 @@ cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
     Work w;
     w.KB = static_cast<int>(ceil_div(K, 128));
     w.N = N;
-    w.units_m = static_cast<int>(ceil_div(M, PAIR ? 256 : 128));
+    w.tiles_m = static_cast<int>(ceil_div(M, 128));
     w.tiles_n = static_cast<int>(ceil_div(N, kBN));
-    w.group = PAIR ? kGroupM / 2 : kGroupM;
     // fp32: pieces of whole scale groups
     w.segs = BF16 ? 1 : static_cast<int>(ceil_div(w.KB, kPieceBlocks));
     w.seg_kb = static_cast<int>(ceil_div(ceil_div(w.KB, w.segs), 4) * 4);
     w.segs = static_cast<int>(ceil_div(w.KB, w.seg_kb));
     // a last round that fills at most half of the SMs goes in halves
-    const int slots = PAIR ? di.num_sms / 2 : di.num_sms;
-    const int tiles = w.units_m * w.tiles_n, rem = tiles % slots;
-    w.full = rem <= slots / 2 ? tiles - rem : tiles;
+    const int tiles = w.tiles_m * w.tiles_n, rem = tiles % di.num_sms;
+    w.full = rem <= di.num_sms / 2 ? tiles - rem : tiles;
     w.items = w.full + 2 * (tiles - w.full);
-    const int grid = (w.items < slots ? w.items : slots) * (PAIR ? 2 : 1);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = static_cast<unsigned>(grid);
-    cfg.blockDim = kGThreads;
-    cfg.dynamicSmemBytes = kGemmSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = PAIR ? 2 : 1;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BF16, PAIR>, am, bm, om, sa, sb, out, M, N, w, tma_out);
+    const int grid = w.items < di.num_sms ? w.items : di.num_sms;
+    return launch_pdl(fp8_gemm_kernel<BF16>, dim3(grid), dim3(kGThreads), kGemmSmem, stream, am, bm, om, sa, sb, out, M,
+                      N, w, tma_out);
 }
 
 template <bool BF16>
 cudaError_t run_gemm(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
                      void *out, const DeviceInfo &di, cudaStream_t stream)
 {
-    if (few_tiles(M, N, di.num_sms))
-        return run_split<BF16>(a, sa, b, sb, M, N, K, out, di, stream);
-    return use_pairs(M, N, di.num_sms) ? run_tiles<BF16, true>(a, sa, b, sb, M, N, K, out, di, stream)
-                                       : run_tiles<BF16, false>(a, sa, b, sb, M, N, K, out, di, stream);
+    return use_split(M, N, K, di.num_sms) ? run_split<BF16>(a, sa, b, sb, M, N, K, out, di, stream)
+                                          : run_tiles<BF16>(a, sa, b, sb, M, N, K, out, di, stream);
 }
 
 }  // namespace

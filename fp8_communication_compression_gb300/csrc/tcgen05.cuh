@@ -104,19 +104,39 @@ __host__ __device__ constexpr uint32_t idesc_scale_byte(uint32_t idesc, int i)
     return idesc | (static_cast<uint32_t>(i) << 4) | (static_cast<uint32_t>(i) << 29);
 }
 
+// One lane of the warp (the same one each time), chosen in a way that keeps
+// what it guards warp-uniform: the tensor-core instructions below take their
+// operands from uniform registers, and in a branch on the lane index every one
+// of them has to be moved there first.  Executed by the whole warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+// The low word of smem_desc_k_sw128's descriptor; the high word is the same
+// for every address.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t smem_addr) { return ((smem_addr & 0x3FFFFu) >> 4) | 0x10000u; }
+constexpr uint32_t kSmemDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
 // D[tmem] (+)= A[smem] * B[smem]^T for one 128 x N x 32 step of E4M3 values,
 // each product row scaled by its E8M0 byte at sfa_tmem (4 columns: row r in
 // lane r % 32 of column r / 32, repeated in all four lane quarters) and
-// sfb_tmem (the same for B's rows); issued by one thread.
-__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t sfa_tmem, uint32_t sfb_tmem, bool accumulate)
+// sfb_tmem (the same for B's rows); issued by one thread.  a and b: low words
+// of the operands' descriptors.
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa_tmem,
+                                         uint32_t sfb_tmem, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
-        "r"(static_cast<uint32_t>(accumulate))
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tmov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(kSmemDescHi)
         : "memory");
 }
 
@@ -142,30 +162,19 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
                  : "memory");
 }
 
-// The same arrival at this barrier of every CTA of the cluster in `mask`.
-__device__ __forceinline__ void mma_commit_cluster(uint32_t bar, uint16_t mask)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     bar),
-                 "h"(mask)
-                 : "memory");
-}
-
 // ----------------------------------------------------- epilogue loads --
 
-// 16 consecutive fp32 columns, as tmem_load_32.
-__device__ __forceinline__ void tmem_load_16(uint32_t taddr, float (&v)[16])
+// 8 consecutive fp32 columns, as tmem_load_32.
+__device__ __forceinline__ void tmem_load_8(uint32_t taddr, float (&v)[8])
 {
-    uint32_t r[16];
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
         v[i] = __uint_as_float(r[i]);
 }
 
@@ -223,17 +232,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-                 : "memory");
-}
-
-// The same into the shared memory of every CTA of the cluster in `mask`, at
-// the same offset, completing on the barrier at the same offset there.
-__device__ __forceinline__ void tma_load_2d_cluster(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y,
-                                                    uint32_t bar, uint16_t mask)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-                 " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(mask)
                  : "memory");
 }
 

@@ -122,7 +122,7 @@ def row_values(codes, scale):
 PRODUCTS = [(1, 1, 16), (1, 128, 128), (1, 200, 4096), (3, 5, 48), (16, 200, 272), (17, 130, 128), (37, 640, 2560),
             (64, 300, 1024), (127, 129, 144), (128, 256, 128), (129, 257, 1040), (200, 1000, 640), (1, 4096, 16),
             (5, 3000, 400), (1300, 2304, 256), (1301, 2305, 272), (2000, 2100, 1040), (100, 20000, 144),
-            (4100, 700, 16), (2600, 2900, 144)]
+            (4100, 700, 16), (2600, 2900, 144), (20, 260, 1680), (300, 300, 6160), (129, 130, 6544)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
