@@ -673,7 +673,7 @@ NormPlan plan_norm(int64_t T, int d, int tensors, int max_threads, int regs, int
         const uint32_t slot = static_cast<uint32_t>(tensors) * 2 * d;
         while (per_sm > 1 && 4 * slot + 2048 > kSmemPerSm / per_sm)
             --per_sm;
-        const uint32_t room = kSmemPerSm / per_sm - 2048;
+        const uint32_t room = kSmemPerSm / per_sm - 2048 - 128;  // static arrays; the ring's alignment
         p.slots = static_cast<int>(room / slot);
         p.slots = p.slots > kMaxSlots ? kMaxSlots : p.slots;
         p.smem = 128 + p.slots * slot;

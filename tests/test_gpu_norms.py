@@ -200,3 +200,11 @@ def test_outputs_stay_inside_their_buffers():
         for t, _, n in outs:
             assert (t[:G] == 0xA5).all() and (t[G + n:] == 0xA5).all()
     assert api.taco_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("mode,d", [("channel", 7200), ("none", 14400), ("full", 4608), ("full", 5760), ("full", 7680),
+                                    ("token", 3600), ("full", 11520)])
+def test_rows_that_fill_shared_memory(mode, d):
+    # widths whose ring slots divide the room without a rest
+    test_forward(3, d, mode)
+    test_backward(3, d, mode)
