@@ -30,7 +30,17 @@
 // the loads do not wait for the two block-wide sums that every row needs;
 // outputs go straight from registers in 16-byte stores.  Two rows at a time
 // (up to 4096 columns) share a barrier and hide each other's latencies.
-// Rows that are not a multiple of 16 bytes are read element by element.
+//
+// Rows that are not a multiple of 16 bytes start anywhere inside a 16-byte
+// granule of memory.  A CTA's rows are a multiple of eight apart, so all of
+// them start at the same place, `shift` elements into one.  The ring holds a
+// row's granules; a thread joins its eight columns from two of them, and
+// stores the granule that ends in its columns, with the first elements from
+// the lane below.  (Threads that take granules instead of columns would skip
+// that, but then a row's sums, and so its last bits, depend on which row of
+// the tensor it is.)  8192 x 4095: 88 us forward and 128 backward, against
+// 254 and 331 with loads and stores of single elements, and 45 and 78 at 4096
+// columns; bound by the integer instructions that join and split.
 //
 // The gains' gradients are summed over a CTA's rows in registers, written as
 // one partial row per CTA, and added over the CTAs in a fixed order by a
@@ -89,7 +99,7 @@ __device__ __forceinline__ uint4 pack8(const F8 &x)
                       f32x2_to_bf16x2(x.v[2].x, x.v[2].y), f32x2_to_bf16x2(x.v[3].x, x.v[3].y));
 }
 
-// Columns c .. c + 7 of fp32 vectors of d values (zeros past the end).
+// Columns c .. c + 7 of fp32 vectors of d values, zeros past the end.
 template <bool VEC> __device__ __forceinline__ F8 load_f32x8(const float *p, int c, int d)
 {
     F8 x;
@@ -112,29 +122,86 @@ template <bool VEC> __device__ __forceinline__ F8 load_f32x8(const float *p, int
     return x;
 }
 
-template <bool VEC> __device__ __forceinline__ void store_bf16x8(uint16_t *p, int c, int d, const F8 &x)
+// q's first n elements, zeros after them.
+__device__ __forceinline__ uint4 first_elements(const uint4 &q, int n)
 {
-    const uint4 q = pack8(x);
-    if (VEC) {
-        if (c < d)
-            stg128_stream(p + c, q);
-    } else {
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < d)
-                p[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < 4; ++j)
+        w[j] &= 2 * j + 1 < n ? 0xFFFFFFFFu : 2 * j < n ? 0x0000FFFFu : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Elements e .. e + 7 of the sixteen in a, b (e the same in all lanes).
+__device__ __forceinline__ uint4 join(const uint4 &a, const uint4 &b, int e)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (e & 4) {
+#pragma unroll
+        for (int j = 0; j < 6; ++j)
+            w[j] = w[j + 2];
     }
+    if (e & 2) {
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+            w[j] = w[j + 1];
+    }
+    const uint32_t bits = 16 * (e & 1);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// Elements first .. last - 1 of q to p + first ..
+__device__ __forceinline__ void store_elements(uint16_t *p, const uint4 &q, int first, int last)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j >= first && j < last)
+            p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+}
+
+// Columns c .. c + 7 of the row p, which starts `shift` elements into a
+// granule (all lanes of a warp, with 256 columns, call this).
+template <bool VEC> __device__ __forceinline__ void store_bf16x8(uint16_t *p, int c, int shift, int d, const F8 &x)
+{
+    uint4 q = pack8(x);
+    if (VEC || shift == 0) {
+        if (c + 8 <= d)
+            stg128_stream(p + c, q);
+        else if (!VEC)
+            store_elements(p + c, q, 0, d - c);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    uint4 below;
+    below.x = __shfl_up_sync(0xFFFFFFFFu, q.x, 1);
+    below.y = __shfl_up_sync(0xFFFFFFFFu, q.y, 1);
+    below.z = __shfl_up_sync(0xFFFFFFFFu, q.z, 1);
+    below.w = __shfl_up_sync(0xFFFFFFFFu, q.w, 1);
+    // the warp's first granule starts in the warp below, its last one ends in
+    // the warp above: lanes 0 and 31 store what is the warp's own in them
+    if (lane == 0 || lane == 31)
+        store_elements(p + c, q, lane ? 8 - shift : 0, min(lane ? 8 : 8 - shift, d - c));
+    if (lane == 0)
+        return;
+    q = join(below, q, 8 - shift);
+    if (c - shift + 8 <= d)
+        stg128_stream(p + c - shift, q);
+    else
+        store_elements(p + c - shift, q, 0, d - c + shift);
 }
 
 // The CTA's rows blockIdx.x, + gridDim.x, ...: NT bf16 tensors' rows, NT
-// row-sized pieces to a slot.  `row` and `slot` are those of the first row
-// being worked on, row(i) and slot i places on those of the ones after it.
+// row-sized pieces to a slot, each from the granule that its row starts in.
+// `row` and `slot` are those of the first row being worked on, row(i) and
+// slot i places on those of the ones after it.
 template <int NT, bool VEC> struct RowRing {
     const uint16_t *src[NT];
-    uint32_t buf, bars, slots, row_bytes;
+    uint32_t buf, bars, slots, pitch;  // pitch: bytes of a piece
     int64_t T, row0;
     int d;
+    int shift;  // elements between a granule's start and a row's, the same for all rows of the CTA
     uint32_t slot = 0, phase = 0;
     bool dead = false;
 
@@ -144,27 +211,36 @@ template <int NT, bool VEC> struct RowRing {
         const uint32_t s = slot + i;
         return s >= slots ? s - slots : s;
     }
+    // Elements from row r's start to the end of the tensor's whole granules:
+    // copies take no more than those, what lies behind is read directly.
+    __device__ __forceinline__ int64_t whole(int64_t r) const { return (T * d & ~int64_t(7)) - r * d; }
     __device__ __forceinline__ void issue(int64_t r, uint32_t s)  // row r into slot s (one thread)
     {
         if (r >= T)
             return;
         const uint32_t bar = bars + 8 * s;
-        mbar_arrive_expect_tx(bar, NT * row_bytes);
+        uint32_t bytes = pitch;
+        if (!VEC)
+            bytes = 2 * static_cast<uint32_t>(min(static_cast<int64_t>((shift + d + 7) & ~7), whole(r) + shift));
+        mbar_arrive_expect_tx(bar, NT * bytes);
+        if (!VEC && bytes == 0)
+            return;
 #pragma unroll
         for (int k = 0; k < NT; ++k)
-            bulk_load(buf + (s * NT + k) * row_bytes, src[k] + r * d, row_bytes, bar);
+            bulk_load(buf + (s * NT + k) * pitch, src[k] + r * d - shift, bytes, bar);
     }
     __device__ __forceinline__ void start()
     {
         row0 = blockIdx.x;
-        if (VEC && threadIdx.x == 0)
+        shift = VEC ? 0 : static_cast<int>(blockIdx.x & 7) * (d & 7) & 7;
+        if (threadIdx.x == 0)
             for (uint32_t s = 0; s < slots; ++s)
                 issue(row(s), s);
     }
-    // Row i has landed (or is read directly).
+    // Row i has landed.
     __device__ __forceinline__ void wait(int i)
     {
-        if (VEC && !dead && row(i) < T && !mbar_wait(bars + 8 * slot_of(i), phase ^ (slot + i >= slots))) {
+        if (!dead && row(i) < T && !mbar_wait(bars + 8 * slot_of(i), phase ^ (slot + i >= slots))) {
             atomicOr(&g_norm_error, kErrNorm);
             dead = true;
             // the thread that issues stops issuing: wait for what is in flight
@@ -176,24 +252,32 @@ template <int NT, bool VEC> struct RowRing {
     // Columns c .. c + 7 of tensor k's row i, zeros past the end.
     __device__ __forceinline__ uint4 get(int i, int k, int c) const
     {
-        if (row(i) >= T)
+        if (row(i) >= T || c >= d || dead)
             return make_uint4(0, 0, 0, 0);
+        const uint32_t at = buf + (slot_of(i) * NT + k) * pitch + 2 * c;
+        uint4 q;
         if (VEC) {
-            if (c >= d || dead)
-                return make_uint4(0, 0, 0, 0);
-            return lds128(buf + (slot_of(i) * NT + k) * row_bytes + 2 * c);
-        }
-        const uint16_t *p = src[k] + row(i) * d + c;
-        uint32_t e[8];
+            q = lds128(at);
+        } else if (c + 8 > whole(row(i))) {
+            const uint16_t *p = src[k] + row(i) * d + c;
+            uint32_t e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            e[j] = c + j < d ? __ldg(p + j) : 0u;
-        return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+            for (int j = 0; j < 8; ++j)
+                e[j] = c + j < d ? __ldg(p + j) : 0u;
+            q = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        } else {
+            q = lds128(at);
+            if (shift != 0)
+                q = join(q, lds128(at + 16), shift);
+            if (c + 8 > d)
+                q = first_elements(q, d - c);
+        }
+        return q;
     }
     // Every thread has read row i (a barrier lies behind): refill its slot.
     __device__ __forceinline__ void refill(int i)
     {
-        if (VEC && threadIdx.x == 0 && !dead)
+        if (threadIdx.x == 0 && !dead)
             issue(row(i + static_cast<int>(slots)), slot_of(i));
     }
     __device__ __forceinline__ void next(int rows)
@@ -258,6 +342,9 @@ template <int WARPS, int K> __device__ __forceinline__ void block_sum(float (&v)
         v[k] = P == 1 ? sum : __shfl_sync(0xFFFFFFFFu, sum, k * L);
 }
 
+// Bytes of a row's piece in the ring: whole granules from the one it starts in.
+__host__ __device__ inline uint32_t ring_pitch(int d) { return d % 8 == 0 ? 2 * d : 2 * ((d + 7) / 8 * 8 + 8); }
+
 template <int NT, bool VEC>
 __device__ __forceinline__ void ring_init(RowRing<NT, VEC> &ring, uint8_t *smem, uint32_t bars, int64_t T, int d,
                                           int slots)
@@ -265,10 +352,10 @@ __device__ __forceinline__ void ring_init(RowRing<NT, VEC> &ring, uint8_t *smem,
     ring.buf = (smem_u32(smem) + 127u) & ~127u;
     ring.bars = bars;
     ring.slots = slots;
-    ring.row_bytes = 2 * d;
+    ring.pitch = ring_pitch(d);
     ring.T = T;
     ring.d = d;
-    if (VEC && threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
         for (int s = 0; s < slots; ++s)
             mbar_init(bars + 8 * s, 1);
         fence_barrier_init();
@@ -279,9 +366,8 @@ __device__ __forceinline__ void ring_init(RowRing<NT, VEC> &ring, uint8_t *smem,
 
 // ---------------------------------------------------------------- forward --
 
-// V groups of 8 columns a thread (group v: columns 8 (threadIdx.x + v
-// blockDim.x)), RPI rows at a time; GATE a gate mode; FP8: n as codes and
-// scales.
+// V units of 8 columns a thread (unit threadIdx.x + v blockDim.x), RPI rows
+// at a time; GATE a gate mode; FP8: n as codes and scales.
 template <int V, int RPI, int GATE, bool FP8, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     norm_forward_kernel(const uint16_t *__restrict__ y, const uint16_t *__restrict__ h,
@@ -369,7 +455,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                     ss = fma2(h2[i][v].v[j], h2[i][v].v[j], ss);
                 }
                 if (ring.row(i) < T)
-                    store_bf16x8<VEC>(h_out + ring.row(i) * d, c, d, h2[i][v]);
+                    store_bf16x8<VEC>(h_out + ring.row(i) * d, c, ring.shift, d, h2[i][v]);
             }
             sum[i] = ss.x + ss.y;
         }
@@ -409,7 +495,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                     if ((threadIdx.x & 15) == 0 && c < d)
                         n_scale[fp8_scale_at(row, c >> 7, (d + 511) / 512)] = static_cast<uint8_t>(byte);
                 } else {
-                    store_bf16x8<VEC>(static_cast<uint16_t *>(n_out) + row * d, c, d, n);
+                    store_bf16x8<VEC>(static_cast<uint16_t *>(n_out) + row * d, c, ring.shift, d, n);
                 }
             }
         }
@@ -539,7 +625,7 @@ __global__ void __launch_bounds__(MAXT, 1)
                     o.v[j] = s2 * G[i][v].v[j];
                 }
                 if (ring.row(i) < T)
-                    store_bf16x8<VEC>(dh + ring.row(i) * d, c, d, o);
+                    store_bf16x8<VEC>(dh + ring.row(i) * d, c, ring.shift, d, o);
                 // y r_y G: the sum over tokens behind dg_post and a channel
                 // gate's gradient
                 const F8 y8 = unpack8(qy[i][v]);
@@ -560,7 +646,7 @@ __global__ void __launch_bounds__(MAXT, 1)
                 }
                 if constexpr (GATE == kGateFull)
                     if (ring.row(i) < T)
-                        store_bf16x8<VEC>(static_cast<uint16_t *>(dgate) + ring.row(i) * d, c, d, o);
+                        store_bf16x8<VEC>(static_cast<uint16_t *>(dgate) + ring.row(i) * d, c, ring.shift, d, o);
             }
             dot[i] = dd.x + dd.y;
         }
@@ -589,7 +675,7 @@ __global__ void __launch_bounds__(MAXT, 1)
                         u = u * w.v[j];
                     o.v[j] = fma2(u, G[i][v].v[j], o.v[j] * cy);
                 }
-                store_bf16x8<VEC>(dy + row * d, c, d, o);
+                store_bf16x8<VEC>(dy + row * d, c, ring.shift, d, o);
             }
         }
     }
@@ -648,7 +734,7 @@ __global__ void __launch_bounds__(512)
     }
 }
 
-// Threads, groups of 8 columns a thread, ring slots and CTAs of a shape.
+// Threads, units a thread, ring slots and CTAs of a shape.
 struct NormPlan {
     int threads, v, slots, grid;
     uint32_t smem;
@@ -656,8 +742,9 @@ struct NormPlan {
 
 constexpr uint32_t kSmemPerSm = 227 * 1024;
 
-// max_threads: the most threads with one group of columns each; regs: the
-// registers a thread of the kernel takes, for how many CTAs share an SM.
+// tensors: rows to a slot; max_threads: the most threads with one unit each;
+// regs: the registers a thread of the kernel takes, for how many CTAs share
+// an SM.
 NormPlan plan_norm(int64_t T, int d, int tensors, int max_threads, int regs, int sms)
 {
     NormPlan p;
@@ -666,33 +753,32 @@ NormPlan plan_norm(int64_t T, int d, int tensors, int max_threads, int regs, int
     p.threads = ((units + p.v - 1) / p.v + 31) / 32 * 32;
     int per_sm = 65536 / (regs * p.threads);
     per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
-    p.slots = 0;
-    p.smem = 0;
-    if (d % 8 == 0) {
-        // at least four rows a CTA in the ring where they fit
-        const uint32_t slot = static_cast<uint32_t>(tensors) * 2 * d;
-        while (per_sm > 1 && 4 * slot + 2048 > kSmemPerSm / per_sm)
-            --per_sm;
-        const uint32_t room = kSmemPerSm / per_sm - 2048 - 128;  // static arrays; the ring's alignment
-        p.slots = static_cast<int>(room / slot);
-        p.slots = p.slots > kMaxSlots ? kMaxSlots : p.slots;
-        p.smem = 128 + p.slots * slot;
-    }
-    const int64_t most = static_cast<int64_t>(per_sm) * sms;
+    // at least four rows a CTA in the ring where they fit
+    const uint32_t slot = static_cast<uint32_t>(tensors) * ring_pitch(d);
+    while (per_sm > 1 && 4 * slot + 2048 > kSmemPerSm / per_sm)
+        --per_sm;
+    const uint32_t room = kSmemPerSm / per_sm - 2048 - 128;  // static arrays; the ring's alignment
+    p.slots = static_cast<int>(room / slot);
+    p.slots = p.slots > kMaxSlots ? kMaxSlots : p.slots;
+    p.smem = 128 + p.slots * slot;
+    // a multiple of eight, so that a CTA's rows all start at the same place
+    // of a granule (with fewer CTAs each has one row)
+    int64_t most = static_cast<int64_t>(per_sm) * sms / 8 * 8;
+    most = most < 8 ? 8 : most;
     p.grid = static_cast<int>(T < most ? T : most);
     return p;
 }
 
 NormPlan plan_forward(int64_t T, int d, int gate_mode, int sms)
 {
-    return plan_norm(T, d, gate_mode == kGateFull ? 3 : 2, kMaxThreads, d <= 16 * kMaxThreads ? 96 : 128, sms);
+    const int v1 = 8 * kMaxThreads, regs = d % 8 == 0 ? (d <= 2 * v1 ? 96 : 128) : (d <= v1 ? 104 : 128);
+    return plan_norm(T, d, gate_mode == kGateFull ? 3 : 2, kMaxThreads, regs, sms);
 }
 
-// Backward, one group of columns a thread: two rows at a time in 128
-// registers up to 512 threads, above that (up to 768) one row at a time in
-// 80.  Measured at 8192 rows, one against two rows: 1024 columns 32 and 28
-// us, 4096 96 and 77 us; at 5120, 106 us against 167 with two groups of
-// columns a thread.
+// Backward, one unit a thread: two rows at a time in 128 registers up to 512
+// threads, above that (up to 768) one row at a time in 80.  Measured at 8192
+// rows, one against two rows: 1024 columns 32 and 28 us, 4096 96 and 77 us;
+// at 5120, 106 us against 167 with two units a thread.
 constexpr int kWide = 768;
 bool one_row(int d) { return d > 8 * kMaxThreads && d <= 8 * kWide; }
 
@@ -714,7 +800,7 @@ template <class K> cudaError_t allow_smem(K kernel, int device, std::atomic<bool
     return e;
 }
 
-// Two rows at a time where a thread has one group of columns.
+// Two rows at a time where a thread has one unit.
 constexpr int rows_at_once(int v) { return v == 1 ? 2 : 1; }
 
 template <int V, int GATE, bool FP8, bool VEC>

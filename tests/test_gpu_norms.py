@@ -208,3 +208,43 @@ def test_rows_that_fill_shared_memory(mode, d):
     # widths whose ring slots divide the room without a rest
     test_forward(3, d, mode)
     test_backward(3, d, mode)
+
+
+# rows that start at every place of a 16-byte granule: more rows than CTAs,
+# every shift, both ends of a granule, widths that change the units a thread
+SHIFTED = [(1300, 1), (1301, 3), (1303, 9), (1300, 15), (2000, 66), (650, 250), (500, 1283), (340, 4090), (340, 4095),
+           (200, 5119), (170, 6137), (160, 8186), (160, 10001)]
+
+
+@pytest.mark.parametrize("T,d", SHIFTED)
+@pytest.mark.parametrize("mode", ["none", "full"])
+def test_rows_inside_granules(T, d, mode):
+    test_forward(T, d, mode)
+    test_backward(T, d, mode)
+
+
+@pytest.mark.parametrize("T,d", [(3, 1), (9, 3), (700, 5), (1300, 13), (341, 1001), (161, 8189), (170, 4099)])
+def test_odd_rows_stay_inside_their_buffers(T, d):
+    lib = _lib.load()
+    G = 4096
+    stream = torch.cuda.current_stream().cuda_stream
+    y, h, gp, gq, gate = make(T, d, "full", 21)
+    # inputs between guards of NaN: a value read from outside would show
+    def fenced(t):
+        b = torch.full((t.numel() + 4096,), float("nan"), dtype=t.dtype, device="cuda")
+        b[2048:2048 + t.numel()] = t.flatten()
+        return b, b.data_ptr() + 2048 * t.element_size()
+
+    ins = [fenced(t) for t in (y, h, gate)]
+    out = torch.full((2, T * d + 4096), float("nan"), dtype=torch.bfloat16, device="cuda")
+    at = [out.data_ptr() + 2 * (k * out.shape[1] + 2048) for k in range(2)]
+    at = [a + (-a) % 16 for a in at]
+    assert lib.rmsnorm_gate_residual(ins[0][1], ins[1][1], gp.data_ptr(), gq.data_ptr(), ins[2][1], 3, 1.0, EPS, T, d,
+                                     at[0], at[1], None, stream) == 0
+    torch.cuda.synchronize()
+    want = api.rmsnorm_gate_residual(y, h, gp, gq, gate, 1.0, EPS)
+    for k in range(2):
+        first = (at[k] - out.data_ptr()) // 2 - k * out.shape[1]
+        assert torch.equal(out[k, first:first + T * d].view(T, d), want[k])
+        assert out[k, :first].isnan().all() and out[k, first + T * d:].isnan().all()
+        assert not want[k].isnan().any()
