@@ -445,7 +445,7 @@ def agoq_gemm_laaq_quantize(a: torch.Tensor, b: torch.Tensor, bits: int = 4, blo
 
 # These calls are made once or several times per layer, also for a single
 # token, so what they do on the host counts: the stream is taken as the raw
-# handle (current_stream() builds an object, 3 us on this host's Arm cores),
+# handle (current_stream() builds an object, 3 us on Grace's cores),
 # shapes are read once, and no tensor operation runs besides torch.empty.
 
 _BF = (torch.bfloat16,)

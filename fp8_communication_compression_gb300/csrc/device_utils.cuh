@@ -38,10 +38,9 @@ __device__ __forceinline__ uint64_t global_timer_ns()
 // every kernel made the step slower: 122.1 us against 120.3 us with the
 // 16-element shard reduce, and 132.7 us against 118.9 us with the
 // 32-element one.
-
-// (The calls of the FP8 linear layer and of the norms do: see below.)
 //
-// pdl_trigger() at the start of a kernel lets the next grid of the stream
+// Kernels of the FP8 linear layer and of the norms do, where their grid is
+// small.  pdl_trigger() at the start of a kernel lets the next grid of the stream
 // start as soon as this one's CTAs leave room; every kernel still waits for
 // its predecessor's end in pdl_wait() before it touches memory.  It pays
 // where a layer's kernels are short (a few us) and their launch latency
@@ -50,6 +49,38 @@ __device__ __forceinline__ uint64_t global_timer_ns()
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// -------------------------------------- rows that start inside granules --
+
+// The first n of q's eight 16-bit elements, zeros after them.
+__device__ __forceinline__ uint4 first_elements(const uint4 &q, int n)
+{
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] &= 2 * j + 1 < n ? 0xFFFFFFFFu : 2 * j < n ? 0x0000FFFFu : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Elements e .. e + 7 of the sixteen in a, b (e the same in all lanes; both
+// tests are then uniform).
+__device__ __forceinline__ uint4 join(const uint4 &a, const uint4 &b, int e)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (e & 4) {
+#pragma unroll
+        for (int j = 0; j < 6; ++j)
+            w[j] = w[j + 2];
+    }
+    if (e & 2) {
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+            w[j] = w[j + 1];
+    }
+    const uint32_t bits = 16 * (e & 1);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
 
 // ------------------------------------------------------------- mbarrier --
 

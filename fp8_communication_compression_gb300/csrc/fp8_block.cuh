@@ -20,8 +20,6 @@
 
 namespace taco {
 
-constexpr int kFp8Block = 128;
-
 // Codes are stored in rows padded with zero codes to a multiple of 16 bytes
 // (the stride a TMA tensor map needs).
 __host__ __device__ inline int64_t fp8_pitch(int64_t n) { return (n + 15) & ~int64_t(15); }

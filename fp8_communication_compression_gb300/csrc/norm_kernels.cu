@@ -122,35 +122,6 @@ template <bool VEC> __device__ __forceinline__ F8 load_f32x8(const float *p, int
     return x;
 }
 
-// q's first n elements, zeros after them.
-__device__ __forceinline__ uint4 first_elements(const uint4 &q, int n)
-{
-    uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        w[j] &= 2 * j + 1 < n ? 0xFFFFFFFFu : 2 * j < n ? 0x0000FFFFu : 0u;
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Elements e .. e + 7 of the sixteen in a, b (e the same in all lanes).
-__device__ __forceinline__ uint4 join(const uint4 &a, const uint4 &b, int e)
-{
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (e & 4) {
-#pragma unroll
-        for (int j = 0; j < 6; ++j)
-            w[j] = w[j + 2];
-    }
-    if (e & 2) {
-#pragma unroll
-        for (int j = 0; j < 5; ++j)
-            w[j] = w[j + 1];
-    }
-    const uint32_t bits = 16 * (e & 1);
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
 // Elements first .. last - 1 of q to p + first ..
 __device__ __forceinline__ void store_elements(uint16_t *p, const uint4 &q, int first, int last)
 {

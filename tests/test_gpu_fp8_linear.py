@@ -331,3 +331,20 @@ def test_outputs_stay_inside_their_buffers():
             torch.cuda.synchronize()
             assert intact(t, n)
     assert api.taco_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (2, 3), (9, 7), (7, 15), (130, 129), (257, 1001), (128, 255), (256, 130),
+                                       (300, 1300)])
+def test_rows_inside_granules_between_guards(rows, cols):
+    # a matrix between guards of NaN: a value read from outside would show in
+    # a block's scale
+    g = torch.Generator().manual_seed(rows + cols)
+    x = torch.randn((rows, cols), generator=g).bfloat16().cuda()
+    b = torch.full((x.numel() + 2048,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    b[1024:1024 + x.numel()] = x.flatten()
+    inner = b[1024:1024 + x.numel()].view(rows, cols)
+    codes, scale, codes_t, scale_t = api.fp8_quantize(inner, colwise=True)
+    check_codes(codes, scale, x, False)
+    check_codes(codes_t, scale_t, x.t().contiguous(), False)
+    w = api.fp8_quantize_weight(inner)
+    check_codes(w[0], w[1], x, True)
