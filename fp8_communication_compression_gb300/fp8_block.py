@@ -29,6 +29,8 @@ class Fp8Block:
         f, d = w_up.shape
         if tuple(w_down.shape) != (d, f) or f % (128 * P) or d % 128:
             raise ValueError("w_up must be [f, d] and w_down [d, f], d a multiple of 128 and f of 128 P")
+        if tokens < 1:
+            raise ValueError("tokens must be positive")
         dev = w_up.device
         self.P, self.tokens, self.d, self.f = P, tokens, d, f
         self.gate, self.residual_scale, self.eps = gate, residual_scale, eps
@@ -38,12 +40,16 @@ class Fp8Block:
         # each slice's weights, quantised once (and again after an update)
         self.up = [api.fp8_quantize_weight(w_up[p * fp:(p + 1) * fp]) for p in range(P)]
         self.down = [api.fp8_quantize_weight(w_down[:, p * fp:(p + 1) * fp].contiguous()) for p in range(P)]
+        self._saved = None  # what the backward pass needs of the forward one
         self.sum = api.TwoShotLocal(P, tokens, d, out_dtype=torch.bfloat16, device=dev)
         # FP8 main gradients of the slices' weights: codes and multipliers
-        main = lambda r, c: (torch.zeros((r, c), dtype=torch.uint8, device=dev),
-                             torch.ones(r * c // 128, dtype=torch.float32, device=dev))
-        self.main_up = [main(fp, d) for _ in range(P)]
-        self.main_down = [main(d, fp) for _ in range(P)]
+        self.main_up = [self._main(fp, d, dev) for _ in range(P)]
+        self.main_down = [self._main(d, fp, dev) for _ in range(P)]
+
+    @staticmethod
+    def _main(rows: int, cols: int, dev: torch.device):
+        return (torch.zeros((rows, cols), dtype=torch.uint8, device=dev),
+                torch.ones(rows * cols // 128, dtype=torch.float32, device=dev))
 
     def _reduce(self, parts: list) -> torch.Tensor:
         """The slices' partial sums through the compressed two-shot path."""
@@ -61,6 +67,8 @@ class Fp8Block:
     def backward(self, dout: torch.Tensor, dh1: torch.Tensor):
         """Gradients at out and h1 -> (dy, dh, dgain_post, dgain_pre, dgate);
         the weights' gradients are added to the FP8 main gradients."""
+        if self._saved is None:
+            raise RuntimeError("backward() before forward()")
         y, h, h1, us = self._saved
         _, n = api.rmsnorm_gate_residual(y, h, self.gain_post, self.gain_pre, self.gate, self.residual_scale, self.eps)
         dns = []

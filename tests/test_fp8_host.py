@@ -197,3 +197,13 @@ def test_norm_gradients_against_differences(mode):
                 full = args[:k] + [b] + args[k + 1:]
                 v.append(loss(*full, *([None] if gate is None else [])))
             assert abs((v[0] - v[1]) / (2 * step) - ga[idx]) <= tol * (1 + abs(ga[idx])), (mode, k, idx)
+
+
+def test_block_refuses_shapes_that_do_not_divide():
+    from fp8_communication_compression_gb300 import Fp8Block
+
+    w = lambda r, c: torch.zeros((r, c), dtype=torch.bfloat16)
+    for up, down, tokens, P in ((w(256, 100), w(100, 256), 8, 1), (w(256, 128), w(256, 128), 8, 1),
+                                (w(256, 128), w(128, 256), 8, 3), (w(256, 128), w(128, 256), 0, 2)):
+        with pytest.raises(ValueError):
+            Fp8Block(up, down, tokens, P)
