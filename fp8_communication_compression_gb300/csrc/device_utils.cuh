@@ -278,7 +278,12 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi)
 // Four fp32 -> four E4M3FN codes packed little-endian into one word.
 __device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d)
 {
-    return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(c, d) << 16);
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
 }
 
 // Two E4M3FN codes (low byte = first element) -> two fp32 values (exact:
