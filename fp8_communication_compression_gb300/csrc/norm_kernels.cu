@@ -335,6 +335,28 @@ __device__ __forceinline__ void ring_init(RowRing<NT, VEC> &ring, uint8_t *smem,
     __syncthreads();
 }
 
+// Tokens' gates of the CTA's next kGateRows rows in shared memory (loaded row
+// by row they stood in every round's way: 8192 x 4096 forward 50 us against 46,
+// backward 96 against 79, 8192 x 5120 backward 126 against 111).  The arrays in static shared memory take at most 2 KB together.
+constexpr int kGateRows = 128;
+struct TokenGates {
+    float *at;
+    int used = kGateRows;
+    __device__ __forceinline__ explicit TokenGates(float *rows) : at(rows) {}
+    // `rows` rows at ring.row(0) are about to be worked on, after `rows` others.
+    template <class R> __device__ __forceinline__ void next(int rows, const float *gate, const R &ring)
+    {
+        used += rows;
+        if (used < kGateRows)
+            return;
+        __syncthreads();  // the last of the previous ones have been read
+        for (int i = threadIdx.x; i < kGateRows; i += blockDim.x)
+            at[i] = ring.row(i) < ring.T ? __ldg(gate + ring.row(i)) : 0.0f;
+        __syncthreads();
+        used = 0;
+    }
+};
+
 // ---------------------------------------------------------------- forward --
 
 // V units of 8 columns a thread (unit threadIdx.x + v blockDim.x), RPI rows
@@ -349,6 +371,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     constexpr int NT = GATE == kGateFull ? 3 : 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kMaxSlots];
+    // tokens' gates ahead in shared memory; with more units a thread the
+    // registers that takes cost more (5120 columns: 59 us against 52)
+    constexpr bool AHEAD = GATE == kGateToken && V == 1;
+    __shared__ float gate_rows[AHEAD ? kGateRows : 1];
     __shared__ float red[2][16 * pow2_at_least(RPI)];
     RowRing<NT, VEC> ring;
     ring.src[0] = y;
@@ -375,14 +401,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 gp[v].v[j] = gp[v].v[j] * w.v[j];
         }
     }
+    TokenGates gates(gate_rows);
     for (; ring.row(0) < T; ring.next(RPI)) {
+        if constexpr (AHEAD)
+            gates.next(RPI, static_cast<const float *>(gate), ring);
         uint4 qy[RPI][V], qh[RPI][V], qg[RPI][V];
         float sum[RPI], gt[RPI];
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
             ring.wait(i);
             gt[i] = 1.0f;
-            if constexpr (GATE == kGateToken)
+            if constexpr (AHEAD)
+                gt[i] = gates.at[gates.used + i];
+            else if constexpr (GATE == kGateToken)
                 if (ring.row(i) < T)
                     gt[i] = __ldg(static_cast<const float *>(gate) + ring.row(i));
             float2 ss = both(0.0f);
@@ -493,6 +524,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     constexpr int WARPS = MAXT > 512 ? 32 : 16;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kMaxSlots];
+    __shared__ float gate_rows[GATE == kGateToken ? kGateRows : 1];
     __shared__ float red[2][WARPS * pow2_at_least(3 * RPI)];
     RowRing<NT, VEC> ring;
     ring.src[0] = dn;
@@ -530,7 +562,10 @@ __global__ void __launch_bounds__(MAXT, 1)
         gp[0] = post_gain(8 * threadIdx.x);
         gq[0] = load_f32x8<VEC>(g_pre, 8 * threadIdx.x, d);
     }
+    TokenGates gates(gate_rows);
     for (; ring.row(0) < T; ring.next(RPI)) {
+        if constexpr (GATE == kGateToken)
+            gates.next(RPI, static_cast<const float *>(gate), ring);
         uint4 qn[RPI][V], qd[RPI][V], qy[RPI][V], qh[RPI][V], qg[RPI][V];
         float sum[3 * RPI], gt[RPI];
 #pragma unroll
@@ -538,8 +573,7 @@ __global__ void __launch_bounds__(MAXT, 1)
             ring.wait(i);
             gt[i] = 1.0f;
             if constexpr (GATE == kGateToken)
-                if (ring.row(i) < T)
-                    gt[i] = __ldg(static_cast<const float *>(gate) + ring.row(i));
+                gt[i] = gates.at[gates.used + i];
             float2 s0 = both(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -669,7 +703,11 @@ __global__ void __launch_bounds__(MAXT, 1)
 }
 
 // Sums the CTAs' partial rows in a fixed order: 32 columns a CTA, sixteen
-// groups of rows in turn, then the groups.
+// groups of rows in turn, then the groups.  One CTA an SM leaves 152 rows, so
+// a thread's ten loads of each half are all in flight (in fives: 1.1 us
+// longer).
+constexpr int kGainLoads = 10;
+
 __global__ void __launch_bounds__(512)
     norm_gains_kernel(const float *__restrict__ partial, int ctas, int d, int gate_mode,
                       const float *__restrict__ g_post, const float *__restrict__ gate, float *__restrict__ dg_pre,
@@ -680,10 +718,20 @@ __global__ void __launch_bounds__(512)
     pdl_wait();
     float a = 0.0f, b = 0.0f;
     if (c < d)
-#pragma unroll 5
-        for (int i = grp; i < ctas; i += 16) {
-            a += partial[static_cast<int64_t>(i) * 2 * d + c];
-            b += partial[static_cast<int64_t>(i) * 2 * d + d + c];
+        for (int i0 = grp; i0 < ctas; i0 += 16 * kGainLoads) {
+            float va[kGainLoads], vb[kGainLoads];
+#pragma unroll
+            for (int k = 0; k < kGainLoads; ++k) {
+                const int i = i0 + 16 * k;
+                const float *p = partial + static_cast<int64_t>(i) * 2 * d + c;
+                va[k] = i < ctas ? p[0] : 0.0f;
+                vb[k] = i < ctas ? p[d] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kGainLoads; ++k) {
+                a += va[k];
+                b += vb[k];
+            }
         }
     part[0][grp][lane] = a;
     part[1][grp][lane] = b;
@@ -708,6 +756,7 @@ __global__ void __launch_bounds__(512)
 // Threads, units a thread, ring slots and CTAs of a shape.
 struct NormPlan {
     int threads, v, slots, grid;
+    bool one_row;  // backward: one row at a time with one unit a thread
     uint32_t smem;
 };
 
@@ -719,7 +768,7 @@ constexpr uint32_t kSmemPerSm = 227 * 1024;
 // an SM.
 NormPlan plan_norm(int64_t T, int d, int tensors, int min_rows, int max_threads, int regs, int sms)
 {
-    NormPlan p;
+    NormPlan p = {};
     const int units = (d + 7) / 8;
     p.v = units <= max_threads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
     p.threads = ((units + p.v - 1) / p.v + 31) / 32 * 32;
@@ -751,16 +800,26 @@ NormPlan plan_forward(int64_t T, int d, int gate_mode, bool fp8, int sms)
 }
 
 // Backward, one unit a thread: two rows at a time in 128 registers up to 512
-// threads, above that (up to 768) one row at a time in 80.  Measured at 8192
-// rows, one against two rows: 1024 columns 32 and 28 us, 4096 96 and 77 us;
-// at 5120, 106 us against 167 with two units a thread.
+// threads, above that (up to 768) one row at a time in 80.  Many rows of 2056
+// to 2560 columns are also taken one at a time: two CTAs then share an SM,
+// where the two-row kernel's registers leave room for one of 288 or 320
+// threads.  Measured, one against two rows: 8192 x 1024 30 and 26 us, 8192 x
+// 2048 49 and 45, 8192 x 2304 58 and 64, 8192 x 2560 59 and 65, 4096 x 2560 36
+// and 38, 2048 x 2560 22 and 21, 8192 x 2816 64 and 66 (with a full gate 75
+// and 75), 8192 x 4096 94 and 76, 8192 x 2561 120 and 110; at 5120, 104 us
+// against 167 with two units a thread.
 constexpr int kWide = 768;
-bool one_row(int d) { return d > 8 * kMaxThreads && d <= 8 * kWide; }
+bool one_row(int64_t T, int d, int sms)
+{
+    return (d > 8 * kMaxThreads && d <= 8 * kWide) || (d > 2048 && d <= 2560 && d % 8 == 0 && T >= 24 * sms);
+}
 
 NormPlan plan_backward(int64_t T, int d, int gate_mode, int sms)
 {
-    const bool one = one_row(d);
-    return plan_norm(T, d, gate_mode == kGateFull ? 5 : 4, 4, one ? kWide : kMaxThreads, one ? 80 : 128, sms);
+    const bool one = one_row(T, d, sms);
+    NormPlan p = plan_norm(T, d, gate_mode == kGateFull ? 5 : 4, 4, one ? kWide : kMaxThreads, one ? 80 : 128, sms);
+    p.one_row = one;
+    return p;
 }
 
 constexpr int kMaxDevices = 64;
@@ -849,7 +908,7 @@ cudaError_t backward_gate(const NormPlan &p, const NormBackward &a, int dev, cud
 template <bool VEC> cudaError_t backward_shape(const NormPlan &p, const NormBackward &a, int dev, cudaStream_t s)
 {
     if (p.v == 1)
-        return one_row(static_cast<int>(a.d)) ? backward_gate<1, 1, kWide, VEC>(p, a, dev, s)
+        return p.one_row ? backward_gate<1, 1, kWide, VEC>(p, a, dev, s)
                                               : backward_gate<1, 2, kMaxThreads, VEC>(p, a, dev, s);
     return p.v == 2 ? backward_gate<2, 1, kMaxThreads, VEC>(p, a, dev, s)
                     : backward_gate<4, 1, kMaxThreads, VEC>(p, a, dev, s);

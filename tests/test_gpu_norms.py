@@ -248,3 +248,13 @@ def test_odd_rows_stay_inside_their_buffers(T, d):
         assert torch.equal(out[k, first:first + T * d].view(T, d), want[k])
         assert out[k, :first].isnan().all() and out[k, first + T * d:].isnan().all()
         assert not want[k].isnan().any()
+
+
+@pytest.mark.parametrize("T,d,mode", [(4000, 2304, "channel"), (4000, 2304, "token"), (3648, 2560, "full"),
+                                      (3647, 2560, "none"), (40001, 64, "token"), (20000, 264, "token"),
+                                      (19713, 520, "token")])
+def test_many_rows(T, d, mode):
+    # one row at a time (2056 to 2560 columns); more tokens a CTA than their
+    # gates are held at once
+    test_forward(T, d, mode)
+    test_backward(T, d, mode)
