@@ -361,8 +361,11 @@ struct TokenGates {
 
 // V units of 8 columns a thread (unit threadIdx.x + v blockDim.x), RPI rows
 // at a time; GATE a gate mode; FP8: n as codes and scales.
-template <int V, int RPI, int GATE, bool FP8, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+// Two units a thread of rows inside granules: bounded to the 96 registers
+// with which two CTAs of up to 5440 columns share an SM (8192 x 5119: 91 us
+// against 132 with 118; 8192 x 6001 with a full gate 178 against 163).
+template <int V, int RPI, int GATE, bool FP8, bool VEC, bool DENSE>
+__global__ void __launch_bounds__(V == 2 && !VEC ? 640 : kMaxThreads, DENSE ? 2 : 1)
     norm_forward_kernel(const uint16_t *__restrict__ y, const uint16_t *__restrict__ h,
                         const float *__restrict__ g_post, const float *__restrict__ g_pre,
                         const void *__restrict__ gate, float s, float eps, int64_t T, int d, int slots,
@@ -756,11 +759,20 @@ __global__ void __launch_bounds__(512)
 // Threads, units a thread, ring slots and CTAs of a shape.
 struct NormPlan {
     int threads, v, slots, grid;
+    bool dense;    // forward: registers bounded to 64
     bool one_row;  // backward: one row at a time with one unit a thread
     uint32_t smem;
 };
 
 constexpr uint32_t kSmemPerSm = 227 * 1024;
+
+// CTAs whose registers an SM holds (a quarter of them in each of its four
+// partitions), eight at most.
+int ctas_of(int regs, int threads)
+{
+    const int n = 4 * (16384 / (32 * regs)) / (threads / 32);
+    return n < 1 ? 1 : n > 8 ? 8 : n;
+}
 
 // tensors: rows to a slot; min_rows: the fewest rows in the ring of a CTA that
 // shares its SM; max_threads: the most threads with one unit each;
@@ -772,8 +784,7 @@ NormPlan plan_norm(int64_t T, int d, int tensors, int min_rows, int max_threads,
     const int units = (d + 7) / 8;
     p.v = units <= max_threads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
     p.threads = ((units + p.v - 1) / p.v + 31) / 32 * 32;
-    int per_sm = 65536 / (regs * p.threads);
-    per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+    int per_sm = ctas_of(regs, p.threads);
     const uint32_t slot = static_cast<uint32_t>(tensors) * ring_pitch(d);
     while (per_sm > 1 && min_rows * slot + 2048 + 128 > kSmemPerSm / per_sm)
         --per_sm;
@@ -789,14 +800,33 @@ NormPlan plan_norm(int64_t T, int d, int tensors, int min_rows, int max_threads,
     return p;
 }
 
-// An FP8 output works longer on a row once its sums are there, and gains more
-// from a second CTA than from a fourth row in the ring: 8192 x 5120 with a
-// full gate, three rows against four (one CTA): FP8 63 and 81 us, bf16 71 and
-// 66.
+// An FP8 output works longer on a row once its sums are there, as rows inside
+// granules do, and gains more from a second CTA than from a fourth row in the
+// ring: 8192 x 5120 with a full gate, three rows against four (one CTA): FP8
+// 63 and 81 us, bf16 71 and 66.
+//
+// dense: one unit a thread in 64 registers, where that puts more CTAs on an
+// SM than 96 and those would leave it at most 16 warps; a bf16 output only up
+// to 13 warps a CTA.  Measured at 8192 rows, 96 registers against 64, channel
+// gate, bf16: 1536 columns 16.6 and 16.7 us, 2048 23.7 and 21.1, 2304 26.8
+// and 26.4, 2560 28.3 and 30.6, 2816 40 and 33, 3200 43 and 37, 3584 43.1 and
+// 42.3 (full gate 48 and 53), 4096 45 and 49; FP8: 1536 20.7 and 20.4, 2048
+// 28.9 and 25.2, 2560 33.8 and 34.8, 2816 49 and 40, 3200 53 and 45, 3584 53
+// and 46, 4096 54 and 48.
 NormPlan plan_forward(int64_t T, int d, int gate_mode, bool fp8, int sms)
 {
-    const int v1 = 8 * kMaxThreads, regs = d % 8 == 0 ? (d <= 2 * v1 ? 96 : 128) : (d <= v1 ? 104 : 128);
-    return plan_norm(T, d, gate_mode == kGateFull ? 3 : 2, fp8 ? 3 : 4, kMaxThreads, regs, sms);
+    const bool inside = d % 8 != 0;
+    const int units = (d + 7) / 8, warps = (units + 31) / 32;
+    const int sparse = ctas_of(96, 32 * warps);
+    const bool dense = !inside && units <= kMaxThreads && ctas_of(64, 32 * warps) > sparse && sparse * warps <= 16 &&
+                       (fp8 || warps <= 13);
+    // (a full gate of rows inside granules takes 99)
+    const int regs = dense ? 64
+                     : units > 2 * kMaxThreads ? 128
+                     : inside && units <= kMaxThreads && gate_mode == kGateFull && !fp8 ? 104 : 96;
+    NormPlan p = plan_norm(T, d, gate_mode == kGateFull ? 3 : 2, fp8 || inside ? 3 : 4, kMaxThreads, regs, sms);
+    p.dense = dense;
+    return p;
 }
 
 // Backward, one unit a thread: two rows at a time in 128 registers up to 512
@@ -837,14 +867,17 @@ template <class K> cudaError_t allow_smem(K kernel, int device, std::atomic<bool
 // Two rows at a time where a thread has one unit.
 constexpr int rows_at_once(int v) { return v == 1 ? 2 : 1; }
 
-template <int V, int GATE, bool FP8, bool VEC>
+template <int V, int GATE, bool FP8, bool VEC, bool DENSE = false>
 cudaError_t run_forward(const NormPlan &p, const NormForward &a, int device, cudaStream_t stream)
 {
+    if constexpr (V == 1 && VEC && !DENSE)
+        if (p.dense)
+            return run_forward<V, GATE, FP8, VEC, true>(p, a, device, stream);
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = allow_smem(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC>, device, set);
+    cudaError_t e = allow_smem(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, device, set);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
+    return launch_pdl(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, dim3(p.grid), dim3(p.threads), p.smem, stream,
                       static_cast<const uint16_t *>(a.y), static_cast<const uint16_t *>(a.h), a.g_post, a.g_pre,
                       a.gate, a.residual_scale, a.eps, a.T, static_cast<int>(a.d), p.slots,
                       static_cast<uint16_t *>(a.h_out), a.n_out, a.n_scale);

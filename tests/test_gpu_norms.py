@@ -258,3 +258,9 @@ def test_many_rows(T, d, mode):
     # gates are held at once
     test_forward(T, d, mode)
     test_backward(T, d, mode)
+
+
+@pytest.mark.parametrize("T,d", [(700, 1792), (650, 2048), (320, 2816), (300, 3200), (310, 4096)])
+@pytest.mark.parametrize("mode", MODES)
+def test_forward_with_several_ctas_an_sm(T, d, mode):
+    test_forward(T, d, mode)
