@@ -277,10 +277,13 @@ struct ScaleWalk {
     }
 };
 
+constexpr int kRowLoads = 16;  // rows' loads in flight where they are stored element by element
+
 // 64 bytes of each of a warp's 32 rows (32 bf16 or 16 fp32 columns) from the
 // rows' packed words through the staging area to the output, by TMA where
 // the output's rows allow it (`tma`), else element by element with the lanes
-// along the row.
+// along the row (777 x 5119 x 1300: 10 us, 5120 columns by TMA 9; with a branch
+// after every row 14).
 template <bool BF16>
 __device__ __forceinline__ void store_chunk(const uint32_t (&w)[16], uint32_t stage, int lane, bool tma,
                                             const CUtensorMap *map, void *out, int64_t M, int64_t N, int64_t row0,
@@ -303,29 +306,42 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&w)[16], uint32_t st
         }
     } else {
         __syncwarp();
+        // a round of loads, then their stores: no branch between them
+        const int rows = static_cast<int>(M - row0 < 32 ? M - row0 : 32);
         if constexpr (BF16) {
-            const int64_t col = col0 + lane;
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-                if (row0 + r >= M)
-                    break;
-                uint16_t h;
-                asm volatile("ld.shared.u16 %0, [%1];"
-                             : "=h"(h)
-                             : "r"(stage + 64 * r + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
-                if (col < N)
-                    static_cast<uint16_t *>(out)[(row0 + r) * N + col] = h;
+            const bool inside = col0 + lane < N;
+            uint16_t *p = static_cast<uint16_t *>(out) + row0 * N + col0 + lane;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += kRowLoads) {
+                uint16_t h[kRowLoads];
+#pragma unroll
+                for (int k = 0; k < kRowLoads; ++k) {
+                    const int r = r0 + k;
+                    asm volatile("ld.shared.u16 %0, [%1];"
+                                 : "=h"(h[k])
+                                 : "r"(stage + 64 * r + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
+                }
+#pragma unroll
+                for (int k = 0; k < kRowLoads; ++k, p += N)
+                    if (inside && r0 + k < rows)
+                        *p = h[k];
             }
         } else {  // two rows at a time
-            const int l = lane & 15;
-            const int64_t col = col0 + l;
-#pragma unroll 8
-            for (int r = lane >> 4; r < 32; r += 2) {
-                if (row0 + r >= M)
-                    break;
-                const uint32_t v = lds32(stage + 64 * r + (((l >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (l & 3));
-                if (col < N)
-                    static_cast<uint32_t *>(out)[(row0 + r) * N + col] = v;
+            const int l = lane & 15, up = lane >> 4;
+            const bool inside = col0 + l < N;
+            uint32_t *p = static_cast<uint32_t *>(out) + (row0 + up) * N + col0 + l;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 2 * kRowLoads) {
+                uint32_t v[kRowLoads];
+#pragma unroll
+                for (int k = 0; k < kRowLoads; ++k) {
+                    const int r = r0 + 2 * k + up;
+                    v[k] = lds32(stage + 64 * r + (((l >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (l & 3));
+                }
+#pragma unroll
+                for (int k = 0; k < kRowLoads; ++k, p += 2 * N)
+                    if (inside && r0 + 2 * k + up < rows)
+                        *p = v[k];
             }
         }
         __syncwarp();
