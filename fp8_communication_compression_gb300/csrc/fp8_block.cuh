@@ -24,6 +24,12 @@ namespace taco {
 // (the stride a TMA tensor map needs).
 __host__ __device__ inline int64_t fp8_pitch(int64_t n) { return (n + 15) & ~int64_t(15); }
 
+// Row length of codes that live in a call's workspace: whole 128-byte lines,
+// so that a TMA box of 128 codes touches one line a row.  (A product of 4096 x
+// 4096 over 8176 codes takes 160 us with rows of 8176 bytes, 124 with 8160, a
+// multiple of 32, 108 with 8128, of 64, and 101 over 8192.)
+__host__ __device__ inline int64_t fp8_work_pitch(int64_t n) { return (n + 127) & ~int64_t(127); }
+
 // Scales are stored as the tensor core reads them: a 512-byte piece holds the
 // bytes of 128 rows for four consecutive blocks, row r's four bytes in the
 // word at 16 (r % 32) + 4 (r / 32); pieces [ceil(rows / 128)][ceil(blocks /

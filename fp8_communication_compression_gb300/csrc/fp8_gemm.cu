@@ -903,6 +903,8 @@ template <class K> cudaError_t ensure_smem(K kernel, uint32_t bytes, int device,
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+Scales scales_of(const Fp8Operand &x, int64_t rows) { return {x.scale, ceil_div(rows, 128), x.tiles}; }
+
 struct Plan {
     bool split_kernel;
     int bn, split;
@@ -924,7 +926,7 @@ bool use_split(int64_t M, int64_t N, int64_t K, int sms)
 }
 
 template <bool BF16>
-cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
+cudaError_t run_split(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K,
                       void *out, const DeviceInfo &di, cudaStream_t stream)
 {
     const int KB = static_cast<int>(ceil_div(K, 128));
@@ -935,8 +937,8 @@ cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
     while (split < kMaxSplit && tiles * (split + 1) <= 2 * di.num_sms && KB / (split + 1) >= 2)
         ++split;
     CUtensorMap am, bm;
-    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a), K, M, K, 128, bn) != 0 ||
-        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b), K, N, K, 128, 128) != 0)
+    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a.codes), K, M, a.stride, 128, bn) != 0 ||
+        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b.codes), K, N, b.stride, 128, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
     cudaError_t e = ensure_smem(fp8_gemm_split_kernel<BF16>, kSmemLimit / 2, di.device, set);
@@ -964,17 +966,17 @@ cudaError_t run_split(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, sa, sb, out, M, N, KB, bn, stages, tiles_m,
-                              split);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, scales_of(a, M), scales_of(b, N), out, M, N, KB, bn,
+                              stages, tiles_m, split);
 }
 
 template <bool BF16>
-cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
+cudaError_t run_tiles(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K,
                       void *out, const DeviceInfo &di, cudaStream_t stream)
 {
     CUtensorMap am, bm, om;
-    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a), K, M, K, 128, 128) != 0 ||
-        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b), K, N, K, 128, 128) != 0)
+    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a.codes), K, M, a.stride, 128, 128) != 0 ||
+        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b.codes), K, N, b.stride, 128, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
     cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16>, kGemmSmem, di.device, set);
@@ -1000,16 +1002,16 @@ cudaError_t run_tiles(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, 
     w.full = rem <= di.num_sms / 2 ? tiles - rem : tiles;
     w.items = w.full + 2 * (tiles - w.full);
     const int grid = w.items < di.num_sms ? w.items : di.num_sms;
-    return launch_pdl(fp8_gemm_kernel<BF16>, dim3(grid), dim3(kGThreads), kGemmSmem, stream, am, bm, om, sa, sb, out, M,
-                      N, w, tma_out);
+    return launch_pdl(fp8_gemm_kernel<BF16>, dim3(grid), dim3(kGThreads), kGemmSmem, stream, am, bm, om, scales_of(a, M),
+                      scales_of(b, N), out, M, N, w, tma_out);
 }
 
 template <bool BF16>
-cudaError_t run_gemm(const uint8_t *a, Scales sa, const uint8_t *b, Scales sb, int64_t M, int64_t N, int64_t K,
+cudaError_t run_gemm(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K,
                      void *out, const DeviceInfo &di, cudaStream_t stream)
 {
-    return use_split(M, N, K, di.num_sms) ? run_split<BF16>(a, sa, b, sb, M, N, K, out, di, stream)
-                                          : run_tiles<BF16>(a, sa, b, sb, M, N, K, out, di, stream);
+    return use_split(M, N, K, di.num_sms) ? run_split<BF16>(a, b, M, N, K, out, di, stream)
+                                          : run_tiles<BF16>(a, b, M, N, K, out, di, stream);
 }
 
 }  // namespace
@@ -1028,9 +1030,8 @@ cudaError_t read_fp8_error(uint32_t *flags, bool clear)
     return e;
 }
 
-cudaError_t launch_fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
-                            bool b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, bool out_bf16,
-                            cudaStream_t stream)
+cudaError_t launch_fp8_gemm(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K, void *out,
+                            bool out_bf16, cudaStream_t stream)
 {
     if (K == 0)  // an empty contraction: zeros
         return cudaMemsetAsync(out, 0, static_cast<size_t>(M) * N * (out_bf16 ? 2 : 4), stream);
@@ -1038,9 +1039,7 @@ cudaError_t launch_fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint
     cudaError_t e = current_device_info(&di);
     if (e != cudaSuccess)
         return e;
-    const Scales sa{a_scale, ceil_div(M, 128), false}, sb{b_scale, ceil_div(N, 128), b_scale_tiles};
-    return out_bf16 ? run_gemm<true>(a, sa, b, sb, M, N, K, out, di, stream)
-                    : run_gemm<false>(a, sa, b, sb, M, N, K, out, di, stream);
+    return out_bf16 ? run_gemm<true>(a, b, M, N, K, out, di, stream) : run_gemm<false>(a, b, M, N, K, out, di, stream);
 }
 
 }  // namespace taco

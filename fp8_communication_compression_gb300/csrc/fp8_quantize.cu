@@ -44,12 +44,12 @@ __device__ __forceinline__ uint32_t larger_half_f32(uint32_t w)
 }
 
 // TILE: one scale per 128 x 128 tile; else row blocks (codes) and / or
-// column blocks (codes_t).
+// column blocks (codes_t).  stride, stride_t: bytes from row to row of each.
 template <bool TILE>
 __global__ void __launch_bounds__(kQThreads)
     fp8_quantize_kernel(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t col_tiles,
                         uint8_t *__restrict__ codes, uint8_t *__restrict__ scale, uint8_t *__restrict__ codes_t,
-                        uint8_t *__restrict__ scale_t)
+                        uint8_t *__restrict__ scale_t, int64_t stride, int64_t stride_t)
 {
     __shared__ uint4 tile_t[128 * 8];       // transposed codes: [column][8 chunks of 16 rows], swizzled
     __shared__ uint4 col_max[8][16];        // per warp: packed maxima of the 128 columns
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kQThreads)
     const int64_t tr = blockIdx.x / col_tiles, tc = blockIdx.x - tr * col_tiles;
     const int64_t r0 = tr * 128, c0 = tc * 128;
     const int64_t r = r0 + 8 * rg, c = c0 + 8 * cc;
-    const int64_t pitch = fp8_pitch(cols), pitch_t = fp8_pitch(rows);
+    const int64_t pitch = fp8_pitch(cols), pitch_t = fp8_pitch(rows);  // codes and zeros written of a row
     if (gridDim.x <= kTriggerCtas)
         pdl_trigger();
     pdl_wait();
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kQThreads)
                                        bf16hi_to_f32(b) * f);
             }
             if (r + i < rows && c < pitch)
-                *reinterpret_cast<uint2 *>(codes + (r + i) * pitch + c) = make_uint2(o[0], o[1]);
+                *reinterpret_cast<uint2 *>(codes + (r + i) * stride + c) = make_uint2(o[0], o[1]);
         }
     }
 
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kQThreads)
         for (int it = 0; it < 4; ++it) {
             const int col = 32 * it + (tid >> 3), ch = tid & 7;
             if (c0 + col < cols && r0 + 16 * ch < pitch_t)
-                *reinterpret_cast<uint4 *>(codes_t + (c0 + col) * pitch_t + r0 + 16 * ch) =
+                *reinterpret_cast<uint4 *>(codes_t + (c0 + col) * stride_t + r0 + 16 * ch) =
                     tile_t[col * 8 + (ch ^ ((col >> 3) & 7))];
         }
     }
@@ -235,15 +235,16 @@ __global__ void __launch_bounds__(kQThreads)
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, bool tiles, uint8_t *codes,
-                                uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, cudaStream_t stream)
+                                uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, int64_t stride, int64_t stride_t,
+                                cudaStream_t stream)
 {
     const int64_t col_tiles = (cols + 127) / 128, n = (rows + 127) / 128 * col_tiles;
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
     if (tiles)
         return launch_pdl(fp8_quantize_kernel<true>, dim3(static_cast<unsigned>(n)), kQThreads, 0, stream, x, rows,
-                          cols, col_tiles, codes, scale, codes_t, scale_t);
+                          cols, col_tiles, codes, scale, codes_t, scale_t, stride, stride_t);
     return launch_pdl(fp8_quantize_kernel<false>, dim3(static_cast<unsigned>(n)), kQThreads, 0, stream, x, rows, cols,
-                      col_tiles, codes, scale, codes_t, scale_t);
+                      col_tiles, codes, scale, codes_t, scale_t, stride, stride_t);
 }
 
 }  // namespace taco

@@ -96,15 +96,23 @@ cudaError_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, uint64_t *byte
 
 // Block-scaled FP8 operands (fp8_quantize.cu; format in fp8_block.cuh): codes
 // [rows][pitch(cols)] with their scales, and / or codes_t
-// [cols][pitch(rows)] with scale_t; null codes: that direction is left out.  tiles: one byte per 128 x 128 tile,
+// [cols][pitch(rows)] with scale_t, in rows of stride and stride_t bytes; null
+// codes: that direction is left out.  tiles: one byte per 128 x 128 tile,
 // scale [ceil(cols / 128)][ceil(rows / 128)] and scale_t its transpose.
 cudaError_t launch_fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, bool tiles, uint8_t *codes,
-                                uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, cudaStream_t stream);
-// out[M][N] = A B^T of such operands (fp8_gemm.cu): codes a [M][K], b [N][K]
-// (K the padded row length, a multiple of 16).
-cudaError_t launch_fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
-                            bool b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, bool out_bf16,
-                            cudaStream_t stream);
+                                uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, int64_t stride, int64_t stride_t,
+                                cudaStream_t stream);
+// An operand of a product: codes in rows of `stride` bytes, and their scales
+// (tiles: one byte per 128 x 128 tile).
+struct Fp8Operand {
+    const uint8_t *codes, *scale;
+    int64_t stride;
+    bool tiles;
+};
+// out[M][N] = A B^T (fp8_gemm.cu) over K codes of A's M and B's N rows (K and
+// the strides multiples of 16; A without tiles).
+cudaError_t launch_fp8_gemm(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K, void *out,
+                            bool out_bf16, cudaStream_t stream);
 // fp8_linear for few tokens without a workspace (fp8_decode.cu), where
 // fp8_decode_takes(M, K); scale: a weight's (128 x 128 tiles).
 bool fp8_decode_takes(int64_t M, int64_t K);

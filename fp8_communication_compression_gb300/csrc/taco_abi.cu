@@ -583,6 +583,7 @@ static taco_status fp8_quantize_any(const void *x, int64_t rows, int64_t cols, b
     if (!apart(outs, 4, ins, 1))
         return TACO_ERR_INVALID_ARG;
     return from_cuda(taco::launch_fp8_quantize(x, rows, cols, tiles, codes, scale, codes_t, scale_t,
+                                               taco::fp8_pitch(cols), taco::fp8_pitch(rows),
                                                reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -622,16 +623,17 @@ taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b,
                                                                        : taco::fp8_scale_bytes(N, K))}};
     if (!apart(outs, 1, ins, 4))
         return TACO_ERR_INVALID_ARG;
-    return from_cuda(taco::launch_fp8_gemm(a, a_scale, b, b_scale, b_scale_tiles != 0, M, N, K, out, out_is_bf16 != 0,
-                                           reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(taco::launch_fp8_gemm({a, a_scale, K, false}, {b, b_scale, K, b_scale_tiles != 0}, M, N, K, out,
+                                           out_is_bf16 != 0, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // The pieces of a linear layer's workspace, each 256-byte aligned: a
-// quantised matrix [rows][cols] is its codes and its scales.
+// quantised matrix [rows][cols] is its codes, in rows of fp8_work_pitch(cols)
+// bytes, and its scales.
 static uint64_t fp8_piece(int64_t rows, int64_t cols, uint64_t *scale_at)
 {
     const auto up = [](uint64_t v) { return (v + 255) & ~uint64_t(255); };
-    const uint64_t codes = up(static_cast<uint64_t>(rows) * taco::fp8_pitch(cols));
+    const uint64_t codes = up(static_cast<uint64_t>(rows) * taco::fp8_work_pitch(cols));
     if (scale_at)
         *scale_at = codes;
     return codes + up(taco::fp8_scale_bytes(rows, cols));
@@ -672,10 +674,16 @@ taco_status fp8_linear(const void *x_bf16, const uint8_t *codes, const uint8_t *
         return from_cuda(taco::launch_fp8_decode(x_bf16, codes, scale, M, N, K, y, y_is_bf16 != 0,
                                                  reinterpret_cast<cudaStream_t>(stream)));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t kw = taco::fp8_work_pitch(K);
     fp8_piece(M, K, &scale_at);
-    if (K > 0 && (st = fp8_quantize(x_bf16, M, K, ws, ws + scale_at, nullptr, nullptr, stream)) != TACO_OK)
-        return st;
-    return fp8_gemm(ws, ws + scale_at, codes, scale, 1, M, N, pk, y, y_is_bf16, stream);
+    cudaError_t e = cudaSuccess;
+    if (K > 0)
+        e = taco::launch_fp8_quantize(x_bf16, M, K, false, ws, ws + scale_at, nullptr, nullptr, kw, 0, s);
+    if (e == cudaSuccess)
+        e = taco::launch_fp8_gemm({ws, ws + scale_at, kw, false}, {codes, scale, static_cast<int64_t>(pk), true}, M, N,
+                                  pk, y, y_is_bf16 != 0, s);
+    return from_cuda(e);
 }
 
 taco_status fp8_linear_backward(const void *dy_bf16, const void *x_bf16, const uint8_t *codes_t,
@@ -719,14 +727,18 @@ taco_status fp8_linear_backward(const void *dy_bf16, const void *x_bf16, const u
     uint64_t s0 = 0, s1 = 0, s2 = 0;
     uint8_t *q = ws, *qt = q + fp8_piece(M, N, &s0), *xt = qt + fp8_piece(N, M, &s1);
     fp8_piece(K, M, &s2);
-    if ((st = fp8_quantize(dy_bf16, M, N, want_dx ? q : nullptr, want_dx ? q + s0 : nullptr, want_dw ? qt : nullptr,
-                           want_dw ? qt + s1 : nullptr, stream)) != TACO_OK)
-        return st;
-    if (want_dw && (st = fp8_quantize(x_bf16, M, K, nullptr, nullptr, xt, xt + s2, stream)) != TACO_OK)
-        return st;
-    if (want_dx && (st = fp8_gemm(q, q + s0, codes_t, scale_t, 1, M, K, pn, dx_bf16, 1, stream)) != TACO_OK)
-        return st;
-    return want_dw ? fp8_gemm(qt, qt + s1, xt, xt + s2, 0, N, K, pm, dw, dw_is_bf16, stream) : TACO_OK;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t nw = taco::fp8_work_pitch(N), mw = taco::fp8_work_pitch(M);
+    cudaError_t e = taco::launch_fp8_quantize(dy_bf16, M, N, false, want_dx ? q : nullptr, want_dx ? q + s0 : nullptr,
+                                              want_dw ? qt : nullptr, want_dw ? qt + s1 : nullptr, nw, mw, s);
+    if (e == cudaSuccess && want_dw)
+        e = taco::launch_fp8_quantize(x_bf16, M, K, false, nullptr, nullptr, xt, xt + s2, 0, mw, s);
+    if (e == cudaSuccess && want_dx)
+        e = taco::launch_fp8_gemm({q, q + s0, nw, false}, {codes_t, scale_t, static_cast<int64_t>(pn), true}, M, K, pn,
+                                  dx_bf16, true, s);
+    if (e == cudaSuccess && want_dw)
+        e = taco::launch_fp8_gemm({qt, qt + s1, mw, false}, {xt, xt + s2, mw, false}, N, K, pm, dw, dw_is_bf16 != 0, s);
+    return from_cuda(e);
 }
 
 // Shared checks of the norms around a block.
