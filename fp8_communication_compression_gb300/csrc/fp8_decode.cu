@@ -8,7 +8,8 @@
 // 16 rows of the weight at a time, warp w the blocks w, w + 8, ... of them; a
 // lane loads 16 bytes of two rows, which are the operands of warp-level
 // E4M3 MMAs (16 rows x 8 tokens x 32 values) as they lie in memory, since the
-// contraction's order inside a block is free.  (Decoding the codes in
+// contraction's order inside a block is free.  One token, 4096 x 4096: 5.5 us
+// of device time among others of its kind.  (Decoding the codes in
 // registers and multiplying them one by one took 17.8 us at 16384 x 4096 for
 // one token and 44 for four, bound by instructions.)  A block's four MMAs
 // start from zero; its sum is scaled and added in fp32, and the warps' sums

@@ -13,9 +13,9 @@
 // through a 16 KB tile whose 16-byte chunks are swizzled by the column
 // group, so that both its 8-byte writes and its 16-byte reads take the
 // fewest possible shared-memory cycles.
-// Measured at 8192 x 16384: rows 66 us (6070 GB/s), columns 73, both 105
-// (5100 GB/s), which the conversions bound, not the memory: two to an
-// element.  Where rows are no whole 16-byte granules a thread joins its
+// Measured at 8192 x 16384: rows 66 us (6120 GB/s), columns 73, both 102
+// (5260 GB/s; then it is instructions, 0.71 of the issue slots, that bound
+// it).  Where rows are no whole 16-byte granules a thread joins its
 // eight columns from two granules: 8192 x 16380 in 99, 108 and 138 us (118,
 // 129 and 158 with loads of single elements).
 
