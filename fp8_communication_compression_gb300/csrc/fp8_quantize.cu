@@ -44,18 +44,25 @@ __device__ __forceinline__ uint32_t larger_half_f32(uint32_t w)
 }
 
 // TILE: one scale per 128 x 128 tile; else row blocks (codes) and / or
-// column blocks (codes_t).  stride, stride_t: bytes from row to row of each.
+// column blocks (codes_t).  The CTAs from `second` on take the other matrix
+// (a backward pass quantises two in one launch).
 template <bool TILE>
 __global__ void __launch_bounds__(kQThreads)
-    fp8_quantize_kernel(const uint16_t *__restrict__ x, int64_t rows, int64_t cols, int64_t col_tiles,
-                        uint8_t *__restrict__ codes, uint8_t *__restrict__ scale, uint8_t *__restrict__ codes_t,
-                        uint8_t *__restrict__ scale_t, int64_t stride, int64_t stride_t)
+    fp8_quantize_kernel(const __grid_constant__ Fp8Quantize first, const __grid_constant__ Fp8Quantize other,
+                        unsigned second)
 {
+    const bool is_other = !TILE && blockIdx.x >= second;
+    const Fp8Quantize &job = is_other ? other : first;
+    const uint16_t *__restrict__ x = static_cast<const uint16_t *>(job.x);
+    uint8_t *__restrict__ codes = job.codes, *__restrict__ scale = job.scale;
+    uint8_t *__restrict__ codes_t = job.codes_t, *__restrict__ scale_t = job.scale_t;
+    const int64_t rows = job.rows, cols = job.cols, stride = job.stride, stride_t = job.stride_t;
+    const int64_t col_tiles = (cols + 127) / 128, tile = blockIdx.x - (is_other ? second : 0u);
     __shared__ uint4 tile_t[128 * 8];       // transposed codes: [column][8 chunks of 16 rows], swizzled
     __shared__ uint4 col_max[8][16];        // per warp: packed maxima of the 128 columns
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cc = tid & 15, rg = tid >> 4;  // this thread's columns 8 cc .. + 7 and rows 8 rg .. + 7
-    const int64_t tr = blockIdx.x / col_tiles, tc = blockIdx.x - tr * col_tiles;
+    const int64_t tr = tile / col_tiles, tc = tile - tr * col_tiles;
     const int64_t r0 = tr * 128, c0 = tc * 128;
     const int64_t r = r0 + 8 * rg, c = c0 + 8 * cc;
     const int64_t pitch = fp8_pitch(cols), pitch_t = fp8_pitch(rows);  // codes and zeros written of a row
@@ -234,17 +241,22 @@ __global__ void __launch_bounds__(kQThreads)
 
 }  // namespace
 
-cudaError_t launch_fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, bool tiles, uint8_t *codes,
-                                uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, int64_t stride, int64_t stride_t,
-                                cudaStream_t stream)
+static unsigned tiles_of(const Fp8Quantize &q)
 {
-    const int64_t col_tiles = (cols + 127) / 128, n = (rows + 127) / 128 * col_tiles;
-    const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
-    if (tiles)
-        return launch_pdl(fp8_quantize_kernel<true>, dim3(static_cast<unsigned>(n)), kQThreads, 0, stream, x, rows,
-                          cols, col_tiles, codes, scale, codes_t, scale_t, stride, stride_t);
-    return launch_pdl(fp8_quantize_kernel<false>, dim3(static_cast<unsigned>(n)), kQThreads, 0, stream, x, rows, cols,
-                      col_tiles, codes, scale, codes_t, scale_t, stride, stride_t);
+    return static_cast<unsigned>((q.rows + 127) / 128 * ((q.cols + 127) / 128));
+}
+
+cudaError_t launch_fp8_quantize(const Fp8Quantize &q, bool tiles, cudaStream_t stream)
+{
+    const unsigned n = tiles_of(q);
+    return tiles ? launch_pdl(fp8_quantize_kernel<true>, dim3(n), kQThreads, 0, stream, q, q, n)
+                 : launch_pdl(fp8_quantize_kernel<false>, dim3(n), kQThreads, 0, stream, q, q, n);
+}
+
+cudaError_t launch_fp8_quantize_two(const Fp8Quantize &a, const Fp8Quantize &b, cudaStream_t stream)
+{
+    const unsigned n = tiles_of(a);
+    return launch_pdl(fp8_quantize_kernel<false>, dim3(n + tiles_of(b)), kQThreads, 0, stream, a, b, n);
 }
 
 }  // namespace taco

@@ -94,14 +94,20 @@ cudaError_t launch_gemm_laaq_quantize(const void *a_bf16, const void *b_bf16, in
 // (0 when it takes none).
 cudaError_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, uint64_t *bytes);
 
-// Block-scaled FP8 operands (fp8_quantize.cu; format in fp8_block.cuh): codes
-// [rows][pitch(cols)] with their scales, and / or codes_t
-// [cols][pitch(rows)] with scale_t, in rows of stride and stride_t bytes; null
-// codes: that direction is left out.  tiles: one byte per 128 x 128 tile,
-// scale [ceil(cols / 128)][ceil(rows / 128)] and scale_t its transpose.
-cudaError_t launch_fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, bool tiles, uint8_t *codes,
-                                uint8_t *scale, uint8_t *codes_t, uint8_t *scale_t, int64_t stride, int64_t stride_t,
-                                cudaStream_t stream);
+// Block-scaled FP8 operands (fp8_quantize.cu; format in fp8_block.cuh) of a
+// bf16 matrix x: codes [rows][stride] with their scales, and / or codes_t
+// [cols][stride_t] with scale_t; null codes: that direction is left out.
+// tiles: one byte per 128 x 128 tile, scale [ceil(cols / 128)][ceil(rows /
+// 128)] and scale_t its transpose.
+struct Fp8Quantize {
+    const void *x;
+    int64_t rows, cols;
+    uint8_t *codes, *scale, *codes_t, *scale_t;
+    int64_t stride, stride_t;
+};
+cudaError_t launch_fp8_quantize(const Fp8Quantize &q, bool tiles, cudaStream_t stream);
+// Two matrices in one launch (together less than 2^31 tiles of 128 x 128).
+cudaError_t launch_fp8_quantize_two(const Fp8Quantize &a, const Fp8Quantize &b, cudaStream_t stream);
 // An operand of a product: codes in rows of `stride` bytes, and their scales
 // (tiles: one byte per 128 x 128 tile).
 struct Fp8Operand {

@@ -582,9 +582,9 @@ static taco_status fp8_quantize_any(const void *x, int64_t rows, int64_t cols, b
     const Span ins[1] = {{x, 2 * r * c}};
     if (!apart(outs, 4, ins, 1))
         return TACO_ERR_INVALID_ARG;
-    return from_cuda(taco::launch_fp8_quantize(x, rows, cols, tiles, codes, scale, codes_t, scale_t,
-                                               taco::fp8_pitch(cols), taco::fp8_pitch(rows),
-                                               reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(taco::launch_fp8_quantize({x, rows, cols, codes, scale, codes_t, scale_t, taco::fp8_pitch(cols),
+                                                taco::fp8_pitch(rows)},
+                                               tiles, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 taco_status fp8_quantize(const void *x_bf16, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scale,
@@ -679,7 +679,7 @@ taco_status fp8_linear(const void *x_bf16, const uint8_t *codes, const uint8_t *
     fp8_piece(M, K, &scale_at);
     cudaError_t e = cudaSuccess;
     if (K > 0)
-        e = taco::launch_fp8_quantize(x_bf16, M, K, false, ws, ws + scale_at, nullptr, nullptr, kw, 0, s);
+        e = taco::launch_fp8_quantize({x_bf16, M, K, ws, ws + scale_at, nullptr, nullptr, kw, 0}, false, s);
     if (e == cudaSuccess)
         e = taco::launch_fp8_gemm({ws, ws + scale_at, kw, false}, {codes, scale, static_cast<int64_t>(pk), true}, M, N,
                                   pk, y, y_is_bf16 != 0, s);
@@ -729,10 +729,11 @@ taco_status fp8_linear_backward(const void *dy_bf16, const void *x_bf16, const u
     fp8_piece(K, M, &s2);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int64_t nw = taco::fp8_work_pitch(N), mw = taco::fp8_work_pitch(M);
-    cudaError_t e = taco::launch_fp8_quantize(dy_bf16, M, N, false, want_dx ? q : nullptr, want_dx ? q + s0 : nullptr,
-                                              want_dw ? qt : nullptr, want_dw ? qt + s1 : nullptr, nw, mw, s);
-    if (e == cudaSuccess && want_dw)
-        e = taco::launch_fp8_quantize(x_bf16, M, K, false, nullptr, nullptr, xt, xt + s2, 0, mw, s);
+    const taco::Fp8Quantize quantize_dy = {dy_bf16, M, N, want_dx ? q : nullptr, want_dx ? q + s0 : nullptr,
+                                           want_dw ? qt : nullptr, want_dw ? qt + s1 : nullptr, nw, mw};
+    cudaError_t e = want_dw ? taco::launch_fp8_quantize_two(
+                                  quantize_dy, {x_bf16, M, K, nullptr, nullptr, xt, xt + s2, 0, mw}, s)
+                            : taco::launch_fp8_quantize(quantize_dy, false, s);
     if (e == cudaSuccess && want_dx)
         e = taco::launch_fp8_gemm({q, q + s0, nw, false}, {codes_t, scale_t, static_cast<int64_t>(pn), true}, M, K, pn,
                                   dx_bf16, true, s);
