@@ -28,11 +28,12 @@
 // of its columns in registers.  Rows arrive by bulk copies into a ring of row
 // slots in shared memory, several rows ahead of those being worked on, so
 // the loads do not wait for the two block-wide sums that every row needs;
-// outputs go straight from registers in 16-byte stores.  Two rows at a time
-// (up to 4096 columns) share a barrier and hide each other's latencies.
+// outputs go straight from registers in 16-byte stores.  With one unit a
+// thread two rows at a time share a barrier and hide each other's latencies.
 // Measured with a channel gate at 8192 rows: forward 4096 columns 44 us (6050
-// GB/s), to FP8 48 (4900), 5120 57 (5850), full gate 64 (6550); backward 4096
-// columns 76 (5300), 2560 59 (4230), 5120 104 (4850).
+// GB/s), to FP8 48 (4900), 2048 columns 17 (7750, part of it in L2), 5120 57
+// (5850), full gate 64 (6550); backward 4096 columns 76 (5300), 2560 59
+// (4230), 5120 104 (4850).
 //
 // Rows that are not a multiple of 16 bytes start anywhere inside a 16-byte
 // granule of memory.  A CTA's rows are a multiple of eight apart, so all of
@@ -777,15 +778,14 @@ int ctas_of(int regs, int threads)
     return n < 1 ? 1 : n > 8 ? 8 : n;
 }
 
-// tensors: rows to a slot; min_rows: the fewest rows in the ring of a CTA that
-// shares its SM; max_threads: the most threads with one unit each;
-// regs: the registers a thread of the kernel takes, for how many CTAs share
-// an SM.
-NormPlan plan_norm(int64_t T, int d, int tensors, int min_rows, int max_threads, int regs, int sms)
+// v: units a thread; tensors: rows to a slot; min_rows: the fewest rows in the
+// ring of a CTA that shares its SM; regs: the registers a thread of the
+// kernel takes, for how many CTAs share an SM.
+NormPlan plan_norm(int64_t T, int d, int v, int tensors, int min_rows, int regs, int sms)
 {
     NormPlan p = {};
     const int units = (d + 7) / 8;
-    p.v = units <= max_threads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
+    p.v = v;
     p.threads = ((units + p.v - 1) / p.v + 31) / 32 * 32;
     int per_sm = ctas_of(regs, p.threads);
     const uint32_t slot = static_cast<uint32_t>(tensors) * ring_pitch(d);
@@ -808,26 +808,29 @@ NormPlan plan_norm(int64_t T, int d, int tensors, int min_rows, int max_threads,
 // ring: 8192 x 5120 with a full gate, three rows against four (one CTA): FP8
 // 63 and 81 us, bf16 71 and 66.
 //
-// dense: one unit a thread in 64 registers, where that puts more CTAs on an
-// SM than 96 and those would leave it at most 16 warps; a bf16 output only up
-// to 13 warps a CTA.  Measured at 8192 rows, 96 registers against 64, channel
-// gate, bf16: 1536 columns 16.6 and 16.7 us, 2048 23.7 and 21.1, 2304 26.8
-// and 26.4, 2560 28.3 and 30.6, 2816 40 and 33, 3200 43 and 37, 3584 43.1 and
-// 42.3 (full gate 48 and 53), 4096 45 and 49; FP8: 1536 20.7 and 20.4, 2048
-// 28.9 and 25.2, 2560 33.8 and 34.8, 2816 49 and 40, 3200 53 and 45, 3584 53
-// and 46, 4096 54 and 48.
+//
+// One unit a thread and two rows at a time, or two units and one row, with
+// more and smaller CTAs.  Measured at 8192 rows, channel gate, one unit
+// against two: bf16 1280 columns 13.3 and 13.5 us, 1536 16.5 and 13.2, 2048
+// 21.3 and 17.3, 2560 28.0 and 28.8, 3200 37.0 and 34.6, 3584 43.0 and 39.9,
+// 4096 44.4 and 48.0; FP8 16.3 and 17.1, 20.7 and 16.9, 25.1 and 21.1, 33.9
+// and 27.9, 45.3 and 43.5, 45.7 and 43.5, 48.2 and 44.3 (but both outputs
+// have to come from the same sums).  With a full gate two units stop paying
+// at 3584 columns (47 and 51 us); rows inside granules at 384 units (2945
+// columns 85 and 79 us, 3073 90 and 99).
+//
+// dense: to FP8 with one unit a thread above 448 units (4096 columns: 54 us
+// in 96 registers, one CTA an SM, 48 in 64, two).
 NormPlan plan_forward(int64_t T, int d, int gate_mode, bool fp8, int sms)
 {
     const bool inside = d % 8 != 0;
-    const int units = (d + 7) / 8, warps = (units + 31) / 32;
-    const int sparse = ctas_of(96, 32 * warps);
-    const bool dense = !inside && units <= kMaxThreads && ctas_of(64, 32 * warps) > sparse && sparse * warps <= 16 &&
-                       (fp8 || warps <= 13);
+    const int units = (d + 7) / 8;
+    const int v = units > 2 * kMaxThreads ? 4
+                  : units > kMaxThreads || (units > 160 && units <= (inside ? 384 : 448)) ? 2 : 1;
+    const bool dense = fp8 && !inside && v == 1 && units > 448;
     // (a full gate of rows inside granules takes 99)
-    const int regs = dense ? 64
-                     : units > 2 * kMaxThreads ? 128
-                     : inside && units <= kMaxThreads && gate_mode == kGateFull && !fp8 ? 104 : 96;
-    NormPlan p = plan_norm(T, d, gate_mode == kGateFull ? 3 : 2, fp8 || inside ? 3 : 4, kMaxThreads, regs, sms);
+    const int regs = dense ? 64 : v == 4 ? 128 : inside && v == 1 && gate_mode == kGateFull && !fp8 ? 104 : 96;
+    NormPlan p = plan_norm(T, d, v, gate_mode == kGateFull ? 3 : 2, fp8 || inside ? 3 : 4, regs, sms);
     p.dense = dense;
     return p;
 }
@@ -850,7 +853,8 @@ bool one_row(int64_t T, int d, int sms)
 NormPlan plan_backward(int64_t T, int d, int gate_mode, int sms)
 {
     const bool one = one_row(T, d, sms);
-    NormPlan p = plan_norm(T, d, gate_mode == kGateFull ? 5 : 4, 4, one ? kWide : kMaxThreads, one ? 80 : 128, sms);
+    const int units = (d + 7) / 8, v = one || units <= kMaxThreads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
+    NormPlan p = plan_norm(T, d, v, gate_mode == kGateFull ? 5 : 4, 4, one ? 80 : 128, sms);
     p.one_row = one;
     return p;
 }
@@ -873,7 +877,7 @@ constexpr int rows_at_once(int v) { return v == 1 ? 2 : 1; }
 template <int V, int GATE, bool FP8, bool VEC, bool DENSE = false>
 cudaError_t run_forward(const NormPlan &p, const NormForward &a, int device, cudaStream_t stream)
 {
-    if constexpr (V == 1 && VEC && !DENSE)
+    if constexpr (V == 1 && FP8 && VEC && !DENSE)
         if (p.dense)
             return run_forward<V, GATE, FP8, VEC, true>(p, a, device, stream);
     static std::atomic<bool> set[kMaxDevices];

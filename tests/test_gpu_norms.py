@@ -264,3 +264,10 @@ def test_many_rows(T, d, mode):
 @pytest.mark.parametrize("mode", MODES)
 def test_forward_with_several_ctas_an_sm(T, d, mode):
     test_forward(T, d, mode)
+
+
+@pytest.mark.parametrize("T,d", [(900, 1288), (800, 1536), (700, 2304), (500, 3584), (400, 3592), (700, 1537),
+                                 (400, 2945), (350, 3081)])
+@pytest.mark.parametrize("mode", MODES)
+def test_forward_with_one_or_two_units_a_thread(T, d, mode):
+    test_forward(T, d, mode)
