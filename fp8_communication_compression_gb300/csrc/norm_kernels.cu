@@ -103,11 +103,12 @@ __device__ __forceinline__ uint4 pack8(const F8 &x)
                       f32x2_to_bf16x2(x.v[2].x, x.v[2].y), f32x2_to_bf16x2(x.v[3].x, x.v[3].y));
 }
 
-// Columns c .. c + 7 of fp32 vectors of d values, zeros past the end.
+// Columns c .. c + 7 of fp32 vectors of d values, zeros past the end (VEC: d is
+// a multiple of 8).
 template <bool VEC> __device__ __forceinline__ F8 load_f32x8(const float *p, int c, int d)
 {
     F8 x;
-    if (VEC) {
+    if (VEC || c + 8 <= d || c >= d) {
         float4 a = make_float4(0, 0, 0, 0), b = a;
         if (c < d) {
             a = __ldg(reinterpret_cast<const float4 *>(p + c));
@@ -828,8 +829,7 @@ NormPlan plan_forward(int64_t T, int d, int gate_mode, bool fp8, int sms)
     const int v = units > 2 * kMaxThreads ? 4
                   : units > kMaxThreads || (units > 160 && units <= (inside ? 384 : 448)) ? 2 : 1;
     const bool dense = fp8 && !inside && v == 1 && units > 448;
-    // (a full gate of rows inside granules takes 99)
-    const int regs = dense ? 64 : v == 4 ? 128 : inside && v == 1 && gate_mode == kGateFull && !fp8 ? 104 : 96;
+    const int regs = dense ? 64 : v == 4 ? 128 : 96;
     NormPlan p = plan_norm(T, d, v, gate_mode == kGateFull ? 3 : 2, fp8 || inside ? 3 : 4, regs, sms);
     p.dense = dense;
     return p;
