@@ -908,6 +908,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Scales scales_of(const Fp8Operand &x, int64_t rows) { return {x.scale, ceil_div(rows, 128), x.tiles}; }
 
+// Boxes of 128 codes of `box_rows` rows.
+int operand_map(CUtensorMap *map, const Fp8Operand &x, int64_t rows, int64_t K, int box_rows)
+{
+    return encode_tensor_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(x.codes), K, rows, x.stride,
+                                128, box_rows);
+}
+
 struct Plan {
     bool split_kernel;
     int bn, split;
@@ -940,8 +947,7 @@ cudaError_t run_split(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64
     while (split < kMaxSplit && tiles * (split + 1) <= 2 * di.num_sms && KB / (split + 1) >= 2)
         ++split;
     CUtensorMap am, bm;
-    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a.codes), K, M, a.stride, 128, bn) != 0 ||
-        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b.codes), K, N, b.stride, 128, 128) != 0)
+    if (operand_map(&am, a, M, K, bn) != 0 || operand_map(&bm, b, N, K, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
     cudaError_t e = ensure_smem(fp8_gemm_split_kernel<BF16>, kSmemLimit / 2, di.device, set);
@@ -969,8 +975,8 @@ cudaError_t run_split(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, scales_of(a, M), scales_of(b, N), out, M, N, KB, bn,
-                              stages, tiles_m, split);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, scales_of(a, M), scales_of(b, N), out, M, N,
+                              KB, bn, stages, tiles_m, split);
 }
 
 template <bool BF16>
@@ -978,8 +984,7 @@ cudaError_t run_tiles(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64
                       void *out, const DeviceInfo &di, cudaStream_t stream)
 {
     CUtensorMap am, bm, om;
-    if (encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(a.codes), K, M, a.stride, 128, 128) != 0 ||
-        encode_tensor_map_2d(&bm, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(b.codes), K, N, b.stride, 128, 128) != 0)
+    if (operand_map(&am, a, M, K, 128) != 0 || operand_map(&bm, b, N, K, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
     cudaError_t e = ensure_smem(fp8_gemm_kernel<BF16>, kGemmSmem, di.device, set);
@@ -1005,8 +1010,8 @@ cudaError_t run_tiles(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64
     w.full = rem <= di.num_sms / 2 ? tiles - rem : tiles;
     w.items = w.full + 2 * (tiles - w.full);
     const int grid = w.items < di.num_sms ? w.items : di.num_sms;
-    return launch_pdl(fp8_gemm_kernel<BF16>, dim3(grid), dim3(kGThreads), kGemmSmem, stream, am, bm, om, scales_of(a, M),
-                      scales_of(b, N), out, M, N, w, tma_out);
+    return launch_pdl(fp8_gemm_kernel<BF16>, dim3(grid), dim3(kGThreads), kGemmSmem, stream, am, bm, om,
+                      scales_of(a, M), scales_of(b, N), out, M, N, w, tma_out);
 }
 
 template <bool BF16>

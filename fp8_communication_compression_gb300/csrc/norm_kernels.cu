@@ -342,7 +342,8 @@ __device__ __forceinline__ void ring_init(RowRing<NT, VEC> &ring, uint8_t *smem,
 
 // Tokens' gates of the CTA's next kGateRows rows in shared memory (loaded row
 // by row they stood in every round's way: 8192 x 4096 forward 50 us against 46,
-// backward 96 against 79, 8192 x 5120 backward 126 against 111).  The arrays in static shared memory take at most 2 KB together.
+// backward 96 against 79, 8192 x 5120 backward 126 against 111).  The arrays in
+// static shared memory take at most 2 KB together.
 constexpr int kGateRows = 128;
 struct TokenGates {
     float *at;
@@ -488,7 +489,8 @@ __global__ void __launch_bounds__(V == 2 && !VEC ? 640 : kMaxThreads, DENSE ? 2 
                     uint32_t m = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        m = max(m, max(__float_as_uint(n.v[j].x) & 0x7FFFFFFFu, __float_as_uint(n.v[j].y) & 0x7FFFFFFFu));
+                        m = max(m, max(__float_as_uint(n.v[j].x) & 0x7FFFFFFFu,
+                                       __float_as_uint(n.v[j].y) & 0x7FFFFFFFu));
 #pragma unroll
                     for (int k = 8; k >= 1; k >>= 1)
                         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
@@ -654,7 +656,8 @@ __global__ void __launch_bounds__(MAXT, 1)
                         a_post[v].v[j] = fma2(t, w.v[j], a_post[v].v[j]);
                     } else {
                         dd = fma2(t, gp[0].v[j], dd);
-                        a_post[v].v[j] = GATE == kGateToken ? fma2(gt2, t, a_post[v].v[j]) : __fadd2_rn(a_post[v].v[j], t);
+                        a_post[v].v[j] = GATE == kGateToken ? fma2(gt2, t, a_post[v].v[j])
+                                                            : __fadd2_rn(a_post[v].v[j], t);
                     }
                 }
                 if constexpr (GATE == kGateFull)
@@ -884,7 +887,8 @@ cudaError_t run_forward(const NormPlan &p, const NormForward &a, int device, cud
     cudaError_t e = allow_smem(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, device, set);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, dim3(p.grid), dim3(p.threads), p.smem, stream,
+    return launch_pdl(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, dim3(p.grid), dim3(p.threads),
+                      p.smem, stream,
                       static_cast<const uint16_t *>(a.y), static_cast<const uint16_t *>(a.h), a.g_post, a.g_pre,
                       a.gate, a.residual_scale, a.eps, a.T, static_cast<int>(a.d), p.slots,
                       static_cast<uint16_t *>(a.h_out), a.n_out, a.n_scale);
