@@ -48,12 +48,16 @@
 //   the columns.  No workspace, no atomics, and a fixed summation order.
 //
 // Every mbarrier wait is time-limited; one that runs out sets a flag that
-// taco_device_error() reads, and the CTA winds down.
+// taco_device_error() reads, and the CTA winds down.  Tensor memory is never
+// waited for: no SM holds more CTAs of a kernel than have columns (fp8_plan.h,
+// and kGemmSmem leaves room for one), the next grid may start only after a CTA
+// has its columns, and a cluster's CTAs give them back before they meet.
 
 #include <atomic>
 
 #include "device_utils.cuh"
 #include "fp8_block.cuh"
+#include "fp8_plan.h"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -66,9 +70,6 @@ namespace {
 
 constexpr uint32_t kErrFp8 = 64u;
 constexpr int kThreads = 224;  // split kernel's warps: 0 TMA, 1 MMA, 2-5 epilogue, 6 scales
-constexpr int kMaxStages = 10;
-constexpr uint32_t kTileA = 128 * 128;
-constexpr uint32_t kSmemLimit = 232448;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr)
 {
@@ -95,7 +96,6 @@ struct Scales {
 // Shared-memory layout: a ring of `stages` slots for operand pieces of 128
 // and `bn` rows, `extra` bytes, a ring of scale slots of `sf_bytes` (128 A or
 // lane-side rows, then the others), barriers.
-constexpr int kScaleSlots = 4;
 struct Ring {
     uint32_t base, stage_bytes, scales, sf_bytes, extra, bars;
     int stages;
@@ -114,9 +114,6 @@ struct Ring {
     __device__ __forceinline__ uint32_t drain() const { return bar(2 * kMaxStages + 3 * kScaleSlots + 4); }
     __device__ __forceinline__ uint32_t tmem_slot() const { return bar(2 * kMaxStages + 3 * kScaleSlots + 5); }
 };
-constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 3 * kScaleSlots + 5) + 16;
-
-__host__ __device__ constexpr uint32_t stage_bytes_of(int bn) { return kTileA + 128u * bn; }
 
 // bn: the operand rows beside A's 128 that a stage of this CTA holds.
 __device__ __forceinline__ Ring make_ring(const uint8_t *smem, int bn, int stages, uint32_t sf_bytes, uint32_t extra)
@@ -212,7 +209,6 @@ __device__ __forceinline__ void spread_tile_scales(uint32_t v, uint32_t dst, int
 
 // ------------------------------------------------------------ many tiles --
 
-constexpr int kBN = 256;
 constexpr int kGThreads = 352;             // warps: 0 TMA, 1 MMA, 2 scales, 3-10 epilogue
 constexpr uint32_t kStaging = 8 * 2048;   // 2 KB per epilogue warp
 constexpr int kStages = 4;
@@ -369,12 +365,13 @@ __global__ void __launch_bounds__(kGThreads, 1)
         tmem_alloc(r.tmem_slot(), 512);
         tmem_relinquish_alloc_permit();
     }
-    if (work.items <= 2 * step)
-        pdl_trigger();
-    pdl_wait();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    // (this CTA holds its tensor memory: the next grid's cannot take it first)
+    if (work.items <= 2 * step)
+        pdl_trigger();
+    pdl_wait();
     const uint32_t tmem = lds32(r.tmem_slot());
 
     if (warp == 0) {  // the whole warp, so that operands stay uniform; one thread issues
@@ -658,9 +655,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
     return v;
 }
 
-constexpr int kMaxSplit = 8;               // portable cluster size
-constexpr uint32_t kSplitTmem = 256;       // accumulator: columns 0 .. 127, scales from 128
-
 template <bool BF16> __device__ __forceinline__ void store_one(void *out, int64_t at, float v)
 {
     if constexpr (BF16) {
@@ -697,11 +691,12 @@ __global__ void __launch_bounds__(kThreads)
         tmem_alloc(r.tmem_slot(), kSplitTmem);
         tmem_relinquish_alloc_permit();
     }
-    pdl_trigger();
-    pdl_wait();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    // (this CTA holds its tensor memory: the next grid's cannot take it first)
+    pdl_trigger();
+    pdl_wait();
     const uint32_t tmem = lds32(r.tmem_slot());
 
     if (warp == 0) {
@@ -836,7 +831,14 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
     }
+    // tensor memory goes back before the CTAs wait for one another, so that
+    // none that waits for it waits for a cluster
     tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kSplitTmem);
+    }
     if (split > 1) {
         __syncwarp();
         cluster_sync();
@@ -883,12 +885,6 @@ __global__ void __launch_bounds__(kThreads)
         }
         __syncwarp();
         cluster_sync();  // no CTA leaves while another reads its shared memory
-    } else {
-        __syncthreads();
-    }
-    if (warp == 1) {
-        tc_fence_after_sync();
-        tmem_dealloc(tmem, kSplitTmem);
     }
 }
 
@@ -904,8 +900,6 @@ template <class K> cudaError_t ensure_smem(K kernel, uint32_t bytes, int device,
     return e;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 Scales scales_of(const Fp8Operand &x, int64_t rows) { return {x.scale, ceil_div(rows, 128), x.tiles}; }
 
 // Boxes of 128 codes of `box_rows` rows.
@@ -915,68 +909,34 @@ int operand_map(CUtensorMap *map, const Fp8Operand &x, int64_t rows, int64_t K, 
                                 128, box_rows);
 }
 
-struct Plan {
-    bool split_kernel;
-    int bn, split;
-};
-
-// Which kernel: the split one where the other would leave more than half of
-// the SMs without a tile and either there are at most 64 tokens and the
-// contraction is at least 12 blocks long, or it is at least 48 blocks long and
-// a quarter of the SMs cover the 128 x 128 tiles.  Measured, split against
-// tiles: 37 x 10240 x 2560 8.9 and 12.1 us, 64 x 4096 x 4096 9.3 and 10.9, 64 x
-// 1024 x 1024 6.5 and 5.7, 128 x 4096 x 4096 13.2 and 11.3, 512 x 4096 x 4096
-// 16.3 and 11.7, 300 x 300 x 8192 10.6 and 20.8.
-bool use_split(int64_t M, int64_t N, int64_t K, int sms)
-{
-    const int64_t KB = ceil_div(K, 128);
-    if (ceil_div(M, 128) * ceil_div(N, kBN) >= sms / 2)
-        return false;
-    return (M <= 64 && KB >= 12) || (KB >= 48 && ceil_div(M, 128) * ceil_div(N, 128) * 4 <= sms);
-}
-
 template <bool BF16>
 cudaError_t run_split(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K,
                       void *out, const DeviceInfo &di, cudaStream_t stream)
 {
-    const int KB = static_cast<int>(ceil_div(K, 128));
-    const int bn = static_cast<int>(M >= 128 ? 128 : ceil_div(M, 16) * 16);
-    const int tiles_m = static_cast<int>(ceil_div(M, 128));
-    const int64_t tiles = ceil_div(N, 128) * tiles_m;
-    int split = 1;
-    while (split < kMaxSplit && tiles * (split + 1) <= 2 * di.num_sms && KB / (split + 1) >= 2)
-        ++split;
+    const SplitPlan p = split_plan(M, N, K, di.num_sms);
     CUtensorMap am, bm;
-    if (operand_map(&am, a, M, K, bn) != 0 || operand_map(&bm, b, N, K, 128) != 0)
+    if (operand_map(&am, a, M, K, p.bn) != 0 || operand_map(&bm, b, N, K, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
     cudaError_t e = ensure_smem(fp8_gemm_split_kernel<BF16>, kSmemLimit / 2, di.device, set);
     if (e != cudaSuccess)
         return e;
-    // two CTAs share an SM; the ring also holds the partial sums (512 bytes
-    // a column)
-    const uint32_t per = stage_bytes_of(bn), fixed = 1024 + kScaleSlots * 1024 + kBarBytes;
-    int stages = static_cast<int>((kSmemLimit / 2 - 1024 - fixed) / per);
-    const int need = static_cast<int>(ceil_div(KB, split)), least = static_cast<int>(ceil_div(512 * bn, per));
-    stages = stages > kMaxStages ? kMaxStages : stages;
-    stages = stages > need ? need : stages;
-    stages = stages < least ? least : stages;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = static_cast<unsigned>(tiles * split);
+    cfg.gridDim = static_cast<unsigned>(p.tiles * p.split);
     cfg.blockDim = kThreads;
-    cfg.dynamicSmemBytes = fixed + stages * per;
+    cfg.dynamicSmemBytes = p.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.x = p.split;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, scales_of(a, M), scales_of(b, N), out, M, N,
-                              KB, bn, stages, tiles_m, split);
+                              static_cast<int>(ceil_div(K, 128)), p.bn, p.stages, p.tiles_m, p.split);
 }
 
 template <bool BF16>
