@@ -11,10 +11,10 @@
 //
 // With r_y = 1 / sqrt(mean(y^2) + eps), r_h likewise of h', u = dn g_pre:
 //
-//   G      = dh' + r_h u - h' r_h^3 mean(u h')     (gradient at h')
+//   G      = dh' + r_h (u - h' r_h^2 mean(u h'))    (gradient at h')
 //   dh     = s G
 //   v      = G gate g_post
-//   dy     = r_y v - y r_y^3 mean(v y)
+//   dy     = r_y (v - y r_y^2 mean(v y))
 //   dg_pre = sum_t dn h' r_h,  dg_post = sum_t gate G y r_y
 //   dgate  = G y r_y g_post, summed over what the gate is shared by
 //
@@ -616,9 +616,11 @@ __global__ void __launch_bounds__(MAXT, 1)
         float dot[RPI], ry[RPI];
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
-            // a row past the end is all zeros and adds nothing
+            // a row past the end is all zeros and adds nothing: no product
+            // of two reciprocal roots is formed (they reach 2^75), only of one
+            // with a mean or a value that it brings back into range
             const float r1 = rsqrtf(sum[3 * i] * inv_d + eps);
-            const float2 rh = both(r1), ch = both(-r1 * r1 * r1 * (sum[3 * i + 1] * inv_d));
+            const float2 rh = both(r1), ch = both(-r1 * (r1 * (sum[3 * i + 1] * inv_d)));
             ry[i] = rsqrtf(sum[3 * i + 2] * inv_d + eps);
             const float2 ry2 = both(ry[i]), gt2 = both(gt[i]), s2 = both(s);
             float2 dd = both(0.0f);
@@ -634,9 +636,9 @@ __global__ void __launch_bounds__(MAXT, 1)
                 F8 o;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 u = rh * b.v[j];
-                    a_pre[v].v[j] = fma2(u, a.v[j], a_pre[v].v[j]);
-                    G[i][v].v[j] = fma2(a.v[j], ch, fma2(u, gq[0].v[j], G[i][v].v[j]));
+                    const float2 x = rh * a.v[j];
+                    a_pre[v].v[j] = fma2(x, b.v[j], a_pre[v].v[j]);
+                    G[i][v].v[j] = fma2(x, ch, fma2(rh * b.v[j], gq[0].v[j], G[i][v].v[j]));
                     o.v[j] = s2 * G[i][v].v[j];
                 }
                 if (ring.row(i) < T)
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(MAXT, 1)
             if constexpr (GATE == kGateToken)
                 if (threadIdx.x == 0)
                     static_cast<float *>(dgate)[row] = dot[i];
-            const float2 cy = both(-ry[i] * ry[i] * (gt[i] * dot[i] * inv_d)), rg = both(ry[i] * gt[i]);
+            const float2 cy = both(-ry[i] * (dot[i] * inv_d)), rg = both(ry[i] * gt[i]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = 8 * (threadIdx.x + v * blockDim.x);
@@ -686,10 +688,10 @@ __global__ void __launch_bounds__(MAXT, 1)
                     w = unpack8(qg[i][v]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float2 u = rg * gp[0].v[j];
+                    float2 u = gp[0].v[j];
                     if constexpr (GATE == kGateFull)
                         u = u * w.v[j];
-                    o.v[j] = fma2(u, G[i][v].v[j], o.v[j] * cy);
+                    o.v[j] = rg * fma2(u, G[i][v].v[j], o.v[j] * cy);
                 }
                 store_bf16x8<VEC>(dy + row * d, c, ring.shift, d, o);
             }
