@@ -4,6 +4,13 @@ Argument marshalling only: tensors are checked for device, dtype and
 contiguity, outputs are allocated with torch when the caller passes none,
 and the raw device pointers plus the current CUDA stream are handed to
 libtaco.so.  Every step of the codec runs in the library's kernels.
+
+``stream=`` queues a call's work there instead of on the current stream.  The
+caller orders the two: the inputs (and outputs passed in) have to be ready on
+that stream, stay allocated until it is done with them, and the current stream
+has to wait for it before it reads the results.  What a call allocates itself
+belongs to ``stream``, so it never shares memory with work that is still queued
+on the current one.
 """
 
 from __future__ import annotations
@@ -23,6 +30,29 @@ EPS = 1e-12
 def _stream_handle(stream: torch.cuda.Stream | None) -> ctypes.c_void_p:
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor:
+    """Memory that only a call on ``stream`` touches."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """An output of a call on ``stream``: memory of that stream's pool, kept
+    from reuse until what reads it on the current stream is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _new_like(x: torch.Tensor, stream) -> torch.Tensor:
+    return torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, x.device, stream)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, numel: int | None = None) -> None:
@@ -57,11 +87,11 @@ def taco_compress(x: torch.Tensor, block: int = 128, e_target: float = E_TARGET,
     rows, d = _shape2(x)
     nb = rows * d // block if block else 0
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        codes = _new(x.shape, torch.uint8, x.device, stream)
     if alpha is None:
-        alpha = torch.empty(nb, dtype=torch.float32, device=x.device)
+        alpha = _new(nb, torch.float32, x.device, stream)
     if scale is None:
-        scale = torch.empty(nb, dtype=torch.float32, device=x.device)
+        scale = _new(nb, torch.float32, x.device, stream)
     _need(codes, "codes", _U8, x.numel())
     _need(alpha, "alpha", (torch.float32,))
     _need(scale, "scale", (torch.float32,))
@@ -80,7 +110,7 @@ def taco_decompress(codes: torch.Tensor, alpha: torch.Tensor, scale: torch.Tenso
     _need(scale, "scale", (torch.float32,))
     rows, d = _shape2(codes)
     if out is None:
-        out = torch.empty(codes.shape, dtype=out_dtype, device=codes.device)
+        out = _new(codes.shape, out_dtype, codes.device, stream)
     _need(out, "out", (torch.float32, torch.bfloat16), codes.numel())
     st = _lib.load().taco_decompress(codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(), rows, d,
                                      block, out.data_ptr(), int(out.dtype == torch.bfloat16),
@@ -98,11 +128,11 @@ def taco_compress_int8(x: torch.Tensor, block: int = 128, e_target: float = E_TA
     rows, d = _shape2(x)
     nb = rows * d // block if block else 0
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        codes = _new(x.shape, torch.int8, x.device, stream)
     if alpha is None:
-        alpha = torch.empty(nb, dtype=torch.float32, device=x.device)
+        alpha = _new(nb, torch.float32, x.device, stream)
     if scale is None:
-        scale = torch.empty(nb, dtype=torch.float32, device=x.device)
+        scale = _new(nb, torch.float32, x.device, stream)
     _need(codes, "codes", (torch.int8,), x.numel())
     _need(alpha, "alpha", (torch.float32,))
     _need(scale, "scale", (torch.float32,))
@@ -120,7 +150,7 @@ def taco_decompress_int8(codes: torch.Tensor, alpha: torch.Tensor, scale: torch.
     _need(scale, "scale", (torch.float32,))
     rows, d = _shape2(codes)
     if out is None:
-        out = torch.empty(codes.shape, dtype=out_dtype, device=codes.device)
+        out = _new(codes.shape, out_dtype, codes.device, stream)
     _need(out, "out", (torch.float32, torch.bfloat16), codes.numel())
     st = _lib.load().taco_decompress_int8(codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(), rows,
                                           d, block, out.data_ptr(), int(out.dtype == torch.bfloat16),
@@ -145,11 +175,11 @@ def taco_reduce_shards(codes: Sequence[torch.Tensor], alpha: Sequence[torch.Tens
     rows, d = _shape2(codes[0])
     dev = codes[0].device
     if out_codes is None:
-        out_codes = torch.empty(codes[0].shape, dtype=torch.uint8, device=dev)
+        out_codes = _new(codes[0].shape, torch.uint8, dev, stream)
     if out_alpha is None:
-        out_alpha = torch.empty_like(alpha[0])
+        out_alpha = _new_like(alpha[0], stream)
     if out_scale is None:
-        out_scale = torch.empty_like(scale[0])
+        out_scale = _new_like(scale[0], stream)
     cp, _k1 = _lib.ptr_array([c.data_ptr() for c in codes])
     ap, _k2 = _lib.ptr_array([a.data_ptr() for a in alpha])
     sp, _k3 = _lib.ptr_array([s.data_ptr() for s in scale])
@@ -178,13 +208,13 @@ def taco_reduce_decompress(codes: Sequence[torch.Tensor], alpha: Sequence[torch.
     rows, d = _shape2(codes[0])
     dev = codes[0].device
     if out_codes is None:
-        out_codes = torch.empty(codes[0].shape, dtype=torch.uint8, device=dev)
+        out_codes = _new(codes[0].shape, torch.uint8, dev, stream)
     if out_alpha is None:
-        out_alpha = torch.empty_like(alpha[0])
+        out_alpha = _new_like(alpha[0], stream)
     if out_scale is None:
-        out_scale = torch.empty_like(scale[0])
+        out_scale = _new_like(scale[0], stream)
     if out is None:
-        out = torch.empty(codes[0].shape, dtype=out_dtype, device=dev)
+        out = _new(codes[0].shape, out_dtype, dev, stream)
     _need(out, "out", (torch.float32, torch.bfloat16), codes[0].numel())
     cp, _k1 = _lib.ptr_array([c.data_ptr() for c in codes])
     ap, _k2 = _lib.ptr_array([a.data_ptr() for a in alpha])
@@ -220,9 +250,9 @@ def agoq_reduce_shards(codes: Sequence[torch.Tensor], scale: Sequence[torch.Tens
         _need(codes[p], f"codes[{p}]", _U8, n)
         _need(scale[p], f"scale[{p}]", (torch.float32,))
     if out_codes is None:
-        out_codes = torch.empty(n, dtype=torch.uint8, device=codes[0].device)
+        out_codes = _new(n, torch.uint8, codes[0].device, stream)
     if out_scale is None:
-        out_scale = torch.empty(n // block, dtype=torch.float32, device=codes[0].device)
+        out_scale = _new(n // block, torch.float32, codes[0].device, stream)
     cp, _k1 = _lib.ptr_array([c.data_ptr() for c in codes])
     sp, _k2 = _lib.ptr_array([s.data_ptr() for s in scale])
     st = _lib.load().agoq_reduce_shards(P, cp, sp, n, block, out_codes.data_ptr(), out_scale.data_ptr(),
@@ -238,9 +268,9 @@ def agoq_laaq_quantize(x: torch.Tensor, block: int = 128, bits: int = 4,
     _need(x, "x", _BF16)
     n = x.numel()
     if packed is None:
-        packed = torch.empty(n * bits // 8, dtype=torch.uint8, device=x.device)
+        packed = _new(n * bits // 8, torch.uint8, x.device, stream)
     if scale is None:
-        scale = torch.empty(n // block, dtype=torch.float32, device=x.device)
+        scale = _new(n // block, torch.float32, x.device, stream)
     _need(packed, "packed", (torch.uint8,), n * bits // 8)
     _need(scale, "scale", (torch.float32,))
     st = _lib.load().agoq_laaq_quantize(x.data_ptr(), n, block, bits, packed.data_ptr(),
@@ -255,7 +285,7 @@ def agoq_laaq_dequantize(packed: torch.Tensor, scale: torch.Tensor, n: int, bloc
     _need(packed, "packed", (torch.uint8,), n * bits // 8)
     _need(scale, "scale", (torch.float32,))
     if out is None:
-        out = torch.empty(n, dtype=out_dtype, device=packed.device)
+        out = _new(n, out_dtype, packed.device, stream)
     _need(out, "out", (torch.float32, torch.bfloat16), n)
     st = _lib.load().agoq_laaq_dequantize(packed.data_ptr(), scale.data_ptr(), n, block, bits,
                                           out.data_ptr(), int(out.dtype == torch.bfloat16),
@@ -272,7 +302,7 @@ def agoq_laaq_dequantize_silu(packed: torch.Tensor, scale: torch.Tensor, n: int,
     _need(packed, "packed", (torch.uint8,), n * bits // 8)
     _need(scale, "scale", (torch.float32,))
     if out is None:
-        out = torch.empty(n, dtype=out_dtype, device=packed.device)
+        out = _new(n, out_dtype, packed.device, stream)
     _need(out, "out", (torch.float32, torch.bfloat16), n)
     st = _lib.load().agoq_laaq_dequantize_silu(packed.data_ptr(), scale.data_ptr(), n, block, bits,
                                                out.data_ptr(), int(out.dtype == torch.bfloat16),
@@ -292,7 +322,7 @@ def agoq_laaq_dequantize_rmsnorm(packed: torch.Tensor, scale: torch.Tensor, rows
     _need(scale, "scale", (torch.float32,))
     _need(gamma, "gamma", (torch.float32,), d)
     if out is None:
-        out = torch.empty((rows, d), dtype=out_dtype, device=packed.device)
+        out = _new((rows, d), out_dtype, packed.device, stream)
     _need(out, "out", (torch.float32, torch.bfloat16), rows * d)
     st = _lib.load().agoq_laaq_dequantize_rmsnorm(packed.data_ptr(), scale.data_ptr(), rows, d, block, bits,
                                                   gamma.data_ptr(), eps, out.data_ptr(),
@@ -306,7 +336,7 @@ def taco_e4m3_encode(x: torch.Tensor, out: torch.Tensor | None = None, stream=No
     _need(x, "x", (torch.float32,))
     n = x.numel()
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=x.device)
+        out = _new(n, torch.uint8, x.device, stream)
     _need(out, "out", (torch.uint8,), n)
     st = _lib.load().taco_e4m3_encode(x.data_ptr(), n, out.data_ptr(), _stream_handle(stream))
     _lib.check("taco_e4m3_encode", st)
@@ -374,11 +404,11 @@ def taco_gemm_compress(a: torch.Tensor, b: torch.Tensor, block: int = 128, e_tar
     M, N, K = _gemm_operands(a, b)
     nb = M * N // block if block else 0
     if codes is None:
-        codes = torch.empty((M, N), dtype=torch.uint8, device=a.device)
+        codes = _new((M, N), torch.uint8, a.device, stream)
     if alpha is None:
-        alpha = torch.empty(nb, dtype=torch.float32, device=a.device)
+        alpha = _new(nb, torch.float32, a.device, stream)
     if scale is None:
-        scale = torch.empty(nb, dtype=torch.float32, device=a.device)
+        scale = _new(nb, torch.float32, a.device, stream)
     _need(codes, "codes", _U8, M * N)
     _need(alpha, "alpha", (torch.float32,), nb)
     _need(scale, "scale", (torch.float32,), nb)
@@ -426,9 +456,9 @@ def agoq_gemm_laaq_quantize(a: torch.Tensor, b: torch.Tensor, bits: int = 4, blo
     M, N, K = _gemm_operands(a, b)
     nb = M * N // block if block else 0
     if packed is None:
-        packed = torch.empty(M * N * bits // 8, dtype=torch.uint8, device=a.device)
+        packed = _new(M * N * bits // 8, torch.uint8, a.device, stream)
     if scale is None:
-        scale = torch.empty(nb, dtype=torch.float32, device=a.device)
+        scale = _new(nb, torch.float32, a.device, stream)
     _need(packed, "packed", _U8, M * N * bits // 8)
     _need(scale, "scale", (torch.float32,), nb)
     if y_out is not None:
@@ -456,22 +486,6 @@ _BYTE = (torch.uint8,)
 def _stream_of(t: torch.Tensor, stream) -> int:
     """Raw handle of ``stream``, or of the current stream of t's device."""
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
-    """An output or workspace for a call on ``stream``: memory of the current
-    stream's pool, kept from reuse until work queued on ``stream`` is done."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
-def _new_like(x: torch.Tensor, stream) -> torch.Tensor:
-    t = torch.empty_like(x)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def _need2(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> None:
@@ -628,7 +642,7 @@ def fp8_linear(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
     else:
         _need(out, "out", (dt,), M * N)
     nbytes = _linear_workspace_bytes(M, N, K, 0)
-    ws = _new(nbytes, torch.uint8, x.device, stream) if nbytes else None
+    ws = _workspace(nbytes, x.device, stream) if nbytes else None
     st = _lib.load().fp8_linear(x.data_ptr(), codes.data_ptr(), scale.data_ptr(), M, N, K, out.data_ptr(),
                                 int(dt == torch.bfloat16), _ptr(ws), nbytes, _stream_of(x, stream))
     _lib.check("fp8_linear", st)
@@ -655,7 +669,7 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor, codes_t: torch.Tensor
     dx = _new_like(x, stream) if need_dx else None
     dw = _new((N, K), dt, x.device, stream) if need_dw else None
     nbytes = _linear_workspace_bytes(M, N, K, 1)
-    ws = _new(nbytes, torch.uint8, x.device, stream)
+    ws = _workspace(nbytes, x.device, stream)
     st = _lib.load().fp8_linear_backward(dy.data_ptr(), x.data_ptr(), codes_t.data_ptr(), scale_t.data_ptr(), M, N, K,
                                          dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None,
                                          int(dt == torch.bfloat16), ws.data_ptr(), nbytes, _stream_of(x, stream))
@@ -758,7 +772,7 @@ def rmsnorm_gate_residual_backward(dn: torch.Tensor, dh_new: torch.Tensor, y: to
     dg_pre = _new((d,), torch.float32, dev, stream)
     dgate = None if gate is None else _new_like(gate, stream)
     nbytes = _norm_workspace_bytes(T, d, mode, dev.index)
-    ws = _new(nbytes, torch.uint8, dev, stream)
+    ws = _workspace(nbytes, dev, stream)
     st = _lib.load().rmsnorm_gate_residual_backward(
         dn.data_ptr(), dh_new.data_ptr(), y.data_ptr(), h_new.data_ptr(), gain_post.data_ptr(), gain_pre.data_ptr(),
         _ptr(gate), mode, residual_scale, eps, T, d, dy.data_ptr(), dh.data_ptr(), dg_post.data_ptr(),
