@@ -33,11 +33,6 @@
 //   power limit (1.75 GHz).  Sharing B between two CTAs, by multicast or as a
 //   cta_group::2 pair with six stages of 32 KB, took the same time or a
 //   little longer (88 against 86 us at 8192 x 4096 x 4096).
-//   An fp32 result over more than 1536 values is summed in pieces: the tensor
-//   core's accumulator truncates, which biases long coherent sums (measured
-//   on a weight gradient over 4096 tokens: 1.9e-6 of its norm in one piece,
-//   where an fp32 matrix product has 3.7e-7; 6.2e-7 in pieces), so each piece
-//   is added in the epilogue's registers, rounded.
 //
 // fp8_gemm_split_kernel (few tiles: single tokens to small batches): the
 //   roles of the operands are exchanged - B's rows (weights) take the 128
@@ -46,6 +41,14 @@
 //   splits the contraction; the partial sums meet in distributed shared
 //   memory, added in the order of the split, each CTA finishing a share of
 //   the columns.  No workspace, no atomics, and a fixed summation order.
+//
+// Either kernel sums an fp32 result over more than 1536 values of a CTA in
+// pieces: the tensor core's accumulator truncates, which biases long coherent
+// sums (measured on a weight gradient over 4096 tokens: 1.9e-6 of its norm in
+// one piece, where an fp32 matrix product has 3.7e-7; 6.2e-7 in pieces), so each
+// piece is added in the epilogue's registers, rounded.  A bf16 result is one
+// sum, whose bias is far below its rounding (16384 positive values: 6e-6 of the
+// sum, where bf16's half step is 2^-9 to 2^-8).
 //
 // Every mbarrier wait is time-limited; one that runs out sets a flag that
 // taco_device_error() reads, and the CTA winds down.  Tensor memory is never
@@ -69,7 +72,6 @@ __device__ unsigned int g_fp8_error;
 namespace {
 
 constexpr uint32_t kErrFp8 = 64u;
-constexpr int kThreads = 224;  // split kernel's warps: 0 TMA, 1 MMA, 2-5 epilogue, 6 scales
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr)
 {
@@ -215,7 +217,6 @@ constexpr int kStages = 4;
 constexpr uint32_t kAcc1 = 224;            // second accumulator: columns 224 .. 479
 constexpr uint32_t kSfColumn = 480;        // tensor-memory columns 480 .. 503: scales
 constexpr int kGroupM = 16;                // row tiles walked together (operands shared through L2)
-constexpr int kPieceBlocks = 12;           // fp32: most blocks summed in tensor memory
 constexpr uint32_t kGemmSmem = 1024 + kStages * stage_bytes_of(kBN) + kStaging + kScaleSlots * 1536 + kBarBytes;
 static_assert(kGemmSmem <= kSmemLimit, "shared memory per CTA");
 
@@ -668,9 +669,20 @@ template <bool BF16> __device__ __forceinline__ void store_one(void *out, int64_
 
 // CTA `rank` of the cluster of tile t takes blocks KB rank / S .. KB (rank +
 // 1) / S of the contraction.  Lanes: rows of B (n); columns: rows of A (m),
-// BN of them from a multiple of 128.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads)
+// BN of them from a multiple of 128.  SUMS: SplitPlan::sums.  If not 0, the
+// share is summed in pieces, each of them added in the epilogue's registers: up
+// to 64 columns in two accumulators in turn, the MMAs filling one while the
+// other is read; up to 128 in one, which is all that the columns allow, by
+// twice as many warps.  Two CTAs share an SM either way.
+// Measured, in pieces against one: 256 x 256 x 65536 22.4 and 22.3 us, 512 x 512
+// x 65536 31.5 and 33.5, 64 x 128 x 100000 26.9 and 25.4, 16 x 16384 x 16384
+// 44.0 and 44.3.
+__host__ __device__ constexpr int epilogue_warps(int sums) { return sums == 128 ? 8 : 4; }
+// warps: 0 TMA, 1 MMA, 2 scales, then the epilogue
+__host__ __device__ constexpr int split_threads(int sums) { return 32 * (3 + epilogue_warps(sums)); }
+
+template <bool BF16, int SUMS>
+__global__ void __launch_bounds__(split_threads(SUMS), 2)
     fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                           Scales sa, Scales sb, void *__restrict__ out, int64_t M, int64_t N, int KB, int BN,
                           int stages, int tiles_m, int split)
@@ -684,9 +696,12 @@ __global__ void __launch_bounds__(kThreads)
     const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / split);
     const int groups = (KB + 3) / 4;
+    constexpr int kAccs = SUMS == 64 ? 2 : 1;
+    const int share = kb1 - kb0, pieces = SUMS ? (share + kPieceBlocks - 1) / kPieceBlocks : 1;
+    const int piece = (share + pieces - 1) / pieces;  // blocks of one
 
     if (threadIdx.x == 0)
-        init_barriers(r, sb.tiles ? 2 : 1, 4);
+        init_barriers(r, sb.tiles ? 2 : 1, epilogue_warps(SUMS));
     if (warp == 1) {
         tmem_alloc(r.tmem_slot(), kSplitTmem);
         tmem_relinquish_alloc_permit();
@@ -744,8 +759,21 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t idesc = idesc_mxf8(BN);
         Slot p, f;
         uint32_t set = 0, sf = 0;
+        int i = 0, first = kb0;  // this piece and its first block
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb) {
+            if (SUMS != 0 && kb == first + piece) {
+                if (elect_one())
+                    mma_commit(r.acc_full(i % kAccs));
+                __syncwarp();
+                first = kb;
+                // the last piece in these columns has been read
+                if (++i >= kAccs && !__all_sync(0xFFFFFFFFu, mbar_wait(r.acc_free(i % kAccs), (i / kAccs - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+            }
             if (starts_group(kb, kb0)) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.sf_full(f.s), f.phase))) {
                     ok = false;
@@ -768,19 +796,19 @@ __global__ void __launch_bounds__(kThreads)
             }
             tc_fence_after_sync();
             if (elect_one())
-                mma_block(r, p.s, tmem, sf, sf + 4, idesc, kb, kb != kb0);
+                mma_block(r, p.s, tmem + i % kAccs * SUMS, sf, sf + 4, idesc, kb, kb != first);
             __syncwarp();
             p.next(stages);
         }
         if (elect_one()) {
             if (!ok)
                 report_timeout();
-            mma_commit(ok ? r.acc_full(0) : r.drain());
+            mma_commit(ok ? r.acc_full(i % kAccs) : r.drain());
         }
         __syncwarp();
         if (!ok)
             mbar_wait(r.drain(), 0);
-    } else if (warp == 6) {
+    } else if (warp == 2) {
         if (sb.tiles) {
             Slot f;
             const int g1 = (kb1 + 3) / 4;
@@ -805,30 +833,66 @@ __global__ void __launch_bounds__(kThreads)
     } else {
         const int q = warp & 3, row = 32 * q + lane;
         const int64_t n = n0 + row;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(r.acc_full(0), 0))) {
-            if (lane == 0)
+        const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        auto wait_full = [&](int i) {
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(r.acc_full(i % kAccs), (i / kAccs) & 1));
+            if (!ok && lane == 0)
                 report_timeout();
-        } else {
             tc_fence_after_sync();
-            const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16);
+            return ok;
+        };
+        // once every load of this CTA has landed and been read (acc_full of
+        // the last piece), the ring's memory holds the partial sums, [column]
+        // [128 rows]
+        auto put = [&](int c, float v) {
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(r.base + 4 * (128 * c + row)), "f"(v) : "memory");
+        };
+        if constexpr (SUMS == 0) {
+            if (wait_full(0)) {
 #pragma unroll 1
-            for (int j = 0; j < BN; j += 32) {
-                float x[32];
-                tmem_load_32(tq + j, x);
+                for (int j = 0; j < BN; j += 32) {
+                    float x[32];
+                    tmem_load_32(tq + j, x);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    if (split > 1) {
-                        // every load of this CTA has landed and been read
-                        // (acc_full): the ring's memory holds the partials,
-                        // [column][128 rows]
-                        if (j + c < BN)
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(r.base + 4 * (128 * (j + c) + row)), "f"(x[c])
-                                         : "memory");
-                    } else if (j + c < BN && m0 + j + c < M && n < N) {
-                        store_one<BF16>(out, (m0 + j + c) * N + n, x[c]);
+                    for (int c = 0; c < 32; ++c) {
+                        if (split > 1) {
+                            if (j + c < BN)
+                                put(j + c, x[c]);
+                        } else if (j + c < BN && m0 + j + c < M && n < N) {
+                            store_one<BF16>(out, (m0 + j + c) * N + n, x[c]);
+                        }
                     }
                 }
             }
+        } else {
+            constexpr int kColumns = 4 * SUMS / epilogue_warps(SUMS);
+            const int c0 = kColumns * ((warp - 3) >> 2);  // this warp's columns
+            float sum[kColumns] = {};
+            bool ok = true;
+            for (int i = 0, kb = kb0; ok && kb < kb1; ++i, kb += piece) {
+                if (!(ok = wait_full(i)))
+                    break;
+#pragma unroll
+                for (int j = 0; j < kColumns; j += 8)
+                    if (c0 + j < BN) {
+                        float x[8];
+                        tmem_load_8(tq + i % kAccs * SUMS + c0 + j, x);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            sum[j + c] += x[c];
+                    }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(r.acc_free(i % kAccs));
+            }
+            if (ok)
+#pragma unroll
+                for (int j = 0; j < kColumns; j += 8)
+                    if (c0 + j < BN)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            put(c0 + j + c, sum[j + c]);
         }
     }
     // tensor memory goes back before the CTAs wait for one another, so that
@@ -839,7 +903,7 @@ __global__ void __launch_bounds__(kThreads)
         tc_fence_after_sync();
         tmem_dealloc(tmem, kSplitTmem);
     }
-    if (split > 1) {
+    if (SUMS != 0 || split > 1) {
         __syncwarp();
         cluster_sync();
         // this CTA's share of the columns, a column a warp (four rows a
@@ -850,7 +914,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int p = 0; p < kMaxSplit; ++p)
             parts[p] = map_cluster(r.base, p < split ? p : 0) + 16 * lane;
-        for (int c = rank + split * warp; c < BN && m0 + c < M; c += split * (kThreads / 32)) {
+        for (int c = rank + split * warp; c < BN && m0 + c < M; c += split * (split_threads(SUMS) / 32)) {
             float4 v[kMaxSplit];
 #pragma unroll
             for (int p = 0; p < kMaxSplit; ++p)
@@ -909,21 +973,20 @@ int operand_map(CUtensorMap *map, const Fp8Operand &x, int64_t rows, int64_t K, 
                                 128, box_rows);
 }
 
-template <bool BF16>
-cudaError_t run_split(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K,
-                      void *out, const DeviceInfo &di, cudaStream_t stream)
+template <bool BF16, int SUMS>
+cudaError_t launch_split(const SplitPlan &p, const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K,
+                         void *out, const DeviceInfo &di, cudaStream_t stream)
 {
-    const SplitPlan p = split_plan(M, N, K, di.num_sms);
     CUtensorMap am, bm;
     if (operand_map(&am, a, M, K, p.bn) != 0 || operand_map(&bm, b, N, K, 128) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = ensure_smem(fp8_gemm_split_kernel<BF16>, kSmemLimit / 2, di.device, set);
+    cudaError_t e = ensure_smem(fp8_gemm_split_kernel<BF16, SUMS>, kSmemLimit / 2, di.device, set);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(p.tiles * p.split);
-    cfg.blockDim = kThreads;
+    cfg.blockDim = split_threads(SUMS);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -935,8 +998,22 @@ cudaError_t run_split(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16>, am, bm, scales_of(a, M), scales_of(b, N), out, M, N,
-                              static_cast<int>(ceil_div(K, 128)), p.bn, p.stages, p.tiles_m, p.split);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_split_kernel<BF16, SUMS>, am, bm, scales_of(a, M), scales_of(b, N), out, M,
+                              N, static_cast<int>(ceil_div(K, 128)), p.bn, p.stages, p.tiles_m, p.split);
+}
+
+template <bool BF16>
+cudaError_t run_split(const Fp8Operand &a, const Fp8Operand &b, int64_t M, int64_t N, int64_t K,
+                      void *out, const DeviceInfo &di, cudaStream_t stream)
+{
+    const SplitPlan p = split_plan(M, N, K, di.num_sms, BF16);
+    if constexpr (!BF16) {
+        if (p.sums == 64)
+            return launch_split<BF16, 64>(p, a, b, M, N, K, out, di, stream);
+        if (p.sums == 128)
+            return launch_split<BF16, 128>(p, a, b, M, N, K, out, di, stream);
+    }
+    return launch_split<BF16, 0>(p, a, b, M, N, K, out, di, stream);
 }
 
 template <bool BF16>

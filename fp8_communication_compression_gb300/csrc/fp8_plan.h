@@ -31,12 +31,15 @@ TACO_HOST_DEVICE constexpr uint32_t stage_bytes_of(int bn) { return kTileA + 128
 // Many tiles: width of a tile.
 constexpr int kBN = 256;
 
+// An fp32 result: most blocks summed in tensor memory, whose sums truncate.
+constexpr int kPieceBlocks = 12;
+
 // Few tiles: CTAs that share a contraction (a portable cluster), and the
 // tensor memory of one.  tcgen05.alloc waits without a limit for columns that
 // are not free, so no SM may hold more of these CTAs than have columns: each
 // asks for more than a third of an SM's shared memory.
 constexpr int kMaxSplit = 8;
-constexpr uint32_t kSplitTmem = 256;         // accumulator: columns 0 .. 127, scales from 128
+constexpr uint32_t kSplitTmem = 256;         // accumulators: columns 0 .. 127, scales from 128
 constexpr uint32_t kSplitLeastSmem = kSmemOfSm / 3;
 static_assert(kSmemOfSm / (kSplitLeastSmem + kSmemOfCta) * kSplitTmem <= kTmemColumns,
               "CTAs on an SM whose tensor memory exceeds the SM's");
@@ -63,9 +66,11 @@ struct SplitPlan {
     int split;      // CTAs to a tile
     int stages;
     uint32_t smem;  // dynamic shared memory of a CTA
+    int sums;       // 64 or 128: a CTA's share in pieces, whose sums of up to so many columns are added in registers;
+                    // 0: in one piece
 };
 
-inline SplitPlan split_plan(int64_t M, int64_t N, int64_t K, int sms)
+inline SplitPlan split_plan(int64_t M, int64_t N, int64_t K, int sms, bool out_bf16 = true)
 {
     SplitPlan p;
     const int64_t KB = ceil_div(K, 128);
@@ -75,6 +80,7 @@ inline SplitPlan split_plan(int64_t M, int64_t N, int64_t K, int sms)
     p.split = 1;
     while (p.split < kMaxSplit && p.tiles * (p.split + 1) <= 2 * sms && KB / (p.split + 1) >= 2)
         ++p.split;
+    p.sums = out_bf16 || ceil_div(KB, p.split) <= kPieceBlocks ? 0 : p.bn <= 64 ? 64 : 128;
     // two CTAs share an SM; the ring also holds the partial sums (512 bytes
     // a column)
     const uint32_t per = stage_bytes_of(p.bn), fixed = 1024 + kScaleSlots * 1024 + kBarBytes;

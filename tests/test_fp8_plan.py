@@ -68,3 +68,44 @@ def test_shared_memory_holds_the_ring_and_the_partial_sums(plans):
         assert 1 <= stages <= 10 and 512 * bn <= stages * per
         assert 1024 + stages * per + 4 * 1024 <= smem <= 232448
         assert 1 <= ways <= 8 and ways <= -(-K // 128)  # every CTA has a block
+
+
+SUMS_PROGRAM = r"""
+#include <cstdio>
+#include "fp8_plan.h"
+int main()
+{
+    long long M, N, K;
+    int sms;
+    while (std::scanf("%lld %lld %lld %d", &M, &N, &K, &sms) == 4) {
+        const taco::SplitPlan p = taco::split_plan(M, N, K, sms, false);
+        std::printf("%d %d %lld %d %d %u %d %u\n", taco::use_split(M, N, K, sms), p.bn, static_cast<long long>(p.tiles),
+                    p.split, p.stages, p.smem, p.sums, taco::kSplitTmem);
+    }
+}
+"""
+
+
+def test_fp32_results_are_summed_in_pieces(tmp_path):
+    # no CTA leaves more than 12 blocks to one sum in tensor memory
+    (tmp_path / "plan.cpp").write_text(SUMS_PROGRAM)
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", CSRC, str(tmp_path / "plan.cpp"), "-o",
+                           str(tmp_path / "plan")])
+    shapes = [(M, N, K, sms) for M in SIZES for N in SIZES for K in SIZES if K >= 16 for sms in (152, 148, 20)]
+    out = subprocess.run([str(tmp_path / "plan")], input="\n".join("%d %d %d %d" % s for s in shapes), text=True,
+                         stdout=subprocess.PIPE, check=True).stdout.split("\n")
+    seen = set()
+    for (M, N, K, sms), line in zip(shapes, out):
+        use, bn, tiles, ways, stages, smem, sums, tmem = map(int, line.split())
+        if not use:
+            continue
+        seen.add(sums)
+        share = -(-(-(-K // 128)) // ways)
+        assert sums in (0, 64, 128) and (share <= 12 if sums == 0 else bn <= sums), (M, N, K, sms)
+        # what the sums and two sets of scales take, and what an SM has
+        columns = 128  # one accumulator of up to 128, two of up to 64
+        assert columns + 16 <= tmem and tmem in (256, 512)
+        assert 228 * 1024 // (smem + 1024) * tmem <= 512, (M, N, K, sms)
+        assert 1024 + stages * (128 * 128 + 128 * bn) + 4 * 1024 <= smem <= 232448 and 512 * bn <= stages * (128 + bn) * 128
+        assert 1 <= ways <= 8 and ways <= -(-K // 128)
+    assert seen == {0, 64, 128}
