@@ -35,10 +35,17 @@ constexpr int kTokens = 8;
 constexpr int kUnits = 4;  // 8-value units of the tokens a thread loads together
 constexpr int kAhead = 4;  // blocks whose loads are issued together
 
-// Scale factor 2^(byte - 127); byte 0 is a subnormal, 255 the NaN scale.
-__device__ __forceinline__ float scale_factor(uint32_t byte)
+// Scale factor 2^(byte - 127) as two factors of half the exponent (byte 255:
+// NaN).  A block's sum is multiplied by the product of the first halves of its
+// two scales and then by that of the second ones: 2^(ex + ew) itself may lie
+// outside fp32 where the scaled sum does not.  The halves' products lie inside,
+// and the first multiplication leaves the range only where the result does.
+__device__ __forceinline__ float2 scale_halves(uint32_t byte)
 {
-    return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : byte == 0u ? 0x00400000u : byte << 23);
+    const int e = static_cast<int>(byte) - 127, lo = e >> 1;
+    const float nan = __uint_as_float(0x7FFFFFFFu);
+    return byte == 255u ? make_float2(nan, nan)
+                        : make_float2(__int_as_float((lo + 127) << 23), __int_as_float((e - lo + 127) << 23));
 }
 
 // c += A B for 16 rows, 8 tokens and 32 values.
@@ -53,7 +60,7 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
 
 // Shared memory: the tokens' codes [M][stride] (stride = blocks * 128 + 64
 // bytes, so that a warp's 16-byte reads of eight tokens spread over the
-// banks), their scale factors [blocks][8], and the warps' sums.
+// banks), their scale factors' halves [blocks][8], and the warps' sums.
 __global__ void __launch_bounds__(kDThreads)
     fp8_decode_kernel(const uint16_t *__restrict__ x, const uint8_t *__restrict__ codes,
                       const uint8_t *__restrict__ scale, int M, int64_t N, int K, int P, void *__restrict__ y,
@@ -62,7 +69,7 @@ __global__ void __launch_bounds__(kDThreads)
     extern __shared__ uint8_t smem[];
     __shared__ float part[2][kDWarps][16 * kTokens];
     const int KB = (K + 127) / 128, stride = KB * 128 + 64;
-    float *xscale = reinterpret_cast<float *>(smem + M * stride);
+    float2 *xscale = reinterpret_cast<float2 *>(smem + M * stride);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;  // this lane's rows g, g + 8 (and token g), and its 16 bytes of every 64
     const int64_t row_tiles = (N + 127) / 128, groups = (N + 15) / 16;
@@ -124,7 +131,7 @@ __global__ void __launch_bounds__(kDThreads)
                     f32x4_to_e4m3x4(bf16lo_to_f32(q[u].z) * f, bf16hi_to_f32(q[u].z) * f, bf16lo_to_f32(q[u].w) * f,
                                     bf16hi_to_f32(q[u].w) * f));
                 if ((c & 127) == 0)
-                    xscale[(c >> 7) * kTokens + m] = scale_factor(byte);
+                    xscale[(c >> 7) * kTokens + m] = scale_halves(byte);
             }
         }
     }
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(kDThreads)
             for (int u = 0; u < kAhead; ++u) {
                 const int b = b0 + kDWarps * u;
                 if (b < KB) {
-                    const float f = scale_factor(__ldg(scale + b * row_tiles + tile));
+                    const float2 f = scale_halves(__ldg(scale + b * row_tiles + tile));
                     float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -150,11 +157,11 @@ __global__ void __launch_bounds__(kDThreads)
                         mma_e4m3(c, lo.x, hi.x, lo.y, hi.y, xb.x, xb.y);
                         mma_e4m3(c, lo.z, hi.z, lo.w, hi.w, xb.z, xb.w);
                     }
-                    const float2 s = *reinterpret_cast<const float2 *>(xscale + b * kTokens + 2 * t);
-                    acc[0] = fmaf(c[0], f * s.x, acc[0]);
-                    acc[1] = fmaf(c[1], f * s.y, acc[1]);
-                    acc[2] = fmaf(c[2], f * s.x, acc[2]);
-                    acc[3] = fmaf(c[3], f * s.y, acc[3]);
+                    const float4 s = *reinterpret_cast<const float4 *>(xscale + b * kTokens + 2 * t);
+                    acc[0] = fmaf(c[0] * (f.x * s.x), f.y * s.y, acc[0]);
+                    acc[1] = fmaf(c[1] * (f.x * s.z), f.y * s.w, acc[1]);
+                    acc[2] = fmaf(c[2] * (f.x * s.x), f.y * s.y, acc[2]);
+                    acc[3] = fmaf(c[3] * (f.x * s.z), f.y * s.w, acc[3]);
                     // the block this register holds next, of these rows or
                     // of the CTA's next ones
                     const bool more = b + kDWarps * kAhead < KB;
@@ -195,7 +202,7 @@ constexpr int64_t kMaxK = 16384;
 uint32_t decode_smem(int64_t M, int64_t K)
 {
     const uint32_t KB = static_cast<uint32_t>((K + 127) / 128);
-    return static_cast<uint32_t>(M) * (KB * 128 + 64) + 4 * kTokens * KB;
+    return static_cast<uint32_t>(M) * (KB * 128 + 64) + 8 * kTokens * KB;
 }
 
 }  // namespace
