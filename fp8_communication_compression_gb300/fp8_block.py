@@ -66,10 +66,12 @@ class Fp8Block:
 
     def backward(self, dout: torch.Tensor, dh1: torch.Tensor):
         """Gradients at out and h1 -> (dy, dh, dgain_post, dgain_pre, dgate);
-        the weights' gradients are added to the FP8 main gradients."""
+        the weights' gradients are added to the FP8 main gradients.  Each
+        forward pass serves one backward pass: a second would add the same
+        micro-batch's gradients again."""
         if self._saved is None:
-            raise RuntimeError("backward() before forward()")
-        y, h, h1, us = self._saved
+            raise RuntimeError("backward() without a forward() of its own")
+        (y, h, h1, us), self._saved = self._saved, None
         _, n = api.rmsnorm_gate_residual(y, h, self.gain_post, self.gain_pre, self.gate, self.residual_scale, self.eps)
         dns = []
         for p, u in enumerate(us):
