@@ -22,7 +22,8 @@ from . import api
 
 class Fp8Block:
     """``w_up`` bf16 [f, d] and ``w_down`` bf16 [d, f], f split into P equal
-    slices; ``gate`` as rmsnorm_gate_residual's (None, fp32 [d], or per call)."""
+    slices; ``gate`` as rmsnorm_gate_residual's.  A gate that changes with the
+    tokens is given to forward() instead."""
 
     def __init__(self, w_up: torch.Tensor, w_down: torch.Tensor, tokens: int, P: int = 1,
                  gate: torch.Tensor | None = None, residual_scale: float = 1.0, eps: float = 1e-6):
@@ -37,14 +38,22 @@ class Fp8Block:
         self.gain_post = torch.ones(d, device=dev)
         self.gain_pre = torch.ones(d, device=dev)
         fp = f // P
-        # each slice's weights, quantised once (and again after an update)
-        self.up = [api.fp8_quantize_weight(w_up[p * fp:(p + 1) * fp]) for p in range(P)]
-        self.down = [api.fp8_quantize_weight(w_down[:, p * fp:(p + 1) * fp].contiguous()) for p in range(P)]
-        self._saved = None  # what the backward pass needs of the forward one
+        self.load_weights(w_up, w_down)
         self.sum = api.TwoShotLocal(P, tokens, d, out_dtype=torch.bfloat16, device=dev)
         # FP8 main gradients of the slices' weights: codes and multipliers
         self.main_up = [self._main(fp, d, dev) for _ in range(P)]
         self.main_down = [self._main(d, fp, dev) for _ in range(P)]
+
+    def load_weights(self, w_up: torch.Tensor, w_down: torch.Tensor) -> None:
+        """Quantises each slice's weights: at the start, and after an update.
+        The main gradients stay as they are; a forward pass with the old
+        weights can no longer be followed by its backward pass."""
+        if tuple(w_up.shape) != (self.f, self.d) or tuple(w_down.shape) != (self.d, self.f):
+            raise ValueError(f"w_up must be [{self.f}, {self.d}] and w_down [{self.d}, {self.f}]")
+        self._saved = None  # what the backward pass needs of the forward one
+        fp = self.f // self.P
+        self.up = [api.fp8_quantize_weight(w_up[p * fp:(p + 1) * fp]) for p in range(self.P)]
+        self.down = [api.fp8_quantize_weight(w_down[:, p * fp:(p + 1) * fp].contiguous()) for p in range(self.P)]
 
     @staticmethod
     def _main(rows: int, cols: int, dev: torch.device):
@@ -55,13 +64,15 @@ class Fp8Block:
         """The slices' partial sums through the compressed two-shot path."""
         return self.sum.run(torch.stack(parts)).clone()
 
-    def forward(self, y: torch.Tensor, h: torch.Tensor):
-        """y, h bf16 [tokens, d] -> (out bf16 [tokens, d], h1)."""
-        h1, codes, scale = api.rmsnorm_gate_residual_fp8(y, h, self.gain_post, self.gain_pre, self.gate,
+    def forward(self, y: torch.Tensor, h: torch.Tensor, gate: torch.Tensor | None = None):
+        """y, h bf16 [tokens, d] -> (out bf16 [tokens, d], h1).  ``gate``: this
+        call's, in place of the block's."""
+        gate = self.gate if gate is None else gate
+        h1, codes, scale = api.rmsnorm_gate_residual_fp8(y, h, self.gain_post, self.gain_pre, gate,
                                                          self.residual_scale, self.eps)
         u = [api.fp8_gemm(codes, scale, w[0], w[1]) for w in self.up]
         out = self._reduce([api.fp8_linear(torch.nn.functional.silu(up), w[0], w[1]) for up, w in zip(u, self.down)])
-        self._saved = (y, h, h1, u)
+        self._saved = (y, h, h1, u, gate)
         return out, h1
 
     def backward(self, dout: torch.Tensor, dh1: torch.Tensor):
@@ -71,8 +82,8 @@ class Fp8Block:
         micro-batch's gradients again."""
         if self._saved is None:
             raise RuntimeError("backward() without a forward() of its own")
-        (y, h, h1, us), self._saved = self._saved, None
-        _, n = api.rmsnorm_gate_residual(y, h, self.gain_post, self.gain_pre, self.gate, self.residual_scale, self.eps)
+        (y, h, h1, us, gate), self._saved = self._saved, None
+        _, n = api.rmsnorm_gate_residual(y, h, self.gain_post, self.gain_pre, gate, self.residual_scale, self.eps)
         dns = []
         for p, u in enumerate(us):
             s = torch.sigmoid(u.float())
@@ -84,5 +95,5 @@ class Fp8Block:
             api.agoq_fp8_accumulate(*self.main_up[p], dw)
             dns.append(dn)
         dn = self._reduce(dns)
-        return api.rmsnorm_gate_residual_backward(dn, dh1, y, h1, self.gain_post, self.gain_pre, self.gate,
+        return api.rmsnorm_gate_residual_backward(dn, dh1, y, h1, self.gain_post, self.gain_pre, gate,
                                                   self.residual_scale, self.eps)

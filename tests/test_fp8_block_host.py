@@ -61,3 +61,32 @@ def test_each_backward_pass_takes_its_own_forward_pass(block):
     b.forward(x, x)
     b.backward(x, x)
     assert len(named(calls, "agoq_fp8_accumulate")) == 4
+
+
+def test_a_call_may_bring_its_own_gate(block):
+    b, calls = block
+    x, gate = torch.zeros((T, D), dtype=torch.bfloat16), torch.full((T, 1), 0.5)
+    for given, used in ((gate, gate), (None, b.gate)):
+        calls.clear()
+        b.forward(x, x, given)
+        b.backward(x, x)
+        norms = [c for c in calls if c[0].startswith("rmsnorm")]
+        assert len(norms) == 3 and all(any(a is used for a in args) for _, args, _ in norms)
+
+
+def test_updated_weights_are_quantised_in_place_of_the_old_ones(block):
+    b, calls = block
+    x = torch.zeros((T, D), dtype=torch.bfloat16)
+    main = [m[0] for m in (*b.main_up, *b.main_down)]
+    up, down = torch.ones((F, D), dtype=torch.bfloat16), torch.ones((D, F), dtype=torch.bfloat16)
+    b.load_weights(up, down)
+    assert torch.equal(b.up[0][0], up) and torch.equal(b.down[0][0], down)
+    assert all(m[0] is old for m, old in zip((*b.main_up, *b.main_down), main))
+    with pytest.raises(ValueError):
+        b.load_weights(down, up)
+    b.forward(x, x)
+    b.load_weights(up, down)
+    with pytest.raises(RuntimeError):
+        b.backward(x, x)                  # that forward pass used the old ones
+    b.forward(x, x)
+    b.backward(x, x)
