@@ -130,3 +130,27 @@ def test_memory_the_current_stream_still_reads_survives():
             torch.cuda.synchronize()
             assert bool((kept == 7.0).all())
             assert all(torch.equal(p, q) and bool(torch.isfinite(p).all()) for p, q in zip(got, first))
+
+
+@pytest.mark.gpu
+def test_calls_on_a_branch_of_a_captured_graph():
+    M, N, K = 70, 512, 384
+    g = torch.Generator().manual_seed(91)
+    xs = [torch.randn((M, K), generator=g).bfloat16().cuda() for _ in range(2)]
+    w = api.fp8_quantize_weight(torch.randn((N, K), generator=g).bfloat16().cuda())
+    gain = torch.ones(K, device="cuda")
+    eager = [(api.fp8_linear(x, w[0], w[1]), *api.rmsnorm_gate_residual_backward(x, x, x, x, gain, gain)[:4]) for x in xs]
+    x = xs[0].clone()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = (api.fp8_linear(x, w[0], w[1], stream=side),
+               *api.rmsnorm_gate_residual_backward(x, x, x, x, gain, gain, stream=side)[:4])
+        torch.cuda.current_stream().wait_stream(side)
+    for i in (1, 0):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager[i]))
