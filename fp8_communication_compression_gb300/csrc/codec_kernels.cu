@@ -429,23 +429,6 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-constexpr int kMaxDevices = 64;
-
-// Raises a kernel's dynamic shared-memory limit once per device.  The flag
-// is atomic because host threads may make their first launch concurrently;
-// setting the attribute twice is harmless.
-template <typename K>
-cudaError_t ensure_smem(K kernel, uint32_t bytes, int device, std::atomic<bool> *done)
-{
-    if (done[device].load(std::memory_order_acquire))
-        return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(bytes));
-    if (e == cudaSuccess)
-        done[device].store(true, std::memory_order_release);
-    return e;
-}
-
 }  // namespace
 
 int encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, void *base, uint64_t inner,

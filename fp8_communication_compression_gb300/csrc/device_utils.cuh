@@ -133,6 +133,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
 
 // ------------------------------------------------------------------- TMA --
 
+// Copies `bytes` contiguous bytes (a multiple of 16, both addresses 16-byte
+// aligned) to shared memory and reports them to the mbarrier at `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -20,8 +20,6 @@
 // over its share of the rows, each register of weights reloaded as soon as it
 // is used, so that loads are in flight throughout.
 
-#include <atomic>
-
 #include "device_utils.cuh"
 #include "fp8_block.cuh"
 #include "internal.h"
@@ -196,7 +194,6 @@ __global__ void __launch_bounds__(kDThreads)
     }
 }
 
-constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxK = 16384;
 
 uint32_t decode_smem(int64_t M, int64_t K)
@@ -217,12 +214,8 @@ cudaError_t launch_fp8_decode(const void *x_bf16, const uint8_t *codes, const ui
     if (e != cudaSuccess)
         return e;
     static std::atomic<bool> set[kMaxDevices];
-    if (!set[di.device].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(fp8_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(decode_smem(kTokens, kMaxK)))) != cudaSuccess)
-            return e;
-        set[di.device].store(true, std::memory_order_release);
-    }
+    if ((e = ensure_smem(fp8_decode_kernel, decode_smem(kTokens, kMaxK), di.device, set)) != cudaSuccess)
+        return e;
     const uint32_t smem = decode_smem(M, K);
     const int64_t groups = (N + 15) / 16, most = (smem <= 100 * 1024 ? 2 : 1) * static_cast<int64_t>(di.num_sms);
     return launch_pdl(fp8_decode_kernel, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(kDThreads),

@@ -56,8 +56,6 @@
 // and kGemmSmem leaves room for one), the next grid may start only after a CTA
 // has its columns, and a cluster's CTAs give them back before they meet.
 
-#include <atomic>
-
 #include "device_utils.cuh"
 #include "fp8_block.cuh"
 #include "fp8_plan.h"
@@ -163,13 +161,6 @@ struct Slot {
         }
     }
 };
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 
 // A new group of four blocks starts at kb (or the contraction's range does).
 __device__ __forceinline__ bool starts_group(int kb, int kb0) { return (kb & 3) == 0 || kb == kb0; }
@@ -950,18 +941,6 @@ __global__ void __launch_bounds__(split_threads(SUMS), 2)
         __syncwarp();
         cluster_sync();  // no CTA leaves while another reads its shared memory
     }
-}
-
-constexpr int kMaxDevices = 64;
-
-template <class K> cudaError_t ensure_smem(K kernel, uint32_t bytes, int device, std::atomic<bool> *set)
-{
-    if (set[device].load(std::memory_order_acquire))
-        return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess)
-        set[device].store(true, std::memory_order_release);
-    return e;
 }
 
 Scales scales_of(const Fp8Operand &x, int64_t rows) { return {x.scale, ceil_div(rows, 128), x.tiles}; }

@@ -586,8 +586,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
 }
 
-constexpr int kMaxDevices = 64;
-
 }  // namespace
 
 cudaError_t read_gemm_error(uint32_t *flags, bool clear)
@@ -675,13 +673,9 @@ cudaError_t run_gemm(const CUtensorMap &am, const void *b_bf16, int64_t M, int64
                              BN) != 0)
         return cudaErrorInvalidValue;
     static std::atomic<bool> set[kMaxDevices];
-    if (!set[di.device].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_epilogue_kernel<BN, EPI>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
-        if (e != cudaSuccess)
-            return e;
-        set[di.device].store(true, std::memory_order_release);
-    }
+    cudaError_t e = ensure_smem(gemm_epilogue_kernel<BN, EPI>, C::kSmem, di.device, set);
+    if (e != cudaSuccess)
+        return e;
     const int64_t ntiles = (M / kBM) * (N / BN);
     const TailPlan p = plan_tail(ntiles, K / kBK, BN, di.num_sms, workspace ? workspace_bytes : 0);
     unsigned int *count = p.split > 1 ? static_cast<unsigned int *>(workspace) : nullptr;

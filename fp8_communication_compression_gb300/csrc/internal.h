@@ -1,6 +1,7 @@
 // Host-side declarations shared by the C-ABI layer and the kernel files.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -157,6 +158,21 @@ cudaError_t read_codec_error(uint32_t *flags, bool clear);
 cudaError_t read_gemm_error(uint32_t *flags, bool clear);
 cudaError_t read_fp8_error(uint32_t *flags, bool clear);
 cudaError_t read_norm_error(uint32_t *flags, bool clear);
+
+// Raises a kernel's dynamic shared-memory limit once per device.  The flag
+// is atomic because host threads may make their first launch concurrently;
+// setting the attribute twice is harmless.
+constexpr int kMaxDevices = 64;
+template <typename K>
+cudaError_t ensure_smem(K kernel, uint32_t bytes, int device, std::atomic<bool> *done)
+{
+    if (done[device].load(std::memory_order_acquire))
+        return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess)
+        done[device].store(true, std::memory_order_release);
+    return e;
+}
 
 // Launches `kernel` with programmatic stream serialization allowed, so that
 // it can be scheduled while the previous kernel in the stream drains (every

@@ -50,8 +50,6 @@
 // one partial row per CTA, and added over the CTAs in a fixed order by a
 // second small kernel: no atomics, the same bits every time.
 
-#include <atomic>
-
 #include "device_utils.cuh"
 #include "fp8_block.cuh"
 #include "internal.h"
@@ -69,13 +67,6 @@ constexpr int kMaxSlots = 8;
 
 // Gate modes (include/taco.h).
 constexpr int kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3;
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 
 // Eight values in four float2 registers: the arithmetic runs as packed
 // fp32x2 instructions (two lanes each).
@@ -367,8 +358,9 @@ struct TokenGates {
 
 // V units of 8 columns a thread (unit threadIdx.x + v blockDim.x), RPI rows
 // at a time; GATE a gate mode; FP8: n as codes and scales.
-// Two units a thread of rows inside granules: bounded to the 96 registers
-// with which two CTAs of up to 5440 columns share an SM (8192 x 5119: 91 us
+// Two units a thread of rows inside granules: the bound of 640 threads, more
+// than any launch has, is there for the 96 registers that it leaves, with
+// which two CTAs of up to 5440 columns share an SM (8192 x 5119: 91 us
 // against 132 with 118; 8192 x 6001 with a full gate 178 against 163).
 template <int V, int RPI, int GATE, bool FP8, bool VEC, bool DENSE>
 __global__ void __launch_bounds__(V == 2 && !VEC ? 640 : kMaxThreads, DENSE ? 2 : 1)
@@ -775,6 +767,7 @@ struct NormPlan {
 };
 
 constexpr uint32_t kSmemPerSm = 227 * 1024;
+constexpr uint32_t kMaxSmem = kSmemPerSm - 2048;  // of a CTA, beside its static arrays
 
 // CTAs whose registers an SM holds (a quarter of them in each of its four
 // partitions), eight at most.
@@ -813,7 +806,6 @@ NormPlan plan_norm(int64_t T, int d, int v, int tensors, int min_rows, int regs,
 // granules do, and gains more from a second CTA than from a fourth row in the
 // ring: 8192 x 5120 with a full gate, three rows against four (one CTA): FP8
 // 63 and 81 us, bf16 71 and 66.
-//
 //
 // One unit a thread and two rows at a time, or two units and one row, with
 // more and smaller CTAs.  Measured at 8192 rows, channel gate, one unit
@@ -864,18 +856,6 @@ NormPlan plan_backward(int64_t T, int d, int gate_mode, int sms)
     return p;
 }
 
-constexpr int kMaxDevices = 64;
-
-template <class K> cudaError_t allow_smem(K kernel, int device, std::atomic<bool> *set)
-{
-    if (set[device].load(std::memory_order_acquire))
-        return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
-    if (e == cudaSuccess)
-        set[device].store(true, std::memory_order_release);
-    return e;
-}
-
 // Two rows at a time where a thread has one unit.
 constexpr int rows_at_once(int v) { return v == 1 ? 2 : 1; }
 
@@ -886,7 +866,7 @@ cudaError_t run_forward(const NormPlan &p, const NormForward &a, int device, cud
         if (p.dense)
             return run_forward<V, GATE, FP8, VEC, true>(p, a, device, stream);
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = allow_smem(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, device, set);
+    cudaError_t e = ensure_smem(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, kMaxSmem, device, set);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(norm_forward_kernel<V, rows_at_once(V), GATE, FP8, VEC, DENSE>, dim3(p.grid), dim3(p.threads),
@@ -900,7 +880,7 @@ template <int V, int RPI, int MAXT, int GATE, bool VEC>
 cudaError_t run_backward(const NormPlan &p, const NormBackward &a, int device, cudaStream_t stream)
 {
     static std::atomic<bool> set[kMaxDevices];
-    cudaError_t e = allow_smem(norm_backward_kernel<V, RPI, MAXT, GATE, VEC>, device, set);
+    cudaError_t e = ensure_smem(norm_backward_kernel<V, RPI, MAXT, GATE, VEC>, kMaxSmem, device, set);
     if (e != cudaSuccess)
         return e;
     e = launch_pdl(norm_backward_kernel<V, RPI, MAXT, GATE, VEC>, dim3(p.grid), dim3(p.threads), p.smem, stream,
