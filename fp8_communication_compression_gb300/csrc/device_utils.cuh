@@ -40,11 +40,11 @@ __device__ __forceinline__ uint64_t global_timer_ns()
 // 32-element one.
 //
 // Kernels of the FP8 linear layer and of the norms do, where their grid is
-// small.  pdl_trigger() at the start of a kernel lets the next grid of the stream
-// start as soon as this one's CTAs leave room; every kernel still waits for
-// its predecessor's end in pdl_wait() before it touches memory.  It pays
-// where a layer's kernels are short (a few us) and their launch latency
-// shows.
+// small.  pdl_trigger() at the start of a kernel (of a product: once the CTA has
+// its tensor memory) lets the next grid of the stream start as soon as this
+// one's CTAs leave room; every kernel still waits for its predecessor's end in
+// pdl_wait() before it touches memory.  It pays where a layer's kernels are
+// short (a few us) and their launch latency shows.
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

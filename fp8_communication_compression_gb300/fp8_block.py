@@ -11,7 +11,11 @@ the slices' partial outputs, and the FP8 main gradients, run together.
 ``out`` and ``h1`` go into the next block's norms.  The backward pass keeps
 y, h1 and the u_p; n and the a_p are recomputed (AGoQ 2.A stores inputs and
 recomputes).  Weight gradients go straight into FP8 main gradients
-(agoq_fp8_accumulate), one micro-batch after the other."""
+(agoq_fp8_accumulate), one micro-batch after the other.
+
+It shows how the calls fit together.  What lies between them is plain torch
+(SiLU and its gradient, the stacking of the partial sums), and the bf16 weight
+gradient passes through memory on its way into the main gradients."""
 
 from __future__ import annotations
 

@@ -526,7 +526,9 @@ taco_status fp8_quantize_weight(const void *x_bf16, int64_t rows, int64_t cols, 
  * a_scale; b: codes [N][K] with b_scale, of rows or, with b_scale_tiles != 0,
  * of 128 x 128 tiles (any alignment).  K is the padded row length, a multiple
  * of 16 (K = 0: zeros).  out is 16-byte aligned.  The summation order is
- * fixed: the same inputs give the same bits.
+ * fixed: the same inputs give the same bits.  The tensor core's sums truncate:
+ * an fp32 result is summed in pieces of at most 1536 values, which are added
+ * rounded; a bf16 result is one sum.
  */
 taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b, const uint8_t *b_scale,
                      int32_t b_scale_tiles, int64_t M, int64_t N, int64_t K, void *out, int32_t out_is_bf16,
@@ -545,7 +547,8 @@ taco_status fp8_gemm(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b,
  *
  * The workspace (256-byte aligned, at least the bytes that
  * fp8_linear_workspace_bytes gives; its contents need not be kept) holds the
- * quantised activations.
+ * quantised activations.  Up to eight tokens the blocks of 128 are summed one by
+ * one and added in fp32, scaled, over the whole range of the scales.
  */
 taco_status fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward, uint64_t *bytes);
 taco_status fp8_linear(const void *x_bf16, const uint8_t *codes, const uint8_t *scale, int64_t M, int64_t N,
@@ -573,7 +576,9 @@ taco_status fp8_linear_backward(const void *dy_bf16, const void *x_bf16, const u
  *   TACO_GATE_FULL     bf16 [T][d], 16-byte aligned
  * n_scale null: n is bf16 [T][d].  Else n holds FP8 codes [T][fp8_pitch(d)]
  * and n_scale (16-byte aligned) their fp8_scale_bytes(T, d) scale bytes.
- * 1 <= d <= TACO_NORM_MAX_D; eps > 0.
+ * 1 <= d <= TACO_NORM_MAX_D; eps > 0, of any size.  Squares are summed in
+ * fp32: a row whose mean square leaves fp32's range (values of about 1e19) has
+ * an infinite norm, and its normalised values are zero.
  *
  * The backward pass takes dn and dh_out (gradients at n and h_out, bf16
  * [T][d]), y and h_out, and gives dy, dh (bf16 [T][d]), dg_post, dg_pre (fp32

@@ -67,3 +67,16 @@ def test_forward_with_a_small_eps(T, d, eps):
     assert ((h2.cpu().double() - ref_h).abs() <= half_step(ref_h) + u * mag).all()
     rn = (ref_n / torch.where(ref_h == 0, torch.ones_like(ref_h), ref_h)).abs()
     assert ((n.cpu().double() - ref_n).abs() <= half_step(ref_n) + u * (ref_n.abs() + rn * mag)).all()
+
+
+def test_values_whose_squares_leave_the_range():
+    # an infinite norm: the normalised values are zero, and the other rows are untouched
+    T, d = 4, 320
+    y, h, gp, gq, _ = make(T, d, "none", 64)
+    ref_h, ref_n = api.rmsnorm_gate_residual(y, h, gp, gq, None, 0.5)
+    y[1], h[2] = 1e20, -1e20
+    h2, n = api.rmsnorm_gate_residual(y, h, gp, gq, None, 0.5)
+    assert torch.equal(h2[1], (0.5 * h[1].float()).bfloat16())
+    assert not n[2].any() and torch.isfinite(n).all()
+    for r in (0, 3):
+        assert torch.equal(h2[r], ref_h[r]) and torch.equal(n[r], ref_n[r])
