@@ -58,6 +58,17 @@ SIGNATURES = {
     "rmsnorm_gate_residual_workspace_bytes": (ctypes.c_int, [_I64, _I64, _I32, _P]),
     "rmsnorm_gate_residual_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32, _F32, _F32, _I64, _I64,
                                                       _P, _P, _P, _P, _P, _P, _U64, _P]),
+    "token_logprob": (ctypes.c_int, [_P, _I32, _P, _I64, _I64, _I64, _F32, _P, _P, _P]),
+    "token_logprob_backward": (ctypes.c_int, [_P, _P, _I32, _P, _P, _I64, _I64, _I64, _F32, _P, _P]),
+    "policy_loss": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F32, _F32, _F32, _F32, _F32,
+                                   _P, _P, _P, _P, _P]),
+    "preference_loss_workspace_bytes": (ctypes.c_int, [_I64, _I64, _P]),
+    "preference_loss": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I64, _I64, _I64, _I64, _F32, _F32, _F32, _I32, _F32,
+                                       _P, _P, _P, _P, _P, _P, _U64, _P]),
+    "grad_norm_workspace_bytes": (ctypes.c_int, [_I64, _P]),
+    "grad_norm": (ctypes.c_int, [_P, _I64, _F32, _P, _P, _U64, _P]),
+    "adamw_step": (ctypes.c_int, [_P, _I64, _I32, ctypes.c_double, ctypes.c_double, _F32, _F32, _P, _F32, _P, _U64,
+                                  _P, _P]),
     "taco_host_pipeline_create": (ctypes.c_int, [_I32, _I64, _I64, _I32, _I32, _I32,
                                                  ctypes.POINTER(ctypes.c_void_p),
                                                  ctypes.POINTER(ctypes.c_uint64)]),
@@ -67,6 +78,18 @@ SIGNATURES = {
     "taco_watchdog_selftest": (ctypes.c_int, [_P]),
     "taco_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _I32]),
 }
+
+
+class GradTensor(ctypes.Structure):
+    """grad_tensor of include/taco.h."""
+    _fields_ = [("grad", _P), ("grad_scale", _P), ("n", _I64), ("grad_type", _I32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """adamw_tensor of include/taco.h."""
+    _fields_ = [("param", _P), ("copy_bf16", _P), ("grad", _P), ("grad_scale", _P), ("m", _P), ("v", _P),
+                ("m_scale", _P), ("v_scale", _P), ("n", _I64), ("lr", _F32), ("weight_decay", _F32),
+                ("grad_type", _I32)]
 
 
 class TacoError(RuntimeError):

@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
-from typing import Sequence
+from typing import NamedTuple, Sequence
 
 import torch
 
@@ -779,6 +779,217 @@ def rmsnorm_gate_residual_backward(dn: torch.Tensor, dh_new: torch.Tensor, y: to
         dg_pre.data_ptr(), _ptr(dgate), ws.data_ptr(), nbytes, _stream_of(y, stream))
     _lib.check("rmsnorm_gate_residual_backward", st)
     return dy, dh, dg_post, dg_pre, dgate
+
+
+# ------------------------------------------ losses over the vocabulary --
+
+_LOGITS = (torch.bfloat16, torch.float32)
+_I64 = (torch.int64,)
+
+
+class PolicyLoss(NamedTuple):
+    """``loss`` fp32 [], the sum of ``token_loss`` fp32 [T]; ``logp`` fp32 [T];
+    ``dlogits`` like the logits (None without a gradient)."""
+    loss: torch.Tensor
+    token_loss: torch.Tensor
+    logp: torch.Tensor
+    dlogits: torch.Tensor | None
+
+
+class PreferenceLoss(NamedTuple):
+    """``loss`` fp32 []; ``margin`` fp32 [pairs]; ``logratio`` fp32 [2 pairs],
+    each sequence's; ``logp`` fp32 [T]; ``dlogits`` like the logits (None
+    without a gradient)."""
+    loss: torch.Tensor
+    margin: torch.Tensor
+    logratio: torch.Tensor
+    logp: torch.Tensor
+    dlogits: torch.Tensor | None
+
+
+def _logits_args(logits, targets, vocab):
+    """(T, V, N, bf16) of logits [..., N] and targets with T elements."""
+    _need(logits, "logits", _LOGITS)
+    shape = logits.shape
+    if len(shape) < 2:
+        raise ValueError("logits must have at least two dimensions")
+    N = shape[-1]
+    T = 1
+    for n in shape[:-1]:
+        T *= n
+    _need(targets, "targets", _I64, T)
+    V = N if vocab is None else vocab
+    if not 1 <= V <= N:
+        raise ValueError(f"vocab is {V}, expected 1 to {N}")
+    return T, V, N, int(logits.dtype is torch.bfloat16)
+
+
+def _dlogits(logits, need_grad, dlogits, stream):
+    if not need_grad:
+        if dlogits is not None:
+            raise ValueError("dlogits without need_grad")
+        return None
+    if dlogits is None:
+        return _new_like(logits, stream)
+    _need(dlogits, "dlogits", (logits.dtype,))
+    if dlogits.shape != logits.shape:
+        raise ValueError(f"dlogits has shape {tuple(dlogits.shape)} and logits {tuple(logits.shape)}")
+    return dlogits
+
+
+def token_logprob(logits: torch.Tensor, targets: torch.Tensor, vocab: int | None = None, temperature: float = 1.0,
+                  stream=None):
+    """Log probability of each row's token: logits bf16 or fp32 [..., N], of
+    which the first ``vocab`` columns count, targets int64 with one token a
+    row (T in all; a negative one: no token, zeros).  Returns (logp fp32 [T],
+    lse fp32 [T]), lse the log of the sum of exp(logits / temperature)."""
+    T, V, N, bf16 = _logits_args(logits, targets, vocab)
+    logp = _new(T, torch.float32, logits.device, stream)
+    lse = _new(T, torch.float32, logits.device, stream)
+    st = _lib.load().token_logprob(logits.data_ptr(), bf16, targets.data_ptr(), T, V, N, temperature,
+                                   logp.data_ptr(), lse.data_ptr(), _stream_of(logits, stream))
+    _lib.check("token_logprob", st)
+    return logp, lse
+
+
+def token_logprob_backward(dlogp: torch.Tensor, logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                           vocab: int | None = None, temperature: float = 1.0, dlogits: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """Gradient of token_logprob at the logits from dlogp fp32 [T] and the
+    forward's lse; ``dlogits`` may be the logits themselves.  Rows with dlogp
+    = 0 or without a token get zeros, and their logits are not read."""
+    T, V, N, bf16 = _logits_args(logits, targets, vocab)
+    _need(dlogp, "dlogp", _F32, T)
+    _need(lse, "lse", _F32, T)
+    out = _dlogits(logits, True, dlogits, stream)
+    st = _lib.load().token_logprob_backward(dlogp.data_ptr(), logits.data_ptr(), bf16, targets.data_ptr(),
+                                            lse.data_ptr(), T, V, N, temperature, out.data_ptr(),
+                                            _stream_of(logits, stream))
+    _lib.check("token_logprob_backward", st)
+    return out
+
+
+def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                weights: torch.Tensor, ref_logp: torch.Tensor | None = None, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl: float = 0.0, vocab: int | None = None, temperature: float = 1.0,
+                grad_scale: float = 1.0, need_grad: bool = True, dlogits: torch.Tensor | None = None,
+                stream=None) -> PolicyLoss:
+    """Clipped policy loss and its gradient at the logits, in one pass over
+    them.  Per row, with r = exp(logp - old_logp) and d = ref_logp - logp:
+
+        w (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(d) - 1 - d))
+
+    logits and targets as token_logprob's; old_logp, advantages, weights and
+    ref_logp fp32 with T values.  ``weights`` holds the mask and the
+    normalisation (1 / tokens, say): rows of weight 0 do not count, whatever
+    their other inputs hold.  The gradient is multiplied by ``grad_scale``;
+    ``dlogits`` may be the logits themselves."""
+    T, V, N, bf16 = _logits_args(logits, targets, vocab)
+    _need(old_logp, "old_logp", _F32, T)
+    _need(advantages, "advantages", _F32, T)
+    _need(weights, "weights", _F32, T)
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", _F32, T)
+    elif kl != 0.0:
+        raise ValueError("a KL term needs ref_logp")
+    out = _dlogits(logits, need_grad, dlogits, stream)
+    buf = _new(2 * T + 1, torch.float32, logits.device, stream)
+    loss, token_loss, logp = buf[2 * T], buf[:T], buf[T:2 * T]
+    at = buf.data_ptr()
+    st = _lib.load().policy_loss(logits.data_ptr(), bf16, targets.data_ptr(), old_logp.data_ptr(),
+                                 advantages.data_ptr(), weights.data_ptr(), _ptr(ref_logp), T, V, N, temperature,
+                                 clip_low, clip_high, kl, grad_scale, at + 8 * T, at, at + 4 * T, _ptr(out),
+                                 _stream_of(logits, stream))
+    _lib.check("policy_loss", st)
+    return PolicyLoss(loss, token_loss, logp, out)
+
+
+def preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torch.Tensor,
+                    ref_logp: torch.Tensor | None = None, beta: float = 0.1, label_smoothing: float = 0.0,
+                    mean: bool = False, vocab: int | None = None, temperature: float = 1.0, grad_scale: float = 1.0,
+                    need_grad: bool = True, dlogits: torch.Tensor | None = None, stream=None) -> PreferenceLoss:
+    """Preference loss of pairs of sequences and its gradient at the logits.
+
+    logits and targets as token_logprob's; sequence i is the rows offsets[i]
+    to offsets[i + 1] - 1 (int64 [2 pairs + 1], on the device), the preferred
+    one of a pair first.  ref_logp fp32, T values: the reference model's
+    token_logprob.  With s_i the sum (``mean``: the mean) of logp - ref_logp
+    over a sequence's tokens and z = beta (s_2i - s_2i+1), the loss is the
+    mean of -(1 - label_smoothing) log sig(z) - label_smoothing log sig(-z).
+    Rows in no sequence, and those without a token, do not count."""
+    T, V, N, bf16 = _logits_args(logits, targets, vocab)
+    _need(offsets, "offsets", _I64)
+    if offsets.dim() != 1 or offsets.numel() < 3 or offsets.numel() % 2 == 0:
+        raise ValueError(f"offsets has shape {tuple(offsets.shape)}, expected (2 pairs + 1,)")
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", _F32, T)
+    pairs = offsets.numel() // 2
+    out = _dlogits(logits, need_grad, dlogits, stream)
+    buf = _new(T + 3 * pairs + 1, torch.float32, logits.device, stream)
+    logp, logratio, margin, loss = buf[:T], buf[T:T + 2 * pairs], buf[T + 2 * pairs:T + 3 * pairs], buf[T + 3 * pairs]
+    nbytes = 4 * (2 * T + pairs)
+    ws = _workspace(nbytes, logits.device, stream)
+    at = buf.data_ptr()
+    st = _lib.load().preference_loss(logits.data_ptr(), bf16, targets.data_ptr(), offsets.data_ptr(), _ptr(ref_logp),
+                                     T, V, N, pairs, temperature, beta, label_smoothing, int(mean), grad_scale,
+                                     at + 4 * (T + 3 * pairs), at + 4 * (T + 2 * pairs), at + 4 * T, at, _ptr(out),
+                                     ws.data_ptr(), nbytes, _stream_of(logits, stream))
+    _lib.check("preference_loss", st)
+    return PreferenceLoss(loss, margin, logratio, logp, out)
+
+
+# ------------------------------------------------------- the optimizer --
+
+_GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.uint8: 2, torch.float8_e4m3fn: 2}
+
+
+def _grad_of(g, name: str, numel: int | None, device: int):
+    """(pointer, scale pointer, values, type) of a gradient: a fp32 or bf16
+    tensor, or an FP8 main gradient (codes, scale)."""
+    scale = None
+    if type(g) is tuple:
+        g, scale = g
+    if not isinstance(g, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor or a tuple (codes, scale)")
+    kind = _GRAD_TYPES.get(g.dtype)
+    if kind is None or (kind == 2) != (scale is not None):
+        raise TypeError(f"{name} must be fp32, bf16, or FP8 codes with their scale")
+    n = g.numel()
+    if g.get_device() != device or not g.is_contiguous() or (numel is not None and n != numel):
+        raise ValueError(f"{name} must be contiguous, on cuda:{device}" + ("" if numel is None else f", with {numel} values"))
+    if scale is None:
+        return g.data_ptr(), None, n, kind
+    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or scale.get_device() != device \
+            or not scale.is_contiguous() or scale.numel() != -(-n // 128):
+        raise ValueError(f"{name}: the scale must be fp32 with {-(-n // 128)} values, contiguous, on cuda:{device}")
+    return g.data_ptr(), scale.data_ptr(), n, kind
+
+
+def _grad_norm(table, count: int, device: torch.device, grad_scale: float, out: torch.Tensor, stream) -> torch.Tensor:
+    v = ctypes.c_uint64(0)
+    lib = _lib.load()
+    _lib.check("grad_norm_workspace_bytes", lib.grad_norm_workspace_bytes(count, ctypes.byref(v)))
+    ws = _workspace(v.value, device, stream)
+    st = lib.grad_norm(table, count, grad_scale, out.data_ptr(), ws.data_ptr(), v.value, _stream_of(out, stream))
+    _lib.check("grad_norm", st)
+    return out
+
+
+def grad_norm(grads: Sequence, grad_scale: float = 1.0, stream=None) -> torch.Tensor:
+    """|grad_scale| times the 2-norm of all gradients together, fp32 []: each
+    a fp32 or bf16 tensor, or an FP8 main gradient (codes, scale), as
+    agoq_fp8_accumulate keeps it.  Summed in a fixed order."""
+    if not grads:
+        raise ValueError("grads must not be empty")
+    first = grads[0][0] if type(grads[0]) is tuple else grads[0]
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("grads must be CUDA tensors")
+    table = (_lib.GradTensor * len(grads))()
+    device = first.get_device()
+    for i, g in enumerate(grads):
+        table[i] = _lib.GradTensor(*_grad_of(g, f"grads[{i}]", None, device))
+    out = _new((), torch.float32, first.device, stream)
+    return _grad_norm(table, len(grads), first.device, grad_scale, out, stream)
 
 
 def taco_device_error(clear: bool = True) -> int:

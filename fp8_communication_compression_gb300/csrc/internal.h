@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/taco.h"
+
 namespace taco {
 
 // Per-device facts the launchers need (cached on first use).
@@ -152,6 +154,51 @@ struct NormBackward {
 };
 cudaError_t launch_norm_backward(const NormBackward &a, cudaStream_t stream);
 cudaError_t norm_backward_workspace(int64_t T, int64_t d, int gate_mode, uint64_t *bytes);
+
+// The losses over the vocabulary (loss_kernels.cu).  Logits [T][N] in bf16 or
+// fp32, their first V columns in use.
+struct LossRows {
+    const void *logits;
+    const int64_t *targets;
+    int64_t T, V, N;
+    float temperature, inv_temperature, grad_scale;
+    float *logp, *lse, *coef;            // forward; coef: zeroed in rows that do not count (may be null)
+    const int64_t *offsets;              // rows outside offsets[0] .. offsets[sequences] do not count (may be null)
+    int64_t sequences;
+    const float *dlogp;                  // backward (with lse)
+    const float *old_logp, *advantages, *weights, *ref_logp;  // policy loss
+    float clip_lo, clip_hi, kl;
+    float *token_loss;
+    void *dlogits;                       // may be null in the policy and the preference loss
+};
+struct PairArgs {
+    const int64_t *targets, *offsets;
+    int64_t T, pairs;
+    const float *logp, *ref_logp;
+    float beta, smoothing;
+    bool mean;
+    float *margin, *logratio, *pair_loss, *coef;
+};
+cudaError_t launch_logprob(const LossRows &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_logprob_backward(const LossRows &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_policy_loss(const LossRows &a, bool bf16, float *loss, cudaStream_t stream);
+cudaError_t launch_preference_loss(const LossRows &a, const PairArgs &p, bool bf16, float *loss, cudaStream_t stream);
+
+// The optimizer (adamw_kernels.cu).  `tensors` are host arrays.
+constexpr int kAdamWTensors = 320, kNormTensors = 720;  // of one launch
+int grad_norm_launches(int64_t count);
+cudaError_t grad_norm_workspace(int64_t count, uint64_t *bytes);
+cudaError_t launch_grad_norm(const grad_tensor *tensors, int64_t count, float grad_scale, float *norm,
+                             void *workspace, cudaStream_t stream);
+struct AdamWStep {
+    double beta1, beta2;
+    float eps, grad_scale, max_norm;                // max_norm 0: no clipping
+    const float *norm, *lr_factor;                  // each may be null
+    uint64_t seed;
+    int64_t *state;
+};
+cudaError_t launch_adamw(const adamw_tensor *tensors, int64_t count, bool bits8, const AdamWStep &h,
+                         cudaStream_t stream);
 
 cudaError_t launch_watchdog_selftest(cudaStream_t stream);
 cudaError_t read_codec_error(uint32_t *flags, bool clear);

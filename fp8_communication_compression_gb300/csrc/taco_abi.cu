@@ -838,6 +838,251 @@ taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, c
                                                 reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Shared checks of the losses over the vocabulary.
+static taco_status check_loss(int64_t T, int64_t V, int64_t N, float temperature)
+{
+    if (T < 0 || V < 1 || N < V || !positive_finite(temperature) || !positive_finite(1.0f / temperature))
+        return TACO_ERR_INVALID_ARG;
+    if (T >= (int64_t(1) << 31) || N > (int64_t(1) << 31))
+        return TACO_ERR_UNSUPPORTED;
+    return TACO_OK;
+}
+
+static taco::LossRows loss_rows(const void *logits, const int64_t *targets, int64_t T, int64_t V, int64_t N,
+                                float temperature)
+{
+    taco::LossRows a = {};
+    a.logits = logits, a.targets = targets;
+    a.T = T, a.V = V, a.N = N;
+    a.temperature = temperature, a.inv_temperature = 1.0f / temperature, a.grad_scale = 1.0f;
+    return a;
+}
+
+taco_status token_logprob(const void *logits, int32_t logits_bf16, const int64_t *targets, int64_t T, int64_t V,
+                          int64_t N, float temperature, float *logp, float *lse, taco_stream_t stream)
+{
+    taco_status st = check_loss(T, V, N, temperature);
+    if (st != TACO_OK || T == 0)
+        return st;
+    if (!logits || !targets || !logp || !lse)
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(targets, 8) || !aligned(logp, 4) || !aligned(lse, 4))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t t = T, all = t * N * (logits_bf16 ? 2 : 4);
+    const Span outs[2] = {{logp, 4 * t}, {lse, 4 * t}};
+    const Span ins[2] = {{logits, all}, {targets, 8 * t}};
+    if (!apart(outs, 2, ins, 2))
+        return TACO_ERR_INVALID_ARG;
+    taco::LossRows a = loss_rows(logits, targets, T, V, N, temperature);
+    a.logp = logp, a.lse = lse;
+    return from_cuda(taco::launch_logprob(a, logits_bf16 != 0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+taco_status token_logprob_backward(const float *dlogp, const void *logits, int32_t logits_bf16,
+                                   const int64_t *targets, const float *lse, int64_t T, int64_t V, int64_t N,
+                                   float temperature, void *dlogits, taco_stream_t stream)
+{
+    taco_status st = check_loss(T, V, N, temperature);
+    if (st != TACO_OK || T == 0)
+        return st;
+    if (!dlogp || !logits || !targets || !lse || !dlogits)
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(targets, 8) || !aligned(dlogp, 4) ||
+        !aligned(lse, 4))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t t = T, all = t * N * (logits_bf16 ? 2 : 4);
+    const Span outs[1] = {{dlogits, all}};
+    const Span ins[4] = {{targets, 8 * t}, {dlogp, 4 * t}, {lse, 4 * t}, {logits, logits == dlogits ? 0 : all}};
+    if (!apart(outs, 1, ins, 4))
+        return TACO_ERR_INVALID_ARG;
+    taco::LossRows a = loss_rows(logits, targets, T, V, N, temperature);
+    a.dlogp = dlogp, a.lse = const_cast<float *>(lse), a.dlogits = dlogits;
+    return from_cuda(taco::launch_logprob_backward(a, logits_bf16 != 0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+taco_status policy_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const float *old_logp,
+                        const float *advantages, const float *weights, const float *ref_logp, int64_t T, int64_t V,
+                        int64_t N, float temperature, float clip_low, float clip_high, float kl, float grad_scale,
+                        float *loss, float *token_loss, float *logp, void *dlogits, taco_stream_t stream)
+{
+    taco_status st = check_loss(T, V, N, temperature);
+    if (st != TACO_OK)
+        return st;
+    if (!(clip_low >= 0.0f && clip_low <= 1.0f) || !(clip_high >= 0.0f) || !std::isfinite(clip_high) ||
+        !std::isfinite(kl) || !std::isfinite(grad_scale) || (kl != 0.0f && !ref_logp && T > 0))
+        return TACO_ERR_INVALID_ARG;
+    if (!loss || (T > 0 && (!logits || !targets || !old_logp || !advantages || !weights || !token_loss || !logp)))
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(loss, 4) ||
+        (T > 0 && (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(targets, 8) || !aligned(old_logp, 4) ||
+                   !aligned(advantages, 4) || !aligned(weights, 4) || !aligned(ref_logp, 4) ||
+                   !aligned(token_loss, 4) || !aligned(logp, 4))))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t t = T, all = t * N * (logits_bf16 ? 2 : 4);
+    const Span outs[4] = {{loss, 4}, {token_loss, 4 * t}, {logp, 4 * t}, {dlogits, dlogits ? all : 0}};
+    const Span ins[6] = {{targets, 8 * t},  {old_logp, 4 * t},
+                         {advantages, 4 * t}, {weights, 4 * t},
+                         {ref_logp, ref_logp ? 4 * t : 0}, {logits, logits == dlogits ? 0 : all}};
+    if (!apart(outs, 4, ins, 6))
+        return TACO_ERR_INVALID_ARG;
+    taco::LossRows a = loss_rows(logits, targets, T, V, N, temperature);
+    a.old_logp = old_logp, a.advantages = advantages, a.weights = weights, a.ref_logp = kl != 0.0f ? ref_logp : nullptr;
+    a.clip_lo = 1.0f - clip_low, a.clip_hi = 1.0f + clip_high, a.kl = kl, a.grad_scale = grad_scale;
+    a.token_loss = token_loss, a.logp = logp, a.dlogits = dlogits;
+    return from_cuda(
+        taco::launch_policy_loss(a, logits_bf16 != 0, loss, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+taco_status preference_loss_workspace_bytes(int64_t T, int64_t pairs, uint64_t *bytes)
+{
+    if (!bytes || T < 0 || pairs < 1)
+        return TACO_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (T >= (int64_t(1) << 31) || pairs >= (int64_t(1) << 30))
+        return TACO_ERR_UNSUPPORTED;
+    *bytes = 4 * (2 * static_cast<uint64_t>(T) + pairs);  // lse, the gradients at logp, the pairs' losses
+    return TACO_OK;
+}
+
+taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const int64_t *offsets,
+                            const float *ref_logp, int64_t T, int64_t V, int64_t N, int64_t pairs, float temperature,
+                            float beta, float label_smoothing, int32_t mean, float grad_scale, float *loss,
+                            float *margin, float *logratio, float *logp, void *dlogits, void *workspace,
+                            uint64_t workspace_bytes, taco_stream_t stream)
+{
+    taco_status st = check_loss(T, V, N, temperature);
+    uint64_t need = 0;
+    if (st != TACO_OK || (st = preference_loss_workspace_bytes(T, pairs, &need)) != TACO_OK)
+        return st;
+    if (!std::isfinite(beta) || !(label_smoothing >= 0.0f && label_smoothing <= 1.0f) || !std::isfinite(grad_scale))
+        return TACO_ERR_INVALID_ARG;
+    if (!offsets || !loss || !margin || !logratio || !workspace || workspace_bytes < need ||
+        (T > 0 && (!logits || !targets || !logp)))
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(offsets, 8) || !aligned(loss, 4) || !aligned(margin, 4) || !aligned(logratio, 4) ||
+        !aligned(workspace, 256) ||
+        (T > 0 && (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(targets, 8) || !aligned(ref_logp, 4) ||
+                   !aligned(logp, 4))))
+        return TACO_ERR_MISALIGNED;
+    const uint64_t t = T, b = pairs, all = t * N * (logits_bf16 ? 2 : 4);
+    const Span outs[6] = {{loss, 4}, {margin, 4 * b}, {logratio, 8 * b}, {logp, 4 * t}, {dlogits, dlogits ? all : 0},
+                          {workspace, need}};
+    const Span ins[4] = {{targets, 8 * t},
+                         {offsets, 8 * (2 * b + 1)},
+                         {ref_logp, ref_logp ? 4 * t : 0},
+                         {logits, logits == dlogits ? 0 : all}};
+    if (!apart(outs, 6, ins, 4) || (logits && overlap(workspace, need, logits, all)))
+        return TACO_ERR_INVALID_ARG;
+    float *ws = static_cast<float *>(workspace);
+    taco::LossRows a = loss_rows(logits, targets, T, V, N, temperature);
+    a.logp = logp, a.lse = ws, a.coef = ws + T, a.dlogp = ws + T;
+    a.offsets = offsets, a.sequences = 2 * pairs;
+    a.grad_scale = grad_scale, a.dlogits = dlogits;
+    const taco::PairArgs p = {targets, offsets, T,      pairs,    logp,         ref_logp, beta,
+                              label_smoothing, mean != 0, margin, logratio, ws + 2 * T, ws + T};
+    return from_cuda(
+        taco::launch_preference_loss(a, p, logits_bf16 != 0, loss, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// A gradient of n > 0 values.
+static taco_status check_grad(const void *grad, const float *scale, int32_t type, int64_t n)
+{
+    if (type < TACO_GRAD_F32 || type > TACO_GRAD_FP8 || !grad || (type == TACO_GRAD_FP8) != (scale != nullptr))
+        return TACO_ERR_INVALID_ARG;
+    if (n > (int64_t(1) << 40))
+        return TACO_ERR_UNSUPPORTED;
+    return aligned(grad, 16) && aligned(scale, 4) ? TACO_OK : TACO_ERR_MISALIGNED;
+}
+
+static uint64_t grad_bytes(int32_t type, uint64_t n) { return type == TACO_GRAD_F32 ? 4 * n : type == TACO_GRAD_BF16 ? 2 * n : n; }
+
+taco_status grad_norm_workspace_bytes(int64_t count, uint64_t *bytes)
+{
+    if (!bytes || count < 0)
+        return TACO_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (count > (int64_t(1) << 24))
+        return TACO_ERR_UNSUPPORTED;
+    return from_cuda(taco::grad_norm_workspace(count, bytes));
+}
+
+taco_status grad_norm(const grad_tensor *tensors, int64_t count, float grad_scale, float *norm, void *workspace,
+                      uint64_t workspace_bytes, taco_stream_t stream)
+{
+    uint64_t need = 0, total = 0;
+    taco_status st = grad_norm_workspace_bytes(count, &need);
+    if (st != TACO_OK)
+        return st;
+    if (!norm || !std::isfinite(grad_scale) || (count > 0 && (!tensors || !workspace || workspace_bytes < need)))
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(norm, 4) || !aligned(workspace, 256))
+        return TACO_ERR_MISALIGNED;
+    const Span outs[2] = {{norm, 4}, {workspace, need}};
+    for (int64_t i = 0; i < count; ++i) {
+        const grad_tensor &t = tensors[i];
+        if (t.n < 0)
+            return TACO_ERR_INVALID_ARG;
+        if (t.n == 0)
+            continue;
+        if ((st = check_grad(t.grad, t.grad_scale, t.grad_type, t.n)) != TACO_OK)
+            return st;
+        const uint64_t n = t.n;
+        const Span ins[2] = {{t.grad, grad_bytes(t.grad_type, n)}, {t.grad_scale, t.grad_scale ? (n + 127) / 128 * 4 : 0}};
+        if (!apart(outs, 2, ins, 2))
+            return TACO_ERR_INVALID_ARG;
+        if ((total += n) > (uint64_t(1) << 42))
+            return TACO_ERR_UNSUPPORTED;
+    }
+    return from_cuda(taco::launch_grad_norm(tensors, count, grad_scale, norm, workspace,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+taco_status adamw_step(const adamw_tensor *tensors, int64_t count, int32_t state_bits, double beta1, double beta2,
+                       float eps, float grad_scale, const float *norm, float max_norm, const float *lr_factor,
+                       uint64_t seed, int64_t *state, taco_stream_t stream)
+{
+    if (count < 0 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !positive_finite(eps) ||
+        !std::isfinite(grad_scale) || !(max_norm >= 0.0f) || !std::isfinite(max_norm) || (max_norm > 0.0f && !norm))
+        return TACO_ERR_INVALID_ARG;
+    if ((state_bits != 8 && state_bits != 32) || count > (int64_t(1) << 24))
+        return TACO_ERR_UNSUPPORTED;
+    if (count == 0)
+        return TACO_OK;
+    if (!tensors || !state)
+        return TACO_ERR_INVALID_ARG;
+    if (!aligned(state, 8) || !aligned(norm, 4) || !aligned(lr_factor, 4))
+        return TACO_ERR_MISALIGNED;
+    uint64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const adamw_tensor &t = tensors[i];
+        if (t.n < 0 || !std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
+            return TACO_ERR_INVALID_ARG;
+        if (t.n == 0)
+            continue;
+        taco_status st = check_grad(t.grad, t.grad_scale, t.grad_type, t.n);
+        if (st != TACO_OK)
+            return st;
+        const bool bits8 = state_bits == 8;
+        if (!t.param || !t.m || !t.v || (bits8 && (!t.m_scale || !t.v_scale)))
+            return TACO_ERR_INVALID_ARG;
+        if (!aligned(t.param, 16) || !aligned(t.copy_bf16, 16) || !aligned(t.m, 16) || !aligned(t.v, 16) ||
+            (bits8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
+            return TACO_ERR_MISALIGNED;
+        const uint64_t n = t.n, sc = (n + 127) / 128 * 4, sb = bits8 ? n : 4 * n;
+        const Span outs[7] = {{t.param, 4 * n}, {t.copy_bf16, t.copy_bf16 ? 2 * n : 0}, {t.m, sb}, {t.v, sb},
+                              {t.m_scale, bits8 ? sc : 0}, {t.v_scale, bits8 ? sc : 0}, {state, 16}};
+        const Span ins[4] = {{t.grad, grad_bytes(t.grad_type, n)}, {t.grad_scale, t.grad_scale ? sc : 0},
+                             {norm, norm ? 4u : 0u}, {lr_factor, lr_factor ? 4u : 0u}};
+        if (!apart(outs, 7, ins, 4))
+            return TACO_ERR_INVALID_ARG;
+        if ((total += n) > (uint64_t(1) << 42))
+            return TACO_ERR_UNSUPPORTED;
+    }
+    return from_cuda(taco::launch_adamw(tensors, count, state_bits == 8,
+                                        {beta1, beta2, eps, grad_scale, max_norm, norm, lr_factor, seed, state},
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
 struct taco_host_pipeline {
     taco::HostPipeline *impl;
 };

@@ -1,0 +1,70 @@
+"""The output layer of a model trained with Fp8Block: logits from an FP8
+linear layer, a loss over the vocabulary with its gradient at the logits, and
+the layer's backward pass into an FP8 main gradient.
+
+    logits = Q(x) W^T                            W [vocab, d], padded to 128 rows
+    loss, dlogits                                policy_loss or preference_loss
+    dx = Q(dlogits) W;  main += Q(dlogits)^T Q(x)
+
+The gradient takes the logits' place: they are the largest tensor of a step."""
+
+from __future__ import annotations
+
+import torch
+
+from . import api
+
+
+class Fp8Head:
+    """``w`` bf16 [vocab, d], d a multiple of 128.  The rows up to the next
+    multiple of 128 are zeros, and their logits do not count.  ``main``: the
+    weight's FP8 main gradient (codes [rows, d], multipliers)."""
+
+    def __init__(self, w: torch.Tensor):
+        vocab, d = w.shape
+        if d % 128 or not vocab:
+            raise ValueError("w must be [vocab, d], d a multiple of 128")
+        self.vocab, self.d, self.rows = vocab, d, -(-vocab // 128) * 128
+        self.load_weights(w)
+        self.main = (torch.zeros((self.rows, d), dtype=torch.uint8, device=w.device),
+                     torch.ones(self.rows * d // 128, dtype=torch.float32, device=w.device))
+
+    def load_weights(self, w: torch.Tensor) -> None:
+        """Quantises the weight: at the start, and after an update.  ``w``: bf16
+        [vocab, d] or [rows, d] (what an update of the padded weight gives;
+        its rows from ``vocab`` on have to be zeros)."""
+        if w.shape not in ((self.vocab, self.d), (self.rows, self.d)):
+            raise ValueError(f"w must be [{self.vocab}, {self.d}] or [{self.rows}, {self.d}]")
+        if w.shape[0] < self.rows:
+            w = torch.nn.functional.pad(w, (0, 0, 0, self.rows - w.shape[0]))
+        self.w = api.fp8_quantize_weight(w)
+
+    def logits(self, x: torch.Tensor) -> torch.Tensor:
+        """x bf16 [..., d] -> bf16 [..., rows]."""
+        return api.fp8_linear(x, self.w[0], self.w[1])
+
+    def token_logprob(self, x: torch.Tensor, targets: torch.Tensor, temperature: float = 1.0) -> torch.Tensor:
+        """Log probabilities fp32 [T] of the targets: a reference model's, or
+        the policy's at the time of sampling."""
+        return api.token_logprob(self.logits(x), targets, self.vocab, temperature)[0]
+
+    def policy_loss(self, x: torch.Tensor, targets: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                    weights: torch.Tensor, **options):
+        """(api.policy_loss's result, dx bf16 like x); the weight's gradient is
+        added to ``main``.  ``options``: api.policy_loss's."""
+        logits = self.logits(x)
+        got = api.policy_loss(logits, targets, old_logp, advantages, weights, vocab=self.vocab, dlogits=logits,
+                              **options)
+        return got, self._backward(logits, x)
+
+    def preference_loss(self, x: torch.Tensor, targets: torch.Tensor, offsets: torch.Tensor,
+                        ref_logp: torch.Tensor | None = None, **options):
+        """(api.preference_loss's result, dx bf16 like x), likewise."""
+        logits = self.logits(x)
+        got = api.preference_loss(logits, targets, offsets, ref_logp, vocab=self.vocab, dlogits=logits, **options)
+        return got, self._backward(logits, x)
+
+    def _backward(self, dlogits: torch.Tensor, x: torch.Tensor) -> torch.Tensor:
+        dx, dw = api.fp8_linear_backward(dlogits, x, self.w[2], self.w[3], dw_dtype=torch.bfloat16)
+        api.agoq_fp8_accumulate(*self.main, dw)
+        return dx

@@ -1,0 +1,137 @@
+"""AdamW over many tensors at once, with states in 32 or in 8 bits, from fp32
+or bf16 gradients or straight from FP8 main gradients (agoq_fp8_accumulate).
+
+    g = c grad,  c = grad_scale min(1, max_norm / (norm + 1e-6))
+    m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+    p = p - lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+
+The weights are fp32; each may have a bf16 copy, which the step writes too (what
+fp8_quantize_weight reads).  In 8 bits m and r = sqrt(v) are E4M3 codes with one
+fp32 multiplier per block of 128, rounded up with the probability of the rest:
+the format and the hash stand in include/taco.h (adamw_step)."""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Sequence
+
+import torch
+
+from . import _lib, api
+
+
+class AdamW:
+    """``params``: fp32 tensors, updated in place; ``copies``: bf16 tensors of
+    the same sizes, or None in places or altogether.  ``lr`` and
+    ``weight_decay``: one number, or one a tensor.  ``state_bits``: 32 or 8.
+    ``max_norm``: the norm that the gradients are clipped to; a step whose norm
+    is not finite is then left out.  ``seed``: of the 8-bit states' rounding.
+
+    ``m`` and ``v`` hold all tensors' states in one buffer each (in 8 bits
+    ``v`` holds r, and ``m_scale`` and ``v_scale`` the multipliers); tensor i's
+    part begins at ``starts[i]``, a multiple of 128.  ``steps`` (int64 [2] on the
+    device) counts the steps done in its first value.  One object's steps belong
+    on one stream, or on streams that wait for one another."""
+
+    def __init__(self, params: Sequence[torch.Tensor], copies: Sequence[torch.Tensor | None] | None = None,
+                 lr: float | Sequence[float] = 1e-3, betas: tuple[float, float] = (0.9, 0.95), eps: float = 1e-8,
+                 weight_decay: float | Sequence[float] = 0.0, state_bits: int = 32, max_norm: float | None = None,
+                 seed: int = 0):
+        params = list(params)
+        if not params:
+            raise ValueError("params must not be empty")
+        copies = [None] * len(params) if copies is None else list(copies)
+        each = lambda v: [float(v)] * len(params) if isinstance(v, (int, float)) else [float(x) for x in v]
+        lrs, decays = each(lr), each(weight_decay)
+        if not len(copies) == len(lrs) == len(decays) == len(params):
+            raise ValueError("copies, lr and weight_decay must have one entry a tensor")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0 and eps > 0.0):
+            raise ValueError("betas must lie in [0, 1) and eps be positive")
+        if max_norm is not None and not max_norm > 0.0:
+            raise ValueError("max_norm must be positive")
+        for i, p in enumerate(params):
+            api._need(p, f"params[{i}]", (torch.float32,))
+            if copies[i] is not None:
+                api._need(copies[i], f"copies[{i}]", (torch.bfloat16,), p.numel())
+        every = params + [c for c in copies if c is not None]
+        if any(t.device != params[0].device for t in every):
+            raise ValueError("params and copies must be on one device")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in every if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("params and copies must not overlap")
+        self.params, self.copies = params, copies
+        self.betas, self.eps, self.state_bits, self.max_norm, self.seed = betas, eps, state_bits, max_norm, seed
+        self.device = params[0].device
+        self.sizes = [p.numel() for p in params]
+        self.starts, at = [], 0
+        for n in self.sizes:
+            self.starts.append(at)
+            at += -(-n // 128) * 128
+        new = lambda n, dt: torch.zeros(n, dtype=dt, device=self.device)
+        dt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        self.m, self.v = new(at, dt), new(at, dt)
+        self.m_scale = torch.ones(at // 128, device=self.device) if state_bits == 8 else None
+        self.v_scale = torch.ones(at // 128, device=self.device) if state_bits == 8 else None
+        self.steps = new(2, torch.int64)
+        size = self.m.element_size()
+        self._table = (_lib.AdamWTensor * len(params))()
+        self._norms = (_lib.GradTensor * len(params))()
+        for i, (p, c, start) in enumerate(zip(params, copies, self.starts)):
+            t = self._table[i]
+            t.param, t.copy_bf16, t.n, t.lr, t.weight_decay = p.data_ptr(), api._ptr(c), p.numel(), lrs[i], decays[i]
+            t.m, t.v = self.m.data_ptr() + start * size, self.v.data_ptr() + start * size
+            if state_bits == 8:
+                t.m_scale, t.v_scale = (s.data_ptr() + start // 128 * 4 for s in (self.m_scale, self.v_scale))
+
+    def step(self, grads: Sequence, grad_scale: float = 1.0, lr_factor: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor | None:
+        """One step from one gradient a tensor (a fp32 or bf16 tensor, or an FP8
+        main gradient (codes, scale)), each multiplied by ``grad_scale``.
+        ``lr_factor``: a factor of all learning rates, one fp32 value on the
+        device.  Returns the gradients' norm before clipping, fp32 [] (None
+        without ``max_norm``).  A captured step can be replayed: it counts
+        itself, and reads ``lr_factor`` when it runs."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
+        if lr_factor is not None:
+            api._need(lr_factor, "lr_factor", (torch.float32,), 1)
+        device, table, norms = self.params[0].get_device(), self._table, self._norms
+        for i, (g, n) in enumerate(zip(grads, self.sizes)):
+            grad, scale, _, kind = api._grad_of(g, f"grads[{i}]", n, device)
+            t = table[i]
+            t.grad, t.grad_scale, t.grad_type = grad, scale, kind
+            if self.max_norm is not None:
+                t = norms[i]
+                t.grad, t.grad_scale, t.n, t.grad_type = grad, scale, n, kind
+        norm = None
+        if self.max_norm is not None:
+            norm = api._new((), torch.float32, self.device, stream)
+            api._grad_norm(norms, len(norms), self.device, grad_scale, norm, stream)
+        st = _lib.load().adamw_step(table, len(table), self.state_bits, self.betas[0], self.betas[1], self.eps,
+                                    grad_scale, api._ptr(norm), self.max_norm or 0.0, api._ptr(lr_factor),
+                                    ctypes.c_uint64(self.seed & (1 << 64) - 1), self.steps.data_ptr(),
+                                    api._stream_of(self.steps, stream))
+        _lib.check("adamw_step", st)
+        return norm
+
+    def state_dict(self) -> dict:
+        """The states and the number of steps, as copies."""
+        d = {"step": int(self.steps[0]), "m": self.m.clone(), "v": self.v.clone()}
+        if self.state_bits == 8:
+            d.update(m_scale=self.m_scale.clone(), v_scale=self.v_scale.clone())
+        return d
+
+    def load_state_dict(self, state: dict) -> None:
+        """Takes over what state_dict() gave (of an AdamW with the same sizes
+        and state_bits)."""
+        names = ("m", "v", "m_scale", "v_scale") if self.state_bits == 8 else ("m", "v")
+        for name in names:
+            mine = getattr(self, name)
+            if state[name].shape != mine.shape or state[name].dtype != mine.dtype:
+                raise ValueError(f"{name} has shape {tuple(state[name].shape)} and type {state[name].dtype}, "
+                                 f"expected {tuple(mine.shape)} and {mine.dtype}")
+        for name in names:
+            getattr(self, name).copy_(state[name])
+        self.steps.copy_(torch.tensor([int(state["step"]), 0]))

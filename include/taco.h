@@ -602,6 +602,133 @@ taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, c
                                            void *dy, void *dh, float *dg_post, float *dg_pre, void *dgate,
                                            void *workspace, uint64_t workspace_bytes, taco_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Losses over the vocabulary, with their gradients at the logits.
+ *
+ * Logits [T][N], bf16 or fp32 (logits_bf16), 16-byte aligned; the first V
+ * columns of a row are the vocabulary, the others (padding) do not take part
+ * and get zero gradients.  a = targets[t] is row t's token, x_j its logits:
+ *
+ *   lse = log sum_j exp(x_j / temperature),  logp = x_a / temperature - lse
+ *   dlogits_j = dlogp / temperature (1[j = a] - exp(x_j / temperature - lse))
+ *
+ * A row with a negative target has no token: its logits are not read, its
+ * results and gradients are zero.  A target of V or more makes its row's
+ * results and gradients NaN.  Logits of -inf have probability 0; a row of
+ * -inf alone, with +inf or with a NaN gives NaN.  Everything is computed in
+ * fp32 and rounded once, when it is stored.  The sums' order is fixed for a
+ * given T, V, N and row: the same inputs give the same bits.
+ *
+ * temperature > 0, 1 <= V <= N, T < 2^31.  dlogits, of the logits' type and
+ * layout, may be the logits themselves.
+ *
+ * token_logprob - logp and lse, fp32 [T].
+ *
+ * token_logprob_backward - dlogits from dlogp fp32 [T] and the forward's lse.
+ * Rows with dlogp = 0 get zeros; their logits are not read.
+ *
+ * policy_loss - per row, with r = exp(logp - old_logp), A = advantages[t] and
+ * d = ref_logp - logp:
+ *   token_loss = w (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                   + kl (exp(d) - 1 - d))
+ * and its gradient times grad_scale; loss (one fp32 value): the sum of
+ * token_loss.  weights fp32 [T] hold the mask and the normalisation: rows of
+ * weight 0 do not count, whatever their other inputs hold, and give zeros.
+ * ref_logp null: no KL term.  dlogits null: no gradient.
+ *
+ * preference_loss - `pairs` pairs of sequences: sequence i is the rows
+ * offsets[i] .. offsets[i + 1] - 1 (int64 [2 pairs + 1], not decreasing, on the
+ * device; bounds outside 0 .. T are taken as 0 or T), the even ones preferred to the odd ones
+ * behind them.  With s_i the sum of logp - ref_logp over its tokens (mean != 0:
+ * their mean; 0 for a sequence without tokens), logratio[i] = s_i,
+ * margin = z = beta (s_2i - s_2i+1), loss the mean over the pairs of
+ *   -(1 - label_smoothing) log sig(z) - label_smoothing log sig(-z).
+ * ref_logp null: zeros.  Rows outside the sequences do not count.
+ * logp fp32 [T], logratio fp32 [2 pairs], margin fp32 [pairs]; dlogits null:
+ * no gradient.  The workspace is 256-byte aligned.
+ */
+taco_status token_logprob(const void *logits, int32_t logits_bf16, const int64_t *targets, int64_t T, int64_t V,
+                          int64_t N, float temperature, float *logp, float *lse, taco_stream_t stream);
+taco_status token_logprob_backward(const float *dlogp, const void *logits, int32_t logits_bf16,
+                                   const int64_t *targets, const float *lse, int64_t T, int64_t V, int64_t N,
+                                   float temperature, void *dlogits, taco_stream_t stream);
+taco_status policy_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const float *old_logp,
+                        const float *advantages, const float *weights, const float *ref_logp, int64_t T, int64_t V,
+                        int64_t N, float temperature, float clip_low, float clip_high, float kl, float grad_scale,
+                        float *loss, float *token_loss, float *logp, void *dlogits, taco_stream_t stream);
+taco_status preference_loss_workspace_bytes(int64_t T, int64_t pairs, uint64_t *bytes);
+taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const int64_t *offsets,
+                            const float *ref_logp, int64_t T, int64_t V, int64_t N, int64_t pairs, float temperature,
+                            float beta, float label_smoothing, int32_t mean, float grad_scale, float *loss,
+                            float *margin, float *logratio, float *logp, void *dlogits, void *workspace,
+                            uint64_t workspace_bytes, taco_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The optimizer.  Both calls take many tensors at once, as host arrays of
+ * descriptions that are read during the call.
+ *
+ * A gradient is fp32, bf16, or an FP8 main gradient: E4M3 codes [n] and one
+ * fp32 multiplier per block of 128, [ceil(n / 128)] (agoq_fp8_accumulate).
+ *
+ * grad_norm - norm (one fp32 value) = |grad_scale| sqrt(sum of g^2) over all
+ * tensors, in a fixed order.  Squares are fp32: values of about 1e19 and more
+ * give an infinite norm.  The workspace is 256-byte aligned.
+ *
+ * adamw_step - one step t = state[0] + 1 for all tensors, in place:
+ *   g = c grad, c = grad_scale min(1, max_norm / (norm + 1e-6))
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ * with lr = the tensor's lr times lr_factor (one fp32 value on the device;
+ * null: 1).  param fp32; copy_bf16 (may be null) gets the new weights rounded.
+ * state int64 [2] on the device: the steps done, and a counter that is zero
+ * between calls; the step counts itself, so that a captured call can be
+ * replayed.  norm null: no clipping (max_norm must be 0).  A norm that is not
+ * finite leaves the whole step out: nothing changes, state[0] neither.
+ *
+ * state_bits 32: m and v fp32 [n].  state_bits 8: E4M3 codes of m and of
+ * r = sqrt(v), with fp32 multipliers [ceil(n / 128)] in m_scale and v_scale:
+ * multiplier amax / 448 (1 for a block whose values are all below 2^-100, held as
+ * zeros), codes rounded up with the probability of the rest.  With y = |x|
+ * 448 / amax and E4M3's step at y, the code's magnitude is
+ * floor(y / step + (u + 1/2) / 65536) steps, u 16 bits of a hash of the element
+ * e of tensor i in step t: with
+ *   mix(x): x = (x ^ x >> 16) * 0x9E3779B1; x = (x ^ x >> 15) * 0x85A308D3; x ^ x >> 16
+ * (32 bits), k = mix(mix(mix(mix(seed's low word) ^ its high word) ^ (t - 1)) ^ i),
+ * k = mix(k ^ e >> 32) where that is not 0, h = mix((e * 0x13198A2F) ^ k): u =
+ * h's low half for m, its high half for r.  r's code is at least 1 where v > 0.
+ * m and v are read as code * multiplier and its square; a block with an Inf or
+ * a NaN is held as NaN.
+ *
+ * Pointers are 16-byte aligned, multipliers, norm and lr_factor 4-byte, state
+ * 8-byte.  No two tensors of a call may overlap.  0 <= beta < 1, eps > 0.
+ */
+#define TACO_GRAD_F32 0
+#define TACO_GRAD_BF16 1
+#define TACO_GRAD_FP8 2
+typedef struct {
+    const void *grad;
+    const float *grad_scale; /* TACO_GRAD_FP8 */
+    int64_t n;
+    int32_t grad_type;
+} grad_tensor;
+typedef struct {
+    float *param;
+    void *copy_bf16;
+    const void *grad;
+    const float *grad_scale; /* TACO_GRAD_FP8 */
+    void *m, *v;
+    float *m_scale, *v_scale; /* state_bits 8 */
+    int64_t n;
+    float lr, weight_decay;
+    int32_t grad_type;
+} adamw_tensor;
+taco_status grad_norm_workspace_bytes(int64_t count, uint64_t *bytes);
+taco_status grad_norm(const grad_tensor *tensors, int64_t count, float grad_scale, float *norm, void *workspace,
+                      uint64_t workspace_bytes, taco_stream_t stream);
+taco_status adamw_step(const adamw_tensor *tensors, int64_t count, int32_t state_bits, double beta1, double beta2,
+                       float eps, float grad_scale, const float *norm, float max_norm, const float *lr_factor,
+                       uint64_t seed, int64_t *state, taco_stream_t stream);
+
 /*
  * taco_device_error - watchdog flags of the kernels on the current device.
  * Every in-kernel wait gives up after about a second and sets a bit here
