@@ -23,19 +23,38 @@
 //
 // A row may start anywhere inside a 16-byte granule: threads take whole
 // granules of memory, and those at a row's ends leave out what is not its own.
+//
+// Bound by HBM.  The forward pass streams a row through registers.  Where the
+// gradient is wanted too, a row's granules come by bulk copies into shared
+// memory, are summed as they arrive, and are read again from there once the
+// sum is known: the logits cross the memory once.  A cluster of CTAs shares a
+// row that is long, or whose kind is few, and adds its parts' sums through
+// distributed shared memory.
 
 #include "device_utils.cuh"
 #include "internal.h"
 
 #include <cfloat>
+#include <cstring>
 
 namespace taco {
 
+// Watchdog flag of this file's kernels (bit 8), read by taco_device_error().
+__device__ unsigned int g_loss_error;
+
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kErrLoss = 256u;
+// log2 e = kLog2e + kLog2eLow: with one rounded factor alone all differences
+// would be scaled wrongly by the same 2^-26, and so would a sequence's sum.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxCluster = 8;
+constexpr int kChunkSteps = 2;  // granules a thread takes from a chunk in shared memory
+constexpr int kMaxChunks = 64;
 
-enum Mode { kForward, kPolicy, kBackward };
+enum Mode { kForward, kPolicy };
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -43,42 +62,57 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xFF800000); }
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7FFFFFFF); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // The granules of one row: G elements each, of type E (bf16 as uint16_t, or
-// float).
+// float).  Granules first .. last - 1 hold nothing but values of the row's V
+// columns; of those before and behind, single elements may be the row's.
 template <typename E> struct Row {
     static constexpr int G = 16 / sizeof(E);
-    const E *x;         // the first granule (the row starts `shift` elements in)
+    const E *x;      // granule 0; the row starts `shift` elements in
     int shift;
-    int64_t left;       // elements from x to the end of the tensor
+    int first, last; // interior
+    int end;         // behind the granule with the last of the N columns
+    int64_t left;    // elements from x to the end of the tensor
+    int V, N;
 
-    __device__ Row(const void *logits, int64_t row, int64_t T, int64_t N)
+    __device__ Row(const LossRows &a, int64_t row)
     {
-        const int64_t at = row * N;
+        const int64_t at = row * a.N;
+        V = static_cast<int>(a.V), N = static_cast<int>(a.N);
         shift = static_cast<int>(at & (G - 1));
-        x = static_cast<const E *>(logits) + (at - shift);
-        left = T * N - (at - shift);
+        x = static_cast<const E *>(a.logits) + (at - shift);
+        left = a.T * a.N - (at - shift);
+        first = shift ? 1 : 0;
+        last = static_cast<int>((static_cast<int64_t>(shift) + V) / G);
+        last = last < first ? first : last;
+        end = static_cast<int>((static_cast<int64_t>(shift) + N + G - 1) / G);
     }
 
-    __device__ uint4 load(int64_t k) const
+    __device__ uint4 load(int k) const
     {
-        if ((k + 1) * G <= left) {
-            uint4 v;
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "l"(x + k * G));
-            return v;
-        }
-        E e[G];
-#pragma unroll
-        for (int j = 0; j < G; ++j)
-            e[j] = k * G + j < left ? x[k * G + j] : E(0);
         uint4 v;
-        memcpy(&v, e, 16);
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(x + static_cast<int64_t>(k) * G));
         return v;
     }
+    // Element j of granule k is column col(k, j).
+    __device__ int64_t col(int k, int j) const { return static_cast<int64_t>(k) * G + j - shift; }
+    // A granule at a row's end, element by element: `other` in places of no
+    // column of the vocabulary.
+    __device__ void load_edge(int k, float other, float (&f)[G]) const
+    {
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const int64_t c = col(k, j);
+            f[j] = c >= 0 && c < V ? element(x + static_cast<int64_t>(k) * G + j) : other;
+        }
+    }
+    static __device__ __forceinline__ float element(const uint16_t *p) { return __uint_as_float(uint32_t(*p) << 16); }
+    static __device__ __forceinline__ float element(const float *p) { return *p; }
 };
 
 __device__ __forceinline__ void values(const uint4 &q, float (&f)[8])
@@ -105,113 +139,301 @@ __device__ __forceinline__ uint4 packed(const float (&f)[4])
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
+// exp2 of (x - m) log2(e) / tau for two values.
+struct Scale {
+    float hi, lo;  // log2(e) / tau
+    float inv_temperature;
+    __device__ explicit Scale(float inv) : hi(inv * kLog2e), inv_temperature(inv)
+    {
+        lo = fmaf(inv, kLog2e, -hi) + inv * kLog2eLow;
+    }
+    __device__ __forceinline__ float2 exponent(float2 x, float2 minus_m) const
+    {
+        const float2 d = __fadd2_rn(x, minus_m);
+        return __ffma2_rn(d, both(lo), __fmul2_rn(d, both(hi)));
+    }
+    __device__ __forceinline__ float exponent(float x, float m) const
+    {
+        const float d = x - m;
+        return fmaf(d, lo, d * hi);
+    }
+};
+
 // A maximum and a sum relative to it.
 struct Sum {
     float m, s;
 };
-__device__ __forceinline__ Sum join(Sum a, Sum b, float c)
+__device__ __forceinline__ Sum join(Sum a, Sum b, const Scale &c)
 {
     const float m = fmaxf(a.m, b.m);
-    return {m, a.s * ex2((a.m - m) * c) + b.s * ex2((b.m - m) * c)};
+    return {m, a.s * ex2(c.exponent(a.m, m)) + b.s * ex2(c.exponent(b.m, m))};
 }
 
-__device__ __forceinline__ float load_element(const uint16_t *p) { return __uint_as_float(uint32_t(*p) << 16); }
-__device__ __forceinline__ float load_element(const float *p) { return *p; }
+// Adds n values (n even).
+template <int n> __device__ __forceinline__ void accumulate(Sum &z, const float (&f)[n], const Scale &c)
+{
+    float m = fmaxf(f[0], f[1]);
+#pragma unroll
+    for (int j = 2; j < n; j += 2)
+        m = fmaxf(m, fmaxf(f[j], f[j + 1]));
+    if (m > z.m) {
+        z.s *= ex2(c.exponent(z.m, m));
+        z.m = m;
+    }
+    const float2 minus = both(-z.m);
+    float2 s[2] = {make_float2(z.s, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+    for (int j = 0; j < n; j += 2) {
+        const float2 y = c.exponent(make_float2(f[j], f[j + 1]), minus);
+        s[j / 2 % 2] = __fadd2_rn(s[j / 2 % 2], make_float2(ex2(y.x), ex2(y.y)));
+    }
+    s[0] = __fadd2_rn(s[0], s[1]);
+    z.s = s[0].x + s[0].y;
+}
 
-// One CTA a row.
-template <typename E, int MODE> __global__ void __launch_bounds__(1024) row_kernel(const LossRows a)
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The sum of CTA `rank` of the cluster at the same place of its shared memory.
+__device__ __forceinline__ Sum remote(const Sum *mine, uint32_t rank)
+{
+    uint32_t at;
+    Sum z;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(z.m), "=f"(z.s) : "r"(at) : "memory");
+    return z;
+}
+
+// Writes the gradient coef (1[target] - inv exp2(x - ref)) of a row: what all
+// of it takes.
+template <typename E> struct Gradient {
+    static constexpr int G = Row<E>::G;
+    const Row<E> &x;
+    const Scale &c;
+    E *out;             // as Row::x
+    float coef, scaled; // coef and -coef inv
+    float minus;        // -ref
+    int64_t target;
+    int at;             // the target's granule
+
+    __device__ Gradient(const Row<E> &row, const LossRows &a, const Scale &scale, float k, float inv, float ref,
+                        int64_t token)
+        : x(row), c(scale), out(static_cast<E *>(a.dlogits) + (row.x - static_cast<const E *>(a.logits))),
+          coef(k * a.inv_temperature), scaled(-coef * inv), minus(-ref), target(token),
+          at(static_cast<int>((token + row.shift) / G))
+    {
+    }
+    __device__ __forceinline__ void compute(const float (&f)[G], int k, float (&d)[G]) const
+    {
+#pragma unroll
+        for (int j = 0; j < G; j += 2) {
+            const float2 y = c.exponent(make_float2(f[j], f[j + 1]), both(minus));
+            const float2 e = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)), both(scaled));
+            d[j] = e.x, d[j + 1] = e.y;
+        }
+        if (k == at) {
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+                if (x.col(k, j) == target)
+                    d[j] += coef;
+        }
+    }
+    __device__ __forceinline__ void interior(int k, const uint4 &q) const
+    {
+        float f[G], d[G];
+        values(q, f);
+        compute(f, k, d);
+        stg128_stream(out + static_cast<int64_t>(k) * G, packed(d));
+    }
+    // A granule that is not all the vocabulary's: zeros behind it, nothing
+    // outside the row.  zero: the whole row is.
+    __device__ void edge(int k, bool zero) const
+    {
+        float f[G], d[G];
+        if (!zero) {
+            x.load_edge(k, neg_inf(), f);
+            compute(f, k, d);
+        }
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+            d[j] = zero || x.col(k, j) >= x.V ? 0.0f : d[j];
+        store(k, d);
+    }
+    __device__ __forceinline__ void store(int k, const float (&d)[G]) const
+    {
+        const uint4 q = packed(d);
+        E *p = out + static_cast<int64_t>(k) * G;
+        if (x.col(k, 0) >= 0 && x.col(k, G) <= x.N) {
+            stg128_stream(p, q);
+            return;
+        }
+        E e[G];
+        memcpy(e, &q, 16);
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+            if (x.col(k, j) >= 0 && x.col(k, j) < x.N)
+                p[j] = e[j];
+    }
+};
+
+// One row a cluster of `parts` CTAs (1: no cluster).  RESIDENT: the part of
+// the row is kept in shared memory between the passes.
+template <typename E, int MODE, bool CLUSTER, bool RESIDENT>
+__global__ void __launch_bounds__(512) row_kernel(const __grid_constant__ LossRows a, int parts, int chunks, int trigger)
 {
     constexpr int G = Row<E>::G;
-    __shared__ Sum part[32];
+    extern __shared__ __align__(128) uint4 held[];
+    __shared__ Sum part[16], mine;
+    __shared__ __align__(8) uint64_t bars[kMaxChunks];
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+    const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+    if (trigger)
+        pdl_trigger();
+    if (RESIDENT && tid == 0) {
+        for (int i = 0; i < chunks; ++i)
+            mbar_init(smem_u32(&bars[i]), 1);
+        fence_barrier_init();
+    }
+    if (RESIDENT)
+        __syncthreads();
     pdl_wait();
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x, threads = blockDim.x;
-    const Row<E> x(a.logits, row, a.T, a.N);
+    const int64_t row = CLUSTER ? blockIdx.x / parts : blockIdx.x;
+    const Row<E> x(a, row);
     const int64_t target = a.targets[row];
-    bool active = target >= 0;
     float weight = 1.0f;
+    bool active = target >= 0;
     if (MODE == kPolicy) {
         weight = a.weights[row];
         active = active && weight != 0.0f;
     }
     if (MODE == kForward && a.offsets)
         active = active && row >= a.offsets[0] && row < a.offsets[a.sequences];
-    if (MODE == kBackward) {
-        weight = a.dlogp[row];
-        active = active && weight != 0.0f;
-    }
-    const int64_t granules = (x.shift + a.V + G - 1) / G;
-    const float c = a.inv_temperature * kLog2e;
-    float coef = 0.0f, ref = 0.0f, inv = 0.0f;  // dlogits = coef / tau (1[j = a] - inv exp2((x - ref) c))
+    // this CTA's interior granules
+    const int each = (x.last - x.first + parts - 1) / parts;
+    const int lo = min(x.last, x.first + rank * each), hi = min(x.last, lo + each);
+    const Scale c(a.inv_temperature);
+    Sum z = {-FLT_MAX, 0.0f};
+    float coef = 0.0f, inv = 0.0f;
     if (active) {
-        const float xa = target < a.V ? load_element(x.x + x.shift + target) : __int_as_float(0x7FFFFFFF);
-        if (MODE != kBackward) {
-            Sum z = {-FLT_MAX, 0.0f};
-            for (int64_t k = tid; k < granules; k += threads) {
-                float f[G];
-                values(x.load(k), f);
-                float m = z.m;
-#pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    const int64_t col = k * G + j - x.shift;
-                    if (col < 0 || col >= a.V)
-                        f[j] = neg_inf();
-                    m = fmaxf(m, f[j]);
+        float xa = 0.0f, adv = 0.0f, old = 0.0f, ref_logp = 0.0f;
+        xa = target < x.V ? Row<E>::element(x.x + x.shift + target) : quiet_nan();
+        if (MODE == kPolicy) {
+            adv = a.advantages[row], old = a.old_logp[row];
+            ref_logp = a.ref_logp ? a.ref_logp[row] : 0.0f;
+        }
+        if (RESIDENT) {
+            const int chunk = threads * kChunkSteps;
+            if (tid == 0) {
+                for (int i = 0, k = lo; k < hi; ++i, k += chunk) {
+                    const uint32_t bytes = static_cast<uint32_t>(min(chunk, hi - k)) * 16, bar = smem_u32(&bars[i]);
+                    mbar_arrive_expect_tx(bar, bytes);
+                    bulk_load(smem_u32(held + (k - lo)), x.x + static_cast<int64_t>(k) * G, bytes, bar);
                 }
-                z.s *= ex2((z.m - m) * c);
-#pragma unroll
-                for (int j = 0; j < G; ++j)
-                    z.s += ex2((f[j] - m) * c);
-                z.m = m;
             }
+            for (int i = 0, k = lo; k < hi; ++i, k += chunk) {
+                if (!mbar_wait(smem_u32(&bars[i]), 0) && lane == 0)
+                    atomicOr(&g_loss_error, kErrLoss);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                z = join(z, {__shfl_xor_sync(~0u, z.m, o), __shfl_xor_sync(~0u, z.s, o)}, c);
-            if ((tid & 31) == 0)
-                part[tid >> 5] = z;
-            __syncthreads();
-            z = part[0];
-            for (int w = 1; w < threads / 32; ++w)
-                z = join(z, part[w], c);
-            const float ln_s = logf(z.s);
-            const float logp = (xa - z.m) * a.inv_temperature - ln_s;
-            ref = z.m;
-            inv = 1.0f / z.s;
-            if (MODE == kForward && tid == 0) {
-                a.logp[row] = logp;
-                a.lse[row] = z.m * a.inv_temperature + ln_s;
-            }
-            if (MODE == kPolicy) {
-                const float adv = a.advantages[row], r = expf(logp - a.old_logp[row]);
-                const float free = adv == 0.0f ? 0.0f : r * adv;
-                const float held = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * adv;
-                float loss = -fminf(free, held), slope = free <= held ? -free : 0.0f;
-                if (isnan(r))
-                    loss = slope = r;
-                if (a.ref_logp) {
-                    const float d = a.ref_logp[row] - logp, em1 = expm1f(d);
-                    loss += a.kl * (em1 - d);
-                    slope -= a.kl * em1;
-                }
-                coef = weight * slope * a.grad_scale;
-                if (tid == 0) {
-                    a.token_loss[row] = weight * loss;
-                    a.logp[row] = logp;
+                for (int j = 0; j < kChunkSteps; ++j) {
+                    const int g = k + tid + j * threads;
+                    if (g < hi) {
+                        float f[G];
+                        values(held[g - lo], f);
+                        accumulate(z, f, c);
+                    }
                 }
             }
         } else {
-            // exp(x / tau - lse) = exp2((x - hi) c) exp2(-lo c), hi + lo = lse tau
-            const float lse = a.lse[row], hi = lse * a.temperature;
-            const float lo = fmaf(lse, a.temperature, -hi);
-            ref = hi;
-            inv = isfinite(lo) ? ex2(-lo * c) : 1.0f;
-            coef = weight * a.grad_scale;
-            if (target >= a.V)
-                coef = __int_as_float(0x7FFFFFFF);
+            int k = lo + tid;
+            for (; k + 3 * threads < hi; k += 4 * threads) {
+                uint4 q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[j] = x.load(k + j * threads);
+                float f[4 * G];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float g[G];
+                    values(q[j], g);
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+                        f[j * G + i] = g[i];
+                }
+                accumulate(z, f, c);
+            }
+            for (; k < hi; k += threads) {
+                float f[G];
+                values(x.load(k), f);
+                accumulate(z, f, c);
+            }
         }
-    } else if (tid == 0) {
-        if (MODE != kBackward)
-            a.logp[row] = 0.0f;
+        // what of the row lies in granules with other elements
+        if (rank == 0 && tid == 0 && x.first > 0) {
+            float f[G];
+            x.load_edge(0, neg_inf(), f);
+            accumulate(z, f, c);
+        }
+        if (rank == parts - 1 && tid == threads - 1 && x.col(x.last, 0) < x.V) {
+            float f[G];
+            x.load_edge(x.last, neg_inf(), f);
+            accumulate(z, f, c);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            z = join(z, {__shfl_xor_sync(~0u, z.m, o), __shfl_xor_sync(~0u, z.s, o)}, c);
+        if (lane == 0)
+            part[tid >> 5] = z;
+        __syncthreads();
+        z = lane < threads / 32 ? part[lane] : Sum{-FLT_MAX, 0.0f};
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            z = join(z, {__shfl_xor_sync(~0u, z.m, o), __shfl_xor_sync(~0u, z.s, o)}, c);
+        z = {__shfl_sync(~0u, z.m, 0), __shfl_sync(~0u, z.s, 0)};
+        if (CLUSTER) {
+            if (tid == 0)
+                mine = z;
+            cluster_arrive();
+            cluster_wait();
+            z = lane < parts ? remote(&mine, lane) : Sum{-FLT_MAX, 0.0f};
+            cluster_arrive();  // no more reads from here; waited for at the end
+#pragma unroll
+            for (int o = kMaxCluster / 2; o > 0; o >>= 1)
+                z = join(z, {__shfl_xor_sync(~0u, z.m, o), __shfl_xor_sync(~0u, z.s, o)}, c);
+            z = {__shfl_sync(~0u, z.m, 0), __shfl_sync(~0u, z.s, 0)};
+        }
+        const float ln_s = logf(z.s);
+        const float logp = (xa - z.m) * a.inv_temperature - ln_s;
+        if (MODE == kForward && rank == 0 && tid == 0) {
+            a.logp[row] = logp;
+            a.lse[row] = z.m * a.inv_temperature + ln_s;
+        }
+        if (MODE == kPolicy) {
+            const float r = expf(logp - old);
+            const float free = adv == 0.0f ? 0.0f : r * adv;
+            const float held_at = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * adv;
+            float loss = -fminf(free, held_at), slope = free <= held_at ? -free : 0.0f;
+            if (isnan(r))
+                loss = slope = r;
+            if (a.ref_logp) {
+                const float d = ref_logp - logp, em1 = expm1f(d);
+                loss += a.kl * (em1 - d);
+                slope -= a.kl * em1;
+            }
+            coef = weight * slope * a.grad_scale;
+            inv = 1.0f / z.s;
+            if (rank == 0 && tid == 0) {
+                a.token_loss[row] = weight * loss;
+                a.logp[row] = logp;
+            }
+        }
+    } else if (rank == 0 && tid == 0) {
+        a.logp[row] = 0.0f;
         if (MODE == kForward)
             a.lse[row] = 0.0f;
         if (MODE == kForward && a.coef)
@@ -219,35 +441,73 @@ template <typename E, int MODE> __global__ void __launch_bounds__(1024) row_kern
         if (MODE == kPolicy)
             a.token_loss[row] = 0.0f;
     }
-    if (MODE == kForward || !a.dlogits)
-        return;
-    coef *= a.inv_temperature;
-    const float scaled = coef * inv;
-    E *out = static_cast<E *>(a.dlogits) + (x.x - static_cast<const E *>(a.logits));
-    const int64_t all = (x.shift + a.N + G - 1) / G;
-    for (int64_t k = tid; k < all; k += threads) {
-        float f[G], d[G];
-        const bool any = active && coef != 0.0f && k < granules;  // a clipped row's gradient is zero
-        if (any)
-            values(x.load(k), f);
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-            const int64_t col = k * G + j - x.shift;
-            d[j] = any && col < a.V ? -scaled * ex2((f[j] - ref) * c) + (col == target ? coef : 0.0f) : 0.0f;
-        }
-        const uint4 q = packed(d);
-        const int64_t col = k * G - x.shift;
-        if (col >= 0 && col + G <= a.N) {
-            stg128_stream(out + k * G, q);
+    if (MODE == kPolicy && a.dlogits) {
+        const Gradient<E> d(x, a, c, coef, inv, z.m, target);
+        const bool zero = !(coef != 0.0f);  // also a clipped row's
+        if (zero) {
+            for (int k = lo + tid; k < hi; k += threads)
+                stg128_stream(d.out + static_cast<int64_t>(k) * G, make_uint4(0, 0, 0, 0));
+        } else if (RESIDENT) {
+            for (int k = lo + tid; k < hi; k += threads)
+                d.interior(k, held[k - lo]);
         } else {
-            E e[G];
-            memcpy(e, &q, 16);
-#pragma unroll
-            for (int j = 0; j < G; ++j)
-                if (col + j >= 0 && col + j < a.N)
-                    out[k * G + j] = e[j];
+            for (int k = lo + tid; k < hi; k += threads)
+                d.interior(k, x.load(k));
         }
+        if (rank == 0 && tid == 0 && x.first > 0)
+            d.edge(0, zero);
+        if (rank == parts - 1)
+            for (int k = max(x.last, x.first) + tid; k < x.end; k += threads)
+                d.edge(k, zero);
     }
+    if (CLUSTER && active)
+        cluster_wait();
+}
+
+// The gradient from a given lse; `parts` CTAs a row, each on its own.
+template <typename E>
+__global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ LossRows a, int parts, int trigger)
+{
+    constexpr int G = Row<E>::G;
+    if (trigger)
+        pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, threads = blockDim.x, rank = blockIdx.x % parts;
+    const int64_t row = blockIdx.x / parts;
+    const Row<E> x(a, row);
+    const int64_t target = a.targets[row];
+    const float weight = a.dlogp[row];
+    const bool zero = target < 0 || weight == 0.0f;
+    const int each = (x.last - x.first + parts - 1) / parts;
+    const int lo = min(x.last, x.first + rank * each), hi = min(x.last, lo + each);
+    const Scale c(a.inv_temperature);
+    // exp(x / tau - lse) = exp2(c (x - hi)) exp2(-c lo), hi + lo = lse tau
+    const float lse = a.lse[row], at = lse * a.temperature;
+    const float low = fmaf(lse, a.temperature, -at);
+    const float inv = fabsf(low) <= FLT_MAX ? ex2(-low * c.hi) : 1.0f;
+    const Gradient<E> d(x, a, c, target < x.V ? weight * a.grad_scale : quiet_nan(), inv, at, target);
+    int k = lo + tid;
+    if (zero) {
+        for (; k < hi; k += threads)
+            stg128_stream(d.out + static_cast<int64_t>(k) * G, make_uint4(0, 0, 0, 0));
+    } else {
+        for (; k + 3 * threads < hi; k += 4 * threads) {
+            uint4 q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                q[j] = x.load(k + j * threads);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                d.interior(k + j * threads, q[j]);
+        }
+        for (; k < hi; k += threads)
+            d.interior(k, x.load(k));
+    }
+    if (rank == 0 && tid == 0 && x.first > 0)
+        d.edge(0, zero);
+    if (rank == parts - 1)
+        for (int k = max(x.last, x.first) + tid; k < x.end; k += threads)
+            d.edge(k, zero);
 }
 
 // Sum over a CTA of 1024 threads in a fixed order, in all threads.
@@ -324,15 +584,77 @@ __global__ void __launch_bounds__(256) pair_kernel(const PairArgs a)
     }
 }
 
+template <typename K, typename... Args>
+cudaError_t launch_cluster(K kernel, int64_t ctas, int threads, size_t smem, int cluster, cudaStream_t stream,
+                           Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
+}
+
+// How a launch splits its rows.
+struct Split {
+    int parts, threads;
+};
+
+template <typename E, int MODE, bool CLUSTER, bool RESIDENT>
+cudaError_t launch_row_kernel(const LossRows &a, Split s, size_t smem, int trigger, int device, cudaStream_t stream)
+{
+    const int chunks = static_cast<int>((smem / 16 + s.threads * kChunkSteps - 1) / (s.threads * kChunkSteps));
+    const auto kernel = row_kernel<E, MODE, CLUSTER, RESIDENT>;
+    if (RESIDENT) {
+        static std::atomic<bool> done[kMaxDevices];
+        const cudaError_t e = ensure_smem(kernel, 220 * 1024, device, done);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch_cluster(kernel, a.T * s.parts, s.threads, smem, CLUSTER ? s.parts : 1, stream, a, s.parts, chunks,
+                          trigger);
+}
+
+template <typename E, int MODE> cudaError_t launch_rows(const LossRows &a, cudaStream_t stream)
+{
+    constexpr int G = 16 / sizeof(E);
+    DeviceInfo di;
+    cudaError_t e = current_device_info(&di);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t granules = a.V / G + 1;
+    // the policy loss sums in the same order with and without its gradient
+    const bool grad = MODE == kPolicy;
+    // a part of at most 55 KB leaves room for four CTAs on an SM
+    Split s = {1, 32};
+    while (s.parts < kMaxCluster && grad && (granules + s.parts - 1) / s.parts * 16 > 55 * 1024)
+        s.parts *= 2;
+    while (s.parts < kMaxCluster && a.T * s.parts < 2 * di.num_sms && granules / s.parts >= 512)
+        s.parts *= 2;
+    const int64_t each = (granules + s.parts - 1) / s.parts;
+    while (s.threads < 256 && s.threads * 4 < each)
+        s.threads *= 2;
+    const size_t smem = static_cast<size_t>(each) * 16;
+    const bool resident = grad && smem <= 216 * 1024 && each <= int64_t(kMaxChunks) * s.threads * kChunkSteps;
+    const int trigger = a.T * s.parts <= di.num_sms;
+    if (s.parts > 1)
+        return resident ? launch_row_kernel<E, MODE, true, true>(a, s, smem, trigger, di.device, stream)
+                        : launch_row_kernel<E, MODE, true, false>(a, s, 0, trigger, di.device, stream);
+    return resident ? launch_row_kernel<E, MODE, false, true>(a, s, smem, trigger, di.device, stream)
+                    : launch_row_kernel<E, MODE, false, false>(a, s, 0, trigger, di.device, stream);
+}
+
 template <int MODE> cudaError_t launch_rows(const LossRows &a, bool bf16, cudaStream_t stream)
 {
-    const int64_t granules = (a.N + (bf16 ? 7 : 3)) / (bf16 ? 8 : 4) + 1;
-    int threads = 32;
-    while (threads < 512 && threads * 4 < granules)
-        threads *= 2;
-    const dim3 grid(static_cast<unsigned>(a.T));
-    return bf16 ? launch_pdl(row_kernel<uint16_t, MODE>, grid, threads, 0, stream, a)
-                : launch_pdl(row_kernel<float, MODE>, grid, threads, 0, stream, a);
+    return bf16 ? launch_rows<uint16_t, MODE>(a, stream) : launch_rows<float, MODE>(a, stream);
 }
 
 }  // namespace
@@ -344,7 +666,19 @@ cudaError_t launch_logprob(const LossRows &a, bool bf16, cudaStream_t stream)
 
 cudaError_t launch_logprob_backward(const LossRows &a, bool bf16, cudaStream_t stream)
 {
-    return launch_rows<kBackward>(a, bf16, stream);
+    DeviceInfo di;
+    const cudaError_t e = current_device_info(&di);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t granules = a.N / (bf16 ? 8 : 4) + 1;
+    Split s = {1, 32};
+    while (s.parts < 64 && a.T * s.parts < 4 * di.num_sms && granules / s.parts >= 512)
+        s.parts *= 2;
+    while (s.threads < 256 && s.threads * s.parts * 4 < granules)
+        s.threads *= 2;
+    const int trigger = a.T * s.parts <= di.num_sms;
+    return launch_cluster(bf16 ? backward_kernel<uint16_t> : backward_kernel<float>, a.T * s.parts, s.threads, 0, 1,
+                          stream, a, s.parts, trigger);
 }
 
 cudaError_t launch_policy_loss(const LossRows &a, bool bf16, float *loss, cudaStream_t stream)
@@ -364,10 +698,24 @@ cudaError_t launch_preference_loss(const LossRows &a, const PairArgs &p, bool bf
         return e;
     if ((e = launch_pdl(pair_kernel, dim3(static_cast<unsigned>(p.pairs)), 256, 0, stream, p)) != cudaSuccess)
         return e;
-    if (a.T > 0 && a.dlogits && (e = launch_rows<kBackward>(a, bf16, stream)) != cudaSuccess)
+    if (a.T > 0 && a.dlogits && (e = launch_logprob_backward(a, bf16, stream)) != cudaSuccess)
         return e;
     return launch_pdl(total_kernel, 1, 1024, 0, stream, static_cast<const float *>(p.pair_loss), p.pairs,
                       1.0f / static_cast<float>(p.pairs), loss);
+}
+
+cudaError_t read_loss_error(uint32_t *flags, bool clear)
+{
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_loss_error, sizeof v);
+    if (e != cudaSuccess)
+        return e;
+    *flags = v;
+    if (clear && v) {
+        v = 0;
+        e = cudaMemcpyToSymbol(g_loss_error, &v, sizeof v);
+    }
+    return e;
 }
 
 }  // namespace taco

@@ -843,7 +843,7 @@ static taco_status check_loss(int64_t T, int64_t V, int64_t N, float temperature
 {
     if (T < 0 || V < 1 || N < V || !positive_finite(temperature) || !positive_finite(1.0f / temperature))
         return TACO_ERR_INVALID_ARG;
-    if (T >= (int64_t(1) << 31) || N > (int64_t(1) << 31))
+    if (T >= (int64_t(1) << 31) || N > (int64_t(1) << 31) - 64)
         return TACO_ERR_UNSUPPORTED;
     return TACO_OK;
 }
@@ -1041,7 +1041,8 @@ taco_status adamw_step(const adamw_tensor *tensors, int64_t count, int32_t state
                        float eps, float grad_scale, const float *norm, float max_norm, const float *lr_factor,
                        uint64_t seed, int64_t *state, taco_stream_t stream)
 {
-    if (count < 0 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !positive_finite(eps) ||
+    if (count < 0 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) ||
+        eps < FLT_MIN ||
         !std::isfinite(grad_scale) || !(max_norm >= 0.0f) || !std::isfinite(max_norm) || (max_norm > 0.0f && !norm))
         return TACO_ERR_INVALID_ARG;
     if ((state_bits != 8 && state_bits != 32) || count > (int64_t(1) << 24))
@@ -1153,13 +1154,14 @@ taco_status taco_device_error(uint32_t *flags_out, int32_t clear)
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess)
         return TACO_ERR_CUDA;
-    uint32_t codec = 0, gemm = 0, fp8 = 0, norm = 0;
+    uint32_t codec = 0, gemm = 0, fp8 = 0, norm = 0, loss = 0;
     if ((e = taco::read_codec_error(&codec, clear != 0)) != cudaSuccess ||
         (e = taco::read_gemm_error(&gemm, clear != 0)) != cudaSuccess ||
         (e = taco::read_fp8_error(&fp8, clear != 0)) != cudaSuccess ||
-        (e = taco::read_norm_error(&norm, clear != 0)) != cudaSuccess)
+        (e = taco::read_norm_error(&norm, clear != 0)) != cudaSuccess ||
+        (e = taco::read_loss_error(&loss, clear != 0)) != cudaSuccess)
         return from_cuda(e);
-    *flags_out = codec | gemm | fp8 | norm;
+    *flags_out = codec | gemm | fp8 | norm | loss;
     return TACO_OK;
 }
 

@@ -47,8 +47,8 @@ class AdamW:
             raise ValueError("copies, lr and weight_decay must have one entry a tensor")
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
-        if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0 and eps > 0.0):
-            raise ValueError("betas must lie in [0, 1) and eps be positive")
+        if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0 and eps >= torch.finfo(torch.float32).tiny):
+            raise ValueError("betas must lie in [0, 1) and eps be at least fp32's smallest normal value")
         if max_norm is not None and not max_norm > 0.0:
             raise ValueError("max_norm must be positive")
         for i, p in enumerate(params):

@@ -619,7 +619,7 @@ taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, c
  * fp32 and rounded once, when it is stored.  The sums' order is fixed for a
  * given T, V, N and row: the same inputs give the same bits.
  *
- * temperature > 0, 1 <= V <= N, T < 2^31.  dlogits, of the logits' type and
+ * temperature > 0, 1 <= V <= N <= 2^31 - 64, T < 2^31.  dlogits, of the logits' type and
  * layout, may be the logits themselves.
  *
  * token_logprob - logp and lse, fp32 [T].
@@ -695,12 +695,14 @@ taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64
  *   mix(x): x = (x ^ x >> 16) * 0x9E3779B1; x = (x ^ x >> 15) * 0x85A308D3; x ^ x >> 16
  * (32 bits), k = mix(mix(mix(mix(seed's low word) ^ its high word) ^ (t - 1)) ^ i),
  * k = mix(k ^ e >> 32) where that is not 0, h = mix((e * 0x13198A2F) ^ k): u =
- * h's low half for m, its high half for r.  r's code is at least 1 where v > 0.
+ * h's low half for m, its high half for r.  r's code is at least 1 where v is at
+ * least 2^-126.
  * m and v are read as code * multiplier and its square; a block with an Inf or
  * a NaN is held as NaN.
  *
  * Pointers are 16-byte aligned, multipliers, norm and lr_factor 4-byte, state
- * 8-byte.  No two tensors of a call may overlap.  0 <= beta < 1, eps > 0.
+ * 8-byte.  No two tensors of a call may overlap.  0 <= beta < 1, eps at least
+ * fp32's smallest normal value.
  */
 #define TACO_GRAD_F32 0
 #define TACO_GRAD_BF16 1
@@ -735,7 +737,7 @@ taco_status adamw_step(const adamw_tensor *tensors, int64_t count, int32_t state
  * (bit 0: compressor, bit 1: decompressor, bit 4: taco_watchdog_selftest,
  * bit 5: the GEMMs taco_gemm_compress, agoq_gemm_accumulate and
  * agoq_gemm_laaq_quantize, bit 6: fp8_gemm and the calls built on it, bit 7:
- * rmsnorm_gate_residual and its backward pass).
+ * rmsnorm_gate_residual and its backward pass, bit 8: policy_loss).
  * Synchronises the device.  With clear != 0 the flags are reset to 0 after
  * reading.
  */
