@@ -33,8 +33,9 @@ namespace taco {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                                   // blocks of 128 a warp has in flight
-constexpr int kChunk = kThreads / 32 * kUnroll * 128;        // elements of a chunk
+constexpr int kBlocks = 4;                                   // blocks of 128 a warp has in flight
+constexpr int kChunk = kThreads / 32 * kBlocks * 128;        // values of a chunk of the update
+constexpr int kNormChunk = kThreads * 64;                    // and of the norm
 
 // Tensors of a launch; first[i]: the first chunk of tensor i.
 template <typename D, int MAX> struct Table {
@@ -136,6 +137,73 @@ __device__ __forceinline__ float4 load_grad(const void *g, const float *scale, i
 
 // ------------------------------------------------------------------- norm --
 
+__device__ __forceinline__ uint4 ldg16(const void *p) { return ldg128_stream(p); }
+
+// Squares of a thread's 64 values of a whole chunk, in 16-byte loads; at most
+// 32 terms in a row.
+__device__ __forceinline__ float squares(const grad_tensor &d, int64_t base)
+{
+    const int tid = threadIdx.x;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (d.grad_type == TACO_GRAD_FP8) {
+        const uint8_t *p = static_cast<const uint8_t *>(d.grad) + base + tid * 16;
+        uint4 q[4];
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[i] = ldg16(p + i * kThreads * 16);
+            m[i] = __ldg(d.grad_scale + (base + i * kThreads * 16 + tid * 16) / 128);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+            float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 f;
+                e4m3x2_to_f32x2(w[j / 2] >> (16 * (j % 2)) & 0xFFFFu, f.x, f.y);
+                t = __ffma2_rn(f, f, t);
+            }
+            s[i] = (t.x + t.y) * m[i] * m[i];
+        }
+    } else if (d.grad_type == TACO_GRAD_BF16) {
+        const uint16_t *p = static_cast<const uint16_t *>(d.grad) + base + tid * 8;
+        uint4 q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = ldg16(p + i * kThreads * 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+            float2 t = make_float2(s[i % 4], 0.0f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = make_float2(bf16lo_to_f32(w[j]), bf16hi_to_f32(w[j]));
+                t = __ffma2_rn(f, f, t);
+            }
+            s[i % 4] = t.x + t.y;
+        }
+    } else {
+        const float *p = static_cast<const float *>(d.grad) + base + tid * 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[i] = ldg16(p + (h * 8 + i) * kThreads * 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f[4] = {__uint_as_float(q[i].x), __uint_as_float(q[i].y), __uint_as_float(q[i].z),
+                                    __uint_as_float(q[i].w)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[j] = fmaf(f[j], f[j], s[j]);
+            }
+        }
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
 // Sum of squares of a CTA's chunks, into partial[blockIdx.x].
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<grad_tensor, MAX> t,
@@ -148,14 +216,15 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
         const int i = tensor_of(t, c);
         const grad_tensor &d = t.tensor[i];
-        const int64_t base = static_cast<int64_t>(c - t.first[i]) * kChunk + warp * kUnroll * 128 + lane * 4;
-        float s = 0.0f;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const float4 g = load_grad(d.grad, d.grad_scale, d.grad_type, base + u * 128, d.n);
-            s = fmaf(g.x, g.x, fmaf(g.y, g.y, fmaf(g.z, g.z, fmaf(g.w, g.w, s))));
+        const int64_t base = static_cast<int64_t>(c - t.first[i]) * kNormChunk;
+        if (base + kNormChunk <= d.n) {
+            sum += squares(d, base);
+            continue;
         }
-        sum += s;
+        for (int64_t e = base + threadIdx.x * 4; e < d.n; e += kThreads * 4) {
+            const float4 g = load_grad(d.grad, d.grad_scale, d.grad_type, e, d.n);
+            sum += fmaf(g.x, g.x, fmaf(g.y, g.y, fmaf(g.z, g.z, g.w * g.w)));
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -202,17 +271,6 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x)
     return x ^ (x >> 16);
 }
 
-// |x| scaled into 0 .. 448, to an E4M3 code, up with the probability of the
-// rest: bits (0 .. 65535) and a half of 65536.  Below 2^-6 E4M3's steps are
-// those of [2^-6, 2^-5), so 2^-6 is added there; above, the fraction's 20 low
-// bits are what the code leaves out.
-__device__ __forceinline__ uint32_t code_up(float y, uint32_t bits)
-{
-    const bool low = y < 0.015625f;
-    const uint32_t f = __float_as_uint(low ? y + 0.015625f : y);
-    return ((f + (bits << 4) + 8u) >> 20) - (low ? 968u : 960u);
-}
-
 struct Hyper {
     AdamWStep h;
     uint32_t key;             // of the seed
@@ -222,34 +280,191 @@ struct Hyper {
     float ln_beta1, ln_beta2;
 };
 
-// Codes and multiplier of a block held by a warp, four values a lane.
-template <bool LEAST>
-__device__ __forceinline__ uint32_t to_codes(const float (&x)[4], const uint32_t (&bits)[4], float &scale)
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float root_of(float x)
 {
-    float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        bad |= !(fabsf(x[j]) <= FLT_MAX);
-    top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
-    if (__any_sync(~0u, bad)) {  // an Inf or a NaN: the block is NaN
-        scale = 1.0f;
-        return 0x7F7F7F7Fu;
-    }
-    const bool none = top < 0x1p-100f;  // (448 / amax would leave fp32's range)
-    scale = none ? 1.0f : top / 448.0f;
-    const float inv = none ? 0.0f : 448.0f / top;
-    uint32_t w = 0;
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float inverse(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four values held by a lane.
+struct F4 {
+    float2 a, b;
+};
+__device__ __forceinline__ F4 f4(float4 x) { return {make_float2(x.x, x.y), make_float2(x.z, x.w)}; }
+__device__ __forceinline__ F4 decoded(uint32_t w)
+{
+    F4 f;
+    e4m3x2_to_f32x2(w & 0xFFFFu, f.a.x, f.a.y);
+    e4m3x2_to_f32x2(w >> 16, f.b.x, f.b.y);
+    return f;
+}
+
+// |x| inv, within 0 .. 448, to an E4M3 code, up with the probability of the
+// rest: rest holds 16 random bits in bits 4 .. 19.  Below 2^-6 E4M3's steps are
+// those of [2^-6, 2^-5), so 2^-6 is added there; the 20 low bits of the sum's
+// fraction are what the code leaves out.
+__device__ __forceinline__ uint32_t code_up(float x, float inv, uint32_t rest)
+{
+    const float y = fminf(fabsf(x) * inv, 448.0f);
+    const bool low = y < 0.015625f;
+    const uint32_t f = __float_as_uint(y + (low ? 0.015625f : 0.0f));
+    return (f + rest + (8u - ((low ? 968u : 960u) << 20))) >> 20;
+}
+
+// Largest magnitude of a block held by a warp, as bits (those of an Inf or a
+// NaN are above all others').
+__device__ __forceinline__ uint32_t top_of(const F4 &x)
+{
+    const uint32_t m = 0x7FFFFFFFu;
+    const uint32_t a = max(__float_as_uint(x.a.x) & m, __float_as_uint(x.a.y) & m);
+    const uint32_t b = max(__float_as_uint(x.b.x) & m, __float_as_uint(x.b.y) & m);
+    return __reduce_max_sync(~0u, max(a, b));
+}
+constexpr uint32_t kInf = 0x7F800000u, kLeast = 0x0D800000u;  // kLeast: 2^-100
+
+// A block's codes; ROOT: no signs, and no code of 0 for a value above 0.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t to_codes(const F4 &x, float inv, uint32_t top, const uint32_t (&r)[4])
+{
+    const float v[4] = {x.a.x, x.a.y, x.b.x, x.b.y};
+    uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t c = code_up(fminf(fabsf(x[j]) * inv, 448.0f), bits[j]);
-        if (LEAST)
-            c = c == 0 && x[j] > 0.0f && !none ? 1u : c;
-        else
-            c |= (__float_as_uint(x[j]) >> 24) & 0x80u;
-        w |= c << (8 * j);
+        c[j] = code_up(v[j], inv, (ROOT ? r[j] >> 12 : r[j] << 4) & 0xFFFF0u);
+        if (ROOT)
+            c[j] = max(c[j], min(__float_as_uint(v[j]), 1u));
     }
-    return w;
+    uint32_t w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    if (!ROOT) {
+        const uint32_t lo = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0073);
+        const uint32_t hi = __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0073);
+        w |= __byte_perm(lo, hi, 0x5410) & 0x80808080u;
+    }
+    return top >= kInf ? 0x7F7F7F7Fu : top < kLeast ? 0u : w;
+}
+
+struct Update {
+    float gs, fix2, eps, b1, b2, a1, a2, decay, rate;
+};
+
+__device__ __forceinline__ float2 updated(float2 p, float2 g, float2 &m, float2 &v, float2 &root, const Update &h)
+{
+    m = fma2(both(h.b1), m, both(h.a1) * g);
+    v = fma2(both(h.b2), v, (both(h.a2) * g) * g);
+    root = make_float2(root_of(v.x), root_of(v.y));
+    const float2 d = fma2(root, both(h.fix2), both(h.eps));
+    const float2 u = m * make_float2(inverse(d.x), inverse(d.y));
+    const float2 t = fma2(both(h.rate), u, both(h.decay) * p);
+    return __fadd2_rn(p, make_float2(-t.x, -t.y));
+}
+
+// A warp's four blocks of tensor d, from element `base` on.  All loads are
+// issued first; the blocks' multipliers are loaded, inverted and stored by a
+// lane each (0 .. 3: m, 4 .. 7: r, 8 .. 11: the gradient's).
+template <bool BITS8>
+__device__ __forceinline__ void update_blocks(const adamw_tensor &d, int64_t base, const Update &h, uint32_t key)
+{
+    const int lane = threadIdx.x % 32;
+    const int64_t n = d.n;
+    F4 g[kBlocks], p[kBlocks], m[kBlocks], v[kBlocks];
+    uint32_t mc[kBlocks], vc[kBlocks];
+    float scale = 1.0f;
+    float *const scales = lane < kBlocks ? d.m_scale : d.v_scale;
+    const int64_t mine = base / 128 + lane % kBlocks;
+    const bool exists = mine * 128 < n;
+    if (BITS8 && lane < 2 * kBlocks && exists)
+        scale = scales[mine];
+    if (d.grad_type == TACO_GRAD_FP8 && lane / kBlocks == 2 && exists)
+        scale = d.grad_scale[mine];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t e = base + u * 128 + lane * 4;
+        p[u] = f4(load4(d.param, e, n));
+        if (BITS8) {
+            mc[u] = load4(static_cast<const uint8_t *>(d.m), e, n);
+            vc[u] = load4(static_cast<const uint8_t *>(d.v), e, n);
+        } else {
+            m[u] = f4(load4(static_cast<const float *>(d.m), e, n));
+            v[u] = f4(load4(static_cast<const float *>(d.v), e, n));
+        }
+    }
+    if (d.grad_type == TACO_GRAD_FP8) {
+        uint32_t gc[kBlocks];
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u)
+            gc[u] = load4(static_cast<const uint8_t *>(d.grad), base + u * 128 + lane * 4, n);
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u) {
+            const float2 s = both(__shfl_sync(~0u, scale, 2 * kBlocks + u));
+            const F4 c = decoded(gc[u]);
+            g[u] = {c.a * s, c.b * s};
+        }
+    } else if (d.grad_type == TACO_GRAD_BF16) {
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u) {
+            const uint2 w = load4(static_cast<const uint16_t *>(d.grad), base + u * 128 + lane * 4, n);
+            g[u] = {make_float2(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x)),
+                    make_float2(bf16lo_to_f32(w.y), bf16hi_to_f32(w.y))};
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u)
+            g[u] = f4(load4(static_cast<const float *>(d.grad), base + u * 128 + lane * 4, n));
+    }
+    F4 root[kBlocks];
+    uint32_t top = 0, tops[2 * kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t e = base + u * 128 + lane * 4;
+        if (BITS8) {
+            const float2 ms = both(__shfl_sync(~0u, scale, u)), vs = both(__shfl_sync(~0u, scale, kBlocks + u));
+            m[u] = decoded(mc[u]), v[u] = decoded(vc[u]);
+            m[u] = {m[u].a * ms, m[u].b * ms}, v[u] = {v[u].a * vs, v[u].b * vs};
+            v[u] = {v[u].a * v[u].a, v[u].b * v[u].b};
+        }
+        g[u] = {g[u].a * both(h.gs), g[u].b * both(h.gs)};
+        p[u].a = updated(p[u].a, g[u].a, m[u].a, v[u].a, root[u].a, h);
+        p[u].b = updated(p[u].b, g[u].b, m[u].b, v[u].b, root[u].b, h);
+        store4(d.param, e, n, make_float4(p[u].a.x, p[u].a.y, p[u].b.x, p[u].b.y));
+        if (d.copy_bf16)
+            store4(static_cast<uint16_t *>(d.copy_bf16), e, n,
+                   make_uint2(f32x2_to_bf16x2(p[u].a.x, p[u].a.y), f32x2_to_bf16x2(p[u].b.x, p[u].b.y)));
+        if (!BITS8) {
+            store4(static_cast<float *>(d.m), e, n, make_float4(m[u].a.x, m[u].a.y, m[u].b.x, m[u].b.y));
+            store4(static_cast<float *>(d.v), e, n, make_float4(v[u].a.x, v[u].a.y, v[u].b.x, v[u].b.y));
+        } else {
+            tops[u] = top_of(m[u]), tops[kBlocks + u] = top_of(root[u]);
+            top = lane == u ? tops[u] : lane == kBlocks + u ? tops[kBlocks + u] : top;
+        }
+    }
+    if (!BITS8)
+        return;
+    const bool none = top < kLeast, bad = top >= kInf;  // (448 / amax would leave fp32's range)
+    const float inv = none || bad ? 0.0f : 448.0f / __uint_as_float(top);
+    if (lane < 2 * kBlocks && exists)
+        scales[mine] = none || bad ? 1.0f : __uint_as_float(top) / 448.0f;
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t e = base + u * 128 + lane * 4;
+        uint32_t r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            r[j] = mix((static_cast<uint32_t>(e + j) * 0x13198A2Fu) ^ key);
+        store4(static_cast<uint8_t *>(d.m), e, n,
+               to_codes<false>(m[u], __shfl_sync(~0u, inv, u), tops[u], r));
+        store4(static_cast<uint8_t *>(d.v), e, n,
+               to_codes<true>(root[u], __shfl_sync(~0u, inv, kBlocks + u), tops[kBlocks + u], r));
+    }
 }
 
 template <bool BITS8, int MAX>
@@ -257,109 +472,60 @@ __global__ void __launch_bounds__(kThreads)
     adamw_kernel(const __grid_constant__ Table<adamw_tensor, MAX> t, const __grid_constant__ Hyper hyper)
 {
     pdl_wait();
-    const AdamWStep &h = hyper.h;
-    const uint64_t steps = static_cast<uint64_t>(h.state[0]);
-    float gs = h.grad_scale;
-    bool skip = false;
-    if (h.norm) {
-        const float norm = *h.norm;
-        skip = !(norm <= FLT_MAX);  // a gradient that is not finite: the step is left out
-        if (h.max_norm > 0.0f)
-            gs *= fminf(h.max_norm / (norm + 1e-6f), 1.0f);
+    const AdamWStep &s = hyper.h;
+    const uint64_t steps = static_cast<uint64_t>(s.state[0]);
+    Update h;
+    h.gs = s.grad_scale;
+    if (s.norm) {
+        const float norm = *s.norm;
+        if (!(norm <= FLT_MAX))  // a gradient that is not finite: the step is left out
+            return;
+        if (s.max_norm > 0.0f)
+            h.gs *= fminf(s.max_norm / (norm + 1e-6f), 1.0f);
     }
-    if (skip)
-        return;
     const float time = static_cast<float>(steps + 1);
     const float fix1 = -1.0f / expm1f(time * hyper.ln_beta1);
-    const float fix2 = rsqrtf(-expm1f(time * hyper.ln_beta2));
-    const float factor = h.lr_factor ? *h.lr_factor : 1.0f;
-    const float b1 = hyper.b1, b2 = hyper.b2, a1 = hyper.a1, a2 = hyper.a2;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, chunks = t.first[t.count];
+    h.fix2 = rsqrtf(-expm1f(time * hyper.ln_beta2));
+    h.eps = s.eps, h.b1 = hyper.b1, h.b2 = hyper.b2, h.a1 = hyper.a1, h.a2 = hyper.a2;
+    const float factor = s.lr_factor ? *s.lr_factor : 1.0f;
+    const int chunks = t.first[t.count];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
         const int i = tensor_of(t, c);
         const adamw_tensor &d = t.tensor[i];
-        const int64_t n = d.n;
-        const int64_t base = static_cast<int64_t>(c - t.first[i]) * kChunk + warp * kUnroll * 128;
-        const float lr = d.lr * factor, decay = lr * d.weight_decay, rate = lr * fix1;
+        const int64_t base = static_cast<int64_t>(c - t.first[i]) * kChunk + threadIdx.x / 32 * (kBlocks * 128);
+        if (base >= d.n)
+            continue;
+        const float lr = d.lr * factor;
+        h.decay = lr * d.weight_decay, h.rate = lr * fix1;
         uint32_t key = 0;
         if (BITS8) {
             key = mix(mix(hyper.key ^ static_cast<uint32_t>(steps)) ^ static_cast<uint32_t>(hyper.first_tensor + i));
             if (base >> 32)
                 key = mix(key ^ static_cast<uint32_t>(base >> 32));
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t block = base + u * 128, e = block + lane * 4;
-            if (block >= n)
-                break;
-            const float4 g4 = load_grad(d.grad, d.grad_scale, d.grad_type, e, n);
-            const float4 p4 = load4(d.param, e, n);
-            float4 m4, v4;
-            if (BITS8) {
-                m4 = from_codes(load4(static_cast<const uint8_t *>(d.m), e, n), d.m_scale[block / 128]);
-                v4 = from_codes(load4(static_cast<const uint8_t *>(d.v), e, n), d.v_scale[block / 128]);
-                v4 = make_float4(v4.x * v4.x, v4.y * v4.y, v4.z * v4.z, v4.w * v4.w);
-            } else {
-                m4 = load4(static_cast<const float *>(d.m), e, n);
-                v4 = load4(static_cast<const float *>(d.v), e, n);
-            }
-            const float g[4] = {g4.x * gs, g4.y * gs, g4.z * gs, g4.w * gs};
-            float p[4] = {p4.x, p4.y, p4.z, p4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
-            float root[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[j] = b1 * m[j] + a1 * g[j];
-                v[j] = b2 * v[j] + a2 * g[j] * g[j];
-                root[j] = sqrtf(v[j]);
-                p[j] -= decay * p[j] + rate * __fdividef(m[j], root[j] * fix2 + h.eps);
-            }
-            store4(d.param, e, n, make_float4(p[0], p[1], p[2], p[3]));
-            if (d.copy_bf16)
-                store4(static_cast<uint16_t *>(d.copy_bf16), e, n,
-                       make_uint2(f32x2_to_bf16x2(p[0], p[1]), f32x2_to_bf16x2(p[2], p[3])));
-            if (BITS8) {
-                uint32_t lo[4], hi[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t r = mix((static_cast<uint32_t>(e + j) * 0x13198A2Fu) ^ key);
-                    lo[j] = r & 0xFFFFu;
-                    hi[j] = r >> 16;
-                }
-                float ms, vs;
-                const uint32_t mc = to_codes<false>(m, lo, ms), vc = to_codes<true>(root, hi, vs);
-                store4(static_cast<uint8_t *>(d.m), e, n, mc);
-                store4(static_cast<uint8_t *>(d.v), e, n, vc);
-                if (lane == 0) {
-                    d.m_scale[block / 128] = ms;
-                    d.v_scale[block / 128] = vs;
-                }
-            } else {
-                store4(static_cast<float *>(d.m), e, n, make_float4(m[0], m[1], m[2], m[3]));
-                store4(static_cast<float *>(d.v), e, n, make_float4(v[0], v[1], v[2], v[3]));
-            }
-        }
+        update_blocks<BITS8>(d, base, h, key);
     }
     // the last CTA of the step counts it: every CTA has read the count by then
     if (hyper.last) {
         __syncthreads();
         if (threadIdx.x == 0) {
-            unsigned int *ticket = reinterpret_cast<unsigned int *>(h.state + 1);
+            unsigned int *ticket = reinterpret_cast<unsigned int *>(s.state + 1);
             if (atomicAdd(ticket, 1u) == gridDim.x - 1) {
                 *ticket = 0;
-                h.state[0] = static_cast<int64_t>(steps + 1);
+                s.state[0] = static_cast<int64_t>(steps + 1);
             }
         }
     }
 }
 
-template <typename D, int MAX> int fill(Table<D, MAX> &t, const D *tensors, int64_t count)
+template <typename D, int MAX> int fill(Table<D, MAX> &t, const D *tensors, int64_t count, int chunk)
 {
     t.count = static_cast<int32_t>(count);
     int64_t at = 0;
     for (int64_t i = 0; i < count; ++i) {
         t.tensor[i] = tensors[i];
         t.first[i] = static_cast<int32_t>(at);
-        at += (tensors[i].n + kChunk - 1) / kChunk;
+        at += (tensors[i].n + chunk - 1) / chunk;
     }
     t.first[count] = static_cast<int32_t>(at);
     return static_cast<int>(at);
@@ -382,7 +548,7 @@ template <int MAX>
 cudaError_t norm_launch(const grad_tensor *tensors, int64_t count, double *partial, int *used, cudaStream_t stream)
 {
     Table<grad_tensor, MAX> t;
-    const int chunks = fill(t, tensors, count);
+    const int chunks = fill(t, tensors, count, kNormChunk);
     int grid = 0;
     cudaError_t e = resident(norm_kernel<MAX>, &grid);
     if (e != cudaSuccess)
@@ -397,7 +563,7 @@ template <bool BITS8, int MAX>
 cudaError_t adamw_launch(const adamw_tensor *tensors, int64_t count, const Hyper &h, cudaStream_t stream)
 {
     Table<adamw_tensor, MAX> t;
-    const int chunks = fill(t, tensors, count);
+    const int chunks = fill(t, tensors, count, kChunk);
     int grid = 0;
     cudaError_t e = resident(adamw_kernel<BITS8, MAX>, &grid);
     if (e != cudaSuccess)
