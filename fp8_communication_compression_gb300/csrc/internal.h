@@ -168,7 +168,7 @@ struct LossRows {
     const float *dlogp;                  // backward (with lse)
     const float *old_logp, *advantages, *weights, *ref_logp;  // policy loss
     float clip_lo, clip_hi, kl;
-    float *token_loss;
+    float *token_loss, *loss;
     void *dlogits;                       // may be null in the policy and the preference loss
 };
 struct PairArgs {
@@ -181,7 +181,7 @@ struct PairArgs {
 };
 cudaError_t launch_logprob(const LossRows &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_logprob_backward(const LossRows &a, bool bf16, cudaStream_t stream);
-cudaError_t launch_policy_loss(const LossRows &a, bool bf16, float *loss, cudaStream_t stream);
+cudaError_t launch_policy_loss(const LossRows &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_preference_loss(const LossRows &a, const PairArgs &p, bool bf16, float *loss, cudaStream_t stream);
 
 // The optimizer (adamw_kernels.cu).  `tensors` are host arrays.

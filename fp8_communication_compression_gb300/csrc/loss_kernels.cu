@@ -45,16 +45,21 @@ __device__ unsigned int g_loss_error;
 namespace {
 
 constexpr uint32_t kErrLoss = 256u;
-// log2 e = kLog2e + kLog2eLow: with one rounded factor alone all differences
-// would be scaled wrongly by the same 2^-26, and so would a sequence's sum.
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eLow = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
+// log2 e, and its two parts kLog2eHigh + kLog2eLow, both positive.
+constexpr float kLog2e = 1.4426950408889634f, kLog2eHigh = 1.4426949024200439453125f;
+constexpr float kLog2eLow = static_cast<float>(1.4426950408889634074 - 1.4426949024200439453125);
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCluster = 8;
-constexpr int kChunkSteps = 2;  // granules a thread takes from a chunk in shared memory
-constexpr int kMaxChunks = 64;
 
 enum Mode { kForward, kPolicy };
+
+// A row's token; what lies outside int32 lies outside the vocabulary too (N is
+// at most 2^31 - 64).
+__device__ __forceinline__ int token(const LossRows &a, int64_t row)
+{
+    const int64_t t = a.targets[row];
+    return t < 0 ? -1 : t < 0x7FFFFFF0 ? static_cast<int>(t) : 0x7FFFFFF0;
+}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -62,34 +67,53 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float inverse(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xFF800000); }
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7FFFFFFF); }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+__device__ __forceinline__ void values8(const uint4 &q, float *f)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = bf16lo_to_f32(w[j]);
+        f[2 * j + 1] = bf16hi_to_f32(w[j]);
+    }
+}
+__device__ __forceinline__ void values4(const uint4 &q, float *f)
+{
+    f[0] = __uint_as_float(q.x), f[1] = __uint_as_float(q.y);
+    f[2] = __uint_as_float(q.z), f[3] = __uint_as_float(q.w);
+}
 
 // The granules of one row: G elements each, of type E (bf16 as uint16_t, or
 // float).  Granules first .. last - 1 hold nothing but values of the row's V
 // columns; of those before and behind, single elements may be the row's.
 template <typename E> struct Row {
     static constexpr int G = 16 / sizeof(E);
+    const LossRows *a;
     const E *x;      // granule 0; the row starts `shift` elements in
     int shift;
     int first, last; // interior
-    int end;         // behind the granule with the last of the N columns
-    int64_t left;    // elements from x to the end of the tensor
-    int V, N;
 
-    __device__ Row(const LossRows &a, int64_t row)
+    __device__ __forceinline__ Row(const LossRows &args, int64_t row) : a(&args)
     {
-        const int64_t at = row * a.N;
-        V = static_cast<int>(a.V), N = static_cast<int>(a.N);
-        shift = static_cast<int>(at & (G - 1));
-        x = static_cast<const E *>(a.logits) + (at - shift);
-        left = a.T * a.N - (at - shift);
+        const int64_t at = row * a->N;
+        shift = static_cast<int>(at) & (G - 1);
+        x = static_cast<const E *>(a->logits) + (at - shift);
         first = shift ? 1 : 0;
-        last = static_cast<int>((static_cast<int64_t>(shift) + V) / G);
-        last = last < first ? first : last;
-        end = static_cast<int>((static_cast<int64_t>(shift) + N + G - 1) / G);
+        last = max(first, (shift + V()) / G);
     }
+    __device__ __forceinline__ int V() const { return static_cast<int>(a->V); }
+    __device__ __forceinline__ int N() const { return static_cast<int>(a->N); }
+    // behind the granule with the last of the N columns
+    __device__ __forceinline__ int end() const { return (shift + N() + G - 1) / G; }
 
     __device__ uint4 load(int k) const
     {
@@ -100,35 +124,28 @@ template <typename E> struct Row {
         return v;
     }
     // Element j of granule k is column col(k, j).
-    __device__ int64_t col(int k, int j) const { return static_cast<int64_t>(k) * G + j - shift; }
+    __device__ __forceinline__ int col(int k, int j) const { return k * G + j - shift; }
     // A granule at a row's end, element by element: `other` in places of no
     // column of the vocabulary.
     __device__ void load_edge(int k, float other, float (&f)[G]) const
     {
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-            const int64_t c = col(k, j);
-            f[j] = c >= 0 && c < V ? element(x + static_cast<int64_t>(k) * G + j) : other;
+            const int c = col(k, j);
+            f[j] = c >= 0 && c < V() ? element(x + static_cast<int64_t>(k) * G + j) : other;
         }
     }
     static __device__ __forceinline__ float element(const uint16_t *p) { return __uint_as_float(uint32_t(*p) << 16); }
     static __device__ __forceinline__ float element(const float *p) { return *p; }
+    // A granule of -inf.
+    static __device__ __forceinline__ uint4 nothing()
+    {
+        const uint32_t w = G == 8 ? 0xFF80FF80u : 0xFF800000u;
+        return make_uint4(w, w, w, w);
+    }
+    static __device__ __forceinline__ void values(const uint4 &q, float *f) { G == 8 ? values8(q, f) : values4(q, f); }
 };
 
-__device__ __forceinline__ void values(const uint4 &q, float (&f)[8])
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[2 * j] = bf16lo_to_f32(w[j]);
-        f[2 * j + 1] = bf16hi_to_f32(w[j]);
-    }
-}
-__device__ __forceinline__ void values(const uint4 &q, float (&f)[4])
-{
-    f[0] = __uint_as_float(q.x), f[1] = __uint_as_float(q.y);
-    f[2] = __uint_as_float(q.z), f[3] = __uint_as_float(q.w);
-}
 __device__ __forceinline__ uint4 packed(const float (&f)[8])
 {
     return make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
@@ -139,23 +156,36 @@ __device__ __forceinline__ uint4 packed(const float (&f)[4])
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
-// exp2 of (x - m) log2(e) / tau for two values.
+// log2(e) / tau in two parts, c = hi + lo: with one rounded factor alone all
+// differences would be scaled wrongly by the same 2^-25, and the error of a
+// sequence's log probabilities would add up.  Both are positive (kLog2eHigh is
+// further below log2 e than its product's rounding), so that -inf stays -inf.  Exponents are x c - m c by two fused steps, from the rounded
+// product mc = fl(m hi); what it is off by is known (rest) and goes into the
+// sum's logarithm.  Where m c leaves fp32's range (rows of the lowest value
+// alone), differences are scaled instead.
 struct Scale {
-    float hi, lo;  // log2(e) / tau
-    float inv_temperature;
-    __device__ explicit Scale(float inv) : hi(inv * kLog2e), inv_temperature(inv)
+    float hi, lo, near, inv_temperature;
+    __device__ explicit Scale(float inv) : hi(inv * kLog2eHigh), near(inv * kLog2e), inv_temperature(inv)
     {
-        lo = fmaf(inv, kLog2e, -hi) + inv * kLog2eLow;
+        lo = fmaxf(fmaf(inv, kLog2eHigh, -hi) + inv * kLog2eLow, FLT_MIN);
     }
-    __device__ __forceinline__ float2 exponent(float2 x, float2 minus_m) const
-    {
-        const float2 d = __fadd2_rn(x, minus_m);
-        return __ffma2_rn(d, both(lo), __fmul2_rn(d, both(hi)));
-    }
+    static __device__ __forceinline__ bool plain(float mc) { return fabsf(mc) <= 1e37f; }
     __device__ __forceinline__ float exponent(float x, float m) const
     {
-        const float d = x - m;
-        return fmaf(d, lo, d * hi);
+        const float mc = m * hi, d = x - m;
+        return plain(mc) ? fmaf(x, lo, fmaf(x, hi, -mc)) : d * near;
+    }
+    // From a sum relative to m to one relative to the larger `to`.
+    __device__ __forceinline__ float factor(float m, float to) const
+    {
+        const float mc = m * hi, tc = to * hi;
+        return ex2(plain(mc) && plain(tc) ? mc - tc : (m - to) * hi);
+    }
+    // The sum is of 2^(x c - m c - rest).
+    __device__ __forceinline__ float rest(float m) const
+    {
+        const float mc = m * hi;
+        return plain(mc) ? -fmaf(m, lo, fmaf(m, hi, -mc)) : 0.0f;
     }
 };
 
@@ -166,29 +196,84 @@ struct Sum {
 __device__ __forceinline__ Sum join(Sum a, Sum b, const Scale &c)
 {
     const float m = fmaxf(a.m, b.m);
-    return {m, a.s * ex2(c.exponent(a.m, m)) + b.s * ex2(c.exponent(b.m, m))};
+    return {m, a.s * c.factor(a.m, m) + b.s * c.factor(b.m, m)};
 }
 
-// Adds n values (n even).
-template <int n> __device__ __forceinline__ void accumulate(Sum &z, const float (&f)[n], const Scale &c)
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
 {
-    float m = fmaxf(f[0], f[1]);
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Largest value of n granules (a NaN is not: it shows in the sum).
+template <typename E, int n> __device__ __forceinline__ float largest(const uint4 (&q)[n])
+{
+    if (sizeof(E) == 2) {
+        uint32_t m = max_bf16x2(max_bf16x2(q[0].x, q[0].y), max_bf16x2(q[0].z, q[0].w));
 #pragma unroll
-    for (int j = 2; j < n; j += 2)
-        m = fmaxf(m, fmaxf(f[j], f[j + 1]));
+        for (int i = 1; i < n; ++i)
+            m = max_bf16x2(m, max_bf16x2(max_bf16x2(q[i].x, q[i].y), max_bf16x2(q[i].z, q[i].w)));
+        return fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m));
+    }
+    float m = -FLT_MAX;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+        m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(q[i].x), __uint_as_float(q[i].y)),
+                           fmaxf(__uint_as_float(q[i].z), __uint_as_float(q[i].w))));
+    return m;
+}
+
+// Adds the values of n granules.
+template <typename E, int n> __device__ __forceinline__ void accumulate(Sum &z, const uint4 (&q)[n], const Scale &c)
+{
+    constexpr int G = Row<E>::G;
+    const float m = largest<E, n>(q);
     if (m > z.m) {
-        z.s *= ex2(c.exponent(z.m, m));
+        z.s *= c.factor(z.m, m);
         z.m = m;
     }
-    const float2 minus = both(-z.m);
-    float2 s[2] = {make_float2(z.s, 0.0f), make_float2(0.0f, 0.0f)};
+    const float mc = z.m * c.hi;
+    if (Scale::plain(mc)) {
+        float2 s[4] = {make_float2(z.s, 0.0f), both(0.0f), both(0.0f), both(0.0f)};
 #pragma unroll
-    for (int j = 0; j < n; j += 2) {
-        const float2 y = c.exponent(make_float2(f[j], f[j + 1]), minus);
-        s[j / 2 % 2] = __fadd2_rn(s[j / 2 % 2], make_float2(ex2(y.x), ex2(y.y)));
+        for (int i = 0; i < n; ++i) {
+            float f[G];
+            Row<E>::values(q[i], f);
+#pragma unroll
+            for (int j = 0; j < G; j += 2) {
+                const float2 x = make_float2(f[j], f[j + 1]);
+                const float2 y = __ffma2_rn(x, both(c.lo), __ffma2_rn(x, both(c.hi), both(-mc)));
+                const int k = (i * G + j) / 2 % 4;
+                s[k] = __fadd2_rn(s[k], make_float2(ex2(y.x), ex2(y.y)));
+            }
+        }
+        s[0] = __fadd2_rn(__fadd2_rn(s[0], s[1]), __fadd2_rn(s[2], s[3]));
+        z.s = s[0].x + s[0].y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            float f[G];
+            Row<E>::values(q[i], f);
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+                z.s += ex2((f[j] - z.m) * c.near);
+        }
     }
-    s[0] = __fadd2_rn(s[0], s[1]);
-    z.s = s[0].x + s[0].y;
+}
+
+template <typename E> __device__ void accumulate_edge(Sum &z, const Row<E> &x, int k, const Scale &c)
+{
+    float f[Row<E>::G], m = z.m;
+    x.load_edge(k, neg_inf(), f);
+#pragma unroll
+    for (int j = 0; j < Row<E>::G; ++j)
+        m = fmaxf(m, f[j]);
+    z.s *= c.factor(z.m, m);
+    z.m = m;
+#pragma unroll
+    for (int j = 0; j < Row<E>::G; ++j)
+        z.s += ex2(c.exponent(f[j], m));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -210,46 +295,63 @@ __device__ __forceinline__ Sum remote(const Sum *mine, uint32_t rank)
     return z;
 }
 
-// Writes the gradient coef (1[target] - inv exp2(x - ref)) of a row: what all
-// of it takes.
+// Writes the gradient k / tau (1[target] - inv exp((x - ref) / tau)) of a row.
+// The exponents take log2(e) / tau rounded: 2^-25 of x - ref, nothing where
+// the probability is large.
 template <typename E> struct Gradient {
     static constexpr int G = Row<E>::G;
     const Row<E> &x;
     const Scale &c;
     E *out;             // as Row::x
     float coef, scaled; // coef and -coef inv
-    float minus;        // -ref
-    int64_t target;
+    float ref, minus;   // ref and -fl(ref c)
+    int target;
     int at;             // the target's granule
 
-    __device__ Gradient(const Row<E> &row, const LossRows &a, const Scale &scale, float k, float inv, float ref,
-                        int64_t token)
+    __device__ Gradient(const Row<E> &row, const LossRows &a, const Scale &scale, float k, float inv, float r,
+                        int t)
         : x(row), c(scale), out(static_cast<E *>(a.dlogits) + (row.x - static_cast<const E *>(a.logits))),
-          coef(k * a.inv_temperature), scaled(-coef * inv), minus(-ref), target(token),
-          at(static_cast<int>((token + row.shift) / G))
+          coef(k * a.inv_temperature), ref(r), minus(-r * scale.near), target(t),
+          at(static_cast<int>((static_cast<uint32_t>(t) + row.shift) / G))
     {
+        const float off = Scale::plain(minus) ? fmaf(r, scale.near, minus) : 0.0f;
+        scaled = -coef * inv * ex2(-off);
     }
-    __device__ __forceinline__ void compute(const float (&f)[G], int k, float (&d)[G]) const
+    __device__ __forceinline__ bool plain() const { return Scale::plain(minus); }
+    template <bool PLAIN> __device__ __forceinline__ void softmax(const float (&f)[G], float (&d)[G]) const
     {
 #pragma unroll
         for (int j = 0; j < G; j += 2) {
-            const float2 y = c.exponent(make_float2(f[j], f[j + 1]), both(minus));
+            const float2 x = make_float2(f[j], f[j + 1]);
+            const float2 y = PLAIN ? __ffma2_rn(x, both(c.near), both(minus))
+                                   : __fmul2_rn(__fadd2_rn(x, both(-ref)), both(c.near));
             const float2 e = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)), both(scaled));
             d[j] = e.x, d[j + 1] = e.y;
         }
-        if (k == at) {
+    }
+    __device__ __forceinline__ void add_target(int k, float (&d)[G]) const
+    {
 #pragma unroll
-            for (int j = 0; j < G; ++j)
-                if (x.col(k, j) == target)
-                    d[j] += coef;
-        }
+        for (int j = 0; j < G; ++j)
+            if (x.col(k, j) == target)
+                d[j] += coef;
+    }
+    __device__ __forceinline__ void zeros(int k) const
+    {
+        stg128_stream(out + static_cast<int64_t>(k) * G, make_uint4(0, 0, 0, 0));
+    }
+    template <bool PLAIN> __device__ __forceinline__ void interior_as(int k, const uint4 &q, bool check) const
+    {
+        float f[G], d[G];
+        Row<E>::values(q, f);
+        softmax<PLAIN>(f, d);
+        if (check && k == at)
+            add_target(k, d);
+        stg128_stream(out + static_cast<int64_t>(k) * G, packed(d));
     }
     __device__ __forceinline__ void interior(int k, const uint4 &q) const
     {
-        float f[G], d[G];
-        values(q, f);
-        compute(f, k, d);
-        stg128_stream(out + static_cast<int64_t>(k) * G, packed(d));
+        plain() ? interior_as<true>(k, q, true) : interior_as<false>(k, q, true);
     }
     // A granule that is not all the vocabulary's: zeros behind it, nothing
     // outside the row.  zero: the whole row is.
@@ -258,18 +360,20 @@ template <typename E> struct Gradient {
         float f[G], d[G];
         if (!zero) {
             x.load_edge(k, neg_inf(), f);
-            compute(f, k, d);
+            plain() ? softmax<true>(f, d) : softmax<false>(f, d);
+            if (k == at)
+                add_target(k, d);
         }
 #pragma unroll
         for (int j = 0; j < G; ++j)
-            d[j] = zero || x.col(k, j) >= x.V ? 0.0f : d[j];
+            d[j] = zero || x.col(k, j) >= x.V() ? 0.0f : d[j];
         store(k, d);
     }
     __device__ __forceinline__ void store(int k, const float (&d)[G]) const
     {
         const uint4 q = packed(d);
         E *p = out + static_cast<int64_t>(k) * G;
-        if (x.col(k, 0) >= 0 && x.col(k, G) <= x.N) {
+        if (x.col(k, 0) >= 0 && x.col(k, G) <= x.N()) {
             stg128_stream(p, q);
             return;
         }
@@ -277,35 +381,67 @@ template <typename E> struct Gradient {
         memcpy(e, &q, 16);
 #pragma unroll
         for (int j = 0; j < G; ++j)
-            if (x.col(k, j) >= 0 && x.col(k, j) < x.N)
+            if (x.col(k, j) >= 0 && x.col(k, j) < x.N())
                 p[j] = e[j];
     }
 };
 
-// One row a cluster of `parts` CTAs (1: no cluster).  RESIDENT: the part of
-// the row is kept in shared memory between the passes.
-template <typename E, int MODE, bool CLUSTER, bool RESIDENT>
-__global__ void __launch_bounds__(512) row_kernel(const __grid_constant__ LossRows a, int parts, int chunks, int trigger)
+// The policy loss's share of a row, from its log probability.
+struct Policy {
+    float advantage, old_logp, ref_logp, weight;
+    __device__ Policy(const LossRows &a, int64_t row, float w)
+        : advantage(a.advantages[row]), old_logp(a.old_logp[row]), ref_logp(a.ref_logp ? a.ref_logp[row] : 0.0f),
+          weight(w)
+    {
+    }
+    // token_loss, and the gradient at logp
+    __device__ float2 at(float logp, const LossRows &a) const
+    {
+        const float r = ex2((logp - old_logp) * kLog2e);
+        const float free = advantage == 0.0f ? 0.0f : r * advantage;
+        const float held = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * advantage;
+        float loss = -fminf(free, held), slope = free <= held ? -free : 0.0f;
+        if (isnan(r))
+            loss = slope = r;
+        if (a.ref_logp) {
+            const float d = ref_logp - logp, em1 = expm1f(d);
+            loss += a.kl * (em1 - d);
+            slope -= a.kl * em1;
+        }
+        return make_float2(weight * loss, weight * slope * a.grad_scale);
+    }
+};
+
+// A warp's sums together, in all lanes.
+__device__ __forceinline__ Sum warp_sum(Sum z, const Scale &c)
+{
+    float m = z.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    z.s *= c.factor(z.m, m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        z.s += __shfl_xor_sync(~0u, z.s, o);
+    return {m, z.s};
+}
+
+// Row by row without shared memory for the logits: one row a cluster of
+// `parts` CTAs (1: no cluster).  The policy loss takes it only for rows that
+// policy_kernel cannot hold.
+template <typename E, int MODE, bool CLUSTER>
+__global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ LossRows a, int parts, int trigger)
 {
     constexpr int G = Row<E>::G;
-    extern __shared__ __align__(128) uint4 held[];
-    __shared__ Sum part[16], mine;
-    __shared__ __align__(8) uint64_t bars[kMaxChunks];
+    __shared__ Sum part[8], mine;
     const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     if (trigger)
         pdl_trigger();
-    if (RESIDENT && tid == 0) {
-        for (int i = 0; i < chunks; ++i)
-            mbar_init(smem_u32(&bars[i]), 1);
-        fence_barrier_init();
-    }
-    if (RESIDENT)
-        __syncthreads();
     pdl_wait();
     const int64_t row = CLUSTER ? blockIdx.x / parts : blockIdx.x;
     const Row<E> x(a, row);
-    const int64_t target = a.targets[row];
+    const int target = token(a, row);
     float weight = 1.0f;
     bool active = target >= 0;
     if (MODE == kPolicy) {
@@ -321,80 +457,29 @@ __global__ void __launch_bounds__(512) row_kernel(const __grid_constant__ LossRo
     Sum z = {-FLT_MAX, 0.0f};
     float coef = 0.0f, inv = 0.0f;
     if (active) {
-        float xa = 0.0f, adv = 0.0f, old = 0.0f, ref_logp = 0.0f;
-        xa = target < x.V ? Row<E>::element(x.x + x.shift + target) : quiet_nan();
-        if (MODE == kPolicy) {
-            adv = a.advantages[row], old = a.old_logp[row];
-            ref_logp = a.ref_logp ? a.ref_logp[row] : 0.0f;
+        const float xa = target < x.V() ? Row<E>::element(x.x + x.shift + target) : quiet_nan();
+        int k = lo + tid;
+        for (; k + 3 * threads < hi; k += 4 * threads) {
+            uint4 q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                q[j] = x.load(k + j * threads);
+            accumulate<E, 4>(z, q, c);
         }
-        if (RESIDENT) {
-            const int chunk = threads * kChunkSteps;
-            if (tid == 0) {
-                for (int i = 0, k = lo; k < hi; ++i, k += chunk) {
-                    const uint32_t bytes = static_cast<uint32_t>(min(chunk, hi - k)) * 16, bar = smem_u32(&bars[i]);
-                    mbar_arrive_expect_tx(bar, bytes);
-                    bulk_load(smem_u32(held + (k - lo)), x.x + static_cast<int64_t>(k) * G, bytes, bar);
-                }
-            }
-            for (int i = 0, k = lo; k < hi; ++i, k += chunk) {
-                if (!mbar_wait(smem_u32(&bars[i]), 0) && lane == 0)
-                    atomicOr(&g_loss_error, kErrLoss);
-#pragma unroll
-                for (int j = 0; j < kChunkSteps; ++j) {
-                    const int g = k + tid + j * threads;
-                    if (g < hi) {
-                        float f[G];
-                        values(held[g - lo], f);
-                        accumulate(z, f, c);
-                    }
-                }
-            }
-        } else {
-            int k = lo + tid;
-            for (; k + 3 * threads < hi; k += 4 * threads) {
-                uint4 q[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    q[j] = x.load(k + j * threads);
-                float f[4 * G];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float g[G];
-                    values(q[j], g);
-#pragma unroll
-                    for (int i = 0; i < G; ++i)
-                        f[j * G + i] = g[i];
-                }
-                accumulate(z, f, c);
-            }
-            for (; k < hi; k += threads) {
-                float f[G];
-                values(x.load(k), f);
-                accumulate(z, f, c);
-            }
+        for (; k < hi; k += threads) {
+            const uint4 q[1] = {x.load(k)};
+            accumulate<E, 1>(z, q, c);
         }
         // what of the row lies in granules with other elements
-        if (rank == 0 && tid == 0 && x.first > 0) {
-            float f[G];
-            x.load_edge(0, neg_inf(), f);
-            accumulate(z, f, c);
-        }
-        if (rank == parts - 1 && tid == threads - 1 && x.col(x.last, 0) < x.V) {
-            float f[G];
-            x.load_edge(x.last, neg_inf(), f);
-            accumulate(z, f, c);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            z = join(z, {__shfl_xor_sync(~0u, z.m, o), __shfl_xor_sync(~0u, z.s, o)}, c);
+        if (rank == 0 && tid == 0 && x.first > 0)
+            accumulate_edge(z, x, 0, c);
+        if (rank == parts - 1 && tid == threads - 1 && x.col(x.last, 0) < x.V())
+            accumulate_edge(z, x, x.last, c);
+        z = warp_sum(z, c);
         if (lane == 0)
             part[tid >> 5] = z;
         __syncthreads();
-        z = lane < threads / 32 ? part[lane] : Sum{-FLT_MAX, 0.0f};
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            z = join(z, {__shfl_xor_sync(~0u, z.m, o), __shfl_xor_sync(~0u, z.s, o)}, c);
-        z = {__shfl_sync(~0u, z.m, 0), __shfl_sync(~0u, z.s, 0)};
+        z = warp_sum(lane < threads / 32 ? part[lane] : Sum{-FLT_MAX, 0.0f}, c);
         if (CLUSTER) {
             if (tid == 0)
                 mine = z;
@@ -402,34 +487,23 @@ __global__ void __launch_bounds__(512) row_kernel(const __grid_constant__ LossRo
             cluster_wait();
             z = lane < parts ? remote(&mine, lane) : Sum{-FLT_MAX, 0.0f};
             cluster_arrive();  // no more reads from here; waited for at the end
-#pragma unroll
-            for (int o = kMaxCluster / 2; o > 0; o >>= 1)
-                z = join(z, {__shfl_xor_sync(~0u, z.m, o), __shfl_xor_sync(~0u, z.s, o)}, c);
-            z = {__shfl_sync(~0u, z.m, 0), __shfl_sync(~0u, z.s, 0)};
+            z = warp_sum(z, c);
         }
-        const float ln_s = logf(z.s);
+        const float ln_s = logf(z.s) + c.rest(z.m) * kLn2;
         const float logp = (xa - z.m) * a.inv_temperature - ln_s;
         if (MODE == kForward && rank == 0 && tid == 0) {
             a.logp[row] = logp;
             a.lse[row] = z.m * a.inv_temperature + ln_s;
         }
         if (MODE == kPolicy) {
-            const float r = expf(logp - old);
-            const float free = adv == 0.0f ? 0.0f : r * adv;
-            const float held_at = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * adv;
-            float loss = -fminf(free, held_at), slope = free <= held_at ? -free : 0.0f;
-            if (isnan(r))
-                loss = slope = r;
-            if (a.ref_logp) {
-                const float d = ref_logp - logp, em1 = expm1f(d);
-                loss += a.kl * (em1 - d);
-                slope -= a.kl * em1;
-            }
-            coef = weight * slope * a.grad_scale;
-            inv = 1.0f / z.s;
+            const float2 loss = Policy(a, row, weight).at(logp, a);
+            coef = loss.y;
+            inv = ex2(-c.rest(z.m)) * inverse(z.s);
             if (rank == 0 && tid == 0) {
-                a.token_loss[row] = weight * loss;
+                a.token_loss[row] = loss.x;
                 a.logp[row] = logp;
+                if (a.T == 1)
+                    *a.loss = loss.x;
             }
         }
     } else if (rank == 0 && tid == 0) {
@@ -438,30 +512,268 @@ __global__ void __launch_bounds__(512) row_kernel(const __grid_constant__ LossRo
             a.lse[row] = 0.0f;
         if (MODE == kForward && a.coef)
             a.coef[row] = 0.0f;
-        if (MODE == kPolicy)
+        if (MODE == kPolicy) {
             a.token_loss[row] = 0.0f;
+            if (a.T == 1)
+                *a.loss = 0.0f;
+        }
     }
     if (MODE == kPolicy && a.dlogits) {
         const Gradient<E> d(x, a, c, coef, inv, z.m, target);
         const bool zero = !(coef != 0.0f);  // also a clipped row's
-        if (zero) {
-            for (int k = lo + tid; k < hi; k += threads)
-                stg128_stream(d.out + static_cast<int64_t>(k) * G, make_uint4(0, 0, 0, 0));
-        } else if (RESIDENT) {
-            for (int k = lo + tid; k < hi; k += threads)
-                d.interior(k, held[k - lo]);
-        } else {
-            for (int k = lo + tid; k < hi; k += threads)
-                d.interior(k, x.load(k));
-        }
+        for (int k = lo + tid; k < hi; k += threads)
+            zero ? d.zeros(k) : d.interior(k, x.load(k));
         if (rank == 0 && tid == 0 && x.first > 0)
             d.edge(0, zero);
         if (rank == parts - 1)
-            for (int k = max(x.last, x.first) + tid; k < x.end; k += threads)
+            for (int k = max(x.last, x.first) + tid; k < x.end(); k += threads)
                 d.edge(k, zero);
     }
     if (CLUSTER && active)
         cluster_wait();
+}
+
+// ------------------------------------------------- the policy loss, rows held --
+
+constexpr int kMaxWarps = 8;
+constexpr int kLine = 32;        // granules of a line: one a lane
+constexpr int kGroup = 4;        // lines of a step
+constexpr int kLines = 8;        // lines of a bulk copy
+constexpr int kMaxLines = 52;    // that a warp holds
+constexpr int kCopies = (kMaxLines + kLines - 1) / kLines;
+
+// Stores z at the same place of CTA `rank`'s shared memory and reports its
+// bytes to the barrier at `bar` there.
+__device__ __forceinline__ void send(Sum *to, uint64_t *bar, uint32_t rank, Sum z)
+{
+    uint32_t at, rbar;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(to)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rbar) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(at),
+                 "r"(__float_as_uint(z.m)), "r"(__float_as_uint(z.s)), "r"(rbar)
+                 : "memory");
+}
+
+// mbar_wait with a hint that lets the warp sleep until the phase completes (a
+// row's warps wait for memory most of the time; polling took a third of the
+// issue slots).  CLUSTER: for what other CTAs of the cluster have stored.
+template <bool CLUSTER> __device__ __forceinline__ bool sleep_until(uint32_t bar, uint32_t parity)
+{
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        if (CLUSTER)
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok)
+                         : "r"(bar), "r"(parity), "r"(10000000u)
+                         : "memory");
+        else
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok)
+                         : "r"(bar), "r"(parity), "r"(10000000u)
+                         : "memory");
+        if (ok)
+            return true;
+        const uint64_t t = global_timer_ns();
+        t0 = t0 ? t0 : t;
+        if (t - t0 > kWaitLimitNs)
+            return false;
+    }
+}
+
+// A warp's lines of a row's interior.
+template <typename E> struct Lines {
+    int from, to;  // lines
+    __device__ __forceinline__ Lines(const Row<E> &x, int warp, int log_warps)
+    {
+        const int all = (x.last - x.first + kLine - 1) / kLine;
+        from = (all * warp) >> log_warps;  // (at most 64 warps of kMaxLines)
+        to = (all * (warp + 1)) >> log_warps;
+    }
+    __device__ __forceinline__ int copies() const { return (to - from + kLines - 1) / kLines; }
+};
+
+// Persistent clusters of `parts` CTAs take row after row.  Each warp has its
+// own lines of the row, copies them into its own shared memory and frees them
+// line by line as it writes the gradient, so that the next row arrives while
+// this one leaves.  The warps' sums go to all CTAs of the cluster by
+// asynchronous stores: a barrier with release semantics would wait for the
+// gradient's stores.  Sums of successive rows use two places in turn: a warp
+// sends its sum of a row only after it has read all sums of the row before.
+template <typename E, bool CLUSTER>
+__global__ void __launch_bounds__(32 * kMaxWarps, 2)
+    policy_kernel(const __grid_constant__ LossRows a, int parts, int max_lines, int trigger)
+{
+    constexpr int G = Row<E>::G;
+    extern __shared__ __align__(128) uint4 shared_lines[];
+    __shared__ Sum sums[2][kMaxWarps * kMaxCluster];
+    __shared__ __align__(8) uint64_t bars[kMaxWarps * kCopies], sums_bar[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+    const int my = rank * warps + warp, all = parts * warps;  // among the cluster's warps
+    const int log_all = __ffs(all) - 1;
+    uint4 *const held = shared_lines + static_cast<int64_t>(warp) * max_lines * kLine;
+    uint64_t *const bar = bars + warp * kCopies;
+    if (trigger)
+        pdl_trigger();
+    if (lane == 0) {
+        for (int i = 0; i < (max_lines + kLines - 1) / kLines; ++i)
+            mbar_init(smem_u32(&bar[i]), 1);
+        if (warp == 0) {
+            mbar_init(smem_u32(&sums_bar[0]), 1);
+            mbar_init(smem_u32(&sums_bar[1]), 1);
+        }
+        fence_barrier_init();
+    }
+    if (CLUSTER) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    pdl_wait();
+
+    const Scale c(a.inv_temperature);
+    const int64_t step = CLUSTER ? gridDim.x / parts : gridDim.x;
+    int64_t row = CLUSTER ? blockIdx.x / parts : blockIdx.x;
+    const auto copy = [&](const Row<E> &x, const Lines<E> &l, int i) {  // lane 0
+        const int from = x.first + (l.from + i * kLines) * kLine;
+        const int to = min(x.last, x.first + min(l.to, l.from + (i + 1) * kLines) * kLine);
+        const uint32_t bytes = static_cast<uint32_t>(to - from) * 16, b = smem_u32(&bar[i]);
+        mbar_arrive_expect_tx(b, bytes);
+        bulk_load(smem_u32(held + i * kLines * kLine), x.x + static_cast<int64_t>(from) * G, bytes, b);
+    };
+    int target = -1;
+    float weight = 0.0f;
+    bool active = false;
+    Row<E> x(a, row);
+    Lines<E> l(x, my, log_all);
+    if (row < a.T) {
+        target = token(a, row), weight = a.weights[row];
+        active = target >= 0 && weight != 0.0f;
+        if (active && lane == 0) {
+            for (int i = 0; i < l.copies(); ++i)
+                copy(x, l, i);
+        }
+    }
+    uint32_t phases = 0, turn = 0;  // turn: rows summed so far
+    for (; row < a.T; row += step) {
+        const int64_t next = row + step;
+        int next_target = -1;
+        float next_weight = 0.0f;
+        if (next < a.T)
+            next_target = token(a, next), next_weight = a.weights[next];
+        Sum z = {-FLT_MAX, 0.0f};
+        float coef = 0.0f, inv = 0.0f;
+        if (active) {
+            const float xa = target < x.V() ? Row<E>::element(x.x + x.shift + target) : quiet_nan();
+            const Policy policy(a, row, weight);
+            if (my == 0 && lane == 0 && x.first > 0)
+                accumulate_edge(z, x, 0, c);
+            if (my == all - 1 && lane == 31 && x.col(x.last, 0) < x.V())
+                accumulate_edge(z, x, x.last, c);
+            const int left = x.last - x.first - l.from * kLine - lane;  // > 32 j: line j has a granule for this lane
+            for (int j = 0; j < l.to - l.from; j += kGroup) {
+                if (j % kLines == 0) {
+                    const int i = j / kLines;
+                    if (!sleep_until<false>(smem_u32(&bar[i]), phases >> i & 1) && lane == 0)
+                        atomicOr(&g_loss_error, kErrLoss);
+                    phases ^= 1u << i;
+                }
+                const uint4 *p = held + j * kLine + lane;
+                uint4 q[kGroup];
+                if (j + kGroup <= l.to - l.from && left + lane >= (j + kGroup) * kLine) {
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i)
+                        q[i] = p[i * kLine];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i)
+                        q[i] = j + i < l.to - l.from && left > (j + i) * kLine ? p[i * kLine] : Row<E>::nothing();
+                }
+                accumulate<E, kGroup>(z, q, c);
+            }
+            __syncwarp();
+            z = warp_sum(z, c);
+            asm volatile("" ::"f"(xa));  // read before anybody may write there
+            Sum *const to = sums[turn & 1];
+            if (CLUSTER) {
+                if (warp == 0 && lane == 0)
+                    mbar_arrive_expect_tx(smem_u32(&sums_bar[turn & 1]), static_cast<uint32_t>(all) * sizeof(Sum));
+                __syncwarp();
+                if (lane < parts)
+                    send(&to[my], &sums_bar[turn & 1], lane, z);
+                if (!sleep_until<true>(smem_u32(&sums_bar[turn & 1]), turn >> 1 & 1) && lane == 0)
+                    atomicOr(&g_loss_error, kErrLoss);
+            } else {
+                if (lane == 0)
+                    to[warp] = z;
+                __syncthreads();
+            }
+            ++turn;
+            z = lane < all ? to[lane] : Sum{-FLT_MAX, 0.0f};
+            if (CLUSTER && lane + 32 < all)
+                z = join(z, to[lane + 32], c);
+            z = warp_sum(z, c);
+            const float logp = (xa - z.m) * a.inv_temperature - (logf(z.s) + c.rest(z.m) * kLn2);
+            const float2 loss = policy.at(logp, a);
+            coef = loss.y;
+            inv = ex2(-c.rest(z.m)) * inverse(z.s);
+            if (my == 0 && lane == 0) {
+                a.token_loss[row] = loss.x;
+                a.logp[row] = logp;
+                if (a.T == 1)
+                    *a.loss = loss.x;
+            }
+        } else if (my == 0 && lane == 0) {
+            a.logp[row] = 0.0f;
+            a.token_loss[row] = 0.0f;
+            if (a.T == 1)
+                *a.loss = 0.0f;
+        }
+        // the gradient; each copy's place is free for the next row behind it
+        const bool zero = !(coef != 0.0f);  // also a clipped row's
+        const Gradient<E> d(x, a, c, coef, inv, z.m, target);
+        const bool plain = d.plain();
+        const bool next_active = next_target >= 0 && next_weight != 0.0f;
+        const Row<E> y(a, next);
+        const Lines<E> yl(y, my, log_all);
+        const int here = l.copies(), there = next_active ? yl.copies() : 0;
+        for (int i = 0; i < max(here, there); ++i) {
+            if (a.dlogits && i < here) {
+                const int lines = min(kLines, l.to - l.from - i * kLines);
+                for (int j = 0; j < lines; j += kGroup) {
+                    const int from = x.first + (l.from + i * kLines + j) * kLine, k = from + lane;
+                    const uint4 *q = held + (i * kLines + j) * kLine + lane;
+                    const bool whole = j + kGroup <= lines && from + kGroup * kLine <= x.last;
+                    // the common case without a check in it
+                    if (whole && plain && !zero && (d.at < from || d.at >= from + kGroup * kLine)) {
+#pragma unroll
+                        for (int h = 0; h < kGroup; ++h)
+                            d.template interior_as<true>(k + h * kLine, q[h * kLine], false);
+                    } else {
+                        for (int h = 0; h < kGroup && j + h < lines && k + h * kLine < x.last; ++h)
+                            zero ? d.zeros(k + h * kLine) : d.interior(k + h * kLine, q[h * kLine]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0 && i < there)
+                copy(y, yl, i);
+        }
+        if (a.dlogits) {
+            if (my == 0 && lane == 0 && x.first > 0)
+                d.edge(0, zero);
+            for (int k = max(x.last, x.first) + my * 32 + lane; k < x.end(); k += all * 32)
+                d.edge(k, zero);
+        }
+        target = next_target, weight = next_weight, active = next_active;
+        x = y, l = yl;
+    }
 }
 
 // The gradient from a given lse; `parts` CTAs a row, each on its own.
@@ -475,7 +787,7 @@ __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ L
     const int tid = threadIdx.x, threads = blockDim.x, rank = blockIdx.x % parts;
     const int64_t row = blockIdx.x / parts;
     const Row<E> x(a, row);
-    const int64_t target = a.targets[row];
+    const int target = token(a, row);
     const float weight = a.dlogp[row];
     const bool zero = target < 0 || weight == 0.0f;
     const int each = (x.last - x.first + parts - 1) / parts;
@@ -484,12 +796,12 @@ __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ L
     // exp(x / tau - lse) = exp2(c (x - hi)) exp2(-c lo), hi + lo = lse tau
     const float lse = a.lse[row], at = lse * a.temperature;
     const float low = fmaf(lse, a.temperature, -at);
-    const float inv = fabsf(low) <= FLT_MAX ? ex2(-low * c.hi) : 1.0f;
-    const Gradient<E> d(x, a, c, target < x.V ? weight * a.grad_scale : quiet_nan(), inv, at, target);
+    const float inv = fabsf(low) <= FLT_MAX ? ex2(-low * c.near) : 1.0f;
+    const Gradient<E> d(x, a, c, target < x.V() ? weight * a.grad_scale : quiet_nan(), inv, at, target);
     int k = lo + tid;
     if (zero) {
         for (; k < hi; k += threads)
-            stg128_stream(d.out + static_cast<int64_t>(k) * G, make_uint4(0, 0, 0, 0));
+            d.zeros(k);
     } else {
         for (; k + 3 * threads < hi; k += 4 * threads) {
             uint4 q[4];
@@ -506,7 +818,7 @@ __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ L
     if (rank == 0 && tid == 0 && x.first > 0)
         d.edge(0, zero);
     if (rank == parts - 1)
-        for (int k = max(x.last, x.first) + tid; k < x.end; k += threads)
+        for (int k = max(x.last, x.first) + tid; k < x.end(); k += threads)
             d.edge(k, zero);
 }
 
@@ -608,48 +920,65 @@ struct Split {
     int parts, threads;
 };
 
-template <typename E, int MODE, bool CLUSTER, bool RESIDENT>
-cudaError_t launch_row_kernel(const LossRows &a, Split s, size_t smem, int trigger, int device, cudaStream_t stream)
+// Persistent rows of the policy loss; *taken = false: too long for them.
+template <typename E> cudaError_t launch_policy(const LossRows &a, bool *taken, cudaStream_t stream)
 {
-    const int chunks = static_cast<int>((smem / 16 + s.threads * kChunkSteps - 1) / (s.threads * kChunkSteps));
-    const auto kernel = row_kernel<E, MODE, CLUSTER, RESIDENT>;
-    if (RESIDENT) {
-        static std::atomic<bool> done[kMaxDevices];
-        const cudaError_t e = ensure_smem(kernel, 220 * 1024, device, done);
-        if (e != cudaSuccess)
-            return e;
-    }
-    return launch_cluster(kernel, a.T * s.parts, s.threads, smem, CLUSTER ? s.parts : 1, stream, a, s.parts, chunks,
-                          trigger);
-}
-
-template <typename E, int MODE> cudaError_t launch_rows(const LossRows &a, cudaStream_t stream)
-{
-    constexpr int G = 16 / sizeof(E);
     DeviceInfo di;
     cudaError_t e = current_device_info(&di);
     if (e != cudaSuccess)
         return e;
-    const int64_t granules = a.V / G + 1;
-    // the policy loss sums in the same order with and without its gradient
-    const bool grad = MODE == kPolicy;
-    // a part of at most 55 KB leaves room for four CTAs on an SM
+    const int64_t lines = (a.V / (16 / sizeof(E)) + 1 + kLine - 1) / kLine;  // of any row, at most
+    // 13 lines a warp and 32 warps fill an SM's shared memory; few rows are
+    // split further, down to one bulk copy a warp
+    int parts = 1, warps = 1;
+    const auto each = [&] { return (lines + parts * warps - 1) / (parts * warps); };
+    while (warps < kMaxWarps && each() > 26)
+        warps *= 2;
+    while (parts < kMaxCluster && each() > 26)
+        parts *= 2;
+    while (warps < kMaxWarps && a.T < di.num_sms && each() > kLines)
+        warps *= 2;
+    while (parts < kMaxCluster && a.T * parts < 2 * di.num_sms && each() > kLines)
+        parts *= 2;
+    *taken = each() <= kMaxLines;
+    if (!*taken)
+        return cudaSuccess;
+    const int max_lines = static_cast<int>(each());
+    const size_t smem = static_cast<size_t>(max_lines) * warps * kLine * 16;
+    const auto kernel = parts > 1 ? policy_kernel<E, true> : policy_kernel<E, false>;
+    static std::atomic<bool> done[2][kMaxDevices];
+    if ((e = ensure_smem(kernel, kMaxLines * kMaxWarps * kLine * 16, di.device, done[parts > 1])) != cudaSuccess)
+        return e;
+    int per_sm = 0;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, warps * 32, smem)) != cudaSuccess)
+        return e;
+    const int64_t clusters = static_cast<int64_t>(di.num_sms) * (per_sm < 1 ? 1 : per_sm) / parts;
+    const int64_t grid = a.T < clusters ? a.T : clusters;
+    return launch_cluster(kernel, grid * parts, warps * 32, smem, parts, stream, a, parts, max_lines,
+                          static_cast<int>(grid * parts <= di.num_sms));
+}
+
+template <typename E, int MODE> cudaError_t launch_rows(const LossRows &a, cudaStream_t stream)
+{
+    if (MODE == kPolicy) {
+        bool taken = false;
+        const cudaError_t e = launch_policy<E>(a, &taken, stream);
+        if (taken || e != cudaSuccess)
+            return e;
+    }
+    DeviceInfo di;
+    const cudaError_t e = current_device_info(&di);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t granules = a.V * sizeof(E) / 16 + 1;
     Split s = {1, 32};
-    while (s.parts < kMaxCluster && grad && (granules + s.parts - 1) / s.parts * 16 > 55 * 1024)
-        s.parts *= 2;
     while (s.parts < kMaxCluster && a.T * s.parts < 2 * di.num_sms && granules / s.parts >= 512)
         s.parts *= 2;
-    const int64_t each = (granules + s.parts - 1) / s.parts;
-    while (s.threads < 256 && s.threads * 4 < each)
+    while (s.threads < 256 && s.threads * s.parts * 4 < granules)
         s.threads *= 2;
-    const size_t smem = static_cast<size_t>(each) * 16;
-    const bool resident = grad && smem <= 216 * 1024 && each <= int64_t(kMaxChunks) * s.threads * kChunkSteps;
     const int trigger = a.T * s.parts <= di.num_sms;
-    if (s.parts > 1)
-        return resident ? launch_row_kernel<E, MODE, true, true>(a, s, smem, trigger, di.device, stream)
-                        : launch_row_kernel<E, MODE, true, false>(a, s, 0, trigger, di.device, stream);
-    return resident ? launch_row_kernel<E, MODE, false, true>(a, s, smem, trigger, di.device, stream)
-                    : launch_row_kernel<E, MODE, false, false>(a, s, 0, trigger, di.device, stream);
+    return launch_cluster(s.parts > 1 ? row_kernel<E, MODE, true> : row_kernel<E, MODE, false>, a.T * s.parts,
+                          s.threads, 0, s.parts, stream, a, s.parts, trigger);
 }
 
 template <int MODE> cudaError_t launch_rows(const LossRows &a, bool bf16, cudaStream_t stream)
@@ -681,14 +1010,14 @@ cudaError_t launch_logprob_backward(const LossRows &a, bool bf16, cudaStream_t s
                           stream, a, s.parts, trigger);
 }
 
-cudaError_t launch_policy_loss(const LossRows &a, bool bf16, float *loss, cudaStream_t stream)
+cudaError_t launch_policy_loss(const LossRows &a, bool bf16, cudaStream_t stream)
 {
     if (a.T > 0) {
         const cudaError_t e = launch_rows<kPolicy>(a, bf16, stream);
-        if (e != cudaSuccess)
+        if (e != cudaSuccess || a.T == 1)  // (one row's loss is the sum)
             return e;
     }
-    return launch_pdl(total_kernel, 1, 1024, 0, stream, static_cast<const float *>(a.token_loss), a.T, 1.0f, loss);
+    return launch_pdl(total_kernel, 1, 1024, 0, stream, static_cast<const float *>(a.token_loss), a.T, 1.0f, a.loss);
 }
 
 cudaError_t launch_preference_loss(const LossRows &a, const PairArgs &p, bool bf16, float *loss, cudaStream_t stream)

@@ -928,9 +928,8 @@ taco_status policy_loss(const void *logits, int32_t logits_bf16, const int64_t *
     taco::LossRows a = loss_rows(logits, targets, T, V, N, temperature);
     a.old_logp = old_logp, a.advantages = advantages, a.weights = weights, a.ref_logp = kl != 0.0f ? ref_logp : nullptr;
     a.clip_lo = 1.0f - clip_low, a.clip_hi = 1.0f + clip_high, a.kl = kl, a.grad_scale = grad_scale;
-    a.token_loss = token_loss, a.logp = logp, a.dlogits = dlogits;
-    return from_cuda(
-        taco::launch_policy_loss(a, logits_bf16 != 0, loss, reinterpret_cast<cudaStream_t>(stream)));
+    a.token_loss = token_loss, a.loss = loss, a.logp = logp, a.dlogits = dlogits;
+    return from_cuda(taco::launch_policy_loss(a, logits_bf16 != 0, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 taco_status preference_loss_workspace_bytes(int64_t T, int64_t pairs, uint64_t *bytes)
