@@ -30,14 +30,16 @@
 
 namespace taco {
 
+// Watchdog flag of this file's kernels (bit 9), read by taco_device_error().
+__device__ unsigned int g_adamw_error;
+
 namespace {
 
+constexpr uint32_t kErrAdamW = 512u;
 constexpr int kThreads = 256;
-constexpr int kBlocks = 4;                                   // blocks of 128 a warp has in flight
-constexpr int kChunk = kThreads / 32 * kBlocks * 128;        // values of a chunk of the update
-constexpr int kNormChunk = kThreads * 64;                    // and of the norm
+constexpr int kNormChunk = kThreads * 64;  // values of a chunk of the norm
 
-// Tensors of a launch; first[i]: the first chunk of tensor i.
+// Tensors of a launch; first[i]: the first chunk (or span) of tensor i.
 template <typename D, int MAX> struct Table {
     D tensor[MAX];
     int32_t first[MAX + 1];
@@ -57,32 +59,33 @@ template <typename D, int MAX> __device__ __forceinline__ int tensor_of(const Ta
     return lo;
 }
 
-// Elements e .. e + 3 of n, zeros past the end.
-__device__ __forceinline__ float4 load4(const float *p, int64_t e, int64_t n)
+// Elements e .. e + 3 of n, zeros past the end (FULL: all are there).  What is
+// stored leaves L2 first: nothing reads it in this step.
+template <bool FULL = false> __device__ __forceinline__ float4 load4(const float *p, int64_t e, int64_t n)
 {
-    if (e + 4 <= n)
+    if (FULL || e + 4 <= n)
         return *reinterpret_cast<const float4 *>(p + e);
     return make_float4(e < n ? p[e] : 0.0f, e + 1 < n ? p[e + 1] : 0.0f, e + 2 < n ? p[e + 2] : 0.0f, 0.0f);
 }
-__device__ __forceinline__ uint32_t load4(const uint8_t *p, int64_t e, int64_t n)
+template <bool FULL = false> __device__ __forceinline__ uint32_t load4(const uint8_t *p, int64_t e, int64_t n)
 {
-    if (e + 4 <= n)
+    if (FULL || e + 4 <= n)
         return *reinterpret_cast<const uint32_t *>(p + e);
     uint32_t w = 0;
     for (int j = 0; j < 3; ++j)
         w |= e + j < n ? uint32_t(p[e + j]) << (8 * j) : 0u;
     return w;
 }
-__device__ __forceinline__ uint2 load4(const uint16_t *p, int64_t e, int64_t n)
+template <bool FULL = false> __device__ __forceinline__ uint2 load4(const uint16_t *p, int64_t e, int64_t n)
 {
-    if (e + 4 <= n)
+    if (FULL || e + 4 <= n)
         return *reinterpret_cast<const uint2 *>(p + e);
     return make_uint2((e < n ? p[e] : 0u) | (e + 1 < n ? uint32_t(p[e + 1]) << 16 : 0u), e + 2 < n ? p[e + 2] : 0u);
 }
-__device__ __forceinline__ void store4(float *p, int64_t e, int64_t n, float4 v)
+template <bool FULL = false> __device__ __forceinline__ void store4(float *p, int64_t e, int64_t n, float4 v)
 {
-    if (e + 4 <= n) {
-        *reinterpret_cast<float4 *>(p + e) = v;
+    if (FULL || e + 4 <= n) {
+        __stcs(reinterpret_cast<float4 *>(p + e), v);
     } else {
         if (e < n)
             p[e] = v.x;
@@ -92,19 +95,19 @@ __device__ __forceinline__ void store4(float *p, int64_t e, int64_t n, float4 v)
             p[e + 2] = v.z;
     }
 }
-__device__ __forceinline__ void store4(uint8_t *p, int64_t e, int64_t n, uint32_t w)
+template <bool FULL = false> __device__ __forceinline__ void store4(uint8_t *p, int64_t e, int64_t n, uint32_t w)
 {
-    if (e + 4 <= n)
-        *reinterpret_cast<uint32_t *>(p + e) = w;
+    if (FULL || e + 4 <= n)
+        __stcs(reinterpret_cast<uint32_t *>(p + e), w);
     else
         for (int j = 0; j < 3; ++j)
             if (e + j < n)
                 p[e + j] = static_cast<uint8_t>(w >> (8 * j));
 }
-__device__ __forceinline__ void store4(uint16_t *p, int64_t e, int64_t n, uint2 w)
+template <bool FULL = false> __device__ __forceinline__ void store4(uint16_t *p, int64_t e, int64_t n, uint2 w)
 {
-    if (e + 4 <= n) {
-        *reinterpret_cast<uint2 *>(p + e) = w;
+    if (FULL || e + 4 <= n) {
+        __stcs(reinterpret_cast<uint2 *>(p + e), w);
     } else {
         if (e < n)
             p[e] = static_cast<uint16_t>(w.x);
@@ -207,55 +210,52 @@ __device__ __forceinline__ float squares(const grad_tensor &d, int64_t base)
 // Sum of squares of a CTA's chunks, into partial[blockIdx.x].
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<grad_tensor, MAX> t,
-                                                        double *partial)
+                                                        TwoPart *partial)
 {
-    __shared__ double part[kThreads / 32];
+    __shared__ TwoPart part[kThreads / 32];
     pdl_wait();
-    double sum = 0.0;
+    TwoPart sum;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, chunks = t.first[t.count];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
         const int i = tensor_of(t, c);
         const grad_tensor &d = t.tensor[i];
         const int64_t base = static_cast<int64_t>(c - t.first[i]) * kNormChunk;
         if (base + kNormChunk <= d.n) {
-            sum += squares(d, base);
+            sum.add(squares(d, base));
             continue;
         }
         for (int64_t e = base + threadIdx.x * 4; e < d.n; e += kThreads * 4) {
             const float4 g = load_grad(d.grad, d.grad_scale, d.grad_type, e, d.n);
-            sum += fmaf(g.x, g.x, fmaf(g.y, g.y, fmaf(g.z, g.z, g.w * g.w)));
+            sum.add(fmaf(g.x, g.x, fmaf(g.y, g.y, fmaf(g.z, g.z, g.w * g.w))));
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(~0u, sum, o);
+    sum.add_lanes();
     if (lane == 0)
         part[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < kThreads / 32; ++w)
-            sum += part[w];
+            sum.add(part[w]);
         partial[blockIdx.x] = sum;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) norm_total_kernel(const double *partial, int n, float scale, float *norm)
+__global__ void __launch_bounds__(1024) norm_total_kernel(const TwoPart *partial, int n, float scale, float *norm)
 {
-    __shared__ double part[kThreads / 32];
+    __shared__ TwoPart part[32];
     pdl_wait();
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        sum += partial[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(~0u, sum, o);
+    TwoPart sum;
+    for (int i = threadIdx.x; i < n; i += 1024)
+        sum.add(partial[i]);
+    sum.add_lanes();
     if (threadIdx.x % 32 == 0)
         part[threadIdx.x / 32] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w)
-            sum += part[w];
-        *norm = static_cast<float>(sqrt(sum) * fabsf(scale));
+    if (threadIdx.x < 32) {
+        sum = part[threadIdx.x];
+        sum.add_lanes();
+        if (threadIdx.x == 0)
+            *norm = sqrtf(sum.value()) * fabsf(scale);
     }
 }
 
@@ -309,52 +309,94 @@ __device__ __forceinline__ F4 decoded(uint32_t w)
     return f;
 }
 
-// |x| inv, within 0 .. 448, to an E4M3 code, up with the probability of the
-// rest: rest holds 16 random bits in bits 4 .. 19.  Below 2^-6 E4M3's steps are
-// those of [2^-6, 2^-5), so 2^-6 is added there; the 20 low bits of the sum's
-// fraction are what the code leaves out.
-__device__ __forceinline__ uint32_t code_up(float x, float inv, uint32_t rest)
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    const float y = fminf(fabsf(x) * inv, 448.0f);
-    const bool low = y < 0.015625f;
-    const uint32_t f = __float_as_uint(y + (low ? 0.015625f : 0.0f));
-    return (f + rest + (8u - ((low ? 968u : 960u) << 20))) >> 20;
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
+// A block's states are held as zeros below kLeast (2^-100): their factors would
+// leave fp32's range.  From kMost (2^120) on, and where r holds an Inf or a NaN
+// (their bits are above all others'), both are held as NaN.  m needs no test of
+// its own: what makes it so large or no number makes r infinite or no number.
+constexpr uint32_t kLeast = 0x0D800000u, kMost = 0x7B800000u;
 
-// Largest magnitude of a block held by a warp, as bits (those of an Inf or a
-// NaN are above all others').
-__device__ __forceinline__ uint32_t top_of(const F4 &x)
-{
-    const uint32_t m = 0x7FFFFFFFu;
-    const uint32_t a = max(__float_as_uint(x.a.x) & m, __float_as_uint(x.a.y) & m);
-    const uint32_t b = max(__float_as_uint(x.b.x) & m, __float_as_uint(x.b.y) & m);
-    return __reduce_max_sync(~0u, max(a, b));
-}
-constexpr uint32_t kInf = 0x7F800000u, kLeast = 0x0D800000u;  // kLeast: 2^-100
-
-// A block's codes; ROOT: no signs, and no code of 0 for a value above 0.
-template <bool ROOT>
-__device__ __forceinline__ uint32_t to_codes(const F4 &x, float inv, uint32_t top, const uint32_t (&r)[4])
+// Four values, their magnitudes at most 448, to codes: up with the probability
+// of the rest.  A code is what stands above the 20 low bits of a value's bits; to
+// these are added 16 random bits (rest, in bits 4 .. 19) and a half of the last
+// one, and what remains is an E4M3 value.  (The largest may come out a few units
+// in the last place above 448: it stays 448, as the sum's low bits are at most
+// 0xFFFF8 + 7.)  LOW: there are values below 2^-6, where E4M3's steps are those
+// of [2^-6, 2^-5): 2^-6 is added to those first.  ROOT: no code of 0 for a value
+// above 0.
+template <bool LOW, bool ROOT>
+__device__ __forceinline__ uint32_t to_codes(const F4 &x, const uint32_t (&rest)[4])
 {
     const float v[4] = {x.a.x, x.a.y, x.b.x, x.b.y};
-    uint32_t c[4];
+    float z[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        c[j] = code_up(v[j], inv, (ROOT ? r[j] >> 12 : r[j] << 4) & 0xFFFF0u);
-        if (ROOT)
-            c[j] = max(c[j], min(__float_as_uint(v[j]), 1u));
+        if (LOW) {
+            const float y = fabsf(v[j]), add = y < 0.015625f ? 0.015625f : 0.0f;
+            const float q = __uint_as_float((__float_as_uint(y + add) + rest[j] + 8u) & 0xFFF00000u) - add;
+            z[j] = copysignf(ROOT && v[j] > 0.0f ? fmaxf(q, 0.001953125f) : q, v[j]);
+        } else {
+            z[j] = __uint_as_float((__float_as_uint(v[j]) + rest[j] + 8u) & 0xFFF00000u);
+        }
     }
-    uint32_t w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-    if (!ROOT) {
-        const uint32_t lo = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0073);
-        const uint32_t hi = __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0073);
-        w |= __byte_perm(lo, hi, 0x5410) & 0x80808080u;
+    return f32x4_to_e4m3x4(z[0], z[1], z[2], z[3]);
+}
+
+// A block's new states m and root = sqrt(v) (a lane's four values of each) to
+// codes and multipliers; x: the elements' numbers' hash so far.
+struct Codes {
+    uint32_t m, r;
+    float m_scale, r_scale;
+};
+__device__ __noinline__ Codes unusual_codes(Codes c, F4 y, F4 z, uint4 um, uint4 ur, uint32_t top_m, uint32_t top_r)
+{
+    const uint32_t a[4] = {um.x, um.y, um.z, um.w}, b[4] = {ur.x, ur.y, ur.z, ur.w};
+    c.m = to_codes<true, false>(y, a), c.r = to_codes<true, true>(z, b);
+    if (top_m < kLeast)
+        c.m = 0u, c.m_scale = 1.0f;
+    if (top_r < kLeast)
+        c.r = 0u, c.r_scale = 1.0f;
+    if (top_r >= kMost || top_m >= kMost)
+        c.m = c.r = 0x7F7F7F7Fu, c.m_scale = c.r_scale = 1.0f;
+    return c;
+}
+__device__ __forceinline__ Codes to_codes(const F4 &m, const F4 &root, uint32_t x0, uint32_t key)
+{
+    const uint32_t top_m = __reduce_max_sync(
+        ~0u, __float_as_uint(fmaxf(fmaxf(fabsf(m.a.x), fabsf(m.a.y)), fmaxf(fabsf(m.b.x), fabsf(m.b.y)))));
+    const uint32_t top_r = __reduce_max_sync(
+        ~0u, __float_as_uint(max_nan(max_nan(root.a.x, root.a.y), max_nan(root.b.x, root.b.y))));
+    const float inv_m = 448.0f * inverse(__uint_as_float(top_m)), inv_r = 448.0f * inverse(__uint_as_float(top_r));
+    const F4 y = {m.a * both(inv_m), m.b * both(inv_m)}, z = {root.a * both(inv_r), root.b * both(inv_r)};
+    // the last shift of the hash h: u = low half of h ^ h >> 16 for m, high half for r
+    uint32_t um[4], ur[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t x = x0 + j * 0x13198A2Fu;
+        uint32_t h = (x ^ (x >> 16) ^ key) * 0x9E3779B1u;
+        h = (h ^ (h >> 15)) * 0x85A308D3u;
+        ur[j] = (h >> 12) & 0xFFFF0u;
+        um[j] = ((h >> 12) ^ (h << 4)) & 0xFFFF0u;
     }
-    return top >= kInf ? 0x7F7F7F7Fu : top < kLeast ? 0u : w;
+    Codes c;
+    c.m_scale = __uint_as_float(top_m) * (1.0f / 448.0f), c.r_scale = __uint_as_float(top_r) * (1.0f / 448.0f);
+    const float least = fminf(fminf(fminf(fabsf(y.a.x), fabsf(y.a.y)), fminf(fabsf(y.b.x), fabsf(y.b.y))),
+                              fminf(fminf(z.a.x, z.a.y), fminf(z.b.x, z.b.y)));
+    const bool usual = top_m >= kLeast && top_r >= kLeast && top_r < kMost;
+    if (__any_sync(~0u, !(least >= 0.015625f)) || !usual)
+        return unusual_codes(c, y, z, make_uint4(um[0], um[1], um[2], um[3]),
+                             make_uint4(ur[0], ur[1], ur[2], ur[3]), top_m, top_r);
+    c.m = to_codes<false, false>(y, um), c.r = to_codes<false, true>(z, ur);
+    return c;
 }
 
 struct Update {
-    float gs, fix2, eps, b1, b2, a1, a2, decay, rate;
+    float gs, fix2, eps, b1, b2, a1, a2, minus_decay, minus_rate;
 };
 
 __device__ __forceinline__ float2 updated(float2 p, float2 g, float2 &m, float2 &v, float2 &root, const Update &h)
@@ -364,113 +406,121 @@ __device__ __forceinline__ float2 updated(float2 p, float2 g, float2 &m, float2 
     root = make_float2(root_of(v.x), root_of(v.y));
     const float2 d = fma2(root, both(h.fix2), both(h.eps));
     const float2 u = m * make_float2(inverse(d.x), inverse(d.y));
-    const float2 t = fma2(both(h.rate), u, both(h.decay) * p);
-    return __fadd2_rn(p, make_float2(-t.x, -t.y));
+    return __fadd2_rn(p, fma2(both(h.minus_rate), u, both(h.minus_decay) * p));
 }
 
-// A warp's four blocks of tensor d, from element `base` on.  All loads are
-// issued first; the blocks' multipliers are loaded, inverted and stored by a
-// lane each (0 .. 3: m, 4 .. 7: r, 8 .. 11: the gradient's).
+// The memory of a warp's blocks on their way: weights, m, v, gradients, in this
+// order.
+template <bool BITS8> struct Slot {
+    static constexpr int blocks = BITS8 ? 4 : 2, values = 128 * blocks;
+    static constexpr int slots = 2;  // of a warp: one in use, one on its way
+    static constexpr int state = (BITS8 ? 1 : 4) * values;
+    static constexpr int m = 4 * values, v = m + state, grad = v + state;
+};
+__host__ __device__ __forceinline__ int grad_size(int type)
+{
+    return type == TACO_GRAD_F32 ? 4 : type == TACO_GRAD_BF16 ? 2 : 1;
+}
+
+// One block of 128 from what a lane has of it: new weights and states, stored
+// at element e = block + 4 lane of n.
+template <bool BITS8, bool FULL>
+__device__ __forceinline__ void update_block(const adamw_tensor &d, int64_t block, const Update &h, uint32_t key, F4 p,
+                                             F4 g, F4 m, F4 v)
+{
+    const int lane = threadIdx.x % 32;
+    const int64_t n = d.n, e = block + lane * 4;
+    F4 root;
+    p.a = updated(p.a, g.a, m.a, v.a, root.a, h);
+    p.b = updated(p.b, g.b, m.b, v.b, root.b, h);
+    store4<FULL>(d.param, e, n, make_float4(p.a.x, p.a.y, p.b.x, p.b.y));
+    if (d.copy_bf16)
+        store4<FULL>(static_cast<uint16_t *>(d.copy_bf16), e, n,
+                     make_uint2(f32x2_to_bf16x2(p.a.x, p.a.y), f32x2_to_bf16x2(p.b.x, p.b.y)));
+    if (!BITS8) {
+        store4<FULL>(static_cast<float *>(d.m), e, n, make_float4(m.a.x, m.a.y, m.b.x, m.b.y));
+        store4<FULL>(static_cast<float *>(d.v), e, n, make_float4(v.a.x, v.a.y, v.b.x, v.b.y));
+        return;
+    }
+    // (key: key ^ key >> 16, so that the hash's first shift is taken of the number alone)
+    const Codes c = to_codes(m, root, static_cast<uint32_t>(e) * 0x13198A2Fu, key);
+    store4<FULL>(static_cast<uint8_t *>(d.m), e, n, c.m);
+    store4<FULL>(static_cast<uint8_t *>(d.v), e, n, c.r);
+    if (lane == 0) {
+        d.m_scale[block / 128] = c.m_scale;
+        d.v_scale[block / 128] = c.r_scale;
+    }
+}
+
+__device__ __forceinline__ F4 times(const F4 &x, float s) { return {x.a * both(s), x.b * both(s)}; }
+__device__ __forceinline__ F4 squared(const F4 &x) { return {x.a * x.a, x.b * x.b}; }
+__device__ __forceinline__ F4 from_bf16(uint2 w)
+{
+    return {make_float2(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x)), make_float2(bf16lo_to_f32(w.y), bf16hi_to_f32(w.y))};
+}
+template <typename T> __device__ __forceinline__ T shared_at(uint32_t at);
+template <> __device__ __forceinline__ float4 shared_at<float4>(uint32_t at)
+{
+    const uint4 v = lds128(at);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <> __device__ __forceinline__ uint2 shared_at<uint2>(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+template <> __device__ __forceinline__ uint32_t shared_at<uint32_t>(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+
+// The end of a tensor: blocks that are not all there, straight from memory.
 template <bool BITS8>
-__device__ __forceinline__ void update_blocks(const adamw_tensor &d, int64_t base, const Update &h, uint32_t key)
+__device__ __noinline__ void update_tail(const adamw_tensor &d, int64_t base, const Update &h, uint32_t key)
 {
     const int lane = threadIdx.x % 32;
     const int64_t n = d.n;
-    F4 g[kBlocks], p[kBlocks], m[kBlocks], v[kBlocks];
-    uint32_t mc[kBlocks], vc[kBlocks];
-    float scale = 1.0f;
-    float *const scales = lane < kBlocks ? d.m_scale : d.v_scale;
-    const int64_t mine = base / 128 + lane % kBlocks;
-    const bool exists = mine * 128 < n;
-    if (BITS8 && lane < 2 * kBlocks && exists)
-        scale = scales[mine];
-    if (d.grad_type == TACO_GRAD_FP8 && lane / kBlocks == 2 && exists)
-        scale = d.grad_scale[mine];
-#pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-        const int64_t e = base + u * 128 + lane * 4;
-        p[u] = f4(load4(d.param, e, n));
+#pragma unroll 1
+    for (int64_t block = base; block < n && block < base + Slot<BITS8>::values; block += 128) {
+        const int64_t e = block + lane * 4;
+        const F4 g = f4(load_grad(d.grad, d.grad_scale, d.grad_type, e, n));
+        F4 m, v;
         if (BITS8) {
-            mc[u] = load4(static_cast<const uint8_t *>(d.m), e, n);
-            vc[u] = load4(static_cast<const uint8_t *>(d.v), e, n);
+            m = times(decoded(load4(static_cast<const uint8_t *>(d.m), e, n)), d.m_scale[block / 128]);
+            v = squared(times(decoded(load4(static_cast<const uint8_t *>(d.v), e, n)), d.v_scale[block / 128]));
         } else {
-            m[u] = f4(load4(static_cast<const float *>(d.m), e, n));
-            v[u] = f4(load4(static_cast<const float *>(d.v), e, n));
+            m = f4(load4(static_cast<const float *>(d.m), e, n));
+            v = f4(load4(static_cast<const float *>(d.v), e, n));
         }
-    }
-    if (d.grad_type == TACO_GRAD_FP8) {
-        uint32_t gc[kBlocks];
-#pragma unroll
-        for (int u = 0; u < kBlocks; ++u)
-            gc[u] = load4(static_cast<const uint8_t *>(d.grad), base + u * 128 + lane * 4, n);
-#pragma unroll
-        for (int u = 0; u < kBlocks; ++u) {
-            const float2 s = both(__shfl_sync(~0u, scale, 2 * kBlocks + u));
-            const F4 c = decoded(gc[u]);
-            g[u] = {c.a * s, c.b * s};
-        }
-    } else if (d.grad_type == TACO_GRAD_BF16) {
-#pragma unroll
-        for (int u = 0; u < kBlocks; ++u) {
-            const uint2 w = load4(static_cast<const uint16_t *>(d.grad), base + u * 128 + lane * 4, n);
-            g[u] = {make_float2(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x)),
-                    make_float2(bf16lo_to_f32(w.y), bf16hi_to_f32(w.y))};
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < kBlocks; ++u)
-            g[u] = f4(load4(static_cast<const float *>(d.grad), base + u * 128 + lane * 4, n));
-    }
-    F4 root[kBlocks];
-    uint32_t top = 0, tops[2 * kBlocks];
-#pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-        const int64_t e = base + u * 128 + lane * 4;
-        if (BITS8) {
-            const float2 ms = both(__shfl_sync(~0u, scale, u)), vs = both(__shfl_sync(~0u, scale, kBlocks + u));
-            m[u] = decoded(mc[u]), v[u] = decoded(vc[u]);
-            m[u] = {m[u].a * ms, m[u].b * ms}, v[u] = {v[u].a * vs, v[u].b * vs};
-            v[u] = {v[u].a * v[u].a, v[u].b * v[u].b};
-        }
-        g[u] = {g[u].a * both(h.gs), g[u].b * both(h.gs)};
-        p[u].a = updated(p[u].a, g[u].a, m[u].a, v[u].a, root[u].a, h);
-        p[u].b = updated(p[u].b, g[u].b, m[u].b, v[u].b, root[u].b, h);
-        store4(d.param, e, n, make_float4(p[u].a.x, p[u].a.y, p[u].b.x, p[u].b.y));
-        if (d.copy_bf16)
-            store4(static_cast<uint16_t *>(d.copy_bf16), e, n,
-                   make_uint2(f32x2_to_bf16x2(p[u].a.x, p[u].a.y), f32x2_to_bf16x2(p[u].b.x, p[u].b.y)));
-        if (!BITS8) {
-            store4(static_cast<float *>(d.m), e, n, make_float4(m[u].a.x, m[u].a.y, m[u].b.x, m[u].b.y));
-            store4(static_cast<float *>(d.v), e, n, make_float4(v[u].a.x, v[u].a.y, v[u].b.x, v[u].b.y));
-        } else {
-            tops[u] = top_of(m[u]), tops[kBlocks + u] = top_of(root[u]);
-            top = lane == u ? tops[u] : lane == kBlocks + u ? tops[kBlocks + u] : top;
-        }
-    }
-    if (!BITS8)
-        return;
-    const bool none = top < kLeast, bad = top >= kInf;  // (448 / amax would leave fp32's range)
-    const float inv = none || bad ? 0.0f : 448.0f / __uint_as_float(top);
-    if (lane < 2 * kBlocks && exists)
-        scales[mine] = none || bad ? 1.0f : __uint_as_float(top) / 448.0f;
-#pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-        const int64_t e = base + u * 128 + lane * 4;
-        uint32_t r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            r[j] = mix((static_cast<uint32_t>(e + j) * 0x13198A2Fu) ^ key);
-        store4(static_cast<uint8_t *>(d.m), e, n,
-               to_codes<false>(m[u], __shfl_sync(~0u, inv, u), tops[u], r));
-        store4(static_cast<uint8_t *>(d.v), e, n,
-               to_codes<true>(root[u], __shfl_sync(~0u, inv, kBlocks + u), tops[kBlocks + u], r));
+        update_block<BITS8, false>(d, block, h, key, f4(load4(d.param, e, n)), times(g, h.gs), m, v);
     }
 }
 
+constexpr int kTogether = 4;  // blocks whose instructions are mixed
+
+// Persistent warps take spans of `units` times Slot::values values of a tensor
+// in turn (Table::first counts spans).  A unit's values come by bulk copies into
+// a slot of the warp's own, two units ahead of their use; its blocks'
+// multipliers by a lane each (0 .. 3: m, 4 .. 7: r, 8 .. 11: the gradient's).
 template <bool BITS8, int MAX>
-__global__ void __launch_bounds__(kThreads)
-    adamw_kernel(const __grid_constant__ Table<adamw_tensor, MAX> t, const __grid_constant__ Hyper hyper)
+__global__ void __launch_bounds__(kThreads, 2)
+    adamw_kernel(const __grid_constant__ Table<adamw_tensor, MAX> t, const __grid_constant__ Hyper hyper, int units,
+                 int slot_bytes)
 {
+    using S = Slot<BITS8>;
+    extern __shared__ __align__(128) uint8_t slots[];
+    __shared__ __align__(8) uint64_t bars[kThreads / 32 * S::slots];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, spans = t.first[t.count];
+    const uint32_t slot = smem_u32(slots) + warp * S::slots * slot_bytes, bar = smem_u32(bars + warp * S::slots);
+    if (lane == 0) {
+        for (int i = 0; i < S::slots; ++i)
+            mbar_init(bar + 8 * i, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
     pdl_wait();
     const AdamWStep &s = hyper.h;
     const uint64_t steps = static_cast<uint64_t>(s.state[0]);
@@ -483,27 +533,116 @@ __global__ void __launch_bounds__(kThreads)
         if (s.max_norm > 0.0f)
             h.gs *= fminf(s.max_norm / (norm + 1e-6f), 1.0f);
     }
+    // the next unit to fetch: tensor -1 behind the last.  The last span comes
+    // first: the norm has just read its gradients
+    int span = blockIdx.x * (kThreads / 32) + warp, next_left = 0, next_tensor = -1;
+    int64_t next_base = 0;
+    const auto locate = [&] {
+        next_tensor = -1;
+        if (span >= spans)
+            return;
+        const int at = spans - 1 - span;
+        next_tensor = tensor_of(t, at);
+        next_base = static_cast<int64_t>(at - t.first[next_tensor]) * units * S::values;
+        const int64_t rest = (t.tensor[next_tensor].n - next_base + S::values - 1) / S::values;
+        next_left = rest < units ? static_cast<int>(rest) : units;
+        span += gridDim.x * (kThreads / 32);
+    };
+    struct Unit {
+        int tensor;
+        int64_t base;
+        float scale;
+    } unit, ahead[S::slots - 1];  // the one to update, and those behind it
+    const uint64_t once = policy_evict_first();
+    const auto fetch = [&](Unit &at, int i) {
+        if (next_left == 0)
+            locate();
+        at.tensor = next_tensor, at.base = next_base;
+        if (next_tensor < 0)
+            return;
+        --next_left, next_base += S::values;
+        const adamw_tensor &d = t.tensor[at.tensor];
+        if (at.base + S::values > d.n)
+            return;
+        if (lane == 0) {
+            const uint32_t to = slot + i * slot_bytes, b = bar + 8 * i, gb = grad_size(d.grad_type);
+            mbar_arrive_expect_tx(b, S::grad + gb * S::values);
+            bulk_load_hint(to, d.param + at.base, 4 * S::values, b, once);
+            bulk_load_hint(to + S::m, static_cast<const uint8_t *>(d.m) + at.base * (BITS8 ? 1 : 4), S::state, b, once);
+            bulk_load_hint(to + S::v, static_cast<const uint8_t *>(d.v) + at.base * (BITS8 ? 1 : 4), S::state, b, once);
+            bulk_load_hint(to + S::grad, static_cast<const uint8_t *>(d.grad) + at.base * gb, gb * S::values, b, once);
+        }
+        if (BITS8 || d.grad_type == TACO_GRAD_FP8) {
+            const float *scales = lane >= 8 ? d.grad_scale : lane >= 4 ? d.v_scale : d.m_scale;
+            if (lane < 12 && lane % 4 < S::blocks && (BITS8 || lane >= 8) && scales)
+                at.scale = scales[at.base / 128 + lane % 4];
+        }
+    };
+    locate();
+    fetch(unit, 0);
+#pragma unroll
+    for (int i = 1; i < S::slots; ++i)
+        fetch(ahead[i - 1], i);
     const float time = static_cast<float>(steps + 1);
-    const float fix1 = -1.0f / expm1f(time * hyper.ln_beta1);
+    const float fix1 = 1.0f / expm1f(time * hyper.ln_beta1);  // -1 / (1 - beta1^t)
     h.fix2 = rsqrtf(-expm1f(time * hyper.ln_beta2));
     h.eps = s.eps, h.b1 = hyper.b1, h.b2 = hyper.b2, h.a1 = hyper.a1, h.a2 = hyper.a2;
+    h.minus_decay = h.minus_rate = 0.0f;
     const float factor = s.lr_factor ? *s.lr_factor : 1.0f;
-    const int chunks = t.first[t.count];
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int i = tensor_of(t, c);
-        const adamw_tensor &d = t.tensor[i];
-        const int64_t base = static_cast<int64_t>(c - t.first[i]) * kChunk + threadIdx.x / 32 * (kBlocks * 128);
-        if (base >= d.n)
-            continue;
-        const float lr = d.lr * factor;
-        h.decay = lr * d.weight_decay, h.rate = lr * fix1;
-        uint32_t key = 0;
-        if (BITS8) {
-            key = mix(mix(hyper.key ^ static_cast<uint32_t>(steps)) ^ static_cast<uint32_t>(hyper.first_tensor + i));
-            if (base >> 32)
-                key = mix(key ^ static_cast<uint32_t>(base >> 32));
+    const uint32_t step_key = mix(hyper.key ^ static_cast<uint32_t>(steps));
+    uint32_t phases = 0, key = 0, high = 0;
+    int tensor = -1;  // that h and key are of, as is the numbers' high word
+    adamw_tensor d;
+    for (int i = 0; unit.tensor >= 0;) {
+        const Unit at = unit;
+        if (at.tensor != tensor)
+            d = t.tensor[at.tensor];
+        if (at.tensor != tensor || static_cast<uint32_t>(at.base >> 32) != high) {
+            tensor = at.tensor, high = static_cast<uint32_t>(at.base >> 32);
+            const float lr = d.lr * factor;
+            h.minus_decay = -lr * d.weight_decay, h.minus_rate = lr * fix1;
+            key = mix(step_key ^ static_cast<uint32_t>(hyper.first_tensor + tensor));
+            if (high)
+                key = mix(key ^ high);
+            key ^= key >> 16;
         }
-        update_blocks<BITS8>(d, base, h, key);
+        if (at.base + S::values <= d.n) {
+            if (!mbar_sleep<false>(bar + 8 * i, phases >> i & 1) && lane == 0)
+                atomicOr(&g_adamw_error, kErrAdamW);
+            phases ^= 1u << i;
+            const uint32_t from = slot + i * slot_bytes, four = lane * 4;
+#pragma unroll kTogether
+            for (int u = 0; u < S::blocks; ++u) {
+                const uint32_t k = u * 128 + four;
+                F4 g, m, v;
+                if (d.grad_type == TACO_GRAD_FP8)
+                    g = times(decoded(shared_at<uint32_t>(from + S::grad + k)),
+                              __shfl_sync(~0u, at.scale, 8 + u) * h.gs);
+                else if (d.grad_type == TACO_GRAD_BF16)
+                    g = times(from_bf16(shared_at<uint2>(from + S::grad + 2 * k)), h.gs);
+                else
+                    g = times(f4(shared_at<float4>(from + S::grad + 4 * k)), h.gs);
+                if (BITS8) {
+                    m = times(decoded(shared_at<uint32_t>(from + S::m + k)), __shfl_sync(~0u, at.scale, u));
+                    v = squared(times(decoded(shared_at<uint32_t>(from + S::v + k)),
+                                      __shfl_sync(~0u, at.scale, 4 + u)));
+                } else {
+                    m = f4(shared_at<float4>(from + S::m + 4 * k));
+                    v = f4(shared_at<float4>(from + S::v + 4 * k));
+                }
+                update_block<BITS8, true>(d, at.base + u * 128, h, key, f4(shared_at<float4>(from + 4 * k)), g, m,
+                                          v);
+            }
+            __syncwarp();
+        } else {
+            update_tail<BITS8>(d, at.base, h, key);
+        }
+        unit = ahead[0];
+#pragma unroll
+        for (int j = 2; j < S::slots; ++j)
+            ahead[j - 2] = ahead[j - 1];
+        fetch(ahead[S::slots - 2], i);
+        i = i + 1 < S::slots ? i + 1 : 0;
     }
     // the last CTA of the step counts it: every CTA has read the count by then
     if (hyper.last) {
@@ -531,13 +670,13 @@ template <typename D, int MAX> int fill(Table<D, MAX> &t, const D *tensors, int6
     return static_cast<int>(at);
 }
 
-template <typename K> cudaError_t resident(K kernel, int *grid)
+template <typename K> cudaError_t resident(K kernel, size_t smem, int *grid)
 {
     DeviceInfo di;
     cudaError_t e = current_device_info(&di);
     int per_sm = 0;
     if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
     *grid = di.num_sms * (per_sm < 1 ? 1 : per_sm);
     return e;
 }
@@ -545,12 +684,12 @@ template <typename K> cudaError_t resident(K kernel, int *grid)
 constexpr int kNormGrid = 2048;  // partial sums of a launch (at most)
 
 template <int MAX>
-cudaError_t norm_launch(const grad_tensor *tensors, int64_t count, double *partial, int *used, cudaStream_t stream)
+cudaError_t norm_launch(const grad_tensor *tensors, int64_t count, TwoPart *partial, int *used, cudaStream_t stream)
 {
     Table<grad_tensor, MAX> t;
     const int chunks = fill(t, tensors, count, kNormChunk);
     int grid = 0;
-    cudaError_t e = resident(norm_kernel<MAX>, &grid);
+    cudaError_t e = resident(norm_kernel<MAX>, 0, &grid);
     if (e != cudaSuccess)
         return e;
     grid = grid < kNormGrid ? grid : kNormGrid;
@@ -562,14 +701,36 @@ cudaError_t norm_launch(const grad_tensor *tensors, int64_t count, double *parti
 template <bool BITS8, int MAX>
 cudaError_t adamw_launch(const adamw_tensor *tensors, int64_t count, const Hyper &h, cudaStream_t stream)
 {
-    Table<adamw_tensor, MAX> t;
-    const int chunks = fill(t, tensors, count, kChunk);
-    int grid = 0;
-    cudaError_t e = resident(adamw_kernel<BITS8, MAX>, &grid);
+    constexpr int kValues = Slot<BITS8>::values;
+    int size = 1;
+    for (int64_t i = 0; i < count; ++i)
+        size = tensors[i].n > 0 && grad_size(tensors[i].grad_type) > size ? grad_size(tensors[i].grad_type) : size;
+    const int slot = Slot<BITS8>::grad + size * Slot<BITS8>::values;
+    const size_t smem = static_cast<size_t>(kThreads / 32) * Slot<BITS8>::slots * slot;
+    const auto kernel = adamw_kernel<BITS8, MAX>;
+    DeviceInfo di;
+    cudaError_t e = current_device_info(&di);
     if (e != cudaSuccess)
         return e;
-    grid = grid < chunks ? grid : chunks < 1 ? 1 : chunks;
-    return launch_pdl(adamw_kernel<BITS8, MAX>, grid, kThreads, 0, stream, t, h);
+    static std::atomic<bool> done[kMaxDevices];
+    if ((e = ensure_smem(kernel, kThreads / 32 * Slot<BITS8>::slots * (Slot<BITS8>::grad + 4 * Slot<BITS8>::values), di.device,
+                         done)) != cudaSuccess)
+        return e;
+    int grid = 0;
+    if ((e = resident(kernel, smem, &grid)) != cudaSuccess)
+        return e;
+    // spans as long as leave every warp four of them: looking one up costs as much
+    // as a quarter of a unit
+    int64_t units = 0;
+    for (int64_t i = 0; i < count; ++i)
+        units += (tensors[i].n + kValues - 1) / kValues;
+    const int64_t each = units / (4 * (kThreads / 32) * static_cast<int64_t>(grid));
+    const int span = each < 1 ? 1 : each > 16 ? 16 : static_cast<int>(each);
+    Table<adamw_tensor, MAX> t;
+    const int spans = fill(t, tensors, count, kValues * span);
+    const int need = (spans + kThreads / 32 - 1) / (kThreads / 32);
+    grid = grid < need ? grid : need < 1 ? 1 : need;
+    return launch_pdl(kernel, grid, kThreads, smem, stream, t, h, span, slot);
 }
 
 }  // namespace
@@ -578,14 +739,14 @@ int grad_norm_launches(int64_t count) { return static_cast<int>((count + kNormTe
 
 cudaError_t grad_norm_workspace(int64_t count, uint64_t *bytes)
 {
-    *bytes = static_cast<uint64_t>(grad_norm_launches(count)) * kNormGrid * sizeof(double);
+    *bytes = static_cast<uint64_t>(grad_norm_launches(count)) * kNormGrid * sizeof(TwoPart);
     return cudaSuccess;
 }
 
 cudaError_t launch_grad_norm(const grad_tensor *tensors, int64_t count, float grad_scale, float *norm,
                              void *workspace, cudaStream_t stream)
 {
-    double *partial = static_cast<double *>(workspace);
+    TwoPart *partial = static_cast<TwoPart *>(workspace);
     int total = 0;
     for (int64_t i = 0; i < count; i += kNormTensors) {
         const int64_t n = count - i < kNormTensors ? count - i : kNormTensors;
@@ -596,7 +757,7 @@ cudaError_t launch_grad_norm(const grad_tensor *tensors, int64_t count, float gr
             return e;
         total += used;
     }
-    return launch_pdl(norm_total_kernel, 1, kThreads, 0, stream, static_cast<const double *>(partial), total,
+    return launch_pdl(norm_total_kernel, 1, 1024, 0, stream, static_cast<const TwoPart *>(partial), total,
                       grad_scale, norm);
 }
 
@@ -627,6 +788,20 @@ cudaError_t launch_adamw(const adamw_tensor *tensors, int64_t count, bool bits8,
         i += n;
     } while (i < count);
     return cudaSuccess;
+}
+
+cudaError_t read_adamw_error(uint32_t *flags, bool clear)
+{
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_adamw_error, sizeof v);
+    if (e != cudaSuccess)
+        return e;
+    *flags = v;
+    if (clear && v) {
+        v = 0;
+        e = cudaMemcpyToSymbol(g_adamw_error, &v, sizeof v);
+    }
+    return e;
 }
 
 }  // namespace taco

@@ -131,6 +131,37 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
+// mbar_wait with a hint that lets the warp sleep until the phase completes, for
+// kernels all of whose warps wait for memory (in the policy loss polling took a
+// tenth of the instructions).  CLUSTER: for what other CTAs have stored.
+template <bool CLUSTER> __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity)
+{
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        if (CLUSTER)
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok)
+                         : "r"(bar), "r"(parity), "r"(10000000u)
+                         : "memory");
+        else
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok)
+                         : "r"(bar), "r"(parity), "r"(10000000u)
+                         : "memory");
+        if (ok)
+            return true;
+        const uint64_t t = global_timer_ns();
+        t0 = t0 ? t0 : t;
+        if (t - t0 > kWaitLimitNs)
+            return false;
+    }
+}
+
 // ------------------------------------------------------------------- TMA --
 
 // Copies `bytes` contiguous bytes (a multiple of 16, both addresses 16-byte
@@ -139,6 +170,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// The same with an L2 cache policy.
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t pol)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar), "l"(pol)
                  : "memory");
 }
 
@@ -268,6 +308,38 @@ __device__ __forceinline__ float2 add2_rounded(float2 a, float2 b)
 {
     return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
+
+// ------------------------------------------------------------ long sums --
+
+// A sum in two fp32 parts: what each addition rounds off is kept (Knuth's
+// two-sum).  As exact as fp64 for sums of some thousand terms, which the fp64
+// units would take ten times as long for.
+struct TwoPart {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float t = __fadd_rn(hi, x), b = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
+        hi = t;
+    }
+    __device__ __forceinline__ void add(const TwoPart &x)
+    {
+        add(x.hi);
+        lo += x.lo;
+    }
+    __device__ __forceinline__ void add_lanes()  // of a warp: in all of them
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            TwoPart x;
+            x.hi = __shfl_xor_sync(~0u, hi, o);
+            x.lo = __shfl_xor_sync(~0u, lo, o);
+            add(x);
+        }
+    }
+    // A sum that has left fp32's range, or of something that is no number, is hi.
+    __device__ __forceinline__ float value() const { return fabsf(hi) <= 3.4028234e38f ? hi + lo : hi; }
+};
 
 // ----------------------------------------------------------- conversions --
 

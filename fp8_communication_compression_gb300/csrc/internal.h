@@ -206,6 +206,7 @@ cudaError_t read_gemm_error(uint32_t *flags, bool clear);
 cudaError_t read_fp8_error(uint32_t *flags, bool clear);
 cudaError_t read_norm_error(uint32_t *flags, bool clear);
 cudaError_t read_loss_error(uint32_t *flags, bool clear);
+cudaError_t read_adamw_error(uint32_t *flags, bool clear);
 
 // Raises a kernel's dynamic shared-memory limit once per device.  The flag
 // is atomic because host threads may make their first launch concurrently;

@@ -554,37 +554,6 @@ __device__ __forceinline__ void send(Sum *to, uint64_t *bar, uint32_t rank, Sum 
                  : "memory");
 }
 
-// mbar_wait with a hint that lets the warp sleep until the phase completes (a
-// row's warps wait for memory most of the time; polling took a third of the
-// issue slots).  CLUSTER: for what other CTAs of the cluster have stored.
-template <bool CLUSTER> __device__ __forceinline__ bool sleep_until(uint32_t bar, uint32_t parity)
-{
-    uint64_t t0 = 0;
-    for (;;) {
-        uint32_t ok;
-        if (CLUSTER)
-            asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                         "selp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(ok)
-                         : "r"(bar), "r"(parity), "r"(10000000u)
-                         : "memory");
-        else
-            asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                         "selp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(ok)
-                         : "r"(bar), "r"(parity), "r"(10000000u)
-                         : "memory");
-        if (ok)
-            return true;
-        const uint64_t t = global_timer_ns();
-        t0 = t0 ? t0 : t;
-        if (t - t0 > kWaitLimitNs)
-            return false;
-    }
-}
-
 // A warp's lines of a row's interior.
 template <typename E> struct Lines {
     int from, to;  // lines
@@ -680,7 +649,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2)
             for (int j = 0; j < l.to - l.from; j += kGroup) {
                 if (j % kLines == 0) {
                     const int i = j / kLines;
-                    if (!sleep_until<false>(smem_u32(&bar[i]), phases >> i & 1) && lane == 0)
+                    if (!mbar_sleep<false>(smem_u32(&bar[i]), phases >> i & 1) && lane == 0)
                         atomicOr(&g_loss_error, kErrLoss);
                     phases ^= 1u << i;
                 }
@@ -707,7 +676,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2)
                 __syncwarp();
                 if (lane < parts)
                     send(&to[my], &sums_bar[turn & 1], lane, z);
-                if (!sleep_until<true>(smem_u32(&sums_bar[turn & 1]), turn >> 1 & 1) && lane == 0)
+                if (!mbar_sleep<true>(smem_u32(&sums_bar[turn & 1]), turn >> 1 & 1) && lane == 0)
                     atomicOr(&g_loss_error, kErrLoss);
             } else {
                 if (lane == 0)
@@ -785,7 +754,9 @@ __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ L
         pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, threads = blockDim.x, rank = blockIdx.x % parts;
-    const int64_t row = blockIdx.x / parts;
+    // from the last row on: L2 holds what the forward pass or a product has
+    // touched last
+    const int64_t row = a.T - 1 - blockIdx.x / parts;
     const Row<E> x(a, row);
     const int target = token(a, row);
     const float weight = a.dlogp[row];
@@ -822,41 +793,33 @@ __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ L
             d.edge(k, zero);
 }
 
-// Sum over a CTA of 1024 threads in a fixed order, in all threads.
-__device__ double block_sum(double v, double *part)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(~0u, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w)
-        v += part[w];
-    return v;
-}
-
 // out = scale * sum of x: one CTA, in a fixed order.
 __global__ void __launch_bounds__(1024) total_kernel(const float *x, int64_t n, float scale, float *out)
 {
-    __shared__ double part[32];
+    __shared__ TwoPart part[32];
     pdl_wait();
-    double v = 0.0;
+    TwoPart v;
     for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
-        v += x[i];
-    v = block_sum(v, part);
-    if (threadIdx.x == 0)
-        *out = static_cast<float>(v * scale);
+        v.add(x[i]);
+    v.add_lanes();
+    if (threadIdx.x % 32 == 0)
+        part[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        v = part[threadIdx.x];
+        v.add_lanes();
+        if (threadIdx.x == 0)
+            *out = v.value() * scale;
+    }
 }
 
 // One CTA a pair: the sequences' log ratios, the pair's loss, and the
-// gradients at its tokens' log probabilities.  The sums are fp64: the margin is
-// a small difference of long sums.
+// gradients at its tokens' log probabilities.  The sums are in two parts: the
+// margin is a small difference of long ones.
 __global__ void __launch_bounds__(256) pair_kernel(const PairArgs a)
 {
-    __shared__ double part[32];
+    __shared__ TwoPart part[2][8];
+    __shared__ int counts[2][8];
     pdl_wait();
     const int64_t pair = blockIdx.x;
     int64_t at[3];
@@ -864,32 +827,54 @@ __global__ void __launch_bounds__(256) pair_kernel(const PairArgs a)
         const int64_t o = a.offsets[2 * pair + i];
         at[i] = o < 0 ? 0 : o > a.T ? a.T : o;
     }
-    double ratio[2], count[2];
+#pragma unroll
     for (int i = 0; i < 2; ++i) {
-        double s = 0.0, n = 0.0;
+        TwoPart s;
+        int n = 0;
         for (int64_t t = at[i] + threadIdx.x; t < at[i + 1]; t += blockDim.x)
             if (a.targets[t] >= 0) {
-                s += static_cast<double>(a.logp[t]) - (a.ref_logp ? a.ref_logp[t] : 0.0f);
-                n += 1.0;
+                s.add(a.logp[t]);
+                if (a.ref_logp)
+                    s.add(-a.ref_logp[t]);
+                ++n;
             }
-        ratio[i] = block_sum(s, part);
-        count[i] = a.mean ? fmax(block_sum(n, part), 1.0) : 1.0;
-        ratio[i] /= count[i];
+        s.add_lanes();
+        n = __reduce_add_sync(~0u, n);
+        if (threadIdx.x % 32 == 0)
+            part[i][threadIdx.x / 32] = s, counts[i][threadIdx.x / 32] = n;
     }
-    const float z = static_cast<float>(a.beta * (ratio[0] - ratio[1]));
+    __syncthreads();
+    float ratio[2], count[2];
+    TwoPart gap;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        TwoPart s;
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            s.add(part[i][w]);
+            n += counts[i][w];
+        }
+        count[i] = a.mean ? static_cast<float>(n > 0 ? n : 1) : 1.0f;
+        ratio[i] = s.value() / count[i];
+        if (i)
+            s.hi = -s.hi, s.lo = -s.lo;
+        gap.add(s);
+    }
+    const float z = a.beta * (a.mean ? ratio[0] - ratio[1] : gap.value());
     const float e = expf(-fabsf(z)), soft = log1pf(e);  // -log sig(|z|)
     const float down = z >= 0.0f ? soft : soft - z, up = z >= 0.0f ? soft + z : soft;
     const float sig = z >= 0.0f ? 1.0f / (1.0f + e) : e / (1.0f + e);
     const float far = z >= 0.0f ? e / (1.0f + e) : 1.0f / (1.0f + e);  // sig(-z)
     if (threadIdx.x == 0) {
         a.margin[pair] = z;
-        a.logratio[2 * pair] = static_cast<float>(ratio[0]);
-        a.logratio[2 * pair + 1] = static_cast<float>(ratio[1]);
+        a.logratio[2 * pair] = ratio[0];
+        a.logratio[2 * pair + 1] = ratio[1];
         a.pair_loss[pair] = (1.0f - a.smoothing) * down + a.smoothing * up;
     }
     const float slope = (a.smoothing * sig - (1.0f - a.smoothing) * far) * a.beta / static_cast<float>(a.pairs);
     for (int i = 0; i < 2; ++i) {
-        const float g = (i ? -slope : slope) / static_cast<float>(count[i]);
+        const float g = (i ? -slope : slope) / count[i];
         for (int64_t t = at[i] + threadIdx.x; t < at[i + 1]; t += blockDim.x)
             if (a.targets[t] >= 0)
                 a.coef[t] = g;

@@ -1153,14 +1153,15 @@ taco_status taco_device_error(uint32_t *flags_out, int32_t clear)
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess)
         return TACO_ERR_CUDA;
-    uint32_t codec = 0, gemm = 0, fp8 = 0, norm = 0, loss = 0;
+    uint32_t codec = 0, gemm = 0, fp8 = 0, norm = 0, loss = 0, adamw = 0;
     if ((e = taco::read_codec_error(&codec, clear != 0)) != cudaSuccess ||
         (e = taco::read_gemm_error(&gemm, clear != 0)) != cudaSuccess ||
         (e = taco::read_fp8_error(&fp8, clear != 0)) != cudaSuccess ||
         (e = taco::read_norm_error(&norm, clear != 0)) != cudaSuccess ||
-        (e = taco::read_loss_error(&loss, clear != 0)) != cudaSuccess)
+        (e = taco::read_loss_error(&loss, clear != 0)) != cudaSuccess ||
+        (e = taco::read_adamw_error(&adamw, clear != 0)) != cudaSuccess)
         return from_cuda(e);
-    *flags_out = codec | gemm | fp8 | norm | loss;
+    *flags_out = codec | gemm | fp8 | norm | loss | adamw;
     return TACO_OK;
 }
 

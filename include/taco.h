@@ -697,8 +697,8 @@ taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64
  * k = mix(k ^ e >> 32) where that is not 0, h = mix((e * 0x13198A2F) ^ k): u =
  * h's low half for m, its high half for r.  r's code is at least 1 where v is at
  * least 2^-126.
- * m and v are read as code * multiplier and its square; a block with an Inf or
- * a NaN is held as NaN.
+ * m and v are read as code * multiplier and its square; a block with an Inf, a
+ * NaN or a value of 2^120 and more is held as NaN.
  *
  * Pointers are 16-byte aligned, multipliers, norm and lr_factor 4-byte, state
  * 8-byte.  No two tensors of a call may overlap.  0 <= beta < 1, eps at least
@@ -737,7 +737,8 @@ taco_status adamw_step(const adamw_tensor *tensors, int64_t count, int32_t state
  * (bit 0: compressor, bit 1: decompressor, bit 4: taco_watchdog_selftest,
  * bit 5: the GEMMs taco_gemm_compress, agoq_gemm_accumulate and
  * agoq_gemm_laaq_quantize, bit 6: fp8_gemm and the calls built on it, bit 7:
- * rmsnorm_gate_residual and its backward pass, bit 8: policy_loss).
+ * rmsnorm_gate_residual and its backward pass, bit 8: policy_loss, bit 9:
+ * adamw_step).
  * Synchronises the device.  With clear != 0 the flags are reset to 0 after
  * reading.
  */
