@@ -67,8 +67,8 @@ SIGNATURES = {
                                        _P, _P, _P, _P, _P, _P, _U64, _P]),
     "grad_norm_workspace_bytes": (ctypes.c_int, [_I64, _P]),
     "grad_norm": (ctypes.c_int, [_P, _I64, _F32, _P, _P, _U64, _P]),
-    "adamw_step": (ctypes.c_int, [_P, _I64, _I32, ctypes.c_double, ctypes.c_double, _F32, _F32, _P, _F32, _P, _U64,
-                                  _P, _P]),
+    "adamw_step": (ctypes.c_int, [_P, _I64, _I32, ctypes.c_double, ctypes.c_double, _F32, _F32, _F32, _P, _P, _U64,
+                                  _P, _P, _U64, _P]),
     "taco_host_pipeline_create": (ctypes.c_int, [_I32, _I64, _I64, _I32, _I32, _I32,
                                                  ctypes.POINTER(ctypes.c_void_p),
                                                  ctypes.POINTER(ctypes.c_uint64)]),

@@ -965,14 +965,11 @@ def _grad_of(g, name: str, numel: int | None, device: int):
     return g.data_ptr(), scale.data_ptr(), n, kind
 
 
-def _grad_norm(table, count: int, device: torch.device, grad_scale: float, out: torch.Tensor, stream) -> torch.Tensor:
+@functools.lru_cache(maxsize=4096)
+def _norm_partials_bytes(count: int) -> int:
     v = ctypes.c_uint64(0)
-    lib = _lib.load()
-    _lib.check("grad_norm_workspace_bytes", lib.grad_norm_workspace_bytes(count, ctypes.byref(v)))
-    ws = _workspace(v.value, device, stream)
-    st = lib.grad_norm(table, count, grad_scale, out.data_ptr(), ws.data_ptr(), v.value, _stream_of(out, stream))
-    _lib.check("grad_norm", st)
-    return out
+    _lib.check("grad_norm_workspace_bytes", _lib.load().grad_norm_workspace_bytes(count, ctypes.byref(v)))
+    return int(v.value)
 
 
 def grad_norm(grads: Sequence, grad_scale: float = 1.0, stream=None) -> torch.Tensor:
@@ -989,7 +986,12 @@ def grad_norm(grads: Sequence, grad_scale: float = 1.0, stream=None) -> torch.Te
     for i, g in enumerate(grads):
         table[i] = _lib.GradTensor(*_grad_of(g, f"grads[{i}]", None, device))
     out = _new((), torch.float32, first.device, stream)
-    return _grad_norm(table, len(grads), first.device, grad_scale, out, stream)
+    nbytes = _norm_partials_bytes(len(grads))
+    ws = _workspace(nbytes, first.device, stream)
+    st = _lib.load().grad_norm(table, len(grads), grad_scale, out.data_ptr(), ws.data_ptr(), nbytes,
+                               _stream_of(out, stream))
+    _lib.check("grad_norm", st)
+    return out
 
 
 def taco_device_error(clear: bool = True) -> int:

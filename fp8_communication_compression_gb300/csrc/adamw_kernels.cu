@@ -17,7 +17,9 @@
 // m by eps alone in the next step.
 //
 // A launch takes its tensors' descriptions as parameters, so that nothing is
-// copied or kept, and finds the tensor of each chunk by bisection.  Bound by
+// copied or kept.  Warps take spans of the tensors in turn, and find each span's
+// tensor by bisection.  (One long part of all values for each warp, found once,
+// takes 5 % longer: the parts with many tensors' ends finish last.)  Bound by
 // HBM; a lane takes four consecutive elements, a warp one block of 128, whose
 // maximum is one warp reduction.
 
@@ -37,30 +39,56 @@ namespace {
 
 constexpr uint32_t kErrAdamW = 512u;
 constexpr int kThreads = 256;
-constexpr int kNormChunk = kThreads * 64;  // values of a chunk of the norm
+constexpr int kNormUnit = 2048;  // values of the norm's units
 
-// Tensors of a launch; first[i]: the first chunk (or span) of tensor i.
+// Tensors of a launch, in spans of `span` values; first[i]: the first span of
+// tensor i.
 template <typename D, int MAX> struct Table {
     D tensor[MAX];
     int32_t first[MAX + 1];
-    int32_t count;
+    int32_t count, span;
 };
 
-template <typename D, int MAX> __device__ __forceinline__ int tensor_of(const Table<D, MAX> &t, int chunk)
-{
-    int lo = 0, hi = t.count;  // first[lo] <= chunk < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (t.first[mid] <= chunk)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
+// The spans that a warp takes.  LAST_FIRST: from the last one on (the update
+// begins with the gradients that the norm has read last: they are in L2 yet).
+template <typename D, int MAX, bool LAST_FIRST> struct Walk {
+    const Table<D, MAX> &t;
+    int64_t base;       // the next values: those of `tensor` from here on
+    int left;           // units of them in this span
+    int tensor;
+    int span;           // the next span
 
-// Elements e .. e + 3 of n, zeros past the end (FULL: all are there).  What is
-// stored leaves L2 first: nothing reads it in this step.
+    __device__ __forceinline__ Walk(const Table<D, MAX> &table) : t(table), left(0), span(blockIdx.x * (kThreads / 32) + threadIdx.x / 32)
+    {
+    }
+    // The next unit of `values` values, from `base` on: false behind the last.
+    // A following call goes on behind it.
+    __device__ __forceinline__ bool step(int values)
+    {
+        if (--left > 0) {
+            base += values;
+            return true;
+        }
+        if (span >= t.first[t.count])
+            return false;
+        const int at = LAST_FIRST ? t.first[t.count] - 1 - span : span;
+        int lo = 0, hi = t.count;  // first[lo] <= at < first[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (t.first[mid] <= at)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        tensor = lo;
+        base = static_cast<int64_t>(at - t.first[lo]) * t.span;
+        left = static_cast<int>((min(t.tensor[lo].n - base, int64_t(t.span)) + values - 1) / values);
+        span += gridDim.x * (kThreads / 32);
+        return true;
+    }
+};
+
+// Elements e .. e + 3 of n, zeros past the end (FULL: all are there).
 template <bool FULL = false> __device__ __forceinline__ float4 load4(const float *p, int64_t e, int64_t n)
 {
     if (FULL || e + 4 <= n)
@@ -140,22 +168,22 @@ __device__ __forceinline__ float4 load_grad(const void *g, const float *scale, i
 
 // ------------------------------------------------------------------- norm --
 
-__device__ __forceinline__ uint4 ldg16(const void *p) { return ldg128_stream(p); }
+__device__ __forceinline__ uint4 ldg16(const void *p) { return __ldg(static_cast<const uint4 *>(p)); }
 
-// Squares of a thread's 64 values of a whole chunk, in 16-byte loads; at most
-// 32 terms in a row.
+// Squares of a lane's 64 values of a whole unit, in 16-byte loads; at most 32
+// terms in a row.
 __device__ __forceinline__ float squares(const grad_tensor &d, int64_t base)
 {
-    const int tid = threadIdx.x;
+    const int lane = threadIdx.x % 32;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (d.grad_type == TACO_GRAD_FP8) {
-        const uint8_t *p = static_cast<const uint8_t *>(d.grad) + base + tid * 16;
+        const uint8_t *p = static_cast<const uint8_t *>(d.grad) + base + lane * 16;
         uint4 q[4];
         float m[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            q[i] = ldg16(p + i * kThreads * 16);
-            m[i] = __ldg(d.grad_scale + (base + i * kThreads * 16 + tid * 16) / 128);
+            q[i] = ldg16(p + i * 512);
+            m[i] = __ldg(d.grad_scale + base / 128 + i * 4 + lane / 8);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -170,11 +198,11 @@ __device__ __forceinline__ float squares(const grad_tensor &d, int64_t base)
             s[i] = (t.x + t.y) * m[i] * m[i];
         }
     } else if (d.grad_type == TACO_GRAD_BF16) {
-        const uint16_t *p = static_cast<const uint16_t *>(d.grad) + base + tid * 8;
+        const uint16_t *p = static_cast<const uint16_t *>(d.grad) + base + lane * 8;
         uint4 q[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            q[i] = ldg16(p + i * kThreads * 8);
+            q[i] = ldg16(p + i * 256);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
@@ -187,27 +215,26 @@ __device__ __forceinline__ float squares(const grad_tensor &d, int64_t base)
             s[i % 4] = t.x + t.y;
         }
     } else {
-        const float *p = static_cast<const float *>(d.grad) + base + tid * 4;
+        const float *p = static_cast<const float *>(d.grad) + base + lane * 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint4 q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                q[i] = ldg16(p + (h * 8 + i) * kThreads * 4);
+                q[i] = ldg16(p + (h * 8 + i) * 128);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float f[4] = {__uint_as_float(q[i].x), __uint_as_float(q[i].y), __uint_as_float(q[i].z),
-                                    __uint_as_float(q[i].w)};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[j] = fmaf(f[j], f[j], s[j]);
+                s[0] = fmaf(__uint_as_float(q[i].x), __uint_as_float(q[i].x), s[0]);
+                s[1] = fmaf(__uint_as_float(q[i].y), __uint_as_float(q[i].y), s[1]);
+                s[2] = fmaf(__uint_as_float(q[i].z), __uint_as_float(q[i].z), s[2]);
+                s[3] = fmaf(__uint_as_float(q[i].w), __uint_as_float(q[i].w), s[3]);
             }
         }
     }
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// Sum of squares of a CTA's chunks, into partial[blockIdx.x].
+// Sum of squares of a CTA's units, into partial[blockIdx.x].
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<grad_tensor, MAX> t,
                                                         TwoPart *partial)
@@ -215,18 +242,23 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     __shared__ TwoPart part[kThreads / 32];
     pdl_wait();
     TwoPart sum;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, chunks = t.first[t.count];
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int i = tensor_of(t, c);
-        const grad_tensor &d = t.tensor[i];
-        const int64_t base = static_cast<int64_t>(c - t.first[i]) * kNormChunk;
-        if (base + kNormChunk <= d.n) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    Walk<grad_tensor, MAX, false> walk(t);
+    while (walk.step(kNormUnit)) {
+        const int64_t base = walk.base;
+        const grad_tensor &d = t.tensor[walk.tensor];
+        if (base + kNormUnit <= d.n) {
             sum.add(squares(d, base));
             continue;
         }
-        for (int64_t e = base + threadIdx.x * 4; e < d.n; e += kThreads * 4) {
-            const float4 g = load_grad(d.grad, d.grad_scale, d.grad_type, e, d.n);
-            sum.add(fmaf(g.x, g.x, fmaf(g.y, g.y, fmaf(g.z, g.z, g.w * g.w))));
+        for (int64_t e = base + lane * 4; e < d.n; e += 512) {
+            float4 g[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                g[j] = load_grad(d.grad, d.grad_scale, d.grad_type, e + j * 128, d.n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum.add(fmaf(g[j].x, g[j].x, fmaf(g[j].y, g[j].y, fmaf(g[j].z, g[j].z, g[j].w * g[j].w))));
         }
     }
     sum.add_lanes();
@@ -240,23 +272,31 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     }
 }
 
-__global__ void __launch_bounds__(1024) norm_total_kernel(const TwoPart *partial, int n, float scale, float *norm)
+// The norm from n partial sums, in all threads of a CTA of kThreads, in a fixed
+// order.
+__device__ __forceinline__ float norm_of(const TwoPart *partial, int n, float scale)
 {
-    __shared__ TwoPart part[32];
-    pdl_wait();
+    __shared__ TwoPart part[kThreads / 32];
     TwoPart sum;
-    for (int i = threadIdx.x; i < n; i += 1024)
+    for (int i = threadIdx.x; i < n; i += kThreads)
         sum.add(partial[i]);
     sum.add_lanes();
     if (threadIdx.x % 32 == 0)
         part[threadIdx.x / 32] = sum;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        sum = part[threadIdx.x];
-        sum.add_lanes();
-        if (threadIdx.x == 0)
-            *norm = sqrtf(sum.value()) * fabsf(scale);
-    }
+    sum = TwoPart();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+        sum.add(part[w]);
+    return sqrtf(sum.value()) * fabsf(scale);
+}
+
+__global__ void __launch_bounds__(kThreads) norm_total_kernel(const TwoPart *partial, int n, float scale, float *norm)
+{
+    pdl_wait();
+    const float v = norm_of(partial, n, scale);
+    if (threadIdx.x == 0)
+        *norm = v;
 }
 
 // ------------------------------------------------------------------ AdamW --
@@ -273,6 +313,8 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x)
 
 struct Hyper {
     AdamWStep h;
+    const TwoPart *partial;   // of the gradients' squares: `partials` of them, or 0
+    int32_t partials;
     uint32_t key;             // of the seed
     int32_t first_tensor;     // of this launch
     int32_t last;             // the step's last launch counts it
@@ -501,19 +543,17 @@ __device__ __noinline__ void update_tail(const adamw_tensor &d, int64_t base, co
 
 constexpr int kTogether = 4;  // blocks whose instructions are mixed
 
-// Persistent warps take spans of `units` times Slot::values values of a tensor
-// in turn (Table::first counts spans).  A unit's values come by bulk copies into
-// a slot of the warp's own, two units ahead of their use; its blocks'
-// multipliers by a lane each (0 .. 3: m, 4 .. 7: r, 8 .. 11: the gradient's).
+// Persistent warps; a unit's values come by bulk copies into a slot of the
+// warp's own, while the one before is worked on, its blocks' multipliers by a
+// lane each (0 .. 3: m, 4 .. 7: r, 8 .. 11: the gradient's).
 template <bool BITS8, int MAX>
 __global__ void __launch_bounds__(kThreads, 2)
-    adamw_kernel(const __grid_constant__ Table<adamw_tensor, MAX> t, const __grid_constant__ Hyper hyper, int units,
-                 int slot_bytes)
+    adamw_kernel(const __grid_constant__ Table<adamw_tensor, MAX> t, const __grid_constant__ Hyper hyper, int slot_bytes)
 {
     using S = Slot<BITS8>;
     extern __shared__ __align__(128) uint8_t slots[];
     __shared__ __align__(8) uint64_t bars[kThreads / 32 * S::slots];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, spans = t.first[t.count];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t slot = smem_u32(slots) + warp * S::slots * slot_bytes, bar = smem_u32(bars + warp * S::slots);
     if (lane == 0) {
         for (int i = 0; i < S::slots; ++i)
@@ -526,41 +566,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t steps = static_cast<uint64_t>(s.state[0]);
     Update h;
     h.gs = s.grad_scale;
-    if (s.norm) {
-        const float norm = *s.norm;
-        if (!(norm <= FLT_MAX))  // a gradient that is not finite: the step is left out
-            return;
-        if (s.max_norm > 0.0f)
-            h.gs *= fminf(s.max_norm / (norm + 1e-6f), 1.0f);
-    }
-    // the next unit to fetch: tensor -1 behind the last.  The last span comes
-    // first: the norm has just read its gradients
-    int span = blockIdx.x * (kThreads / 32) + warp, next_left = 0, next_tensor = -1;
-    int64_t next_base = 0;
-    const auto locate = [&] {
-        next_tensor = -1;
-        if (span >= spans)
-            return;
-        const int at = spans - 1 - span;
-        next_tensor = tensor_of(t, at);
-        next_base = static_cast<int64_t>(at - t.first[next_tensor]) * units * S::values;
-        const int64_t rest = (t.tensor[next_tensor].n - next_base + S::values - 1) / S::values;
-        next_left = rest < units ? static_cast<int>(rest) : units;
-        span += gridDim.x * (kThreads / 32);
-    };
+    Walk<adamw_tensor, MAX, true> walk(t);
+    const uint64_t once = policy_evict_first();
     struct Unit {
-        int tensor;
+        int tensor;  // -1: behind the last
         int64_t base;
         float scale;
     } unit, ahead[S::slots - 1];  // the one to update, and those behind it
-    const uint64_t once = policy_evict_first();
     const auto fetch = [&](Unit &at, int i) {
-        if (next_left == 0)
-            locate();
-        at.tensor = next_tensor, at.base = next_base;
-        if (next_tensor < 0)
+        at.tensor = -1;
+        if (!walk.step(S::values))
             return;
-        --next_left, next_base += S::values;
+        at.base = walk.base, at.tensor = walk.tensor;
         const adamw_tensor &d = t.tensor[at.tensor];
         if (at.base + S::values > d.n)
             return;
@@ -578,11 +595,26 @@ __global__ void __launch_bounds__(kThreads, 2)
                 at.scale = scales[at.base / 128 + lane % 4];
         }
     };
-    locate();
     fetch(unit, 0);
 #pragma unroll
     for (int i = 1; i < S::slots; ++i)
         fetch(ahead[i - 1], i);
+    if (hyper.partials) {  // while the first values are on their way
+        const float norm = norm_of(hyper.partial, hyper.partials, s.grad_scale);
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            *s.norm = norm;
+        if (!(norm <= FLT_MAX)) {  // a gradient that is not finite: the step is left out
+            if (unit.tensor >= 0 && unit.base + S::values <= t.tensor[unit.tensor].n)
+                mbar_sleep<false>(bar, 0);
+#pragma unroll
+            for (int i = 1; i < S::slots; ++i)
+                if (ahead[i - 1].tensor >= 0 && ahead[i - 1].base + S::values <= t.tensor[ahead[i - 1].tensor].n)
+                    mbar_sleep<false>(bar + 8 * i, 0);
+            return;
+        }
+        if (s.max_norm > 0.0f)
+            h.gs *= fminf(s.max_norm / (norm + 1e-6f), 1.0f);
+    }
     const float time = static_cast<float>(steps + 1);
     const float fix1 = 1.0f / expm1f(time * hyper.ln_beta1);  // -1 / (1 - beta1^t)
     h.fix2 = rsqrtf(-expm1f(time * hyper.ln_beta2));
@@ -592,11 +624,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t step_key = mix(hyper.key ^ static_cast<uint32_t>(steps));
     uint32_t phases = 0, key = 0, high = 0;
     int tensor = -1;  // that h and key are of, as is the numbers' high word
-    adamw_tensor d;
     for (int i = 0; unit.tensor >= 0;) {
         const Unit at = unit;
-        if (at.tensor != tensor)
-            d = t.tensor[at.tensor];
+        const adamw_tensor &d = t.tensor[at.tensor];
         if (at.tensor != tensor || static_cast<uint32_t>(at.base >> 32) != high) {
             tensor = at.tensor, high = static_cast<uint32_t>(at.base >> 32);
             const float lr = d.lr * factor;
@@ -657,17 +687,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-template <typename D, int MAX> int fill(Table<D, MAX> &t, const D *tensors, int64_t count, int chunk)
+// Spans of the tensors for units of `values` values: as long as leave each of
+// the resident warps four of them, and 16 units at most.  Returns the CTAs.
+template <typename D, int MAX> int fill(Table<D, MAX> &t, const D *tensors, int64_t count, int values, int resident)
 {
+    int64_t units = 0, at = 0;
+    for (int64_t i = 0; i < count; ++i)
+        units += (tensors[i].n + values - 1) / values;
+    const int64_t each = units / (4 * static_cast<int64_t>(resident) * (kThreads / 32));
     t.count = static_cast<int32_t>(count);
-    int64_t at = 0;
+    t.span = values * static_cast<int32_t>(each < 1 ? 1 : each > 16 ? 16 : each);
     for (int64_t i = 0; i < count; ++i) {
         t.tensor[i] = tensors[i];
         t.first[i] = static_cast<int32_t>(at);
-        at += (tensors[i].n + chunk - 1) / chunk;
+        at += (tensors[i].n + t.span - 1) / t.span;
     }
     t.first[count] = static_cast<int32_t>(at);
-    return static_cast<int>(at);
+    const int64_t need = (at + kThreads / 32 - 1) / (kThreads / 32);
+    return need < 1 ? 1 : need < resident ? static_cast<int>(need) : resident;
 }
 
 template <typename K> cudaError_t resident(K kernel, size_t smem, int *grid)
@@ -687,13 +724,11 @@ template <int MAX>
 cudaError_t norm_launch(const grad_tensor *tensors, int64_t count, TwoPart *partial, int *used, cudaStream_t stream)
 {
     Table<grad_tensor, MAX> t;
-    const int chunks = fill(t, tensors, count, kNormChunk);
     int grid = 0;
     cudaError_t e = resident(norm_kernel<MAX>, 0, &grid);
     if (e != cudaSuccess)
         return e;
-    grid = grid < kNormGrid ? grid : kNormGrid;
-    grid = grid < chunks ? grid : chunks < 1 ? 1 : chunks;
+    grid = fill(t, tensors, count, kNormUnit, grid < kNormGrid ? grid : kNormGrid);
     *used = grid;
     return launch_pdl(norm_kernel<MAX>, grid, kThreads, 0, stream, t, partial);
 }
@@ -701,7 +736,6 @@ cudaError_t norm_launch(const grad_tensor *tensors, int64_t count, TwoPart *part
 template <bool BITS8, int MAX>
 cudaError_t adamw_launch(const adamw_tensor *tensors, int64_t count, const Hyper &h, cudaStream_t stream)
 {
-    constexpr int kValues = Slot<BITS8>::values;
     int size = 1;
     for (int64_t i = 0; i < count; ++i)
         size = tensors[i].n > 0 && grad_size(tensors[i].grad_type) > size ? grad_size(tensors[i].grad_type) : size;
@@ -719,27 +753,37 @@ cudaError_t adamw_launch(const adamw_tensor *tensors, int64_t count, const Hyper
     int grid = 0;
     if ((e = resident(kernel, smem, &grid)) != cudaSuccess)
         return e;
-    // spans as long as leave every warp four of them: looking one up costs as much
-    // as a quarter of a unit
-    int64_t units = 0;
-    for (int64_t i = 0; i < count; ++i)
-        units += (tensors[i].n + kValues - 1) / kValues;
-    const int64_t each = units / (4 * (kThreads / 32) * static_cast<int64_t>(grid));
-    const int span = each < 1 ? 1 : each > 16 ? 16 : static_cast<int>(each);
     Table<adamw_tensor, MAX> t;
-    const int spans = fill(t, tensors, count, kValues * span);
-    const int need = (spans + kThreads / 32 - 1) / (kThreads / 32);
-    grid = grid < need ? grid : need < 1 ? 1 : need;
-    return launch_pdl(kernel, grid, kThreads, smem, stream, t, h, span, slot);
+    grid = fill(t, tensors, count, Slot<BITS8>::values, grid);
+    return launch_pdl(kernel, grid, kThreads, smem, stream, t, h, slot);
 }
 
 }  // namespace
 
-int grad_norm_launches(int64_t count) { return static_cast<int>((count + kNormTensors - 1) / kNormTensors); }
-
 cudaError_t grad_norm_workspace(int64_t count, uint64_t *bytes)
 {
-    *bytes = static_cast<uint64_t>(grad_norm_launches(count)) * kNormGrid * sizeof(TwoPart);
+    *bytes = static_cast<uint64_t>((count + kNormTensors - 1) / kNormTensors) * kNormGrid * sizeof(TwoPart);
+    return cudaSuccess;
+}
+
+// The partial sums of all gradients' squares into `partial`; how many.
+template <typename T, typename F>
+static cudaError_t launch_squares(const T *tensors, int64_t count, F gradient, TwoPart *partial, int *total,
+                                  cudaStream_t stream)
+{
+    *total = 0;
+    grad_tensor some[kNormTensors];
+    for (int64_t i = 0; i < count; i += kNormTensors) {
+        const int64_t n = count - i < kNormTensors ? count - i : kNormTensors;
+        for (int64_t j = 0; j < n; ++j)
+            some[j] = gradient(tensors[i + j]);
+        int used = 0;
+        const cudaError_t e = n <= 32 ? norm_launch<32>(some, n, partial + *total, &used, stream)
+                                      : norm_launch<kNormTensors>(some, n, partial + *total, &used, stream);
+        if (e != cudaSuccess)
+            return e;
+        *total += used;
+    }
     return cudaSuccess;
 }
 
@@ -748,24 +792,29 @@ cudaError_t launch_grad_norm(const grad_tensor *tensors, int64_t count, float gr
 {
     TwoPart *partial = static_cast<TwoPart *>(workspace);
     int total = 0;
-    for (int64_t i = 0; i < count; i += kNormTensors) {
-        const int64_t n = count - i < kNormTensors ? count - i : kNormTensors;
-        int used = 0;
-        const cudaError_t e = n <= 32 ? norm_launch<32>(tensors + i, n, partial + total, &used, stream)
-                                      : norm_launch<kNormTensors>(tensors + i, n, partial + total, &used, stream);
-        if (e != cudaSuccess)
-            return e;
-        total += used;
-    }
-    return launch_pdl(norm_total_kernel, 1, 1024, 0, stream, static_cast<const TwoPart *>(partial), total,
+    const cudaError_t e = launch_squares(tensors, count, [](const grad_tensor &t) { return t; }, partial, &total, stream);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(norm_total_kernel, 1, kThreads, 0, stream, static_cast<const TwoPart *>(partial), total,
                       grad_scale, norm);
 }
 
 cudaError_t launch_adamw(const adamw_tensor *tensors, int64_t count, bool bits8, const AdamWStep &step,
-                         cudaStream_t stream)
+                         void *workspace, cudaStream_t stream)
 {
     Hyper h;
     h.h = step;
+    h.partial = static_cast<TwoPart *>(workspace);
+    h.partials = 0;
+    if (step.norm) {
+        int total = 0;
+        const cudaError_t e = launch_squares(
+            tensors, count, [](const adamw_tensor &t) { return grad_tensor{t.grad, t.grad_scale, t.n, t.grad_type}; },
+            static_cast<TwoPart *>(workspace), &total, stream);
+        if (e != cudaSuccess)
+            return e;
+        h.partials = total;
+    }
     h.key = mix(mix(static_cast<uint32_t>(step.seed)) ^ static_cast<uint32_t>(step.seed >> 32));
     h.b1 = static_cast<float>(step.beta1), h.a1 = static_cast<float>(1.0 - step.beta1);
     h.b2 = static_cast<float>(step.beta2), h.a2 = static_cast<float>(1.0 - step.beta2);

@@ -177,28 +177,29 @@ struct PairArgs {
     const float *logp, *ref_logp;
     float beta, smoothing;
     bool mean;
-    float *margin, *logratio, *pair_loss, *coef;
+    float *loss, *margin, *logratio, *pair_loss, *coef;
 };
 cudaError_t launch_logprob(const LossRows &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_logprob_backward(const LossRows &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_policy_loss(const LossRows &a, bool bf16, cudaStream_t stream);
-cudaError_t launch_preference_loss(const LossRows &a, const PairArgs &p, bool bf16, float *loss, cudaStream_t stream);
+cudaError_t launch_preference_loss(const LossRows &a, const PairArgs &p, bool bf16, cudaStream_t stream);
 
 // The optimizer (adamw_kernels.cu).  `tensors` are host arrays.
 constexpr int kAdamWTensors = 320, kNormTensors = 720;  // of one launch
-int grad_norm_launches(int64_t count);
 cudaError_t grad_norm_workspace(int64_t count, uint64_t *bytes);
 cudaError_t launch_grad_norm(const grad_tensor *tensors, int64_t count, float grad_scale, float *norm,
                              void *workspace, cudaStream_t stream);
 struct AdamWStep {
     double beta1, beta2;
     float eps, grad_scale, max_norm;                // max_norm 0: no clipping
-    const float *norm, *lr_factor;                  // each may be null
+    float *norm;                                    // null: not computed
+    const float *lr_factor;                         // may be null
     uint64_t seed;
     int64_t *state;
 };
+// workspace: grad_norm_workspace's, where there is a norm.
 cudaError_t launch_adamw(const adamw_tensor *tensors, int64_t count, bool bits8, const AdamWStep &h,
-                         cudaStream_t stream);
+                         void *workspace, cudaStream_t stream);
 
 cudaError_t launch_watchdog_selftest(cudaStream_t stream);
 cudaError_t read_codec_error(uint32_t *flags, bool clear);

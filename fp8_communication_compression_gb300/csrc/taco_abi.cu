@@ -978,9 +978,8 @@ taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64
     a.offsets = offsets, a.sequences = 2 * pairs;
     a.grad_scale = grad_scale, a.dlogits = dlogits;
     const taco::PairArgs p = {targets, offsets, T,      pairs,    logp,         ref_logp, beta,
-                              label_smoothing, mean != 0, margin, logratio, ws + 2 * T, ws + T};
-    return from_cuda(
-        taco::launch_preference_loss(a, p, logits_bf16 != 0, loss, reinterpret_cast<cudaStream_t>(stream)));
+                              label_smoothing, mean != 0, loss, margin, logratio, ws + 2 * T, ws + T};
+    return from_cuda(taco::launch_preference_loss(a, p, logits_bf16 != 0, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // A gradient of n > 0 values.
@@ -988,7 +987,7 @@ static taco_status check_grad(const void *grad, const float *scale, int32_t type
 {
     if (type < TACO_GRAD_F32 || type > TACO_GRAD_FP8 || !grad || (type == TACO_GRAD_FP8) != (scale != nullptr))
         return TACO_ERR_INVALID_ARG;
-    if (n > (int64_t(1) << 40))
+    if (n > (int64_t(1) << 38))
         return TACO_ERR_UNSUPPORTED;
     return aligned(grad, 16) && aligned(scale, 4) ? TACO_OK : TACO_ERR_MISALIGNED;
 }
@@ -1029,7 +1028,7 @@ taco_status grad_norm(const grad_tensor *tensors, int64_t count, float grad_scal
         const Span ins[2] = {{t.grad, grad_bytes(t.grad_type, n)}, {t.grad_scale, t.grad_scale ? (n + 127) / 128 * 4 : 0}};
         if (!apart(outs, 2, ins, 2))
             return TACO_ERR_INVALID_ARG;
-        if ((total += n) > (uint64_t(1) << 42))
+        if ((total += n) > (uint64_t(1) << 38))
             return TACO_ERR_UNSUPPORTED;
     }
     return from_cuda(taco::launch_grad_norm(tensors, count, grad_scale, norm, workspace,
@@ -1037,50 +1036,61 @@ taco_status grad_norm(const grad_tensor *tensors, int64_t count, float grad_scal
 }
 
 taco_status adamw_step(const adamw_tensor *tensors, int64_t count, int32_t state_bits, double beta1, double beta2,
-                       float eps, float grad_scale, const float *norm, float max_norm, const float *lr_factor,
-                       uint64_t seed, int64_t *state, taco_stream_t stream)
+                       float eps, float grad_scale, float max_norm, float *norm, const float *lr_factor, uint64_t seed,
+                       int64_t *state, void *workspace, uint64_t workspace_bytes, taco_stream_t stream)
 {
-    if (count < 0 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) ||
-        eps < FLT_MIN ||
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) || eps < FLT_MIN ||
         !std::isfinite(grad_scale) || !(max_norm >= 0.0f) || !std::isfinite(max_norm) || (max_norm > 0.0f && !norm))
         return TACO_ERR_INVALID_ARG;
-    if ((state_bits != 8 && state_bits != 32) || count > (int64_t(1) << 24))
+    uint64_t need = 0, total = 0;
+    taco_status st = grad_norm_workspace_bytes(count, &need);
+    if (st != TACO_OK)
+        return st;
+    if (state_bits != 8 && state_bits != 32)
         return TACO_ERR_UNSUPPORTED;
     if (count == 0)
         return TACO_OK;
-    if (!tensors || !state)
+    if (!tensors || !state || (norm && (!workspace || workspace_bytes < need)))
         return TACO_ERR_INVALID_ARG;
-    if (!aligned(state, 8) || !aligned(norm, 4) || !aligned(lr_factor, 4))
+    if (!aligned(state, 8) || !aligned(norm, 4) || !aligned(lr_factor, 4) || !aligned(workspace, 256))
         return TACO_ERR_MISALIGNED;
-    uint64_t total = 0;
+    const bool bits8 = state_bits == 8;
+    const Span common[3] = {{state, 16}, {norm, norm ? 4u : 0u}, {workspace, norm ? need : 0}};
+    const Span factor[1] = {{lr_factor, lr_factor ? 4u : 0u}};
+    if (!apart(common, 3, factor, 1))
+        return TACO_ERR_INVALID_ARG;
     for (int64_t i = 0; i < count; ++i) {
         const adamw_tensor &t = tensors[i];
         if (t.n < 0 || !std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
             return TACO_ERR_INVALID_ARG;
         if (t.n == 0)
             continue;
-        taco_status st = check_grad(t.grad, t.grad_scale, t.grad_type, t.n);
-        if (st != TACO_OK)
+        if ((st = check_grad(t.grad, t.grad_scale, t.grad_type, t.n)) != TACO_OK)
             return st;
-        const bool bits8 = state_bits == 8;
         if (!t.param || !t.m || !t.v || (bits8 && (!t.m_scale || !t.v_scale)))
             return TACO_ERR_INVALID_ARG;
         if (!aligned(t.param, 16) || !aligned(t.copy_bf16, 16) || !aligned(t.m, 16) || !aligned(t.v, 16) ||
             (bits8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
             return TACO_ERR_MISALIGNED;
         const uint64_t n = t.n, sc = (n + 127) / 128 * 4, sb = bits8 ? n : 4 * n;
-        const Span outs[7] = {{t.param, 4 * n}, {t.copy_bf16, t.copy_bf16 ? 2 * n : 0}, {t.m, sb}, {t.v, sb},
-                              {t.m_scale, bits8 ? sc : 0}, {t.v_scale, bits8 ? sc : 0}, {state, 16}};
-        const Span ins[4] = {{t.grad, grad_bytes(t.grad_type, n)}, {t.grad_scale, t.grad_scale ? sc : 0},
-                             {norm, norm ? 4u : 0u}, {lr_factor, lr_factor ? 4u : 0u}};
-        if (!apart(outs, 7, ins, 4))
+        const Span outs[6] = {{t.param, 4 * n}, {t.copy_bf16, t.copy_bf16 ? 2 * n : 0}, {t.m, sb}, {t.v, sb},
+                              {t.m_scale, bits8 ? sc : 0}, {t.v_scale, bits8 ? sc : 0}};
+        const Span ins[3] = {{t.grad, grad_bytes(t.grad_type, n)}, {t.grad_scale, t.grad_scale ? sc : 0}, factor[0]};
+        if (!apart(outs, 6, ins, 3))
             return TACO_ERR_INVALID_ARG;
-        if ((total += n) > (uint64_t(1) << 42))
+        for (const Span &c : common)
+            for (const Span *o = outs; o < outs + 6; ++o)
+                if (overlap(c.p, c.n, o->p, o->n))
+                    return TACO_ERR_INVALID_ARG;
+        for (int k = 0; k < 2; ++k)
+            if (overlap(norm, common[1].n, ins[k].p, ins[k].n) || overlap(workspace, common[2].n, ins[k].p, ins[k].n))
+                return TACO_ERR_INVALID_ARG;
+        if ((total += n) > (uint64_t(1) << 38))
             return TACO_ERR_UNSUPPORTED;
     }
-    return from_cuda(taco::launch_adamw(tensors, count, state_bits == 8,
+    return from_cuda(taco::launch_adamw(tensors, count, bits8,
                                         {beta1, beta2, eps, grad_scale, max_norm, norm, lr_factor, seed, state},
-                                        reinterpret_cast<cudaStream_t>(stream)));
+                                        workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 struct taco_host_pipeline {

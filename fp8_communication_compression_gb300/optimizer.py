@@ -12,12 +12,15 @@ the format and the hash stand in include/taco.h (adamw_step)."""
 
 from __future__ import annotations
 
-import ctypes
 from typing import Sequence
 
+import numpy as np
 import torch
 
 from . import _lib, api
+
+
+_PLAIN = {torch.float32: 0, torch.bfloat16: 1}  # TACO_GRAD_* of gradients without a scale
 
 
 class AdamW:
@@ -76,8 +79,10 @@ class AdamW:
         self.v_scale = torch.ones(at // 128, device=self.device) if state_bits == 8 else None
         self.steps = new(2, torch.int64)
         size = self.m.element_size()
+        self._index = params[0].get_device()
+        self._seed = seed & (1 << 64) - 1
         self._table = (_lib.AdamWTensor * len(params))()
-        self._norms = (_lib.GradTensor * len(params))()
+        self._rows = np.frombuffer(self._table, dtype=np.dtype(_lib.AdamWTensor))  # the same memory, by columns
         for i, (p, c, start) in enumerate(zip(params, copies, self.starts)):
             t = self._table[i]
             t.param, t.copy_bf16, t.n, t.lr, t.weight_decay = p.data_ptr(), api._ptr(c), p.numel(), lrs[i], decays[i]
@@ -97,22 +102,30 @@ class AdamW:
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
         if lr_factor is not None:
             api._need(lr_factor, "lr_factor", (torch.float32,), 1)
-        device, table, norms = self.params[0].get_device(), self._table, self._norms
-        for i, (g, n) in enumerate(zip(grads, self.sizes)):
-            grad, scale, _, kind = api._grad_of(g, f"grads[{i}]", n, device)
-            t = table[i]
-            t.grad, t.grad_scale, t.grad_type = grad, scale, kind
-            if self.max_norm is not None:
-                t = norms[i]
-                t.grad, t.grad_scale, t.n, t.grad_type = grad, scale, n, kind
-        norm = None
+        pointers, scales, kinds = [], [], []
+        index = self._index
+        for g, n in zip(grads, self.sizes):
+            # the common case checked here: a step of many small tensors is bound by this loop
+            kind = _PLAIN.get(g.dtype) if isinstance(g, torch.Tensor) else None
+            if kind is not None and g.numel() == n and g.get_device() == index and g.is_contiguous():
+                pointers.append(g.data_ptr())
+                scales.append(0)
+            else:
+                grad, scale, _, kind = api._grad_of(g, f"grads[{len(kinds)}]", n, index)
+                pointers.append(grad)
+                scales.append(scale or 0)
+            kinds.append(kind)
+        rows = self._rows
+        rows["grad"], rows["grad_scale"], rows["grad_type"] = pointers, scales, kinds
+        norm = ws = None
+        nbytes = 0
         if self.max_norm is not None:
             norm = api._new((), torch.float32, self.device, stream)
-            api._grad_norm(norms, len(norms), self.device, grad_scale, norm, stream)
-        st = _lib.load().adamw_step(table, len(table), self.state_bits, self.betas[0], self.betas[1], self.eps,
-                                    grad_scale, api._ptr(norm), self.max_norm or 0.0, api._ptr(lr_factor),
-                                    ctypes.c_uint64(self.seed & (1 << 64) - 1), self.steps.data_ptr(),
-                                    api._stream_of(self.steps, stream))
+            nbytes = api._norm_partials_bytes(len(pointers))
+            ws = api._workspace(nbytes, self.device, stream)
+        st = _lib.load().adamw_step(self._table, len(pointers), self.state_bits, self.betas[0], self.betas[1], self.eps,
+                                    grad_scale, self.max_norm or 0.0, api._ptr(norm), api._ptr(lr_factor), self._seed,
+                                    self.steps.data_ptr(), api._ptr(ws), nbytes, api._stream_of(self.steps, stream))
         _lib.check("adamw_step", st)
         return norm
 

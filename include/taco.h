@@ -682,8 +682,11 @@ taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64
  * null: 1).  param fp32; copy_bf16 (may be null) gets the new weights rounded.
  * state int64 [2] on the device: the steps done, and a counter that is zero
  * between calls; the step counts itself, so that a captured call can be
- * replayed.  norm null: no clipping (max_norm must be 0).  A norm that is not
- * finite leaves the whole step out: nothing changes, state[0] neither.
+ * replayed.  norm (one fp32 value, out): the norm that grad_norm gives, for
+ * clipping to max_norm (0: no clipping); one that is not finite leaves the whole
+ * step out: nothing changes, state[0] neither.  norm null: no norm is taken
+ * (max_norm must be 0), and no workspace needed.  The workspace is
+ * grad_norm_workspace_bytes(count) bytes, 256-byte aligned.
  *
  * state_bits 32: m and v fp32 [n].  state_bits 8: E4M3 codes of m and of
  * r = sqrt(v), with fp32 multipliers [ceil(n / 128)] in m_scale and v_scale:
@@ -728,8 +731,8 @@ taco_status grad_norm_workspace_bytes(int64_t count, uint64_t *bytes);
 taco_status grad_norm(const grad_tensor *tensors, int64_t count, float grad_scale, float *norm, void *workspace,
                       uint64_t workspace_bytes, taco_stream_t stream);
 taco_status adamw_step(const adamw_tensor *tensors, int64_t count, int32_t state_bits, double beta1, double beta2,
-                       float eps, float grad_scale, const float *norm, float max_norm, const float *lr_factor,
-                       uint64_t seed, int64_t *state, taco_stream_t stream);
+                       float eps, float grad_scale, float max_norm, float *norm, const float *lr_factor, uint64_t seed,
+                       int64_t *state, void *workspace, uint64_t workspace_bytes, taco_stream_t stream);
 
 /*
  * taco_device_error - watchdog flags of the kernels on the current device.
