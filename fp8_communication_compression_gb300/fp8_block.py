@@ -11,7 +11,8 @@ the slices' partial outputs, and the FP8 main gradients, run together.
 ``out`` and ``h1`` go into the next block's norms.  The backward pass keeps
 y, h1 and the u_p; n and the a_p are recomputed (AGoQ 2.A stores inputs and
 recomputes).  Weight gradients go straight into FP8 main gradients
-(agoq_fp8_accumulate), one micro-batch after the other.
+(agoq_fp8_accumulate), one micro-batch after the other; AdamW (optimizer.py)
+updates fp32 weights from them, and load_weights() takes its bf16 copies.
 
 It shows how the calls fit together.  What lies between them is plain torch
 (SiLU and its gradient, the stacking of the partial sums), and the bf16 weight
@@ -58,6 +59,16 @@ class Fp8Block:
         fp = self.f // self.P
         self.up = [api.fp8_quantize_weight(w_up[p * fp:(p + 1) * fp]) for p in range(self.P)]
         self.down = [api.fp8_quantize_weight(w_down[:, p * fp:(p + 1) * fp].contiguous()) for p in range(self.P)]
+
+    def gradients(self) -> list:
+        """The main gradients (codes, multipliers), as AdamW.step takes them: the
+        up slices' [f / P, d], then the down slices' [d, f / P]."""
+        return [*self.main_up, *self.main_down]
+
+    def zero_gradients(self) -> None:
+        """Back to zero, after an update."""
+        for codes, _ in self.gradients():
+            codes.zero_()
 
     @staticmethod
     def _main(rows: int, cols: int, dev: torch.device):

@@ -39,6 +39,10 @@ class Fp8Head:
             w = torch.nn.functional.pad(w, (0, 0, 0, self.rows - w.shape[0]))
         self.w = api.fp8_quantize_weight(w)
 
+    def zero_gradients(self) -> None:
+        """Back to zero, after an update."""
+        self.main[0].zero_()
+
     def logits(self, x: torch.Tensor) -> torch.Tensor:
         """x bf16 [..., d] -> bf16 [..., rows]."""
         return api.fp8_linear(x, self.w[0], self.w[1])

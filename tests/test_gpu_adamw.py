@@ -126,13 +126,14 @@ def check_step(opt, grads, before, lr, wd, t, coef, tol_coef, scale=1.0):
         assert not pad.any()
 
 
-@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{s[0]}")
-@pytest.mark.parametrize("kinds", KINDS, ids="-".join)
-@pytest.mark.parametrize("bits", [8, 32])
-@pytest.mark.parametrize("clip", [None, 0.01])
+# large sizes are clipped with mixed gradients only
+STEPS = [(s, k, b, c) for c in (None, 0.01) for b in (8, 32) for k in KINDS for s in SIZES
+         if not (c and sum(s) > 100000 and len(k) == 1)]
+
+
+@pytest.mark.parametrize("sizes,kinds,bits,clip", STEPS,
+                         ids=[f"{len(s)}x{s[0]}-{'-'.join(k)}-{b}-{c}" for s, k, b, c in STEPS])
 def test_steps(sizes, kinds, bits, clip):
-    if sum(sizes) > 100000 and (kinds != ("fp8", "f32", "bf16")) and clip:
-        pytest.skip("covered by the mixed gradients")
     gen = torch.Generator().manual_seed(2)
     params = [(0.05 * torch.randn(n, generator=gen)).cuda() for n in sizes]
     copies = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") if i % 3 != 1 else None for i, n in enumerate(sizes)]
