@@ -20,7 +20,7 @@ STATUS_NAMES = {0: "TACO_OK", 1: "TACO_ERR_INVALID_ARG", 2: "TACO_ERR_UNSUPPORTE
 
 # name -> (restype, argtypes); mirrors include/taco.h
 _P = ctypes.c_void_p
-_I64, _I32, _F32, _U64 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_uint64
+_I64, _I32, _F32, _F64, _U64 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_double, ctypes.c_uint64
 _PP = ctypes.POINTER(ctypes.c_void_p)
 SIGNATURES = {
     "taco_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -58,16 +58,16 @@ SIGNATURES = {
     "rmsnorm_gate_residual_workspace_bytes": (ctypes.c_int, [_I64, _I64, _I32, _P]),
     "rmsnorm_gate_residual_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32, _F32, _F32, _I64, _I64,
                                                       _P, _P, _P, _P, _P, _P, _U64, _P]),
-    "token_logprob": (ctypes.c_int, [_P, _I32, _P, _I64, _I64, _I64, _F32, _P, _P, _P]),
-    "token_logprob_backward": (ctypes.c_int, [_P, _P, _I32, _P, _P, _I64, _I64, _I64, _F32, _P, _P]),
-    "policy_loss": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F32, _F32, _F32, _F32, _F32,
+    "token_logprob": (ctypes.c_int, [_P, _I32, _P, _I64, _I64, _I64, _F64, _P, _P, _P]),
+    "token_logprob_backward": (ctypes.c_int, [_P, _P, _I32, _P, _P, _I64, _I64, _I64, _F64, _P, _P]),
+    "policy_loss": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F64, _F32, _F32, _F32, _F32,
                                    _P, _P, _P, _P, _P]),
     "preference_loss_workspace_bytes": (ctypes.c_int, [_I64, _I64, _P]),
-    "preference_loss": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I64, _I64, _I64, _I64, _F32, _F32, _F32, _I32, _F32,
+    "preference_loss": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I64, _I64, _I64, _I64, _F64, _F32, _F32, _I32, _F32,
                                        _P, _P, _P, _P, _P, _P, _U64, _P]),
     "grad_norm_workspace_bytes": (ctypes.c_int, [_I64, _P]),
     "grad_norm": (ctypes.c_int, [_P, _I64, _F32, _P, _P, _U64, _P]),
-    "adamw_step": (ctypes.c_int, [_P, _I64, _I32, ctypes.c_double, ctypes.c_double, _F32, _F32, _F32, _P, _P, _U64,
+    "adamw_step": (ctypes.c_int, [_P, _I64, _I32, _F64, _F64, _F32, _F32, _F32, _P, _P, _U64,
                                   _P, _P, _U64, _P]),
     "taco_host_pipeline_create": (ctypes.c_int, [_I32, _I64, _I64, _I32, _I32, _I32,
                                                  ctypes.POINTER(ctypes.c_void_p),

@@ -288,7 +288,10 @@ __device__ __forceinline__ float norm_of(const TwoPart *partial, int n, float sc
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w)
         sum.add(part[w]);
-    return sqrtf(sum.value()) * fabsf(scale);
+    // the sum's root rounded once: the root of its first part, corrected by the rest
+    const float h = sum.value(), root = sqrtf(h);
+    const float rest = fmaf(-root, root, h) + (sum.lo - (h - sum.hi));
+    return (h > 0.0f && h <= FLT_MAX ? root + 0.5f * rest / root : root) * fabsf(scale);
 }
 
 __global__ void __launch_bounds__(kThreads) norm_total_kernel(const TwoPart *partial, int n, float scale, float *norm)
@@ -319,6 +322,7 @@ struct Hyper {
     int32_t first_tensor;     // of this launch
     int32_t last;             // the step's last launch counts it
     float b1, b2, a1, a2;     // b and 1 - b, each rounded from 64 bits
+    float zero;
     float ln_beta1, ln_beta2;
 };
 
@@ -338,6 +342,24 @@ __device__ __forceinline__ float inverse(float x)
     return y;
 }
 
+// The root near to s, rounded to nearest but for rare ties: a Newton step.  NaN for
+// an infinite v.
+__device__ __forceinline__ float2 rounded_root(float2 v, float2 s)
+{
+    float2 q;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(v.x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(v.y));
+    q = make_float2(fminf(q.x, 0x1p64f), fminf(q.y, 0x1p64f)) * both(0.5f);
+    const float2 e = fma2(make_float2(-s.x, -s.y), s, v);
+    return fma2(e, q, s);
+}
+// 1 / x likewise.
+__device__ __forceinline__ float rounded_inverse(float x)
+{
+    const float r = inverse(x);
+    return fmaf(r, fmaf(-x, r, 1.0f), r);
+}
+
 // Four values held by a lane.
 struct F4 {
     float2 a, b;
@@ -351,10 +373,24 @@ __device__ __forceinline__ F4 decoded(uint32_t w)
     return f;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b)
+// Largest of three values (NaN if one is), of their magnitudes, and smallest of
+// their magnitudes (NaNs left out).
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3_abs(float a, float b, float c)
+{
+    float r;
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 // A block's states are held as zeros below kLeast (2^-100): their factors would
@@ -410,10 +446,11 @@ __device__ __noinline__ Codes unusual_codes(Codes c, F4 y, F4 z, uint4 um, uint4
 __device__ __forceinline__ Codes to_codes(const F4 &m, const F4 &root, uint32_t x0, uint32_t key)
 {
     const uint32_t top_m = __reduce_max_sync(
-        ~0u, __float_as_uint(fmaxf(fmaxf(fabsf(m.a.x), fabsf(m.a.y)), fmaxf(fabsf(m.b.x), fabsf(m.b.y)))));
+        ~0u, __float_as_uint(max3_abs(max3_abs(m.a.x, m.a.y, m.b.x), m.b.y, m.b.y)));
     const uint32_t top_r = __reduce_max_sync(
-        ~0u, __float_as_uint(max_nan(max_nan(root.a.x, root.a.y), max_nan(root.b.x, root.b.y))));
-    const float inv_m = 448.0f * inverse(__uint_as_float(top_m)), inv_r = 448.0f * inverse(__uint_as_float(top_r));
+        ~0u, __float_as_uint(max3_nan(max3_nan(root.a.x, root.a.y, root.b.x), root.b.y, root.b.y)));
+    const float inv_m = 448.0f * rounded_inverse(__uint_as_float(top_m));
+    const float inv_r = 448.0f * rounded_inverse(__uint_as_float(top_r));
     const F4 y = {m.a * both(inv_m), m.b * both(inv_m)}, z = {root.a * both(inv_r), root.b * both(inv_r)};
     // the last shift of the hash h: u = low half of h ^ h >> 16 for m, high half for r
     uint32_t um[4], ur[4];
@@ -427,8 +464,7 @@ __device__ __forceinline__ Codes to_codes(const F4 &m, const F4 &root, uint32_t 
     }
     Codes c;
     c.m_scale = __uint_as_float(top_m) * (1.0f / 448.0f), c.r_scale = __uint_as_float(top_r) * (1.0f / 448.0f);
-    const float least = fminf(fminf(fminf(fabsf(y.a.x), fabsf(y.a.y)), fminf(fabsf(y.b.x), fabsf(y.b.y))),
-                              fminf(fminf(z.a.x, z.a.y), fminf(z.b.x, z.b.y)));
+    const float least = min3_abs(min3_abs(min3_abs(y.a.x, y.a.y, y.b.x), y.b.y, z.a.x), min3_abs(z.a.y, z.b.x, z.b.y), 448.0f);
     const bool usual = top_m >= kLeast && top_r >= kLeast && top_r < kMost;
     if (__any_sync(~0u, !(least >= 0.015625f)) || !usual)
         return unusual_codes(c, y, z, make_uint4(um[0], um[1], um[2], um[3]),
@@ -438,13 +474,19 @@ __device__ __forceinline__ Codes to_codes(const F4 &m, const F4 &root, uint32_t 
 }
 
 struct Update {
-    float gs, fix2, eps, b1, b2, a1, a2, minus_decay, minus_rate;
+    float gs, fix2, eps, b1, b2, a1, a2, zero, minus_decay, minus_rate;
 };
 
+// Each operation of m and v is rounded as the formula stands, without fused steps:
+// what the codes of the next step depend on comes out the same in any
+// implementation that does so (a value that is off by a unit in the last place
+// has another code once in a million, and a block's largest value then another
+// multiplier).
 __device__ __forceinline__ float2 updated(float2 p, float2 g, float2 &m, float2 &v, float2 &root, const Update &h)
 {
-    m = fma2(both(h.b1), m, both(h.a1) * g);
-    v = fma2(both(h.b2), v, (both(h.a2) * g) * g);
+    const float2 zero = both(h.zero);  // (the compiler fuses a product and a sum, but not two fused steps)
+    m = __fadd2_rn(fma2(both(h.b1), m, zero), fma2(both(h.a1), g, zero));
+    v = __fadd2_rn(fma2(both(h.b2), v, zero), fma2(both(h.a2) * g, g, zero));
     root = make_float2(root_of(v.x), root_of(v.y));
     const float2 d = fma2(root, both(h.fix2), both(h.eps));
     const float2 u = m * make_float2(inverse(d.x), inverse(d.y));
@@ -484,6 +526,7 @@ __device__ __forceinline__ void update_block(const adamw_tensor &d, int64_t bloc
         store4<FULL>(static_cast<float *>(d.v), e, n, make_float4(v.a.x, v.a.y, v.b.x, v.b.y));
         return;
     }
+    root.a = rounded_root(v.a, root.a), root.b = rounded_root(v.b, root.b);
     // (key: key ^ key >> 16, so that the hash's first shift is taken of the number alone)
     const Codes c = to_codes(m, root, static_cast<uint32_t>(e) * 0x13198A2Fu, key);
     store4<FULL>(static_cast<uint8_t *>(d.m), e, n, c.m);
@@ -547,7 +590,7 @@ constexpr int kTogether = 4;  // blocks whose instructions are mixed
 // warp's own, while the one before is worked on, its blocks' multipliers by a
 // lane each (0 .. 3: m, 4 .. 7: r, 8 .. 11: the gradient's).
 template <bool BITS8, int MAX>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     adamw_kernel(const __grid_constant__ Table<adamw_tensor, MAX> t, const __grid_constant__ Hyper hyper, int slot_bytes)
 {
     using S = Slot<BITS8>;
@@ -618,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float time = static_cast<float>(steps + 1);
     const float fix1 = 1.0f / expm1f(time * hyper.ln_beta1);  // -1 / (1 - beta1^t)
     h.fix2 = rsqrtf(-expm1f(time * hyper.ln_beta2));
-    h.eps = s.eps, h.b1 = hyper.b1, h.b2 = hyper.b2, h.a1 = hyper.a1, h.a2 = hyper.a2;
+    h.eps = s.eps, h.b1 = hyper.b1, h.b2 = hyper.b2, h.a1 = hyper.a1, h.a2 = hyper.a2, h.zero = hyper.zero;
     h.minus_decay = h.minus_rate = 0.0f;
     const float factor = s.lr_factor ? *s.lr_factor : 1.0f;
     const uint32_t step_key = mix(hyper.key ^ static_cast<uint32_t>(steps));
@@ -646,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t k = u * 128 + four;
                 F4 g, m, v;
                 if (d.grad_type == TACO_GRAD_FP8)
-                    g = times(decoded(shared_at<uint32_t>(from + S::grad + k)),
-                              __shfl_sync(~0u, at.scale, 8 + u) * h.gs);
+                    g = times(times(decoded(shared_at<uint32_t>(from + S::grad + k)),
+                                    __shfl_sync(~0u, at.scale, 8 + u)), h.gs);
                 else if (d.grad_type == TACO_GRAD_BF16)
                     g = times(from_bf16(shared_at<uint2>(from + S::grad + 2 * k)), h.gs);
                 else
@@ -818,6 +861,7 @@ cudaError_t launch_adamw(const adamw_tensor *tensors, int64_t count, bool bits8,
     h.key = mix(mix(static_cast<uint32_t>(step.seed)) ^ static_cast<uint32_t>(step.seed >> 32));
     h.b1 = static_cast<float>(step.beta1), h.a1 = static_cast<float>(1.0 - step.beta1);
     h.b2 = static_cast<float>(step.beta2), h.a2 = static_cast<float>(1.0 - step.beta2);
+    h.zero = 0.0f;
     h.ln_beta1 = static_cast<float>(std::log(step.beta1));
     h.ln_beta2 = static_cast<float>(std::log(step.beta2));
     int64_t i = 0;

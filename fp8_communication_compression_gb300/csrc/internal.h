@@ -161,7 +161,8 @@ struct LossRows {
     const void *logits;
     const int64_t *targets;
     int64_t T, V, N;
-    float temperature, inv_temperature, grad_scale;
+    float temperature, temperature_low, inv_temperature, inv_temperature_low;  // each in two parts
+    float grad_scale;
     float *logp, *lse, *coef;            // forward; coef: zeroed in rows that do not count (may be null)
     const int64_t *offsets;              // rows outside offsets[0] .. offsets[sequences] do not count (may be null)
     int64_t sequences;

@@ -49,6 +49,7 @@ constexpr uint32_t kErrLoss = 256u;
 constexpr float kLog2e = 1.4426950408889634f, kLog2eHigh = 1.4426949024200439453125f;
 constexpr float kLog2eLow = static_cast<float>(1.4426950408889634074 - 1.4426949024200439453125);
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kShort = 2.5e-8f;
 constexpr int kMaxCluster = 8;
 
 enum Mode { kForward, kPolicy };
@@ -159,35 +160,53 @@ __device__ __forceinline__ uint4 packed(const float (&f)[4])
 // log2(e) / tau in two parts, c = hi + lo: with one rounded factor alone all
 // differences would be scaled wrongly by the same 2^-25, and the error of a
 // sequence's log probabilities would add up.  Both are positive (kLog2eHigh is
-// further below log2 e than its product's rounding), so that -inf stays -inf.  Exponents are x c - m c by two fused steps, from the rounded
-// product mc = fl(m hi); what it is off by is known (rest) and goes into the
-// sum's logarithm.  Where m c leaves fp32's range (rows of the lowest value
-// alone), differences are scaled instead.
+// further below log2 e than its product's rounding), so that -inf stays -inf.
+// Exponents are x c - k by two fused steps, k the whole number next to m hi: sums
+// relative to different k are joined by powers of two, exactly; what k is off by
+// is known (rest) and goes into the sum's logarithm.  Where m c leaves fp32's
+// range (rows of the lowest value alone), differences are scaled instead.
 struct Scale {
-    float hi, lo, near, inv_temperature;
-    __device__ explicit Scale(float inv) : hi(inv * kLog2eHigh), near(inv * kLog2e), inv_temperature(inv)
+    float hi, lo, near;
+    __device__ explicit Scale(const LossRows &a)
+        : hi(a.inv_temperature * kLog2eHigh), near(a.inv_temperature * kLog2e)
     {
-        lo = fmaxf(fmaf(inv, kLog2eHigh, -hi) + inv * kLog2eLow, FLT_MIN);
+        lo = fmaxf(fmaf(a.inv_temperature, kLog2eHigh, -hi) + a.inv_temperature * kLog2eLow +
+                       a.inv_temperature_low * kLog2e, FLT_MIN);
     }
-    static __device__ __forceinline__ bool plain(float mc) { return fabsf(mc) <= 1e37f; }
+    static __device__ __forceinline__ bool plain(float k) { return fabsf(k) <= 1e37f; }
+    __device__ __forceinline__ float whole(float m) const { return rintf(m * hi); }
     __device__ __forceinline__ float exponent(float x, float m) const
     {
-        const float mc = m * hi, d = x - m;
-        return plain(mc) ? fmaf(x, lo, fmaf(x, hi, -mc)) : d * near;
+        const float k = whole(m);
+        return plain(k) ? fmaf(x, lo, fmaf(x, hi, -k)) : (x - m) * near;
     }
     // From a sum relative to m to one relative to the larger `to`.
     __device__ __forceinline__ float factor(float m, float to) const
     {
-        const float mc = m * hi, tc = to * hi;
-        return ex2(plain(mc) && plain(tc) ? mc - tc : (m - to) * hi);
+        const float k = whole(m), t = whole(to);
+        return ex2(plain(k) && plain(t) ? k - t : (m - to) * near);
     }
     // The sum is of 2^(x c - m c - rest).
     __device__ __forceinline__ float rest(float m) const
     {
-        const float mc = m * hi;
-        return plain(mc) ? -fmaf(m, lo, fmaf(m, hi, -mc)) : 0.0f;
+        const float k = whole(m);
+        return plain(k) ? -fmaf(m, lo, fmaf(m, hi, -k)) : 0.0f;
+    }
+    // Logarithm of the sum of exp((x - m) / tau).  ex2.approx falls short of 2^y by
+    // 2.5e-8 of it on average (measured; its error is at most 2^-22.5): alike in
+    // all rows, so that a sequence's log probabilities would add it up.
+    __device__ __forceinline__ float log_of(float m, float s) const
+    {
+        return logf(s) + (rest(m) * kLn2 + kShort);
     }
 };
+
+// x / tau, 1 / tau in two parts.
+__device__ __forceinline__ float scaled(float x, const LossRows &a)
+{
+    const float y = x * a.inv_temperature;
+    return fabsf(y) <= FLT_MAX ? fmaf(x, a.inv_temperature, x * a.inv_temperature_low) : y;
+}
 
 // A maximum and a sum relative to it.
 struct Sum {
@@ -233,8 +252,8 @@ template <typename E, int n> __device__ __forceinline__ void accumulate(Sum &z, 
         z.s *= c.factor(z.m, m);
         z.m = m;
     }
-    const float mc = z.m * c.hi;
-    if (Scale::plain(mc)) {
+    const float k = c.whole(z.m);
+    if (Scale::plain(k)) {
         float2 s[4] = {make_float2(z.s, 0.0f), both(0.0f), both(0.0f), both(0.0f)};
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -243,9 +262,9 @@ template <typename E, int n> __device__ __forceinline__ void accumulate(Sum &z, 
 #pragma unroll
             for (int j = 0; j < G; j += 2) {
                 const float2 x = make_float2(f[j], f[j + 1]);
-                const float2 y = __ffma2_rn(x, both(c.lo), __ffma2_rn(x, both(c.hi), both(-mc)));
-                const int k = (i * G + j) / 2 % 4;
-                s[k] = __fadd2_rn(s[k], make_float2(ex2(y.x), ex2(y.y)));
+                const float2 y = __ffma2_rn(x, both(c.lo), __ffma2_rn(x, both(c.hi), both(-k)));
+                const int a = (i * G + j) / 2 % 4;
+                s[a] = __fadd2_rn(s[a], make_float2(ex2(y.x), ex2(y.y)));
             }
         }
         s[0] = __fadd2_rn(__fadd2_rn(s[0], s[1]), __fadd2_rn(s[2], s[3]));
@@ -397,7 +416,7 @@ struct Policy {
     // token_loss, and the gradient at logp
     __device__ float2 at(float logp, const LossRows &a) const
     {
-        const float r = ex2((logp - old_logp) * kLog2e);
+        const float r = expf(logp - old_logp);
         const float free = advantage == 0.0f ? 0.0f : r * advantage;
         const float held = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * advantage;
         float loss = -fminf(free, held), slope = free <= held ? -free : 0.0f;
@@ -453,7 +472,7 @@ __global__ void __launch_bounds__(128) row_kernel(const __grid_constant__ LossRo
     // this CTA's interior granules
     const int each = (x.last - x.first + parts - 1) / parts;
     const int lo = min(x.last, x.first + rank * each), hi = min(x.last, lo + each);
-    const Scale c(a.inv_temperature);
+    const Scale c(a);
     Sum z = {-FLT_MAX, 0.0f};
     float coef = 0.0f, inv = 0.0f;
     if (active) {
@@ -489,11 +508,11 @@ __global__ void __launch_bounds__(128) row_kernel(const __grid_constant__ LossRo
             cluster_arrive();  // no more reads from here; waited for at the end
             z = warp_sum(z, c);
         }
-        const float ln_s = logf(z.s) + c.rest(z.m) * kLn2;
-        const float logp = (xa - z.m) * a.inv_temperature - ln_s;
+        const float ln_s = c.log_of(z.m, z.s);
+        const float logp = scaled(xa - z.m, a) - ln_s;
         if (MODE == kForward && rank == 0 && tid == 0) {
             a.logp[row] = logp;
-            a.lse[row] = z.m * a.inv_temperature + ln_s;
+            a.lse[row] = scaled(z.m, a) + ln_s;
         }
         if (MODE == kPolicy) {
             const float2 loss = Policy(a, row, weight).at(logp, a);
@@ -606,7 +625,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2)
     }
     pdl_wait();
 
-    const Scale c(a.inv_temperature);
+    const Scale c(a);
     const int64_t step = CLUSTER ? gridDim.x / parts : gridDim.x;
     int64_t row = CLUSTER ? blockIdx.x / parts : blockIdx.x;
     const auto copy = [&](const Row<E> &x, const Lines<E> &l, int i) {  // lane 0
@@ -688,7 +707,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2)
             if (CLUSTER && lane + 32 < all)
                 z = join(z, to[lane + 32], c);
             z = warp_sum(z, c);
-            const float logp = (xa - z.m) * a.inv_temperature - (logf(z.s) + c.rest(z.m) * kLn2);
+            const float logp = scaled(xa - z.m, a) - c.log_of(z.m, z.s);
             const float2 loss = policy.at(logp, a);
             coef = loss.y;
             inv = ex2(-c.rest(z.m)) * inverse(z.s);
@@ -763,10 +782,10 @@ __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ L
     const bool zero = target < 0 || weight == 0.0f;
     const int each = (x.last - x.first + parts - 1) / parts;
     const int lo = min(x.last, x.first + rank * each), hi = min(x.last, lo + each);
-    const Scale c(a.inv_temperature);
+    const Scale c(a);
     // exp(x / tau - lse) = exp2(c (x - hi)) exp2(-c lo), hi + lo = lse tau
     const float lse = a.lse[row], at = lse * a.temperature;
-    const float low = fmaf(lse, a.temperature, -at);
+    const float low = fmaf(lse, a.temperature, -at) + lse * a.temperature_low;
     const float inv = fabsf(low) <= FLT_MAX ? ex2(-low * c.near) : 1.0f;
     const Gradient<E> d(x, a, c, target < x.V() ? weight * a.grad_scale : quiet_nan(), inv, at, target);
     int k = lo + tid;

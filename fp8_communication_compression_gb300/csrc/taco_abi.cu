@@ -839,9 +839,10 @@ taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, c
 }
 
 // Shared checks of the losses over the vocabulary.
-static taco_status check_loss(int64_t T, int64_t V, int64_t N, float temperature)
+static taco_status check_loss(int64_t T, int64_t V, int64_t N, double temperature)
 {
-    if (T < 0 || V < 1 || N < V || !positive_finite(temperature) || !positive_finite(1.0f / temperature))
+    if (T < 0 || V < 1 || N < V || !positive_finite(static_cast<float>(temperature)) ||
+        !positive_finite(static_cast<float>(1.0 / temperature)))
         return TACO_ERR_INVALID_ARG;
     if (T >= (int64_t(1) << 31) || N > (int64_t(1) << 31) - 64)
         return TACO_ERR_UNSUPPORTED;
@@ -849,17 +850,21 @@ static taco_status check_loss(int64_t T, int64_t V, int64_t N, float temperature
 }
 
 static taco::LossRows loss_rows(const void *logits, const int64_t *targets, int64_t T, int64_t V, int64_t N,
-                                float temperature)
+                                double temperature)
 {
     taco::LossRows a = {};
     a.logits = logits, a.targets = targets;
     a.T = T, a.V = V, a.N = N;
-    a.temperature = temperature, a.inv_temperature = 1.0f / temperature, a.grad_scale = 1.0f;
+    a.temperature = static_cast<float>(temperature);
+    a.temperature_low = static_cast<float>(temperature - a.temperature);
+    a.inv_temperature = static_cast<float>(1.0 / temperature);
+    a.inv_temperature_low = static_cast<float>(1.0 / temperature - a.inv_temperature);
+    a.grad_scale = 1.0f;
     return a;
 }
 
 taco_status token_logprob(const void *logits, int32_t logits_bf16, const int64_t *targets, int64_t T, int64_t V,
-                          int64_t N, float temperature, float *logp, float *lse, taco_stream_t stream)
+                          int64_t N, double temperature, float *logp, float *lse, taco_stream_t stream)
 {
     taco_status st = check_loss(T, V, N, temperature);
     if (st != TACO_OK || T == 0)
@@ -880,7 +885,7 @@ taco_status token_logprob(const void *logits, int32_t logits_bf16, const int64_t
 
 taco_status token_logprob_backward(const float *dlogp, const void *logits, int32_t logits_bf16,
                                    const int64_t *targets, const float *lse, int64_t T, int64_t V, int64_t N,
-                                   float temperature, void *dlogits, taco_stream_t stream)
+                                   double temperature, void *dlogits, taco_stream_t stream)
 {
     taco_status st = check_loss(T, V, N, temperature);
     if (st != TACO_OK || T == 0)
@@ -902,7 +907,7 @@ taco_status token_logprob_backward(const float *dlogp, const void *logits, int32
 
 taco_status policy_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const float *old_logp,
                         const float *advantages, const float *weights, const float *ref_logp, int64_t T, int64_t V,
-                        int64_t N, float temperature, float clip_low, float clip_high, float kl, float grad_scale,
+                        int64_t N, double temperature, float clip_low, float clip_high, float kl, float grad_scale,
                         float *loss, float *token_loss, float *logp, void *dlogits, taco_stream_t stream)
 {
     taco_status st = check_loss(T, V, N, temperature);
@@ -944,7 +949,7 @@ taco_status preference_loss_workspace_bytes(int64_t T, int64_t pairs, uint64_t *
 }
 
 taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const int64_t *offsets,
-                            const float *ref_logp, int64_t T, int64_t V, int64_t N, int64_t pairs, float temperature,
+                            const float *ref_logp, int64_t T, int64_t V, int64_t N, int64_t pairs, double temperature,
                             float beta, float label_smoothing, int32_t mean, float grad_scale, float *loss,
                             float *margin, float *logratio, float *logp, void *dlogits, void *workspace,
                             uint64_t workspace_bytes, taco_stream_t stream)

@@ -648,17 +648,17 @@ taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, c
  * no gradient.  The workspace is 256-byte aligned.
  */
 taco_status token_logprob(const void *logits, int32_t logits_bf16, const int64_t *targets, int64_t T, int64_t V,
-                          int64_t N, float temperature, float *logp, float *lse, taco_stream_t stream);
+                          int64_t N, double temperature, float *logp, float *lse, taco_stream_t stream);
 taco_status token_logprob_backward(const float *dlogp, const void *logits, int32_t logits_bf16,
                                    const int64_t *targets, const float *lse, int64_t T, int64_t V, int64_t N,
-                                   float temperature, void *dlogits, taco_stream_t stream);
+                                   double temperature, void *dlogits, taco_stream_t stream);
 taco_status policy_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const float *old_logp,
                         const float *advantages, const float *weights, const float *ref_logp, int64_t T, int64_t V,
-                        int64_t N, float temperature, float clip_low, float clip_high, float kl, float grad_scale,
+                        int64_t N, double temperature, float clip_low, float clip_high, float kl, float grad_scale,
                         float *loss, float *token_loss, float *logp, void *dlogits, taco_stream_t stream);
 taco_status preference_loss_workspace_bytes(int64_t T, int64_t pairs, uint64_t *bytes);
 taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64_t *targets, const int64_t *offsets,
-                            const float *ref_logp, int64_t T, int64_t V, int64_t N, int64_t pairs, float temperature,
+                            const float *ref_logp, int64_t T, int64_t V, int64_t N, int64_t pairs, double temperature,
                             float beta, float label_smoothing, int32_t mean, float grad_scale, float *loss,
                             float *margin, float *logratio, float *logp, void *dlogits, void *workspace,
                             uint64_t workspace_bytes, taco_stream_t stream);
