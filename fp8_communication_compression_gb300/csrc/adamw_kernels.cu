@@ -19,9 +19,17 @@
 // A launch takes its tensors' descriptions as parameters, so that nothing is
 // copied or kept.  Warps take spans of the tensors in turn, and find each span's
 // tensor by bisection.  (One long part of all values for each warp, found once,
-// takes 5 % longer: the parts with many tensors' ends finish last.)  Bound by
-// HBM; a lane takes four consecutive elements, a warp one block of 128, whose
-// maximum is one warp reduction.
+// takes 5 % longer: the parts with many tensors' ends finish last.)  A lane takes
+// four consecutive values, a warp one block of 128, whose maximum is one warp
+// reduction.
+//
+// States in 32 bits are bound by HBM: 60M values of 292 tensors with bf16
+// gradients, bf16 copies and clipping 295 us, of which the norm takes 27 (5600
+// GB/s).  States in 8 bits are bound by instructions, about 70 a value (a tenth
+// for the hash, a third for the codes): 201M values with FP8 gradients 572 to 585
+// us, of which the norm takes 40 (5300 GB/s); a kernel without the codes takes
+// 537.  Loads straight into registers, before bulk copies took them over, took
+// 633.
 
 #include "device_utils.cuh"
 #include "internal.h"
