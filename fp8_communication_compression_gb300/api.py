@@ -807,6 +807,13 @@ class PreferenceLoss(NamedTuple):
     dlogits: torch.Tensor | None
 
 
+def _row_values(t, name: str, T: int) -> None:
+    """fp32, one value a row (_need's checks, in fewer steps where they hold)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.numel() == T and t.is_cuda
+            and t.is_contiguous()):
+        _need(t, name, _F32, T)
+
+
 def _logits_args(logits, targets, vocab):
     """(T, V, N, bf16) of logits [..., N] and targets with T elements."""
     _need(logits, "logits", _LOGITS)
@@ -859,8 +866,8 @@ def token_logprob_backward(dlogp: torch.Tensor, logits: torch.Tensor, targets: t
     forward's lse; ``dlogits`` may be the logits themselves.  Rows with dlogp
     = 0 or without a token get zeros, and their logits are not read."""
     T, V, N, bf16 = _logits_args(logits, targets, vocab)
-    _need(dlogp, "dlogp", _F32, T)
-    _need(lse, "lse", _F32, T)
+    _row_values(dlogp, "dlogp", T)
+    _row_values(lse, "lse", T)
     out = _dlogits(logits, True, dlogits, stream)
     st = _lib.load().token_logprob_backward(dlogp.data_ptr(), logits.data_ptr(), bf16, targets.data_ptr(),
                                             lse.data_ptr(), T, V, N, temperature, out.data_ptr(),
@@ -885,16 +892,17 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     their other inputs hold.  The gradient is multiplied by ``grad_scale``;
     ``dlogits`` may be the logits themselves."""
     T, V, N, bf16 = _logits_args(logits, targets, vocab)
-    _need(old_logp, "old_logp", _F32, T)
-    _need(advantages, "advantages", _F32, T)
-    _need(weights, "weights", _F32, T)
+    _row_values(old_logp, "old_logp", T)
+    _row_values(advantages, "advantages", T)
+    _row_values(weights, "weights", T)
     if ref_logp is not None:
-        _need(ref_logp, "ref_logp", _F32, T)
+        _row_values(ref_logp, "ref_logp", T)
     elif kl != 0.0:
         raise ValueError("a KL term needs ref_logp")
     out = _dlogits(logits, need_grad, dlogits, stream)
     buf = _new(2 * T + 1, torch.float32, logits.device, stream)
-    loss, token_loss, logp = buf[2 * T], buf[:T], buf[T:2 * T]
+    token_loss, logp, loss = buf.split((T, T, 1))
+    loss = loss.view(())
     at = buf.data_ptr()
     st = _lib.load().policy_loss(logits.data_ptr(), bf16, targets.data_ptr(), old_logp.data_ptr(),
                                  advantages.data_ptr(), weights.data_ptr(), _ptr(ref_logp), T, V, N, temperature,
@@ -922,11 +930,12 @@ def preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torch.
     if offsets.dim() != 1 or offsets.numel() < 3 or offsets.numel() % 2 == 0:
         raise ValueError(f"offsets has shape {tuple(offsets.shape)}, expected (2 pairs + 1,)")
     if ref_logp is not None:
-        _need(ref_logp, "ref_logp", _F32, T)
+        _row_values(ref_logp, "ref_logp", T)
     pairs = offsets.numel() // 2
     out = _dlogits(logits, need_grad, dlogits, stream)
     buf = _new(T + 3 * pairs + 1, torch.float32, logits.device, stream)
-    logp, logratio, margin, loss = buf[:T], buf[T:T + 2 * pairs], buf[T + 2 * pairs:T + 3 * pairs], buf[T + 3 * pairs]
+    logp, logratio, margin, loss = buf.split((T, 2 * pairs, pairs, 1))
+    loss = loss.view(())
     nbytes = 4 * (2 * T + pairs)
     ws = _workspace(nbytes, logits.device, stream)
     at = buf.data_ptr()

@@ -758,28 +758,20 @@ template <typename D, int MAX> int fill(Table<D, MAX> &t, const D *tensors, int6
     return need < 1 ? 1 : need < resident ? static_cast<int>(need) : resident;
 }
 
-template <typename K> cudaError_t resident(K kernel, size_t smem, int *grid)
-{
-    DeviceInfo di;
-    cudaError_t e = current_device_info(&di);
-    int per_sm = 0;
-    if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
-    *grid = di.num_sms * (per_sm < 1 ? 1 : per_sm);
-    return e;
-}
-
 constexpr int kNormGrid = 2048;  // partial sums of a launch (at most)
 
 template <int MAX>
 cudaError_t norm_launch(const grad_tensor *tensors, int64_t count, TwoPart *partial, int *used, cudaStream_t stream)
 {
     Table<grad_tensor, MAX> t;
-    int grid = 0;
-    cudaError_t e = resident(norm_kernel<MAX>, 0, &grid);
-    if (e != cudaSuccess)
+    static std::atomic<uint64_t> last[kMaxDevices];
+    DeviceInfo di;
+    int per_sm = 0;
+    cudaError_t e = current_device_info(&di);
+    if (e != cudaSuccess || (e = ctas_per_sm(norm_kernel<MAX>, kThreads, 0, di.device, last, &per_sm)) != cudaSuccess)
         return e;
-    grid = fill(t, tensors, count, kNormUnit, grid < kNormGrid ? grid : kNormGrid);
+    const int resident = di.num_sms * per_sm;
+    const int grid = fill(t, tensors, count, kNormUnit, resident < kNormGrid ? resident : kNormGrid);
     *used = grid;
     return launch_pdl(norm_kernel<MAX>, grid, kThreads, 0, stream, t, partial);
 }
@@ -801,11 +793,12 @@ cudaError_t adamw_launch(const adamw_tensor *tensors, int64_t count, const Hyper
     if ((e = ensure_smem(kernel, kThreads / 32 * Slot<BITS8>::slots * (Slot<BITS8>::grad + 4 * Slot<BITS8>::values), di.device,
                          done)) != cudaSuccess)
         return e;
-    int grid = 0;
-    if ((e = resident(kernel, smem, &grid)) != cudaSuccess)
+    static std::atomic<uint64_t> last[kMaxDevices];
+    int per_sm = 0;
+    if ((e = ctas_per_sm(kernel, kThreads, smem, di.device, last, &per_sm)) != cudaSuccess)
         return e;
     Table<adamw_tensor, MAX> t;
-    grid = fill(t, tensors, count, Slot<BITS8>::values, grid);
+    const int grid = fill(t, tensors, count, Slot<BITS8>::values, di.num_sms * per_sm);
     return launch_pdl(kernel, grid, kThreads, smem, stream, t, h, slot);
 }
 

@@ -225,6 +225,26 @@ cudaError_t ensure_smem(K kernel, uint32_t bytes, int device, std::atomic<bool> 
     return e;
 }
 
+// CTAs of `threads` threads and `smem` bytes of dynamic shared memory that fit an
+// SM, at least 1.  The last answer for each device is kept in `last` (the query
+// takes a microsecond), packed into one word.
+template <typename K>
+cudaError_t ctas_per_sm(K kernel, int threads, size_t smem, int device, std::atomic<uint64_t> *last, int *ctas)
+{
+    const uint64_t key = static_cast<uint64_t>(smem) << 32 | static_cast<uint64_t>(threads) << 16;
+    const uint64_t known = last[device].load(std::memory_order_relaxed);
+    if (known && (known & ~uint64_t(0xFFFF)) == key) {
+        *ctas = static_cast<int>(known & 0xFFFF);
+        return cudaSuccess;
+    }
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    *ctas = n < 1 ? 1 : n;
+    if (e == cudaSuccess)
+        last[device].store(key | static_cast<uint64_t>(*ctas), std::memory_order_relaxed);
+    return e;
+}
+
 // Launches `kernel` with programmatic stream serialization allowed, so that
 // it can be scheduled while the previous kernel in the stream drains (every
 // kernel of this library waits for its predecessor with griddepcontrol.wait

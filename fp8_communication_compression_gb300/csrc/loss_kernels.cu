@@ -961,10 +961,11 @@ template <typename E> cudaError_t launch_policy(const LossRows &a, bool *taken, 
     static std::atomic<bool> done[2][kMaxDevices];
     if ((e = ensure_smem(kernel, kMaxLines * kMaxWarps * kLine * 16, di.device, done[parts > 1])) != cudaSuccess)
         return e;
+    static std::atomic<uint64_t> last[2][kMaxDevices];
     int per_sm = 0;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, warps * 32, smem)) != cudaSuccess)
+    if ((e = ctas_per_sm(kernel, warps * 32, smem, di.device, last[parts > 1], &per_sm)) != cudaSuccess)
         return e;
-    const int64_t clusters = static_cast<int64_t>(di.num_sms) * (per_sm < 1 ? 1 : per_sm) / parts;
+    const int64_t clusters = static_cast<int64_t>(di.num_sms) * per_sm / parts;
     const int64_t grid = a.T < clusters ? a.T : clusters;
     return launch_cluster(kernel, grid * parts, warps * 32, smem, parts, stream, a, parts, max_lines,
                           static_cast<int>(grid * parts <= di.num_sms));
