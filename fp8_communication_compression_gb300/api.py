@@ -900,14 +900,12 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     elif kl != 0.0:
         raise ValueError("a KL term needs ref_logp")
     out = _dlogits(logits, need_grad, dlogits, stream)
-    buf = _new(2 * T + 1, torch.float32, logits.device, stream)
-    token_loss, logp, loss = buf.split((T, T, 1))
-    loss = loss.view(())
-    at = buf.data_ptr()
+    dev, f32 = logits.device, torch.float32  # (three allocations take less time than three views of one)
+    loss, token_loss, logp = _new((), f32, dev, stream), _new(T, f32, dev, stream), _new(T, f32, dev, stream)
     st = _lib.load().policy_loss(logits.data_ptr(), bf16, targets.data_ptr(), old_logp.data_ptr(),
                                  advantages.data_ptr(), weights.data_ptr(), _ptr(ref_logp), T, V, N, temperature,
-                                 clip_low, clip_high, kl, grad_scale, at + 8 * T, at, at + 4 * T, _ptr(out),
-                                 _stream_of(logits, stream))
+                                 clip_low, clip_high, kl, grad_scale, loss.data_ptr(), token_loss.data_ptr(),
+                                 logp.data_ptr(), _ptr(out), _stream_of(logits, stream))
     _lib.check("policy_loss", st)
     return PolicyLoss(loss, token_loss, logp, out)
 
@@ -933,16 +931,15 @@ def preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torch.
         _row_values(ref_logp, "ref_logp", T)
     pairs = offsets.numel() // 2
     out = _dlogits(logits, need_grad, dlogits, stream)
-    buf = _new(T + 3 * pairs + 1, torch.float32, logits.device, stream)
-    logp, logratio, margin, loss = buf.split((T, 2 * pairs, pairs, 1))
-    loss = loss.view(())
+    dev, f32 = logits.device, torch.float32
+    loss, margin = _new((), f32, dev, stream), _new(pairs, f32, dev, stream)
+    logratio, logp = _new(2 * pairs, f32, dev, stream), _new(T, f32, dev, stream)
     nbytes = 4 * (2 * T + pairs)
-    ws = _workspace(nbytes, logits.device, stream)
-    at = buf.data_ptr()
+    ws = _workspace(nbytes, dev, stream)
     st = _lib.load().preference_loss(logits.data_ptr(), bf16, targets.data_ptr(), offsets.data_ptr(), _ptr(ref_logp),
                                      T, V, N, pairs, temperature, beta, label_smoothing, int(mean), grad_scale,
-                                     at + 4 * (T + 3 * pairs), at + 4 * (T + 2 * pairs), at + 4 * T, at, _ptr(out),
-                                     ws.data_ptr(), nbytes, _stream_of(logits, stream))
+                                     loss.data_ptr(), margin.data_ptr(), logratio.data_ptr(), logp.data_ptr(),
+                                     _ptr(out), ws.data_ptr(), nbytes, _stream_of(logits, stream))
     _lib.check("preference_loss", st)
     return PreferenceLoss(loss, margin, logratio, logp, out)
 
