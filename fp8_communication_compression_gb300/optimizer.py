@@ -25,7 +25,8 @@ _PLAIN = {torch.float32: 0, torch.bfloat16: 1}  # TACO_GRAD_* of gradients witho
 
 class AdamW:
     """``params``: fp32 tensors, updated in place; ``copies``: bf16 tensors of
-    the same sizes, or None in places or altogether.  ``lr`` and
+    the same sizes, or None in places or altogether; both keep their memory
+    (a step refuses tensors that have got other).  ``lr`` and
     ``weight_decay``: one number, or one a tensor.  ``state_bits``: 32 or 8.
     ``max_norm``: the norm that the gradients are clipped to; a step whose norm
     is not finite is then left out.  ``seed``: of the 8-bit states' rounding.
@@ -78,6 +79,8 @@ class AdamW:
         self.m_scale = torch.ones(at // 128, device=self.device) if state_bits == 8 else None
         self.v_scale = torch.ones(at // 128, device=self.device) if state_bits == 8 else None
         self.steps = new(2, torch.int64)
+        self._kept = every
+        self._at = [t.data_ptr() for t in every]
         size = self.m.element_size()
         self._index = params[0].get_device()
         self._seed = seed & (1 << 64) - 1
@@ -102,6 +105,8 @@ class AdamW:
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
         if lr_factor is not None:
             api._need(lr_factor, "lr_factor", (torch.float32,), 1)
+        if [t.data_ptr() for t in self._kept] != self._at:
+            raise RuntimeError("a tensor of this AdamW has got other memory; make a new one and load its state")
         pointers, scales, kinds = [], [], []
         index = self._index
         for g, n in zip(grads, self.sizes):

@@ -10,7 +10,7 @@ import torch
 
 import fp8_reference as F
 import training_reference as R
-from fp8_communication_compression_gb300 import AdamW, api
+from fp8_communication_compression_gb300 import AdamW, _lib, api
 
 pytestmark = pytest.mark.gpu
 
@@ -306,3 +306,31 @@ def test_elements_beyond_32_bits():
     lo, hi, sc, dsc = R.code_range(m[skip:], dm[skip:], bits & 0xFFFF, False)
     got = F.code_values(opt.m[n - k + skip:n].view(torch.uint8))
     assert ((lo <= got.abs()) & (got.abs() <= hi)).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_what_lies_around_the_tensors_is_left(bits):
+    sizes = [1, 127, 515, 4097, 2048]
+    place = [128 * i + sum(-(-n // 128) * 128 for n in sizes[:i]) for i in range(len(sizes))]
+    total = place[-1] + sizes[-1] + 128
+    p, c = torch.full((total,), 7.0, device="cuda"), torch.full((total,), 7.0, dtype=torch.bfloat16, device="cuda")
+    part = lambda t: [t[a + 64:a + 64 + n] for a, n in zip(place, sizes)]
+    inside = torch.zeros(total, dtype=torch.bool, device="cuda")
+    for t in part(inside):
+        t.fill_(True)
+    opt = AdamW(part(p), part(c), lr=0.1, weight_decay=0.1, state_bits=bits, max_norm=1.0)
+    opt.step([torch.ones(n, device="cuda") for n in sizes])
+    assert (p[~inside] == 7.0).all() and (c[~inside] == 7.0).all()
+    assert (p[inside] != 7.0).all() and torch.equal(c[inside], p[inside].bfloat16())
+
+
+def test_a_tensor_with_other_memory_is_refused():
+    p, g = torch.ones(256, device="cuda"), torch.ones(256, device="cuda")
+    opt = AdamW([p])
+    opt.step([g])
+    with pytest.raises(_lib.TacoError):
+        opt.step([p])                               # its own gradient
+    p.data = torch.ones(256, device="cuda")
+    with pytest.raises(RuntimeError):
+        opt.step([g])
+    assert opt.steps.tolist() == [1, 0]

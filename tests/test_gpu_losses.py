@@ -277,3 +277,22 @@ def test_offsets_beyond_32_bits():
     small = api.token_logprob_backward(d[-4:], last, a[-4:], lse[-4:].contiguous())
     api.token_logprob_backward(d, x, a, lse, dlogits=x)
     assert torch.equal(x[-4:], small) and not x[:-4].any()
+
+
+@pytest.mark.parametrize("dt,V", [(BF, 1000003), (F32, 500001)], ids=["bf16", "f32"])
+def test_rows_longer_than_shared_memory(dt, V):
+    """A vocabulary that a cluster's shared memory does not hold."""
+    T = 3
+    x, a, g = make(T, V, V, dt, 11)
+    logp = R.logprob(x, a, V, 1.0)[0]
+    old = (logp - 0.05).float().cuda()
+    adv, w = torch.tensor([1.0, -1.0, 0.5]).cuda(), torch.tensor([0.5, 0.25, 0.0]).cuda()
+    want = R.policy(x, a, old, adv, w, old, 0.2, 0.2, 0.1, V, 1.0)
+    got = api.policy_loss(x, a, old, adv, w, old, kl=0.1)
+    for name, v in want.items():
+        close(getattr(got, name), v, name)
+    y = x.clone()
+    api.policy_loss(y, a, old, adv, w, old, kl=0.1, dlogits=y)
+    assert torch.equal(y, got.dlogits)
+    one = api.policy_loss(x[:1], a[:1], old[:1], adv[:1], w[:1])       # one row: its loss is the sum
+    assert torch.equal(one.loss, one.token_loss[0]) and one.dlogits.any()
