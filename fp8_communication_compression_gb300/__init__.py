@@ -8,7 +8,8 @@ include/taco.h) with a thin Python binding.
 
 from .api import (HostPipeline, TwoShotLocal, agoq_fp8_accumulate, agoq_laaq_dequantize,
                   agoq_laaq_quantize, agoq_reduce_shards, fp8_gemm, fp8_linear, fp8_linear_backward,
-                  fp8_quantize, fp8_quantize_weight, fp8_scales, grad_norm, policy_loss, preference_loss, rmsnorm_gate_residual, rmsnorm_gate_residual_backward,
+                  fp8_quantize, fp8_quantize_weight, fp8_scales, grad_norm, policy_loss, preference_loss,
+                  rmsnorm_gate_residual, rmsnorm_gate_residual_backward,
                   rmsnorm_gate_residual_fp8, taco_compress,
                   taco_compress_int8, taco_decompress, taco_decompress_int8, taco_device_error,
                   taco_e4m3_encode, taco_reduce_decompress, taco_reduce_shards, token_logprob,
@@ -18,7 +19,8 @@ from .fp8_head import Fp8Head
 from .optimizer import AdamW
 
 __all__ = ["Fp8Block", "Fp8Head", "AdamW", "token_logprob", "token_logprob_backward", "policy_loss",
-           "preference_loss", "grad_norm", "taco_compress", "taco_decompress", "taco_compress_int8", "taco_decompress_int8",
+           "preference_loss", "grad_norm",
+           "taco_compress", "taco_decompress", "taco_compress_int8", "taco_decompress_int8",
            "taco_reduce_shards", "taco_reduce_decompress",
            "agoq_fp8_accumulate", "agoq_laaq_quantize", "agoq_laaq_dequantize",
            "agoq_reduce_shards", "fp8_quantize", "fp8_quantize_weight", "fp8_scales", "fp8_gemm", "fp8_linear",

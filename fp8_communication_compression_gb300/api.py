@@ -962,7 +962,8 @@ def _grad_of(g, name: str, numel: int | None, device: int):
         raise TypeError(f"{name} must be fp32, bf16, or FP8 codes with their scale")
     n = g.numel()
     if g.get_device() != device or not g.is_contiguous() or (numel is not None and n != numel):
-        raise ValueError(f"{name} must be contiguous, on cuda:{device}" + ("" if numel is None else f", with {numel} values"))
+        size = "" if numel is None else f", with {numel} values"
+        raise ValueError(f"{name} must be contiguous, on cuda:{device}{size}")
     if scale is None:
         return g.data_ptr(), None, n, kind
     if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or scale.get_device() != device \

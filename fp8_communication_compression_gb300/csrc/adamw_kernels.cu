@@ -26,7 +26,7 @@
 // States in 32 bits are bound by HBM: 60M values of 292 tensors with bf16
 // gradients, bf16 copies and clipping 295 us, of which the norm takes 27 (5600
 // GB/s).  States in 8 bits are bound by instructions, about 70 a value (a tenth
-// for the hash, a third for the codes): 201M values with FP8 gradients 572 to 585
+// for the hash, a third for the codes): 201M values with FP8 gradients 572 to 597
 // us, of which the norm takes 40 (5300 GB/s); a kernel without the codes takes
 // 537.  Loads straight into registers, before bulk copies took them over, took
 // 633.
@@ -66,7 +66,8 @@ template <typename D, int MAX, bool LAST_FIRST> struct Walk {
     int tensor;
     int span;           // the next span
 
-    __device__ __forceinline__ Walk(const Table<D, MAX> &table) : t(table), left(0), span(blockIdx.x * (kThreads / 32) + threadIdx.x / 32)
+    __device__ __forceinline__ Walk(const Table<D, MAX> &table)
+        : t(table), left(0), span(blockIdx.x * (kThreads / 32) + threadIdx.x / 32)
     {
     }
     // The next unit of `values` values, from `base` on: false behind the last.
@@ -472,7 +473,8 @@ __device__ __forceinline__ Codes to_codes(const F4 &m, const F4 &root, uint32_t 
     }
     Codes c;
     c.m_scale = __uint_as_float(top_m) * (1.0f / 448.0f), c.r_scale = __uint_as_float(top_r) * (1.0f / 448.0f);
-    const float least = min3_abs(min3_abs(min3_abs(y.a.x, y.a.y, y.b.x), y.b.y, z.a.x), min3_abs(z.a.y, z.b.x, z.b.y), 448.0f);
+    const float least = min3_abs(min3_abs(min3_abs(y.a.x, y.a.y, y.b.x), y.b.y, z.a.x),
+                                 min3_abs(z.a.y, z.b.x, z.b.y), 448.0f);
     const bool usual = top_m >= kLeast && top_r >= kLeast && top_r < kMost;
     if (__any_sync(~0u, !(least >= 0.015625f)) || !usual)
         return unusual_codes(c, y, z, make_uint4(um[0], um[1], um[2], um[3]),
@@ -790,8 +792,8 @@ cudaError_t adamw_launch(const adamw_tensor *tensors, int64_t count, const Hyper
     if (e != cudaSuccess)
         return e;
     static std::atomic<bool> done[kMaxDevices];
-    if ((e = ensure_smem(kernel, kThreads / 32 * Slot<BITS8>::slots * (Slot<BITS8>::grad + 4 * Slot<BITS8>::values), di.device,
-                         done)) != cudaSuccess)
+    constexpr int kMostBytes = kThreads / 32 * Slot<BITS8>::slots * (Slot<BITS8>::grad + 4 * Slot<BITS8>::values);
+    if ((e = ensure_smem(kernel, kMostBytes, di.device, done)) != cudaSuccess)
         return e;
     static std::atomic<uint64_t> last[kMaxDevices];
     int per_sm = 0;
@@ -836,7 +838,8 @@ cudaError_t launch_grad_norm(const grad_tensor *tensors, int64_t count, float gr
 {
     TwoPart *partial = static_cast<TwoPart *>(workspace);
     int total = 0;
-    const cudaError_t e = launch_squares(tensors, count, [](const grad_tensor &t) { return t; }, partial, &total, stream);
+    const cudaError_t e =
+        launch_squares(tensors, count, [](const grad_tensor &t) { return t; }, partial, &total, stream);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(norm_total_kernel, 1, kThreads, 0, stream, static_cast<const TwoPart *>(partial), total,

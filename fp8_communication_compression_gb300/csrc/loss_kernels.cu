@@ -304,7 +304,10 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The sum of CTA `rank` of the cluster at the same place of its shared memory.
@@ -454,7 +457,6 @@ __device__ __forceinline__ Sum warp_sum(Sum z, const Scale &c)
 template <typename E, int MODE, bool CLUSTER>
 __global__ void __launch_bounds__(128) row_kernel(const __grid_constant__ LossRows a, int parts, int trigger)
 {
-    constexpr int G = Row<E>::G;
     __shared__ Sum part[4], mine;
     const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
@@ -774,7 +776,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2)
 template <typename E>
 __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ LossRows a, int parts, int trigger)
 {
-    constexpr int G = Row<E>::G;
     if (trigger)
         pdl_trigger();
     pdl_wait();
