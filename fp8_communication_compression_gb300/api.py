@@ -934,7 +934,7 @@ def preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torch.
     dev, f32 = logits.device, torch.float32
     loss, margin = _new((), f32, dev, stream), _new(pairs, f32, dev, stream)
     logratio, logp = _new(2 * pairs, f32, dev, stream), _new(T, f32, dev, stream)
-    nbytes = 4 * (2 * T + pairs)
+    nbytes = 4 * (3 * T + pairs)
     ws = _workspace(nbytes, dev, stream)
     st = _lib.load().preference_loss(logits.data_ptr(), bf16, targets.data_ptr(), offsets.data_ptr(), _ptr(ref_logp),
                                      T, V, N, pairs, temperature, beta, label_smoothing, int(mean), grad_scale,

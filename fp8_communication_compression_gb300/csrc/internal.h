@@ -163,10 +163,11 @@ struct LossRows {
     int64_t T, V, N;
     float temperature, temperature_low, inv_temperature, inv_temperature_low;  // each in two parts
     float grad_scale;
-    float *logp, *lse, *coef;            // forward; coef: zeroed in rows that do not count (may be null)
+    float *logp, *lse;                   // forward, or (max, inv_sum, coef) instead of lse:
+    float *max, *inv_sum, *coef;         // coef: zeroed in rows that do not count
     const int64_t *offsets;              // rows outside offsets[0] .. offsets[sequences] do not count (may be null)
     int64_t sequences;
-    const float *dlogp;                  // backward (with lse)
+    const float *dlogp;                  // backward (with lse, or max and inv_sum)
     const float *old_logp, *advantages, *weights, *ref_logp;  // policy loss
     float clip_lo, clip_hi, kl;
     float *token_loss, *loss;

@@ -166,8 +166,9 @@ __device__ __forceinline__ uint4 packed(const float (&f)[4])
 // further below log2 e than its product's rounding), so that -inf stays -inf.
 // Exponents are x c - k by two fused steps, k the whole number next to m hi: sums
 // relative to different k are joined by powers of two, exactly; what k is off by
-// is known (rest) and goes into the sum's logarithm.  Where m c leaves fp32's
-// range (rows of the lowest value alone), differences are scaled instead.
+// is known (rest) and goes into the sum's logarithm.  Where m c has no fraction
+// left in fp32 (rows of nothing but -1e9, say, or of the lowest value),
+// differences are scaled instead.
 struct Scale {
     float hi, lo, near;
     __device__ explicit Scale(const LossRows &a)
@@ -176,7 +177,7 @@ struct Scale {
         lo = fmaxf(fmaf(a.inv_temperature, kLog2eHigh, -hi) + a.inv_temperature * kLog2eLow +
                        a.inv_temperature_low * kLog2e, FLT_MIN);
     }
-    static __device__ __forceinline__ bool plain(float k) { return fabsf(k) <= 1e37f; }
+    static __device__ __forceinline__ bool plain(float k) { return fabsf(k) <= 4194304.0f; }
     __device__ __forceinline__ float whole(float m) const { return rintf(m * hi); }
     __device__ __forceinline__ float exponent(float x, float m) const
     {
@@ -187,7 +188,7 @@ struct Scale {
     __device__ __forceinline__ float factor(float m, float to) const
     {
         const float k = whole(m), t = whole(to);
-        return ex2(plain(k) && plain(t) ? k - t : (m - to) * near);
+        return ex2(plain(k) && plain(t) ? k - t : (m - to) * near + (rest(m) - rest(to)));
     }
     // The sum is of 2^(x c - m c - rest).
     __device__ __forceinline__ float rest(float m) const
@@ -517,7 +518,12 @@ __global__ void __launch_bounds__(128) row_kernel(const __grid_constant__ LossRo
         const float logp = scaled(xa - z.m, a) - ln_s;
         if (MODE == kForward && rank == 0 && tid == 0) {
             a.logp[row] = logp;
-            a.lse[row] = scaled(z.m, a) + ln_s;
+            if (a.lse) {
+                a.lse[row] = scaled(z.m, a) + ln_s;
+            } else {
+                a.max[row] = z.m;
+                a.inv_sum[row] = ex2(-c.rest(z.m)) * inverse(z.s);
+            }
         }
         if (MODE == kPolicy) {
             const float2 loss = Policy(a, row, weight).at(logp, a);
@@ -533,9 +539,7 @@ __global__ void __launch_bounds__(128) row_kernel(const __grid_constant__ LossRo
     } else if (rank == 0 && tid == 0) {
         a.logp[row] = 0.0f;
         if (MODE == kForward)
-            a.lse[row] = 0.0f;
-        if (MODE == kForward && a.coef)
-            a.coef[row] = 0.0f;
+            *(a.lse ? a.lse + row : a.coef + row) = 0.0f;
         if (MODE == kPolicy) {
             a.token_loss[row] = 0.0f;
             if (a.T == 1)
@@ -772,7 +776,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2)
     }
 }
 
-// The gradient from a given lse; `parts` CTAs a row, each on its own.
+// The gradient from a given lse, or from a row's largest value and the inverse of
+// its sum (exact where an lse has lost the sum beside a large value); `parts`
+// CTAs a row, each on its own.
 template <typename E>
 __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ LossRows a, int parts, int trigger)
 {
@@ -790,10 +796,16 @@ __global__ void __launch_bounds__(256) backward_kernel(const __grid_constant__ L
     const int each = (x.last - x.first + parts - 1) / parts;
     const int lo = min(x.last, x.first + rank * each), hi = min(x.last, lo + each);
     const Scale c(a);
-    // exp(x / tau - lse) = exp2(c (x - hi)) exp2(-c lo), hi + lo = lse tau
-    const float lse = a.lse[row], at = lse * a.temperature;
-    const float low = fmaf(lse, a.temperature, -at) + lse * a.temperature_low;
-    const float inv = fabsf(low) <= FLT_MAX ? ex2(-low * c.near) : 1.0f;
+    float at = 0.0f, inv = 0.0f;
+    if (!zero && a.lse) {
+        // exp(x / tau - lse) = exp2(c (x - at)) exp2(-c low), at + low = lse tau
+        const float lse = a.lse[row];
+        at = lse * a.temperature;
+        const float low = fmaf(lse, a.temperature, -at) + lse * a.temperature_low;
+        inv = fabsf(low) <= FLT_MAX ? ex2(-low * c.near) : 1.0f;
+    } else if (!zero) {
+        at = a.max[row], inv = a.inv_sum[row];
+    }
     const Gradient<E> d(x, a, c, target < x.V() ? weight * a.grad_scale : quiet_nan(), inv, at, target);
     int k = lo + tid;
     if (zero) {

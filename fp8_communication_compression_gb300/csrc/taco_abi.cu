@@ -944,7 +944,8 @@ taco_status preference_loss_workspace_bytes(int64_t T, int64_t pairs, uint64_t *
     *bytes = 0;
     if (T >= (int64_t(1) << 31) || pairs >= (int64_t(1) << 30))
         return TACO_ERR_UNSUPPORTED;
-    *bytes = 4 * (2 * static_cast<uint64_t>(T) + pairs);  // lse, the gradients at logp, the pairs' losses
+    // the rows' largest values, inverse sums and gradients at logp; the pairs' losses
+    *bytes = 4 * (3 * static_cast<uint64_t>(T) + pairs);
     return TACO_OK;
 }
 
@@ -979,11 +980,11 @@ taco_status preference_loss(const void *logits, int32_t logits_bf16, const int64
         return TACO_ERR_INVALID_ARG;
     float *ws = static_cast<float *>(workspace);
     taco::LossRows a = loss_rows(logits, targets, T, V, N, temperature);
-    a.logp = logp, a.lse = ws, a.coef = ws + T, a.dlogp = ws + T;
+    a.logp = logp, a.max = ws, a.inv_sum = ws + T, a.coef = ws + 2 * T, a.dlogp = ws + 2 * T;
     a.offsets = offsets, a.sequences = 2 * pairs;
     a.grad_scale = grad_scale, a.dlogits = dlogits;
     const taco::PairArgs p = {targets, offsets, T,      pairs,    logp,         ref_logp, beta,
-                              label_smoothing, mean != 0, loss, margin, logratio, ws + 2 * T, ws + T};
+                              label_smoothing, mean != 0, loss, margin, logratio, ws + 3 * T, ws + 2 * T};
     return from_cuda(taco::launch_preference_loss(a, p, logits_bf16 != 0, reinterpret_cast<cudaStream_t>(stream)));
 }
 

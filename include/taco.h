@@ -624,7 +624,8 @@ taco_status rmsnorm_gate_residual_backward(const void *dn, const void *dh_out, c
  *
  * token_logprob - logp and lse, fp32 [T].
  *
- * token_logprob_backward - dlogits from dlogp fp32 [T] and the forward's lse.
+ * token_logprob_backward - dlogits from dlogp fp32 [T] and the forward's lse (as
+ * it is given: beside a value of 1e8 its fp32 has no room for the sum's logarithm).
  * Rows with dlogp = 0 get zeros; their logits are not read.
  *
  * policy_loss - per row, with r = exp(logp - old_logp), A = advantages[t] and

@@ -296,3 +296,33 @@ def test_rows_longer_than_shared_memory(dt, V):
     assert torch.equal(y, got.dlogits)
     one = api.policy_loss(x[:1], a[:1], old[:1], adv[:1], w[:1])       # one row: its loss is the sum
     assert torch.equal(one.loss, one.token_loss[0]) and one.dlogits.any()
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("value", [-1e4, -1e6, -3e6, -1e7, -1e9, -1e10, -1e30, 3e6, 1e10, 1e30])
+def test_rows_of_one_large_value(dt, value):
+    """Masked altogether by any value: every token has 1 / V.  Two rows of them
+    hold a value above or below too, whose share is all or nothing."""
+    V = 3001
+    x = torch.full((4, V), value, dtype=dt, device="cuda")
+    x[2, 7], x[3, 7] = x[2, 7] + abs(value) / 2, x[3, 7] - abs(value) / 2
+    a = torch.tensor([0, V - 1, 7, 8]).cuda()
+    logp, lse = api.token_logprob(x, a)
+    want = torch.tensor([-math.log(V), -math.log(V), 0.0, -math.log(V - 1)])
+    # training_reference.logprob's bound: the sum's roundings, and those of ln V
+    tol = (V / 256 + 64) * 2.0 ** -22 + 4 * R.U * (math.log(V) + 1)
+    assert ((logp.cpu() - want).abs() <= tol).all()
+    z = torch.zeros(4, device="cuda")
+    got = api.policy_loss(x, a, logp, z + 1.0, z + 1.0, clip_high=1e3)
+    p = torch.full((4, V), 1.0 / V, dtype=torch.float64)
+    p[2], p[3] = 0.0, 1.0 / (V - 1)
+    p[2, 7], p[3, 7] = 1.0, 0.0
+    hot = torch.zeros(4, V, dtype=torch.float64).scatter_(1, a.cpu()[:, None], 1.0)
+    ref = p - hot                                          # r = 1, A = 1
+    assert ((got.dlogits.cpu().double() - ref).abs() <= R.half_step(ref, dt) + 1e-5 * (p + hot)).all()
+    assert ((got.logp.cpu() - want).abs() <= tol).all()
+    # the preference loss too: slopes of -beta / 2 and beta / 2 (equal margins), halved by the two pairs
+    pairs = api.preference_loss(x, a, torch.arange(5).cuda(), logp, beta=0.4)
+    sign = torch.tensor([-1.0, 1.0, -1.0, 1.0], dtype=torch.float64)[:, None]
+    ref = sign * 0.1 * (hot - p)
+    assert ((pairs.dlogits.cpu().double() - ref).abs() <= R.half_step(ref, dt) + 1e-5 * (p + hot)).all()

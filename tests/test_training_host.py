@@ -65,14 +65,14 @@ def test_preference_validation(lib):
     assert lib.preference_loss_workspace_bytes(-1, 1, ctypes.byref(v)) == INVALID
     assert lib.preference_loss_workspace_bytes(4, 1, None) == INVALID
     assert lib.preference_loss_workspace_bytes(1 << 31, 1, ctypes.byref(v)) == UNSUPPORTED
-    assert lib.preference_loss_workspace_bytes(4, 2, ctypes.byref(v)) == OK and v.value == 4 * (8 + 2)
+    assert lib.preference_loss_workspace_bytes(4, 2, ctypes.byref(v)) == OK and v.value == 4 * (12 + 2)
     f = lambda **k: lib.preference_loss(k.get("x", A), 1, k.get("a", A * 2), k.get("off", A * 3), k.get("ref", A * 4),
                                         k.get("T", 4), 100, 128, k.get("pairs", 2), 1.0, k.get("beta", 0.1),
                                         k.get("ls", 0.0), 0, k.get("gs", 1.0), k.get("loss", A * 5), k.get("m", A * 6),
                                         k.get("r", A * 7), k.get("lp", A * 8), k.get("d", A * 9), k.get("ws", A * 10),
-                                        k.get("n", 40), None)
+                                        k.get("n", 56), None)
     for bad in (dict(pairs=0), dict(ls=-0.1), dict(ls=1.1), dict(ls=math.nan), dict(beta=math.inf), dict(gs=math.nan),
-                dict(n=39), dict(T=-1)):
+                dict(n=55), dict(T=-1)):
         assert f(**bad) == INVALID
     for k in ("x", "a", "off", "loss", "m", "r", "lp", "ws"):
         assert f(**{k: None}) == INVALID
