@@ -26,7 +26,7 @@
 // Bound by HBM.  The forward pass streams a row through registers, four 16-byte
 // loads a thread in flight: 4096 x 50257 in bf16 66 us as a call (6250 GB/s).  The
 // policy loss keeps a row's granules in shared memory between its two readings
-// (policy_kernel): 8192 x 50304 with a quarter of the rows left out 224 to 227 us
+// (policy_kernel): 8192 x 50304 with a quarter of the rows left out 224 to 231 us
 // (6400 GB/s), 293 when each CTA took one row and waited for it, 573 when the row
 // was read from memory twice.  The gradient from a given lse streams likewise:
 // 2048 x 32000 in fp32 82 us (6400 GB/s).  The preference loss needs a pair's
